@@ -379,6 +379,88 @@ int ozaki2_zcrt_debug(int64_t m, int64_t n, int num_moduli, const uint8_t *resid
 /* Workspace bytes for ozaki2_dgemm_debug (larger: raw int32 products). */
 size_t ozaki2_debug_workspace_size(int64_t m, int64_t n, int64_t k, int num_moduli, int mode);
 
+/* ---- INT8 products with scales -------------------------------------------
+ *
+ * The products below take operands that are quantised already, or quantise
+ * 16- or 32-bit activations row by row, on the same INT8 matrix cores that the
+ * emulated products use. Unlike those they are ROW-MAJOR with the inner
+ * dimension contiguous in both operands, the layout of a linear layer:
+ *
+ *   C[i][j] = (sum_h A[i][h] B[j][h]) * a_scale[i] * b_scale[j] + bias[j]
+ *
+ *   t, n, k   rows of A (tokens), rows of B (channels), inner dimension; each
+ *             >= 0, t and n < 2^31, k <= OZAKI2_I8_MAX_K (so that every int32
+ *             sum is exact).
+ *   A, lda    DEVICE int8, element (i, h) at A[i*lda + h], lda >= max(1, k).
+ *   B, ldb    DEVICE int8, element (j, h) at B[j*ldb + h], ldb >= max(1, k).
+ *   a_scale, b_scale   DEVICE binary32 [t], [n].
+ *   bias      DEVICE binary32 [n], or NULL for none.
+ *   C, ldc    DEVICE output of type ctype, element (i, j) at C[i*ldc + j],
+ *             ldc >= max(1, n). C must not overlap the inputs. Elements of C
+ *             between rows (ldc > n) are left as they were.
+ *
+ * The int32 sum is exact. It is rounded to binary32, multiplied by a_scale[i],
+ * then by b_scale[j] and added to the bias in one fused step, each rounding to
+ * nearest, and rounded to ctype, so results do not depend on the kernel, the
+ * tile or the split of k that a size takes. Pointers and pitches may have any
+ * alignment; multiples of 16 bytes are fastest.
+ */
+enum ozaki2_type {
+    OZAKI2_BF16 = 0,
+    OZAKI2_FP16 = 1,
+    OZAKI2_FP32 = 2
+};
+
+/* Largest inner dimension of an int8 product whose sums (of up to 2^14 each)
+ * stay exact in int32. */
+#define OZAKI2_I8_MAX_K ((1 << 17) - 1)
+
+/*
+ * Rows of X (type xtype, element (i, h) at X[i*ldx + h]) as int8 with a scale
+ * each: amax = max_h |X[i][h]|, scale[i] = amax / 127 and
+ * Q[i][h] = rint(X[i][h] * (127 / amax)), in binary32 with ties to even, for
+ * Q[i*ldq + h]. A row of zeros gets scale 0 and zeros; one whose amax is below
+ * 2^-120 gets zeros; one that holds Inf or NaN gets zeros and a NaN scale, so
+ * products with it are NaN. Returns 0, -1..-8 for an invalid argument,
+ * OZAKI2_ERR_UNSUPPORTED (t or k >= 2^31) or OZAKI2_ERR_HIP. Capturable.
+ */
+int ozaki2_quantize_rows(int64_t t, int64_t k, const void *X, int64_t ldx, int xtype, int8_t *Q, int64_t ldq,
+                         float *scale, void *stream);
+
+/*
+ * The product of quantised operands. ozaki2_i8gemm uses the cached workspace
+ * (only sizes whose tiles would leave most compute units idle need any, and a
+ * call that needs none neither takes nor waits for it); the _ws form takes one
+ * of ozaki2_i8gemm_workspace_size bytes (0: may be NULL), 256-byte aligned, and
+ * only enqueues kernels, so it can be captured into a HIP graph. Calls that
+ * share a workspace must be ordered on one stream.
+ * Returns 0, -1..-13 for an invalid argument (the bias is never invalid), -14
+ * for a workspace that is NULL while needed or misaligned,
+ * OZAKI2_ERR_UNSUPPORTED, OZAKI2_ERR_WORKSPACE or OZAKI2_ERR_HIP. t == 0 or
+ * n == 0 returns at once; k == 0 gives the bias (or zeros).
+ */
+int ozaki2_i8gemm(int64_t t, int64_t n, int64_t k, const int8_t *A, int64_t lda, const float *a_scale,
+                  const int8_t *B, int64_t ldb, const float *b_scale, const float *bias, void *C, int64_t ldc,
+                  int ctype, void *stream);
+size_t ozaki2_i8gemm_workspace_size(int64_t t, int64_t n, int64_t k);
+int ozaki2_i8gemm_ws(int64_t t, int64_t n, int64_t k, const int8_t *A, int64_t lda, const float *a_scale,
+                     const int8_t *B, int64_t ldb, const float *b_scale, const float *bias, void *C, int64_t ldc,
+                     int ctype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The layer: rows of X quantised as ozaki2_quantize_rows does, then the product
+ * with B as ozaki2_i8gemm computes it, bit for bit. A few rows (decoding) are
+ * quantised inside the product's kernel and need no workspace.
+ * Returns as ozaki2_i8gemm, with -4..-6 for X, ldx and xtype.
+ */
+int ozaki2_i8linear(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, int xtype, const int8_t *B,
+                    int64_t ldb, const float *b_scale, const float *bias, void *C, int64_t ldc, int ctype,
+                    void *stream);
+size_t ozaki2_i8linear_workspace_size(int64_t t, int64_t n, int64_t k);
+int ozaki2_i8linear_ws(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, int xtype, const int8_t *B,
+                       int64_t ldb, const float *b_scale, const float *bias, void *C, int64_t ldc, int ctype,
+                       void *workspace, size_t workspace_bytes, void *stream);
+
 /* Largest supported number of moduli (20). */
 int ozaki2_max_moduli(void);
 

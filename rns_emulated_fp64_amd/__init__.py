@@ -35,6 +35,8 @@ EXPORTS = (
     "ozaki2_zgemm", "ozaki2_zgemm_ws", "ozaki2_zgemm_debug", "ozaki2_cgemm", "ozaki2_cgemm_ws", "ozaki2_cgemm_debug",
     "ozaki2_zgemm_workspace_size", "ozaki2_dgemm_noalloc", "ozaki2_dgemm_check", "ozaki2_check_workspace_size",
     "ozaki2_crt_check_debug", "ozaki2_zcrt_debug",
+    "ozaki2_quantize_rows", "ozaki2_i8gemm", "ozaki2_i8gemm_ws", "ozaki2_i8gemm_workspace_size",
+    "ozaki2_i8linear", "ozaki2_i8linear_ws", "ozaki2_i8linear_workspace_size",
 )
 
 _lib = None
@@ -100,6 +102,19 @@ def lib() -> ctypes.CDLL:
     L.ozaki2_timing_read.restype = i32
     L.ozaki2_timing_read_calls.argtypes = [p, i32, p]
     L.ozaki2_timing_read_calls.restype = i32
+    L.ozaki2_quantize_rows.argtypes = [i64, i64, p, i64, i32, p, i64, p, p]
+    L.ozaki2_quantize_rows.restype = i32
+    i8 = [i64, i64, i64, p, i64, p, p, i64, p, p, p, i64, i32]
+    L.ozaki2_i8gemm.argtypes = i8 + [p]
+    L.ozaki2_i8gemm_ws.argtypes = i8 + [p, sz, p]
+    i8 = [i64, i64, i64, p, i64, i32, p, i64, p, p, p, i64, i32]
+    L.ozaki2_i8linear.argtypes = i8 + [p]
+    L.ozaki2_i8linear_ws.argtypes = i8 + [p, sz, p]
+    for name in ("ozaki2_i8gemm", "ozaki2_i8linear"):
+        getattr(L, name).restype = i32
+        getattr(L, name + "_ws").restype = i32
+        getattr(L, name + "_workspace_size").argtypes = [i64, i64, i64]
+        getattr(L, name + "_workspace_size").restype = sz
     L.ozaki2_finalize.argtypes = []
     L.ozaki2_finalize.restype = None
     _lib = L
@@ -197,6 +212,38 @@ def ozaki2_cgemm_debug(m, n, k, A, lda, B, ldb, C, ldc, num_moduli, mode, worksp
 
 def ozaki2_zgemm_workspace_size(m, n, k, num_moduli, debug=False) -> int:
     return lib().ozaki2_zgemm_workspace_size(m, n, k, num_moduli, 1 if debug else 0)
+
+
+def ozaki2_quantize_rows(t, k, X, ldx, xtype, Q, ldq, scale, stream=0) -> int:
+    return lib().ozaki2_quantize_rows(t, k, X, ldx, xtype, Q, ldq, scale, stream)
+
+
+def ozaki2_i8gemm(t, n, k, A, lda, a_scale, B, ldb, b_scale, bias, C, ldc, ctype, stream=0) -> int:
+    return lib().ozaki2_i8gemm(t, n, k, A, lda, a_scale, B, ldb, b_scale, bias, C, ldc, ctype, stream)
+
+
+def ozaki2_i8gemm_ws(t, n, k, A, lda, a_scale, B, ldb, b_scale, bias, C, ldc, ctype, workspace, workspace_bytes,
+                     stream=0) -> int:
+    return lib().ozaki2_i8gemm_ws(t, n, k, A, lda, a_scale, B, ldb, b_scale, bias, C, ldc, ctype, workspace,
+                                  workspace_bytes, stream)
+
+
+def ozaki2_i8gemm_workspace_size(t, n, k) -> int:
+    return lib().ozaki2_i8gemm_workspace_size(t, n, k)
+
+
+def ozaki2_i8linear(t, n, k, X, ldx, xtype, B, ldb, b_scale, bias, C, ldc, ctype, stream=0) -> int:
+    return lib().ozaki2_i8linear(t, n, k, X, ldx, xtype, B, ldb, b_scale, bias, C, ldc, ctype, stream)
+
+
+def ozaki2_i8linear_ws(t, n, k, X, ldx, xtype, B, ldb, b_scale, bias, C, ldc, ctype, workspace, workspace_bytes,
+                       stream=0) -> int:
+    return lib().ozaki2_i8linear_ws(t, n, k, X, ldx, xtype, B, ldb, b_scale, bias, C, ldc, ctype, workspace,
+                                    workspace_bytes, stream)
+
+
+def ozaki2_i8linear_workspace_size(t, n, k) -> int:
+    return lib().ozaki2_i8linear_workspace_size(t, n, k)
 
 
 def ozaki2_crt_debug(m, n, num_moduli, residues, e, f, C, ldc, workspace, workspace_bytes, stream=0) -> int:
@@ -345,4 +392,156 @@ def _gemm(A, B, num_moduli, mode, out, workspace, kind):
                          stream)
     if st:
         raise Ozaki2Error(st, entry)
+    return C
+
+
+# ---- INT8 products with scales -----------------------------------------------
+BF16, FP16, FP32 = 0, 1, 2  # enum ozaki2_type
+_TYPES = {"torch.bfloat16": BF16, "torch.float16": FP16, "torch.float32": FP32}
+
+
+def _type_of(dtype, what):
+    try:
+        return _TYPES[str(dtype)]
+    except KeyError:
+        raise TypeError(f"{what} must be bfloat16, float16 or float32, not {dtype}") from None
+
+
+def _rows(x, what, cols=None):
+    """A 2-D tensor with unit stride along its rows (a copy if it has none) and its pitch."""
+    if x.dim() != 2 or (cols is not None and x.shape[1] != cols):
+        raise ValueError(f"{what} must be a matrix" + (f" with {cols} columns" if cols is not None else ""))
+    if x.shape[1] > 1 and x.stride(1) != 1 or x.shape[0] > 1 and x.stride(0) < x.shape[1]:
+        x = x.contiguous()
+    return x, max(x.stride(0) if x.shape[0] > 1 else x.shape[1], 1)
+
+
+def _vector(x, n, dtype, like, what):
+    """A contiguous vector of n values on the device of `like`."""
+    if x.dtype != dtype or x.device != like.device or x.numel() != n:
+        raise ValueError(f"{what} must hold {n} {dtype} values on {like.device}")
+    return x if x.is_contiguous() else x.contiguous()
+
+
+class _On:
+    """The library launches on the current device: makes it the operands' one, and gives their current stream."""
+
+    def __init__(self, x):
+        import torch
+
+        self._device = x.device.index
+        self._other = None if torch.cuda.current_device() == self._device else torch.cuda.device(x.device)
+        self._stream = torch.cuda.current_stream
+
+    def __enter__(self):
+        if self._other is not None:
+            self._other.__enter__()
+        return self._stream(self._device).cuda_stream
+
+    def __exit__(self, *exc):
+        if self._other is not None:
+            self._other.__exit__(*exc)
+
+
+def _workspace(size, given, like):
+    """Pointer and bytes of the caller's workspace, or of a new one from torch's allocator (which may be captured)."""
+    import torch
+
+    if given is not None:
+        if given.device != like.device:
+            raise ValueError(f"workspace must be a tensor on {like.device}")
+        return given, given.data_ptr(), given.numel() * given.element_size()
+    if size == 0:
+        return None, None, 0
+    ws = torch.empty(size, dtype=torch.uint8, device=like.device)
+    return ws, ws.data_ptr(), size
+
+
+def _product_out(t, n, dtype, out, like):
+    import torch
+
+    if out is None:
+        return torch.empty((t, n), dtype=dtype, device=like.device)
+    if out.dtype != dtype or out.device != like.device or tuple(out.shape) != (t, n) or n > 1 and out.stride(1) != 1 \
+            or t > 1 and out.stride(0) < n:
+        raise ValueError(f"out must be a ({t}, {n}) {dtype} tensor on {like.device} with contiguous rows")
+    return out
+
+
+def quantize_rows(X):
+    """Rows of X (float32, float16 or bfloat16) as int8 with a binary32 scale each: (q, scale) with
+    scale = max|x| / 127 and q = rint(x * (127 / max|x|)) (ozaki2_quantize_rows)."""
+    import torch
+
+    xtype = _type_of(X.dtype, "X")
+    if not X.is_cuda:
+        raise TypeError("X must be on a GPU")
+    X, ldx = _rows(X, "X")
+    t, k = X.shape
+    q = torch.empty((t, k), dtype=torch.int8, device=X.device)
+    scale = torch.empty(t, dtype=torch.float32, device=X.device)
+    with _On(X) as stream:
+        st = lib().ozaki2_quantize_rows(t, k, X.data_ptr(), ldx, xtype, q.data_ptr(), max(k, 1), scale.data_ptr(), stream)
+    if st:
+        raise Ozaki2Error(st, "ozaki2_quantize_rows")
+    return q, scale
+
+
+def i8gemm(A, B, a_scale, b_scale, bias=None, out_dtype=None, out=None, workspace=None):
+    """C[t, n] = (sum_k A[t, k] B[n, k]) * a_scale[t] * b_scale[n] + bias[n] for int8 A (t, k) and B (n, k), the
+    layout of a linear layer (ozaki2_i8gemm_ws). The scales and the bias are float32; ``out_dtype`` is bfloat16
+    (default), float16 or float32; ``workspace`` (optional) a tensor of ``ozaki2_i8gemm_workspace_size`` bytes."""
+    import torch
+
+    dt = out_dtype if out_dtype is not None else out.dtype if out is not None else torch.bfloat16
+    ctype = _type_of(dt, "out_dtype")
+    if A.dtype != torch.int8 or B.dtype != torch.int8 or not A.is_cuda or A.device != B.device:
+        raise TypeError("A and B must be int8 tensors on the same GPU")
+    A, lda = _rows(A, "A")
+    t, k = A.shape
+    B, ldb = _rows(B, "B", k)
+    n = B.shape[0]
+    a_scale = _vector(a_scale, t, torch.float32, A, "a_scale")
+    b_scale = _vector(b_scale, n, torch.float32, A, "b_scale")
+    if bias is not None:
+        bias = _vector(bias, n, torch.float32, A, "bias")
+    C = _product_out(t, n, dt, out, A)
+    L = lib()
+    ws, wp, wb = _workspace(L.ozaki2_i8gemm_workspace_size(t, n, k), workspace, A)
+    with _On(A) as stream:
+        st = L.ozaki2_i8gemm_ws(t, n, k, A.data_ptr(), lda, a_scale.data_ptr(), B.data_ptr(), ldb, b_scale.data_ptr(),
+                                None if bias is None else bias.data_ptr(), C.data_ptr(),
+                                max(C.stride(0) if t > 1 else n, 1), ctype, wp, wb, stream)
+    if st:
+        raise Ozaki2Error(st, "ozaki2_i8gemm_ws")
+    return C
+
+
+def i8linear(X, B, b_scale, bias=None, out_dtype=None, out=None, workspace=None):
+    """A linear layer with int8 weights B (n, k) and a scale per channel: the rows of X (t, k; bfloat16, float16 or
+    float32) are quantised as quantize_rows does and multiplied as i8gemm does, bit for bit (ozaki2_i8linear_ws).
+    The result has X's dtype unless ``out_dtype`` or ``out`` says otherwise."""
+    import torch
+
+    xtype = _type_of(X.dtype, "X")
+    dt = out_dtype if out_dtype is not None else out.dtype if out is not None else X.dtype
+    ctype = _type_of(dt, "out_dtype")
+    if B.dtype != torch.int8 or not X.is_cuda or X.device != B.device:
+        raise TypeError("X and int8 B must be on the same GPU")
+    X, ldx = _rows(X, "X")
+    t, k = X.shape
+    B, ldb = _rows(B, "B", k)
+    n = B.shape[0]
+    b_scale = _vector(b_scale, n, torch.float32, X, "b_scale")
+    if bias is not None:
+        bias = _vector(bias, n, torch.float32, X, "bias")
+    C = _product_out(t, n, dt, out, X)
+    L = lib()
+    ws, wp, wb = _workspace(L.ozaki2_i8linear_workspace_size(t, n, k), workspace, X)
+    with _On(X) as stream:
+        st = L.ozaki2_i8linear_ws(t, n, k, X.data_ptr(), ldx, xtype, B.data_ptr(), ldb, b_scale.data_ptr(),
+                                  None if bias is None else bias.data_ptr(), C.data_ptr(),
+                                  max(C.stride(0) if t > 1 else n, 1), ctype, wp, wb, stream)
+    if st:
+        raise Ozaki2Error(st, "ozaki2_i8linear_ws")
     return C

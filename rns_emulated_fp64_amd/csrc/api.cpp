@@ -135,11 +135,12 @@ void timing_slots(hipEvent_t **ev, int **tag, bool *all_phases) {
 }
 
 // ---- cached workspace per device ------------------------------------------
-// One workspace per device serves every ozaki2_dgemm/_sgemm/_zgemm/_cgemm call
-// on it, whatever the stream. The mutex orders the host side; on the device,
-// `done` is recorded on the caller's stream after each product's kernels and
-// the next call's stream waits on it first, so products on different streams
-// take the workspace one after another instead of overwriting each other.
+// One workspace per device serves every cached-workspace call (ozaki2_dgemm and
+// its siblings, ozaki2_i8gemm, ozaki2_i8linear, the xent entries) on it,
+// whatever the stream. The mutex orders the host side; on the device, `done` is
+// recorded on the caller's stream after each call's kernels and the next call's
+// stream waits on it first, so calls on different streams take the workspace
+// one after another instead of overwriting each other.
 struct Cache {
     std::mutex mu;
     std::vector<void *> ptr;
@@ -293,6 +294,34 @@ int front(Elem el, bool cplx, int64_t m, int64_t n, int64_t k, const void *A, in
         if (wbytes < L.total) return OZAKI2_ERR_WORKSPACE;
         return run(el, cplx, m, n, k, A, lda, B, ldb, C, ldc, nmod, mode, (char *)workspace, L, dbg, s);
     }
+    struct Ctx {
+        Elem el;
+        bool cplx;
+        int64_t m, n, k;
+        const void *A;
+        int64_t lda;
+        const void *B;
+        int64_t ldb;
+        void *C;
+        int64_t ldc;
+        int nmod, mode;
+        const Layout *L;
+        const DebugOut *dbg;
+        hipStream_t s;
+    } ctx{el, cplx, m, n, k, A, lda, B, ldb, C, ldc, nmod, mode, &L, dbg, s};
+    return with_workspace(
+        L.total, s,
+        [](void *p, char *ws) {
+            const Ctx &c = *(const Ctx *)p;
+            return run(c.el, c.cplx, c.m, c.n, c.k, c.A, c.lda, c.B, c.ldb, c.C, c.ldc, c.nmod, c.mode, ws, *c.L, c.dbg,
+                       c.s);
+        },
+        &ctx);
+}
+
+}  // namespace
+
+int with_workspace(size_t bytes, hipStream_t s, int (*fn)(void *ctx, char *ws), void *ctx) {
     int dev = 0;
     HIP_TRY(hipGetDevice(&dev));
     std::lock_guard<std::mutex> lk(g_cache.mu);
@@ -307,7 +336,7 @@ int front(Elem el, bool cplx, int64_t m, int64_t n, int64_t k, const void *A, in
         // the previous cached product, on whatever stream, is done with the workspace
         HIP_TRY(hipStreamWaitEvent(s, g_cache.done[dev], 0));
     }
-    if (g_cache.bytes[dev] < L.total) {
+    if (g_cache.bytes[dev] < bytes) {
         if (g_cache.ptr[dev]) {
             HIP_TRY(hipDeviceSynchronize());
             (void)hipFree(g_cache.ptr[dev]);
@@ -315,16 +344,14 @@ int front(Elem el, bool cplx, int64_t m, int64_t n, int64_t k, const void *A, in
             g_cache.bytes[dev] = 0;
         }
         void *p = nullptr;
-        if (hipMalloc(&p, L.total) != hipSuccess) return OZAKI2_ERR_WORKSPACE;
+        if (hipMalloc(&p, bytes) != hipSuccess) return OZAKI2_ERR_WORKSPACE;
         g_cache.ptr[dev] = p;
-        g_cache.bytes[dev] = L.total;
+        g_cache.bytes[dev] = bytes;
     }
-    const int rc = run(el, cplx, m, n, k, A, lda, B, ldb, C, ldc, nmod, mode, (char *)g_cache.ptr[dev], L, dbg, s);
+    const int rc = fn(ctx, (char *)g_cache.ptr[dev]);
     HIP_TRY(hipEventRecord(g_cache.done[dev], s));
     return rc;
 }
-
-}  // namespace
 
 int product_ws(Elem el, int64_t m, int64_t n, int64_t k, const void *A, int64_t lda, const void *B, int64_t ldb,
                void *C, int64_t ldc, int nmod, int mode, void *workspace, size_t wbytes, void *stream) {

@@ -108,6 +108,14 @@ enum class Elem { f64, f32 };
 int product_ws(Elem el, int64_t m, int64_t n, int64_t k, const void *A, int64_t lda, const void *B, int64_t ldb,
                void *C, int64_t ldc, int nmod, int mode, void *workspace, size_t wbytes, void *stream);
 
+// Runs fn(ctx, workspace) on at least `bytes` of the workspace cached for the
+// current device, behind the previous call that used it (see the cached
+// workspace in api.cpp). Returns fn's status or an OZAKI2_ERR_* code.
+int with_workspace(size_t bytes, hipStream_t s, int (*fn)(void *ctx, char *ws), void *ctx);
+
+// Compute units of the current device (kernels.hip).
+int compute_units();
+
 // ---- kernel launchers (kernels.hip). Each returns hipGetLastError(). ----
 // cplx: interleaved complex operands (A, B, C hold (re, im) pairs; leading
 // dimensions count complex elements).

@@ -2231,7 +2231,7 @@ hipError_t launch_quantize(Elem el, const void *A, int64_t m, int64_t lda, const
 // or 256 in the environment forces a shape; the results do not depend on it
 // (the tests run both shapes at every size).
 // Compute units of the current device (cached per device).
-static int compute_units() {
+int compute_units() {
     static std::atomic<int> cu_count[64];
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) dev = 0;

@@ -1,0 +1,385 @@
+// products.hip -- INT8 products with scales, through their C entry points
+// (include/ozaki2.h):
+//
+//   ozaki2_quantize_rows  s[t] = max_k |x[t][k]| / 127, q = rint(x * (127 / max))
+//   ozaki2_i8gemm         C[t][n] = (sum_k A[t][k] B[n][k]) sa[t] sb[n] + bias[n]
+//   ozaki2_i8linear       both: activations quantised row by row, then the product
+//
+// The int32 sums are exact (k < 2^17), so every kernel and every split of k
+// gives the same sums, and the results differ by nothing.
+#include <hip/hip_runtime.h>
+
+#include "common.h"
+#include "ozaki2.h"
+#include "tile.h"
+
+namespace oz2 {
+namespace {
+
+#define HIP_TRY(x)                                    \
+    do {                                              \
+        if ((x) != hipSuccess) return OZAKI2_ERR_HIP; \
+    } while (0)
+
+constexpr size_t kAlign = 256;
+size_t up256(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
+
+// ---- quantisation -------------------------------------------------------------
+// One block per row: the row's values stay in registers between the maximum
+// and the rounding where they fit (NV vectors of 8 per thread), so a row is
+// read once; longer rows are read twice, the second time mostly from the L2.
+// Memory bound.
+constexpr int kQuantThreads = 256;
+template <class T, int NV>
+__global__ __launch_bounds__(kQuantThreads) void k_quantize_rows(const T *__restrict__ X, int64_t ldx, int64_t k,
+                                                                 int8_t *__restrict__ Q, int64_t ldq,
+                                                                 float *__restrict__ scale) {
+    __shared__ uint32_t top[kQuantThreads / 64];
+    const int64_t r = blockIdx.x;
+    const T *x = X + r * ldx;
+    int8_t *q = Q + r * ldq;
+    const int t = threadIdx.x;
+    constexpr int64_t STEP = 8 * kQuantThreads;
+    float keep[NV][8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) load8(x, 8 * t + i * STEP, k, keep[i]);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(keep[i][j]));
+    for (int64_t at = 8 * t + NV * STEP; at < k; at += STEP) {
+        float e[8];
+        load8(x, at, k, e);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(e[j]));
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+    if ((t & 63) == 0) top[t >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kQuantThreads / 64; ++i) m = max(m, top[i]);
+    float s, up;
+    row_scale(m, s, up);
+    if (t == 0) scale[r] = s;
+    auto put = [&](int64_t at, const float(&e)[8]) {
+        const U8 u = quantised8(e, up);
+        if (at + 8 <= k) {
+            *(U8 *)(q + at) = u;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (at + j < k) q[at + j] = (int8_t)(u.w[j >> 2] >> (8 * (j & 3)));
+        }
+    };
+#pragma unroll
+    for (int i = 0; i < NV; ++i) put(8 * t + i * STEP, keep[i]);
+    for (int64_t at = 8 * t + NV * STEP; at < k; at += STEP) {
+        float e[8];
+        load8(x, at, k, e);
+        put(at, e);
+    }
+}
+
+template <class T>
+hipError_t launch_quantize_rows_t(const T *X, int64_t ldx, int64_t t, int64_t k, int8_t *Q, int64_t ldq, float *scale,
+                                  hipStream_t s) {
+    // a grid's x dimension holds 2^31 - 1 blocks, so one launch takes every row
+    if (k <= 8 * kQuantThreads)
+        hipLaunchKernelGGL((k_quantize_rows<T, 1>), dim3((unsigned)t), dim3(kQuantThreads), 0, s, X, ldx, k, Q, ldq, scale);
+    else if (k <= 2 * 8 * kQuantThreads)
+        hipLaunchKernelGGL((k_quantize_rows<T, 2>), dim3((unsigned)t), dim3(kQuantThreads), 0, s, X, ldx, k, Q, ldq, scale);
+    else
+        hipLaunchKernelGGL((k_quantize_rows<T, 4>), dim3((unsigned)t), dim3(kQuantThreads), 0, s, X, ldx, k, Q, ldq, scale);
+    return hipGetLastError();
+}
+
+hipError_t launch_quantize_rows(int type, const void *X, int64_t ldx, int64_t t, int64_t k, int8_t *Q, int64_t ldq,
+                                float *scale, hipStream_t s) {
+    if (type == OZAKI2_BF16) return launch_quantize_rows_t((const __bf16 *)X, ldx, t, k, Q, ldq, scale, s);
+    if (type == OZAKI2_FP16) return launch_quantize_rows_t((const _Float16 *)X, ldx, t, k, Q, ldq, scale, s);
+    return launch_quantize_rows_t((const float *)X, ldx, t, k, Q, ldq, scale, s);
+}
+
+// ---- slices of k, joined ---------------------------------------------------------
+// Sums the int32 planes of k_tile<.., EpiRaw> and applies EpiScale's formula;
+// four outputs per thread. Integer sums: the order does not matter.
+template <class OutT>
+__global__ __launch_bounds__(256) void k_join_scale(const int32_t *__restrict__ planes, int splits, int64_t plane,
+                                                    int64_t ldp, typename EpiScale<OutT>::Args e) {
+    const int64_t a = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+    if (a >= e.na) return;
+    for (int64_t b = blockIdx.y; b < e.nb; b += gridDim.y) {
+        v4i sum = {0, 0, 0, 0};
+        for (int i = 0; i < splits; ++i) sum += *(const v4i *)(planes + i * plane + b * ldp + a);
+        const float sb = e.sb[b];
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+            if (a + v < e.na)
+                e.out[b * e.ldo + a + v] = (OutT)fmaf((float)sum[v] * sb, e.sa[a + v], e.bias ? e.bias[a + v] : 0.f);
+    }
+}
+
+// ---- the product ---------------------------------------------------------------------
+// Up to this many tokens the weights are streamed by k_skinny.
+constexpr int64_t kSkinnyRows = 64;
+
+int splits_of(int64_t t, int64_t n, int64_t k) {
+    if (t <= kSkinnyRows) return 1;
+    TileArgs a{};
+    a.na = n;
+    a.nb = t;
+    a.kbytes = k;
+    a.lda = a.ldb = 16;
+    if (use_persistent_tile(a)) return 1;
+    return tile_splits(n, t, k);
+}
+int64_t plane_pitch(int64_t n) { return (n + 3) / 4 * 4; }
+size_t i8gemm_bytes(int64_t t, int64_t n, int64_t k) {
+    const int s = splits_of(t, n, k);
+    return s > 1 ? (size_t)s * (size_t)t * (size_t)plane_pitch(n) * 4 : 0;
+}
+
+// Activations that the skinny kernel quantises itself: a few rows that fit LDS
+// beside its sums.
+constexpr int64_t kQuantRows = 4, kQuantLds = 48 * 1024;
+int64_t quant_pitch(int64_t k) { return (k + 63) / 64 * 64 + 16; }
+bool quantises_in_product(int64_t t, int64_t k) { return t <= kQuantRows && t * (quant_pitch(k) + 4) <= kQuantLds; }
+
+template <class OutT>
+int product_t(int64_t t, int64_t n, int64_t k, const int8_t *A, int64_t lda, const float *a_scale, const int8_t *B,
+              int64_t ldb, const float *b_scale, const float *bias, void *C, int64_t ldc, char *ws, hipStream_t s) {
+    TileArgs ta{};
+    ta.A = B;  // the weights' index is contiguous in C
+    ta.B = A;
+    ta.lda = ldb;
+    ta.ldb = lda;
+    ta.na = n;
+    ta.nb = t;
+    ta.kbytes = k;
+    const typename EpiScale<OutT>::Args e = {(OutT *)C, ldc, b_scale, a_scale, bias, n, t};
+    if (t <= kSkinnyRows) {
+        HIP_TRY((launch_skinny<MmaI8, EpiScale<OutT>, BRows>(ta, e, {}, s)));
+        return OZAKI2_SUCCESS;
+    }
+    const int splits = splits_of(t, n, k);
+    if (splits == 1) {
+        HIP_TRY((launch_tile<MmaI8, EpiScale<OutT>>(ta, e, 1, s)));
+        return OZAKI2_SUCCESS;
+    }
+    const int64_t ldp = plane_pitch(n), plane = t * ldp;
+    HIP_TRY((launch_tile<MmaI8, EpiRaw>(ta, {(uint32_t *)ws, ldp, plane, n, t}, splits, s)));
+    const dim3 grid((unsigned)((n + 1023) / 1024), (unsigned)(t < 65535 ? t : 65535));
+    hipLaunchKernelGGL((k_join_scale<OutT>), grid, dim3(256), 0, s, (const int32_t *)ws, splits, plane, ldp, e);
+    HIP_TRY(hipGetLastError());
+    return OZAKI2_SUCCESS;
+}
+
+int product(int64_t t, int64_t n, int64_t k, const int8_t *A, int64_t lda, const float *a_scale, const int8_t *B,
+            int64_t ldb, const float *b_scale, const float *bias, void *C, int64_t ldc, int ctype, char *ws,
+            hipStream_t s) {
+    if (ctype == OZAKI2_BF16) return product_t<__bf16>(t, n, k, A, lda, a_scale, B, ldb, b_scale, bias, C, ldc, ws, s);
+    if (ctype == OZAKI2_FP16)
+        return product_t<_Float16>(t, n, k, A, lda, a_scale, B, ldb, b_scale, bias, C, ldc, ws, s);
+    return product_t<float>(t, n, k, A, lda, a_scale, B, ldb, b_scale, bias, C, ldc, ws, s);
+}
+
+template <class XT, class OutT>
+hipError_t few_rows_t(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, const int8_t *B, int64_t ldb,
+                      const float *b_scale, const float *bias, void *C, int64_t ldc, hipStream_t s) {
+    TileArgs ta{};
+    ta.A = B;
+    ta.lda = ldb;
+    ta.na = n;
+    ta.nb = t;
+    ta.kbytes = k;
+    return launch_skinny<MmaI8, EpiScale<OutT>, BQuant<XT>>(
+        ta, {(OutT *)C, ldc, b_scale, nullptr, bias, n, t}, {(const XT *)X, ldx, (int)quant_pitch(k)}, s);
+}
+template <class XT>
+hipError_t few_rows_x(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, const int8_t *B, int64_t ldb,
+                      const float *b_scale, const float *bias, void *C, int64_t ldc, int ctype, hipStream_t s) {
+    if (ctype == OZAKI2_BF16) return few_rows_t<XT, __bf16>(t, n, k, X, ldx, B, ldb, b_scale, bias, C, ldc, s);
+    if (ctype == OZAKI2_FP16) return few_rows_t<XT, _Float16>(t, n, k, X, ldx, B, ldb, b_scale, bias, C, ldc, s);
+    return few_rows_t<XT, float>(t, n, k, X, ldx, B, ldb, b_scale, bias, C, ldc, s);
+}
+hipError_t few_rows(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, int xtype, const int8_t *B, int64_t ldb,
+                    const float *b_scale, const float *bias, void *C, int64_t ldc, int ctype, hipStream_t s) {
+    if (xtype == OZAKI2_BF16) return few_rows_x<__bf16>(t, n, k, X, ldx, B, ldb, b_scale, bias, C, ldc, ctype, s);
+    if (xtype == OZAKI2_FP16) return few_rows_x<_Float16>(t, n, k, X, ldx, B, ldb, b_scale, bias, C, ldc, ctype, s);
+    return few_rows_x<float>(t, n, k, X, ldx, B, ldb, b_scale, bias, C, ldc, ctype, s);
+}
+
+// ---- checks ---------------------------------------------------------------------------
+bool is_type(int type) { return type == OZAKI2_BF16 || type == OZAKI2_FP16 || type == OZAKI2_FP32; }
+bool fits(int64_t t, int64_t n, int64_t k) {
+    const int64_t lim = (int64_t)1 << 31;
+    return t < lim && n < lim && k <= OZAKI2_I8_MAX_K;
+}
+
+// Argument checks of ozaki2_i8gemm in signature order.
+int check_i8gemm(int64_t t, int64_t n, int64_t k, const void *A, int64_t lda, const void *a_scale, const void *B,
+                 int64_t ldb, const void *b_scale, const void *C, int64_t ldc, int ctype) {
+    const bool any = t > 0 && n > 0;
+    if (t < 0) return -1;
+    if (n < 0) return -2;
+    if (k < 0) return -3;
+    if (A == nullptr && any && k > 0) return -4;
+    if (lda < (k > 1 ? k : 1)) return -5;
+    if (a_scale == nullptr && any) return -6;
+    if (B == nullptr && any && k > 0) return -7;
+    if (ldb < (k > 1 ? k : 1)) return -8;
+    if (b_scale == nullptr && any) return -9;
+    if (C == nullptr && any) return -11;
+    if (ldc < (n > 1 ? n : 1)) return -12;
+    if (!is_type(ctype)) return -13;
+    return 0;
+}
+
+struct GemmCall {
+    int64_t t, n, k, lda, ldb, ldc;
+    const int8_t *A, *B;
+    const float *a_scale, *b_scale, *bias;
+    void *C;
+    int ctype;
+    hipStream_t s;
+};
+int run_i8gemm(void *ctx, char *ws) {
+    const GemmCall &c = *(const GemmCall *)ctx;
+    return product(c.t, c.n, c.k, c.A, c.lda, c.a_scale, c.B, c.ldb, c.b_scale, c.bias, c.C, c.ldc, c.ctype, ws, c.s);
+}
+int front_i8gemm(GemmCall c, bool cached, void *workspace, size_t bytes) {
+    const int st = check_i8gemm(c.t, c.n, c.k, c.A, c.lda, c.a_scale, c.B, c.ldb, c.b_scale, c.C, c.ldc, c.ctype);
+    if (st) return st;
+    if (!fits(c.t, c.n, c.k)) return OZAKI2_ERR_UNSUPPORTED;
+    if (c.t == 0 || c.n == 0) return OZAKI2_SUCCESS;
+    const size_t need = i8gemm_bytes(c.t, c.n, c.k);
+    if (need == 0) return run_i8gemm(&c, nullptr);
+    if (cached) return with_workspace(need, c.s, run_i8gemm, &c);
+    if (workspace == nullptr || ((uintptr_t)workspace & (kAlign - 1)) != 0) return -14;
+    if (bytes < need) return OZAKI2_ERR_WORKSPACE;
+    return run_i8gemm(&c, (char *)workspace);
+}
+
+int check_i8linear(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, int xtype, const void *B, int64_t ldb,
+                   const void *b_scale, const void *C, int64_t ldc, int ctype) {
+    const bool any = t > 0 && n > 0;
+    if (t < 0) return -1;
+    if (n < 0) return -2;
+    if (k < 0) return -3;
+    if (X == nullptr && any && k > 0) return -4;
+    if (ldx < (k > 1 ? k : 1)) return -5;
+    if (!is_type(xtype)) return -6;
+    if (B == nullptr && any && k > 0) return -7;
+    if (ldb < (k > 1 ? k : 1)) return -8;
+    if (b_scale == nullptr && any) return -9;
+    if (C == nullptr && any) return -11;
+    if (ldc < (n > 1 ? n : 1)) return -12;
+    if (!is_type(ctype)) return -13;
+    return 0;
+}
+
+struct LinearCall {
+    int64_t t, n, k, ldx, ldb, ldc;
+    const void *X;
+    const int8_t *B;
+    const float *b_scale, *bias;
+    void *C;
+    int xtype, ctype;
+    hipStream_t s;
+};
+// Workspace of ozaki2_i8linear: the quantised rows (pitch a multiple of 128, so
+// the product takes its aligned path on this side whatever k is), their
+// scales, the product's own.
+int64_t q_pitch(int64_t k) { return (k + 127) / 128 * 128; }
+size_t q_bytes(int64_t t, int64_t k) { return up256((size_t)t * (size_t)(q_pitch(k) > 0 ? q_pitch(k) : 128)); }
+size_t i8linear_bytes(int64_t t, int64_t n, int64_t k) {
+    if (quantises_in_product(t, k)) return 0;
+    return q_bytes(t, k) + up256(4 * (size_t)t) + i8gemm_bytes(t, n, k);
+}
+int run_i8linear(void *ctx, char *ws) {
+    const LinearCall &c = *(const LinearCall *)ctx;
+    if (quantises_in_product(c.t, c.k)) {
+        HIP_TRY(few_rows(c.t, c.n, c.k, c.X, c.ldx, c.xtype, c.B, c.ldb, c.b_scale, c.bias, c.C, c.ldc, c.ctype, c.s));
+        return OZAKI2_SUCCESS;
+    }
+    int8_t *q = (int8_t *)ws;
+    float *scale = (float *)(ws + q_bytes(c.t, c.k));
+    char *rest = ws + q_bytes(c.t, c.k) + up256(4 * (size_t)c.t);
+    HIP_TRY(launch_quantize_rows(c.xtype, c.X, c.ldx, c.t, c.k, q, q_pitch(c.k), scale, c.s));
+    return product(c.t, c.n, c.k, q, q_pitch(c.k), scale, c.B, c.ldb, c.b_scale, c.bias, c.C, c.ldc, c.ctype, rest, c.s);
+}
+int front_i8linear(LinearCall c, bool cached, void *workspace, size_t bytes) {
+    const int st = check_i8linear(c.t, c.n, c.k, c.X, c.ldx, c.xtype, c.B, c.ldb, c.b_scale, c.C, c.ldc, c.ctype);
+    if (st) return st;
+    if (!fits(c.t, c.n, c.k)) return OZAKI2_ERR_UNSUPPORTED;
+    if (c.t == 0 || c.n == 0) return OZAKI2_SUCCESS;
+    const size_t need = i8linear_bytes(c.t, c.n, c.k);
+    if (need == 0) return run_i8linear(&c, nullptr);
+    if (cached) return with_workspace(need, c.s, run_i8linear, &c);
+    if (workspace == nullptr || ((uintptr_t)workspace & (kAlign - 1)) != 0) return -14;
+    if (bytes < need) return OZAKI2_ERR_WORKSPACE;
+    return run_i8linear(&c, (char *)workspace);
+}
+
+}  // namespace
+}  // namespace oz2
+
+using namespace oz2;
+
+extern "C" {
+
+int ozaki2_quantize_rows(int64_t t, int64_t k, const void *X, int64_t ldx, int xtype, int8_t *Q, int64_t ldq,
+                         float *scale, void *stream) {
+    if (t < 0) return -1;
+    if (k < 0) return -2;
+    if (X == nullptr && t > 0 && k > 0) return -3;
+    if (ldx < (k > 1 ? k : 1)) return -4;
+    if (!is_type(xtype)) return -5;
+    if (Q == nullptr && t > 0 && k > 0) return -6;
+    if (ldq < (k > 1 ? k : 1)) return -7;
+    if (scale == nullptr && t > 0) return -8;
+    if (t >= ((int64_t)1 << 31) || k >= ((int64_t)1 << 31)) return OZAKI2_ERR_UNSUPPORTED;
+    if (t == 0) return OZAKI2_SUCCESS;
+    HIP_TRY(launch_quantize_rows(xtype, X, ldx, t, k, Q, ldq, scale, (hipStream_t)stream));
+    return OZAKI2_SUCCESS;
+}
+
+int ozaki2_i8gemm(int64_t t, int64_t n, int64_t k, const int8_t *A, int64_t lda, const float *a_scale, const int8_t *B,
+                  int64_t ldb, const float *b_scale, const float *bias, void *C, int64_t ldc, int ctype, void *stream) {
+    return front_i8gemm({t, n, k, lda, ldb, ldc, A, B, a_scale, b_scale, bias, C, ctype, (hipStream_t)stream}, true,
+                        nullptr, 0);
+}
+
+size_t ozaki2_i8gemm_workspace_size(int64_t t, int64_t n, int64_t k) {
+    if (t <= 0 || n <= 0 || k < 0 || !fits(t, n, k)) return 0;
+    return i8gemm_bytes(t, n, k);
+}
+
+int ozaki2_i8gemm_ws(int64_t t, int64_t n, int64_t k, const int8_t *A, int64_t lda, const float *a_scale,
+                     const int8_t *B, int64_t ldb, const float *b_scale, const float *bias, void *C, int64_t ldc,
+                     int ctype, void *workspace, size_t workspace_bytes, void *stream) {
+    return front_i8gemm({t, n, k, lda, ldb, ldc, A, B, a_scale, b_scale, bias, C, ctype, (hipStream_t)stream}, false,
+                        workspace, workspace_bytes);
+}
+
+int ozaki2_i8linear(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, int xtype, const int8_t *B, int64_t ldb,
+                    const float *b_scale, const float *bias, void *C, int64_t ldc, int ctype, void *stream) {
+    return front_i8linear({t, n, k, ldx, ldb, ldc, X, B, b_scale, bias, C, xtype, ctype, (hipStream_t)stream}, true,
+                          nullptr, 0);
+}
+
+size_t ozaki2_i8linear_workspace_size(int64_t t, int64_t n, int64_t k) {
+    if (t <= 0 || n <= 0 || k < 0 || !fits(t, n, k)) return 0;
+    return i8linear_bytes(t, n, k);
+}
+
+int ozaki2_i8linear_ws(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, int xtype, const int8_t *B,
+                       int64_t ldb, const float *b_scale, const float *bias, void *C, int64_t ldc, int ctype,
+                       void *workspace, size_t workspace_bytes, void *stream) {
+    return front_i8linear({t, n, k, ldx, ldb, ldc, X, B, b_scale, bias, C, xtype, ctype, (hipStream_t)stream}, false,
+                          workspace, workspace_bytes);
+}
+
+}  // extern "C"

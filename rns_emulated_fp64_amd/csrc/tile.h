@@ -1,0 +1,931 @@
+// tile.h -- the tiled matrix-core product behind the INT8 product with scales
+// (products.hip) and the linear cross entropy (xent.hip):
+//
+//   R[b][a] = sum_k A[a][k] B[b][k]
+//
+// A and B row-major with the inner dimension contiguous, int8 (exact int32
+// sums) or bf16/fp16 (binary32 sums). R never reaches memory as such: each
+// wavefront hands its accumulators to an epilogue (Epi), which scales and
+// rounds them, reduces them to softmax statistics, or turns them into
+// probabilities. "a" is the operand whose index is contiguous in the output
+// (weight channels, vocabulary entries), "b" the other one (tokens).
+//
+// Three kernels share the fragment layout (the operand order of the
+// 16 x 16 x 64-byte MFMAs: lane L holds row L % 16 and bytes 16 (L / 16) ..
+// + 15 of a 64-byte step of k; in the result lane L holds rows 4 (L / 16) .. + 3
+// of column L % 16):
+//   k_tile_p   256 x 256 tiles, persistent, one wavefront per SIMD: large products
+//   k_tile     128 x 128 tiles, optionally a slice of k per block: the rest
+//   k_skinny   16 to 64 rows of B, weights streamed once from memory: few tokens
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "common.h"
+
+namespace oz2 {
+
+typedef int v4i __attribute__((ext_vector_type(4)));
+typedef float v4f __attribute__((ext_vector_type(4)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+
+// Vectors at any byte address (gfx950 global memory takes unaligned vector
+// accesses of any width).
+struct __attribute__((packed, aligned(1))) U16 { uint32_t w[4]; };
+struct __attribute__((packed, aligned(1))) U8 { uint32_t w[2]; };
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// ---- element types ---------------------------------------------------------
+// BYTES per element, the MFMA of one 64-byte step of k, and the accumulator
+// bits read as a float.
+struct MmaI8 {
+    static constexpr int BYTES = 1;
+    static constexpr bool INT = true;
+    static __device__ __forceinline__ v4i mma(v4i a, v4i b, v4i c) {
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+    }
+    static __device__ __forceinline__ float value(int bits) { return (float)bits; }
+};
+struct MmaBf16 {
+    static constexpr int BYTES = 2;
+    static constexpr bool INT = false;
+    typedef __bf16 Elem;
+    static __device__ __forceinline__ v4i mma(v4i a, v4i b, v4i c) {
+        return __builtin_bit_cast(v4i, __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                                           __builtin_bit_cast(v8bf, a), __builtin_bit_cast(v8bf, b),
+                                           __builtin_bit_cast(v4f, c), 0, 0, 0));
+    }
+    static __device__ __forceinline__ float value(int bits) { return __int_as_float(bits); }
+};
+struct MmaF16 {
+    static constexpr int BYTES = 2;
+    static constexpr bool INT = false;
+    typedef _Float16 Elem;
+    static __device__ __forceinline__ v4i mma(v4i a, v4i b, v4i c) {
+        return __builtin_bit_cast(v4i, __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                                           __builtin_bit_cast(v8h, a), __builtin_bit_cast(v8h, b),
+                                           __builtin_bit_cast(v4f, c), 0, 0, 0));
+    }
+    static __device__ __forceinline__ float value(int bits) { return __int_as_float(bits); }
+};
+
+// Two floats rounded to nearest even as packed 16-bit values.
+template <class T>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+    typedef T v2 __attribute__((ext_vector_type(2)));
+    const v2 p = {(T)x, (T)y};
+    return __builtin_bit_cast(uint32_t, p);
+}
+
+// The lane index, derived anew (opaque to the optimiser, so that neither it
+// nor an address built from it stays live across a main loop in which every
+// register is taken).
+__device__ __forceinline__ int fresh_lane() {
+    int ln;
+    asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(ln));
+    return ln;
+}
+
+// AGPR: the accumulators live in the accumulation registers; keep() makes one
+// stay there up to this point, so that the copies into vector registers are not
+// hoisted into one block that runs out of them.
+template <bool AGPR>
+__device__ __forceinline__ void keep(v4i &acc) {
+    if constexpr (AGPR) asm volatile("" : "+a"(acc));
+}
+
+// ---- arguments of one product ----------------------------------------------
+struct TileArgs {
+    const int8_t *A, *B;
+    int64_t lda, ldb;        // bytes between rows
+    int64_t na, nb;          // rows
+    int64_t kbytes;          // bytes of k per row
+    int tiles_a, tiles_b;
+    int splits;              // k_tile: slices of k, one block each
+    int64_t split_bytes;     // bytes of k per slice (a multiple of 128)
+};
+
+// What an epilogue is told about a wavefront's accumulators: element (i, j, v)
+// of lane L is R[b0 + 16 j + L % 16][a0 + 16 i + 4 (L / 16) + v]. Only a in
+// [amin, na) and b < nb are its own.
+struct TileWhere {
+    int64_t a0, b0, amin;
+    int part;   // index of this wavefront's range of a
+    int split;  // slice of k
+};
+
+// Block order: consecutive block ids go round-robin over the 8 XCDs; each XCD
+// gets one contiguous range of the logical order (groups of 4 tiles of a, all
+// tiles of b), so its L2 serves the panels its blocks share.
+__device__ __forceinline__ void tile_of(int bid, int total, int tiles_a, int tiles_b, int &ta, int &tb) {
+    const int per = total >> 3, rem = total & 7, x = bid & 7;
+    const int lid = x * per + min(x, rem) + (bid >> 3);
+    const int group = 4 * tiles_b;
+    const int g = lid / group, first = 4 * g;
+    const int size = min(tiles_a - first, 4);
+    const int in = lid - g * group;
+    ta = first + in % size;
+    tb = in / size;
+}
+
+// 16 bytes of a row from byte k on, zero from byte kb (the row's end) on. Any
+// alignment; no byte outside [row, row + kb) is read.
+__device__ __forceinline__ v4i load_chunk(const int8_t *row, int64_t k, int64_t kb) {
+    const int64_t left = kb - k;
+    if (left >= 16) return __builtin_bit_cast(v4i, *(const U16 *)(row + k));
+    v4i r = {0, 0, 0, 0};
+    if (left <= 0) return r;
+    if (kb >= 16) {
+        // the row's last 16 bytes, moved down by the bytes that lie before k
+        const U16 u = *(const U16 *)(row + kb - 16);
+        const uint64_t lo = u.w[0] | ((uint64_t)u.w[1] << 32), hi = u.w[2] | ((uint64_t)u.w[3] << 32);
+        const int s = 8 * (16 - (int)left);  // 8 .. 120
+        const uint64_t l = s >= 64 ? hi >> (s - 64) : (lo >> s) | (hi << (64 - s));
+        const uint64_t h = s >= 64 ? 0 : hi >> s;
+        r = (v4i){(int)(uint32_t)l, (int)(l >> 32), (int)(uint32_t)h, (int)(h >> 32)};
+    } else {
+        uint32_t w[4] = {0, 0, 0, 0};
+        for (int i = 0; i < (int)left; ++i) w[i >> 2] |= (uint32_t)(uint8_t)row[k + i] << (8 * (i & 3));
+        r = (v4i){(int)w[0], (int)w[1], (int)w[2], (int)w[3]};
+    }
+    return r;
+}
+
+// ---- epilogues ---------------------------------------------------------------
+
+// Stores 8 consecutive 16-bit or 4 consecutive 32-bit results per lane.
+// The lane's four 16-bit results of two neighbouring tiles (words x[0..1],
+// y[0..1]) are traded between the odd and even rows of 16 lanes, so that each
+// lane gets 8 consecutive ones: of the first tile in even rows, of the second
+// in odd ones.
+__device__ __forceinline__ U16 trade_pair(const uint32_t x[2], const uint32_t y[2]) {
+    const auto p = __builtin_amdgcn_permlane16_swap(x[0], y[0], false, false);
+    const auto q = __builtin_amdgcn_permlane16_swap(x[1], y[1], false, false);
+    return U16{{p[0], q[0], p[1], q[1]}};
+}
+
+template <class T>
+__device__ __forceinline__ void store_some(T *dst, U16 u, int64_t left) {
+    const T *s = (const T *)&u;
+    constexpr int N = 16 / (int)sizeof(T);
+    if (left >= N) {
+        *(U16 *)dst = u;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i < left) dst[i] = s[i];
+    }
+}
+
+// R scaled per row of B and per row of A, plus a bias per row of A:
+// out[b][a] = round(R * sb[b] * sa[a] + bias[a]). The int32 sum is rounded to
+// binary32 once, each product once and the sum with the bias once.
+template <class OutT>
+struct EpiScale {
+    struct Args {
+        OutT *out;
+        int64_t ldo;          // elements
+        const float *sa, *sb; // per row of A, per row of B
+        const float *bias;    // per row of A, or null
+        int64_t na, nb;
+    };
+    static constexpr int STORES = sizeof(OutT) == 2 ? 1 : 2;  // 16-byte stores per two 16 x 16 tiles
+
+    template <class M, int RT, int CT, bool EDGE, bool AGPR = false>
+    static __device__ __forceinline__ void run(v4i (&acc)[RT][CT], const TileWhere &w, const Args &e) {
+        const int lane = fresh_lane();
+        const int64_t b0 = w.b0 + (lane & 15);
+        const int64_t a0 = w.a0 + 4 * (lane >> 4);
+        float sb[CT];
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+            const int64_t b = b0 + 16 * j;
+            sb[j] = e.sb[EDGE && b >= e.nb ? e.nb - 1 : b];
+        }
+        if constexpr (RT == 1) {  // no neighbour to trade with: four results per store
+            static_assert(EDGE, "the short kernel checks every store");
+            float sa[4], bi[4];
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const bool in = a0 + v < e.na;
+                sa[v] = in ? e.sa[a0 + v] : 0.f;
+                bi[v] = in && e.bias ? e.bias[a0 + v] : 0.f;
+            }
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                const int64_t b = b0 + 16 * j;
+                float x[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) x[v] = fmaf(M::value(acc[0][j][v]) * sb[j], sa[v], bi[v]);
+                if (b >= e.nb) continue;
+                OutT *dst = e.out + b * e.ldo + a0;
+                if constexpr (sizeof(OutT) == 4) {
+                    store_some(dst, U16{{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+                                         __float_as_uint(x[3])}}, e.na - a0);
+                } else if (a0 + 4 <= e.na) {
+                    *(U8 *)dst = U8{{pack2<OutT>(x[0], x[1]), pack2<OutT>(x[2], x[3])}};
+                } else {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        if (a0 + v < e.na) dst[v] = (OutT)x[v];
+                }
+            }
+            return;
+        } else {
+        const float *bias = e.bias ? e.bias : e.sa;
+        const uint32_t has_bias = e.bias ? 0xffffffffu : 0u;
+        // where this lane's 16-byte stores begin (see trade_pair)
+        const int64_t st0 = w.a0 + (sizeof(OutT) == 2 ? 16 * ((lane >> 4) & 1) + 8 * (lane >> 5) : 4 * (lane >> 4));
+#pragma unroll
+        for (int i = 0; i < RT; i += 2) {
+            float sa[2][4], bi[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t a = a0 + 16 * (i + h);
+                if (!EDGE || a + 4 <= e.na) {
+                    const U16 u = *(const U16 *)(e.sa + a);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) sa[h][v] = __uint_as_float(u.w[v]);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) sa[h][v] = a + v < e.na ? e.sa[a + v] : 0.f;
+                }
+                // no branch on the bias: without one its place is taken by zeros
+                if (!EDGE || a + 4 <= e.na) {
+                    const U16 u = *(const U16 *)(bias + a);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) bi[h][v] = __uint_as_float(u.w[v] & has_bias);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) bi[h][v] = e.bias && a + v < e.na ? e.bias[a + v] : 0.f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                float x[2][4];
+                keep<AGPR>(acc[i][j]);
+                keep<AGPR>(acc[i + 1][j]);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        x[h][v] = fmaf(M::value(acc[i + h][j][v]) * sb[j], sa[h][v], bi[h][v]);
+                const int64_t b = b0 + 16 * j;
+                OutT *dst = e.out + b * e.ldo + st0 + 16 * i;
+                if constexpr (sizeof(OutT) == 2) {
+                    const uint32_t p[2] = {pack2<OutT>(x[0][0], x[0][1]), pack2<OutT>(x[0][2], x[0][3])};
+                    const uint32_t q[2] = {pack2<OutT>(x[1][0], x[1][1]), pack2<OutT>(x[1][2], x[1][3])};
+                    const U16 u = trade_pair(p, q);
+                    if (!EDGE)
+                        *(U16 *)dst = u;
+                    else if (b < e.nb)
+                        store_some(dst, u, e.na - (st0 + 16 * i));
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const U16 u = {{__float_as_uint(x[h][0]), __float_as_uint(x[h][1]), __float_as_uint(x[h][2]),
+                                        __float_as_uint(x[h][3])}};
+                        if (!EDGE)
+                            *(U16 *)(dst + 16 * h) = u;
+                        else if (b < e.nb)
+                            store_some(dst + 16 * h, u, e.na - (st0 + 16 * (i + h)));
+                    }
+                }
+                // one pair of tiles at a time, so that the reads of the
+                // accumulators are not hoisted into one register-hungry block
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        }
+    }
+};
+
+// The accumulators as they are, one plane of 32-bit words per slice of k:
+// out[split][b][a], joined by the kernels that follow.
+struct EpiRaw {
+    struct Args {
+        uint32_t *out;
+        int64_t ldo, plane;  // elements
+        int64_t na, nb;
+    };
+    static constexpr int STORES = 2;
+    template <class M, int RT, int CT, bool EDGE, bool AGPR = false>
+    static __device__ __forceinline__ void run(v4i (&acc)[RT][CT], const TileWhere &w, const Args &e) {
+        const int lane = fresh_lane();
+        const int64_t b0 = w.b0 + (lane & 15);
+        const int64_t a0 = w.a0 + 4 * (lane >> 4);
+        uint32_t *out = e.out + (int64_t)w.split * e.plane + b0 * e.ldo + a0;
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                const U16 u = {{(uint32_t)acc[i][j][0], (uint32_t)acc[i][j][1], (uint32_t)acc[i][j][2],
+                                (uint32_t)acc[i][j][3]}};
+                uint32_t *dst = out + (int64_t)(16 * j) * e.ldo + 16 * i;
+                if (!EDGE)
+                    *(U16 *)dst = u;
+                else if (b0 + 16 * j < e.nb)
+                    store_some(dst, u, e.na - (a0 + 16 * i));
+            }
+    }
+};
+
+constexpr int kTileStages = 5;  // LDS ring of k_tile: stages of 64 bytes of k
+
+// ---- persistent kernel ---------------------------------------------------------
+template <int N>
+__device__ __forceinline__ void copies_landed_barrier() {
+    asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+// One block of four wavefronts per compute unit walks the 256 x 256 tiles
+// blockIdx.x + i * gridDim.x. Each wavefront owns a 128 x 128 quarter (8 x 8
+// MFMA tiles, 256 accumulators per lane, one wavefront per SIMD).
+//
+// k advances 128 bytes (one cache line of every row, two MFMA steps) per round.
+// A unit, 256 rows x 128 bytes of one operand, is copied global -> LDS without
+// passing through registers; LDS is a ring of five units (160 KiB) in the order
+// A0 B0 A1 B1 A2 ... . In round p the first half (step 0) reads the fragments of
+// step 1 and copies A of round p + 2; the second half (step 1) reads the
+// fragments of round p + 1, step 0, and copies B of round p + 2 into the slot
+// of A of round p, whose last reads the barrier at its start has seen done. The
+// ring runs on across tiles: the next tile's first two rounds are copied during
+// the last two of the current one and land while its epilogue runs.
+//
+// A copy moves 8 rows x 128 bytes, eight consecutive lanes per row, so every
+// request is a whole cache line. (Copies of 16 rows x 64 bytes in fragment
+// order, lane L on row L % 16, reached 0.42 of the INT8 peak at 8192^3 against
+// 0.48 when the pitch was an odd multiple of 64 bytes: they were bound by
+// requests.) In LDS a row takes 128 bytes, its eight 16-byte chunks permuted by
+// c ^ (row / 2 % 8), which spreads the 16 rows of a fragment over all banks.
+//
+// A wavefront issues one instruction per four cycles against 16 cycles per
+// MFMA, so a half keeps at most a few between MFMAs: a fragment read every 3rd,
+// a copy every 6th (M0 with the LDS address after one MFMA, the copy after the
+// next).
+//
+// Counter waits: vector-memory operations of a wavefront complete in order.
+// The barrier needs A and B of round p + 1 and allows the copies of A of round
+// p + 2 (LPW). In the first round of a later tile the previous epilogue's
+// stores, all of them unconditional (EDGE = false), lie between the two and are
+// allowed as well.
+//
+// Edges: a last tile that would reach past na or nb is moved back to end
+// there (na, nb >= 256), so every access is in bounds and no store is
+// conditional; rows that two tiles cover get the same values twice (or the
+// epilogue looks at amin). k is padded to whole rounds: a lane whose 16 bytes
+// lie past the end of the row asks for an offset outside the copy's buffer, and
+// such loads return zeros.
+//
+// Requires: rows, pitches and kbytes multiples of 16 bytes, lda, ldb < 2^24,
+// na, nb >= 256, 256 <= kbytes < 2^30, tiles < 2^31.
+template <class M, class Epi>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_tile_p(TileArgs ta,
+                                                                                           typename Epi::Args ea) {
+    constexpr int RT = 8, CT = 8, NF = RT + CT, NQ = RT * CT, LPW = 8, UNIT = 32 * 1024;
+    constexpr int PRE = 4, RSTEP = 3, CSTEP = 6;
+    constexpr int STORES = RT * CT / 2 * Epi::STORES;
+    constexpr int LATER = LPW + STORES < 63 ? LPW + STORES : 63;  // vmcnt is 6 bits wide
+    static_assert(PRE + RSTEP * (NF - 1) < NQ && PRE + 1 + CSTEP * (LPW - 1) < NQ, "schedule fits a half");
+    __shared__ __attribute__((aligned(1024))) int8_t lds[5 * UNIT];
+
+    const int total = ta.tiles_a * ta.tiles_b;
+    const int G = gridDim.x;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    const int wm = wave >> 1, wn = wave & 1;
+    const int kb = (int)ta.kbytes;
+    const int rounds = (kb + 127) / 128;
+    const uint32_t lda = (uint32_t)ta.lda, ldb = (uint32_t)ta.ldb;
+    auto origin = [&](int b, int &a0, int &b0, int &tile_a) {
+        int tb;
+        tile_of(b, total, ta.tiles_a, ta.tiles_b, tile_a, tb);
+        a0 = (int)min((int64_t)tile_a * 256, ta.na - 256);
+        b0 = (int)min((int64_t)tb * 256, ta.nb - 256);
+    };
+    // every wavefront copies 64 rows of each unit, 8 per copy
+    auto source_a = [&](int a0) { return (uint64_t)(uintptr_t)ta.A + (uint64_t)(a0 + wave * 64) * lda; };
+    auto source_b = [&](int b0) { return (uint64_t)(uintptr_t)ta.B + (uint64_t)(b0 + wave * 64) * ldb; };
+    auto rsrc = [&](uint64_t base, uint32_t ld) {
+        return (v4i){(int)(uint32_t)base, (int)((uint32_t)(base >> 32) & 0xffffu), (int)(63u * ld + 128u), 0x00020000};
+    };
+    // this lane's chunk of a copy's row in the even copies; the odd ones (rows 8
+    // .. 15 of a fragment) have it ^ 4
+    const uint32_t chunk = 16u * ((lane & 7) ^ (lane >> 4));
+    const int k_even = kb - (int)chunk, k_odd = kb - (int)(chunk ^ 64u);
+    const uint32_t lane_a = (uint32_t)(lane >> 3) * lda, lane_b = (uint32_t)(lane >> 3) * ldb;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) int8_t *)lds);
+    const uint32_t wave_lds = lds0 + (uint32_t)(wave * LPW * 1024);
+    // this lane's place in a fragment of step 0; step 1 has it ^ 64
+    const uint32_t place = (uint32_t)(lane & 15) * 128u + 16u * ((lane >> 4) ^ ((lane >> 1) & 7));
+
+    int bid = blockIdx.x;
+    int a0, b0, tile_a, na0 = 0, nb0 = 0, ntile_a = 0;
+    origin(bid, a0, b0, tile_a);
+    uint64_t next_a = source_a(a0), next_b = source_b(b0);
+    uint64_t src_a = next_a, src_b = next_b;
+    int src_k = 0;  // byte of k at which the copies of a round start
+    int nbid = bid + G;
+    // the slots of A and B of this round, of the next one, and of A after that
+    uint32_t s0 = 0, s1 = UNIT, s2 = 2 * UNIT, s3 = 3 * UNIT, s4 = 4 * UNIT;
+
+    v4i acc[RT][CT];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const v4i rs = u ? rsrc(src_b, ldb) : rsrc(src_a, lda);
+            const uint32_t ld = u ? ldb : lda, row = u ? lane_b : lane_a;
+            const uint32_t even = p * 128 < k_even ? row + chunk : 0xfffffff0u;
+            const uint32_t odd = p * 128 < k_odd ? row + (chunk ^ 64u) : 0xfffffff0u;
+#pragma unroll
+            for (int q = 0; q < LPW; ++q)
+                asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds" ::"v"(
+                                 q & 1 ? odd : even),
+                             "s"(rs), "s"((uint32_t)((2 * p + u) * UNIT) + wave_lds + q * 1024u), "s"(8u * q * ld)
+                             : "memory");
+        }
+        src_a += 128;
+        src_b += 128;
+        src_k += 128;
+    }
+    copies_landed_barrier<2 * LPW>();  // A and B of round 0
+    v4i f0[NF], f1[NF];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) f0[r] = *(const v4i *)(lds + wm * 16384 + r * 2048 + place);
+#pragma unroll
+    for (int r = 0; r < CT; ++r) f0[RT + r] = *(const v4i *)(lds + UNIT + wn * 16384 + r * 2048 + place);
+
+    bool later = false;  // a previous tile's stores are in flight
+    // Half of a round: MFMAs on fc, reads of the following step into fn (B
+    // first) from the slots ra, rb, copies of one unit into the slot cs.
+    // SYNC: 0 none, 1 the barrier, 2 the barrier of a tile's first round
+    auto half = [&](auto first, auto sync, uint32_t ra, uint32_t rb, uint32_t at, uint64_t src, uint32_t ld, uint32_t row,
+                    uint32_t cs, v4i(&fc)[NF], v4i(&fn)[NF]) {
+        constexpr int SYNC = decltype(sync)::value;
+        const int8_t *pa = lds + (ra + (uint32_t)wm * 16384u) + at, *pb = lds + (rb + (uint32_t)wn * 16384u) + at;
+        const v4i rs = rsrc(src, ld);
+        const uint32_t cbase = cs + wave_lds;
+        const uint32_t even = src_k < k_even ? row + chunk : 0xfffffff0u;
+        const uint32_t odd = src_k < k_odd ? row + (chunk ^ 64u) : 0xfffffff0u;
+#pragma unroll
+        for (int q = 0; q < NQ; ++q) {
+            // a tile's first half starts from zero
+            acc[q / CT][q % CT] = M::mma(fc[q / CT], fc[RT + q % CT],
+                                         decltype(first)::value ? (v4i){0, 0, 0, 0} : acc[q / CT][q % CT]);
+            __builtin_amdgcn_sched_barrier(0);
+            if (q == PRE - 1) {
+                if constexpr (SYNC == 1) copies_landed_barrier<LPW>();
+                if constexpr (SYNC == 2) {
+                    if (later)
+                        copies_landed_barrier<LATER>();
+                    else
+                        copies_landed_barrier<LPW>();
+                }
+            }
+            if (q >= PRE && (q - PRE) % RSTEP == 0 && (q - PRE) / RSTEP < NF) {
+                const int i = (q - PRE) / RSTEP;
+                if (i < CT)
+                    fn[RT + i] = *(const v4i *)(pb + i * 2048);
+                else
+                    fn[i - CT] = *(const v4i *)(pa + (i - CT) * 2048);
+            }
+            if (q >= PRE && (q - PRE) % CSTEP == 0 && (q - PRE) / CSTEP < LPW)
+                asm volatile("s_add_i32 m0, %0, %1" ::"s"(cbase), "n"((q - PRE) / CSTEP * 1024) : "memory", "scc");
+            if (q > PRE && (q - PRE - 1) % CSTEP == 0 && (q - PRE - 1) / CSTEP < LPW)
+                asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(((q - PRE - 1) / CSTEP) & 1 ? odd : even),
+                             "s"(rs), "s"((uint32_t)((q - PRE - 1) / CSTEP) * 8u * ld)
+                             : "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    };
+    typedef std::integral_constant<int, 0> I0;
+    typedef std::integral_constant<int, 1> I1;
+    typedef std::integral_constant<int, 2> I2;
+    auto round = [&](auto first, int p) {
+        constexpr bool FIRST = decltype(first)::value != 0;
+        if (p + 2 == rounds) {
+            // on to the next tile (after the last one this tile again: in-bounds
+            // copies into slots that nothing reads)
+            if (nbid < total) {
+                origin(nbid, na0, nb0, ntile_a);
+                next_a = source_a(na0);
+                next_b = source_b(nb0);
+            }
+            src_a = next_a;
+            src_b = next_b;
+            src_k = 0;
+        }
+        half(first, I0{}, s0, s1, place ^ 64u, src_a, lda, lane_a, s4, f0, f1);
+        half(I0{}, std::integral_constant<int, FIRST ? 2 : 1>{}, s2, s3, place, src_b, ldb, lane_b, s0, f1, f0);
+        src_a += 128;
+        src_b += 128;
+        src_k += 128;
+        const uint32_t t0 = s0, t1 = s1;
+        s0 = s2;
+        s1 = s3;
+        s2 = s4;
+        s3 = t0;
+        s4 = t1;
+    };
+    while (true) {
+        round(I1{}, 0);
+        for (int p = 1; p < rounds; ++p) round(I0{}, p);
+        const TileWhere w = {(int64_t)a0 + wm * 128, (int64_t)b0 + wn * 128, (int64_t)tile_a * 256, tile_a * 2 + wm, 0};
+        Epi::template run<M, RT, CT, false, true>(acc, w, ea);
+        bid = nbid;
+        if (bid >= total) break;
+        later = true;
+        a0 = na0;
+        b0 = nb0;
+        tile_a = ntile_a;
+        nbid = bid + G;
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the trailing copies land before the block ends
+}
+
+// ---- 128 x 128 tiles -------------------------------------------------------------
+// Four wavefronts of 64 x 64, two blocks per compute unit (80 KiB of LDS each),
+// so one block's epilogue runs beside the other's main loop. Any number of
+// rows: a copy's row is clamped to the last one (its result is not stored).
+// blockIdx.x: tile, blockIdx.y: slice of k.
+//
+// ALIGNED: rows and pitches are 16-byte aligned, and the stages of 64 bytes go
+// global -> LDS in the ring of k_tile_p. Otherwise each lane loads its 16 bytes at
+// any address into registers a stage ahead and writes them to LDS itself.
+template <class M, class Epi, bool ALIGNED>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_tile(TileArgs ta,
+                                                                                         typename Epi::Args ea) {
+    constexpr int RT = 4, CT = 4, NF = RT + CT, NQ = RT * CT, LPW = 4, FA = 8, STAGE = 16 * 1024;
+    constexpr int NST = kTileStages;
+    __shared__ __attribute__((aligned(1024))) int8_t lds[NST * STAGE];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    const int wm = wave >> 1, wn = wave & 1;
+    int tile_a, tile_b;
+    tile_of(blockIdx.x, ta.tiles_a * ta.tiles_b, ta.tiles_a, ta.tiles_b, tile_a, tile_b);
+    const int64_t ta0 = (int64_t)tile_a * 128, tb0 = (int64_t)tile_b * 128;
+    // this block's slice of k: bytes [k0, k1) of every row
+    const int64_t k0 = (int64_t)blockIdx.y * ta.split_bytes;
+    const int64_t k1 = min(k0 + ta.split_bytes, ta.kbytes);
+    const int nk = (int)((k1 - k0) >> 7) * 2;
+
+    v4i acc[RT][CT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < CT; ++j) acc[i][j] = (v4i){0, 0, 0, 0};
+
+    // copies: wavefronts 0 and 1 take the rows of A, 2 and 3 those of B
+    const bool copies_a = wave < 2;
+    const int8_t *base = copies_a ? ta.A : ta.B;
+    const int64_t ld = copies_a ? ta.lda : ta.ldb, rows = copies_a ? ta.na : ta.nb;
+    const int64_t row0 = (copies_a ? ta0 : tb0) + (wave & 1) * 64;
+    const int8_t *from[LPW];
+#pragma unroll
+    for (int q = 0; q < LPW; ++q) from[q] = base + min(row0 + 16 * q + (lane & 15), rows - 1) * ld + k0 + 16 * (lane >> 4);
+    auto frag = [&](const int8_t *st, int r) {
+        return *(const v4i *)(st + (r < RT ? wm * RT + r : FA + wn * CT + (r - RT)) * 1024 + lane * 16);
+    };
+
+    if constexpr (ALIGNED) {
+        __attribute__((address_space(3))) int8_t *lds3 = (__attribute__((address_space(3))) int8_t *)lds;
+        auto copy = [&](int ks_slot, int q) {
+            // past the last stage: the last one again, into a slot that nothing reads
+            const int ks = ks_slot < nk ? ks_slot : nk - 1;
+            __builtin_amdgcn_global_load_lds(from[q] + (int64_t)ks * 64,
+                                             lds3 + (ks_slot % NST) * STAGE + (wave * LPW + q) * 1024, 16, 0, 0);
+        };
+        if (nk > 0) {
+#pragma unroll
+            for (int st = 0; st < NST - 1; ++st)
+#pragma unroll
+                for (int q = 0; q < LPW; ++q) copy(st, q);
+            copies_landed_barrier<(NST - 3) * LPW>();  // stages 0 and 1
+            v4i f0[NF], f1[NF];
+#pragma unroll
+            for (int r = 0; r < NF; ++r) f0[r] = frag(lds, r);
+            constexpr int SG = NQ / LPW, RG = NF / LPW;
+            auto stage = [&](int ks, v4i(&fc)[NF], v4i(&fn)[NF]) {
+                const int8_t *next = lds + ((ks + 1) % NST) * STAGE;
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) {
+                    acc[q / CT][q % CT] = M::mma(fc[q / CT], fc[RT + q % CT], acc[q / CT][q % CT]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    if ((q % SG) < RG) fn[(q / SG) * RG + (q % SG)] = frag(next, (q / SG) * RG + (q % SG));
+                    if ((q % SG) == SG / 2) copy(ks + NST - 1, q / SG);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+                // the stage after next has landed, and every read of the next one is done
+                // before a later copy refills its slot
+                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NST - 3) * LPW) : "memory");
+            };
+            for (int ks = 0; ks < nk; ks += 2) {
+                stage(ks, f0, f1);
+                stage(ks + 1, f1, f0);
+            }
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        }
+    } else if (nk > 0) {
+        v4i hold[LPW];
+#pragma unroll
+        for (int q = 0; q < LPW; ++q) hold[q] = __builtin_bit_cast(v4i, *(const U16 *)from[q]);
+        for (int ks = 0; ks < nk; ++ks) {
+            int8_t *st = lds + (ks & 1) * STAGE;  // its last readers passed the barrier of stage ks - 1
+#pragma unroll
+            for (int q = 0; q < LPW; ++q) *(v4i *)(st + (wave * LPW + q) * 1024 + lane * 16) = hold[q];
+            if (ks + 1 < nk)
+#pragma unroll
+                for (int q = 0; q < LPW; ++q)
+                    hold[q] = __builtin_bit_cast(v4i, *(const U16 *)(from[q] + (int64_t)(ks + 1) * 64));
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            v4i f[NF];
+#pragma unroll
+            for (int r = 0; r < NF; ++r) f[r] = frag(st, r);
+#pragma unroll
+            for (int q = 0; q < NQ; ++q) acc[q / CT][q % CT] = M::mma(f[q / CT], f[RT + q % CT], acc[q / CT][q % CT]);
+        }
+    }
+
+    const TileWhere w = {ta0 + wm * 64, tb0 + wn * 64, ta0, tile_a * 2 + wm, (int)blockIdx.y};
+    for (int64_t k = k0 + (int64_t)nk * 64; k < k1; k += 64) {
+        const int64_t at = k + 16 * (lane >> 4);
+        v4i fb[CT];
+#pragma unroll
+        for (int j = 0; j < CT; ++j)
+            fb[j] = load_chunk(ta.B + min(w.b0 + 16 * j + (lane & 15), ta.nb - 1) * ta.ldb, at, k1);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const v4i fa = load_chunk(ta.A + min(w.a0 + 16 * i + (lane & 15), ta.na - 1) * ta.lda, at, k1);
+#pragma unroll
+            for (int j = 0; j < CT; ++j) acc[i][j] = M::mma(fa, fb[j], acc[i][j]);
+        }
+    }
+    if (w.a0 + 64 <= ta.na && w.b0 + 64 <= ta.nb)
+        Epi::template run<M, RT, CT, false>(acc, w, ea);
+    else if (w.a0 < ta.na && w.b0 < ta.nb)
+        Epi::template run<M, RT, CT, true>(acc, w, ea);
+}
+
+// ---- few rows of B --------------------------------------------------------------
+// BT * 16 rows of B at most, so each weight byte serves one pass and memory
+// bounds the product: a block of W wavefronts takes 16 rows of A, the
+// wavefronts take its 64-byte steps of k in turn (together 64 W consecutive
+// bytes of each row), load A straight into fragments, eight steps in flight,
+// and join their sums through LDS in a fixed order.
+//
+// Src says where fragments of B come from: BRows (memory) or BQuant (quantised
+// by the block itself from 16- or 32-bit activations).
+constexpr int kSkinnySteps = 8;
+
+struct BRows {
+    struct Args {};
+    static constexpr bool QUANT = false;
+};
+
+// Largest magnitude as ordered bits (NaN above infinity above every number).
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+// The step and its inverse for a row whose largest magnitude has these bits:
+// s = amax / 127, up = 127 / amax. A row with Inf or NaN gets a NaN scale and
+// zeros (its outputs are NaN); below 2^-120, where 127 / amax nears the end of
+// binary32, a row becomes zeros.
+__device__ __forceinline__ void row_scale(uint32_t bits, float &s, float &up) {
+    const float amax = __uint_as_float(bits);
+    if (bits >= 0x7f800000u) {
+        s = __uint_as_float(0x7fc00000u);
+        up = 0.f;
+    } else {
+        s = amax / 127.0f;
+        up = amax >= 0x1p-120f ? 127.0f / amax : 0.f;
+    }
+}
+__device__ __forceinline__ int quantised(float x, float up) { return up == 0.f ? 0 : (int)rintf(x * up); }
+
+// Eight elements of a row from element k on as floats, zeros from element kn on.
+template <class T>
+__device__ __forceinline__ void load8(const T *row, int64_t k, int64_t kn, float (&x)[8]) {
+    if (k + 8 <= kn) {
+        T e[8];
+        U16 *u = (U16 *)e;
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) u[i] = *(const U16 *)((const char *)(row + k) + 16 * i);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = (float)e[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = k + i < kn ? (float)row[k + i] : 0.f;
+    }
+}
+__device__ __forceinline__ U8 quantised8(const float (&x)[8], float up) {
+    U8 u = {{0, 0}};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u.w[i >> 2] |= (uint32_t)(uint8_t)quantised(x[i], up) << (8 * (i & 3));
+    return u;
+}
+
+// The block quantises its rows itself: nb * pitch bytes of LDS after the
+// kernel's own, then nb scales, which the epilogue reads through sb.
+template <class T>
+struct BQuant {
+    struct Args {
+        const T *X;
+        int64_t ldx;   // elements
+        int pitch;     // bytes between rows in LDS: kbytes rounded up to 64, plus 16
+    };
+    static constexpr bool QUANT = true;
+};
+
+template <class M, class Epi, int BT, int W, class Src>
+__global__ __launch_bounds__(64 * W) void k_skinny(TileArgs ta, typename Epi::Args ea, typename Src::Args sa) {
+    extern __shared__ __attribute__((aligned(16))) int8_t dyn[];
+    v4i *sums = (v4i *)dyn;  // [W][BT][64]
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    const int64_t a0 = (int64_t)blockIdx.x * 16;
+    const int8_t *arow = ta.A + min(a0 + (lane & 15), ta.na - 1) * ta.lda + 16 * (lane >> 4);
+    const int steps = (int)(ta.kbytes >> 6);  // whole steps
+    constexpr int U = kSkinnySteps;
+    v4i fa[U];
+    auto load_a = [&](int s0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int s = s0 + u * W;
+            if (s < steps) fa[u] = __builtin_bit_cast(v4i, *(const U16 *)(arow + (int64_t)s * 64));
+        }
+    };
+    load_a(wave);  // on their way while the block quantises
+
+    const int8_t *brow[BT];
+    int8_t *rows = dyn + W * BT * 1024;
+    if constexpr (Src::QUANT) {
+        __shared__ uint32_t top[W];
+        float *scale = (float *)(rows + ta.nb * sa.pitch);
+        for (int64_t r = 0; r < ta.nb; ++r) {
+            const auto *x = sa.X + r * sa.ldx;
+            uint32_t m = 0;
+            for (int64_t k = 8 * threadIdx.x; k < ta.kbytes; k += 8 * 64 * W) {
+                float e[8];
+                load8(x, k, ta.kbytes, e);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m = max(m, abs_bits(e[i]));
+            }
+#pragma unroll
+            for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+            __syncthreads();  // top is free again
+            if (lane == 0) top[wave] = m;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < W; ++i) m = max(m, top[i]);
+            float s, up;
+            row_scale(m, s, up);
+            if (threadIdx.x == 0) scale[r] = s;
+            for (int64_t k = 8 * threadIdx.x; k < ((ta.kbytes + 63) & ~(int64_t)63); k += 8 * 64 * W) {
+                float e[8];
+                load8(x, k, ta.kbytes, e);
+                *(U8 *)(rows + r * sa.pitch + k) = quantised8(e, up);
+            }
+        }
+        __syncthreads();
+        ea.sb = scale;
+    } else {
+#pragma unroll
+        for (int j = 0; j < BT; ++j)
+            brow[j] = ta.B + min((int64_t)(16 * j + (lane & 15)), ta.nb - 1) * ta.ldb + 16 * (lane >> 4);
+    }
+    auto load_b = [&](int j, int s) -> v4i {
+        if constexpr (Src::QUANT)
+            return 16 * j + (lane & 15) < ta.nb
+                       ? *(const v4i *)(rows + (16 * j + (lane & 15)) * sa.pitch + s * 64 + 16 * (lane >> 4))
+                       : (v4i){0, 0, 0, 0};
+        else
+            return __builtin_bit_cast(v4i, *(const U16 *)(brow[j] + (int64_t)s * 64));
+    };
+
+    v4i acc[BT];
+#pragma unroll
+    for (int j = 0; j < BT; ++j) acc[j] = (v4i){0, 0, 0, 0};
+    for (int s0 = wave; s0 < steps; s0 += U * W) {
+        if (s0 > wave) load_a(s0);
+        v4i fb[BT][U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < BT; ++j)
+                if (s0 + u * W < steps) fb[j][u] = load_b(j, s0 + u * W);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (s0 + u * W < steps)
+#pragma unroll
+                for (int j = 0; j < BT; ++j) acc[j] = M::mma(fa[u], fb[j][u], acc[j]);
+    }
+    if ((ta.kbytes & 63) && wave == steps % W) {  // the last, partial step
+        const int64_t at = (int64_t)steps * 64 + 16 * (lane >> 4);
+        const v4i a = load_chunk(arow - 16 * (lane >> 4), at, ta.kbytes);
+#pragma unroll
+        for (int j = 0; j < BT; ++j) {
+            v4i b;
+            if constexpr (Src::QUANT)
+                b = load_b(j, steps);
+            else
+                b = load_chunk(brow[j] - 16 * (lane >> 4), at, ta.kbytes);
+            acc[j] = M::mma(a, b, acc[j]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < BT; ++j) sums[(wave * BT + j) * 64 + lane] = acc[j];
+    __syncthreads();
+    for (int j = wave; j < BT; j += W) {
+        v4i t[1][1];
+        t[0][0] = sums[j * 64 + lane];
+#pragma unroll
+        for (int i = 1; i < W; ++i) {
+            const v4i o = sums[(i * BT + j) * 64 + lane];
+            if constexpr (M::INT)
+                t[0][0] += o;
+            else
+                t[0][0] = __builtin_bit_cast(v4i, __builtin_bit_cast(v4f, t[0][0]) + __builtin_bit_cast(v4f, o));
+        }
+        const TileWhere w = {a0, 16 * j, a0, (int)blockIdx.x, 0};
+        Epi::template run<M, 1, 1, true>(t, w, ea);
+    }
+}
+
+// ---- choice of kernel -------------------------------------------------------------
+// Compute units that the choices below plan for (a whole MI355X), so that a
+// workspace size depends on the problem alone.
+constexpr int64_t kPlanUnits = 256;
+
+inline bool aligned16(const TileArgs &t) {
+    return (((uintptr_t)t.A | (uintptr_t)t.B | (uintptr_t)t.lda | (uintptr_t)t.ldb) & 15) == 0;
+}
+
+// Whether the persistent kernel takes a product (see k_tile_p): its needs, and
+// enough 256 x 256 tiles to fill most compute units.
+inline bool use_persistent_tile(const TileArgs &t) {
+    if (!aligned16(t) || (t.kbytes & 15) || t.na < 256 || t.nb < 256 || t.kbytes < 256 || t.kbytes >= (1 << 30) || t.lda >= (1 << 24) || t.ldb >= (1 << 24))
+        return false;
+    const int64_t tiles = ((t.na + 255) / 256) * ((t.nb + 255) / 256);
+    return tiles * 4 >= kPlanUnits * 3;
+}
+
+// Slices of k for k_tile: enough blocks for two per compute unit, at least
+// 1 KiB of k each.
+inline int tile_splits(int64_t na, int64_t nb, int64_t kbytes) {
+    const int64_t tiles = ((na + 127) / 128) * ((nb + 127) / 128);
+    const int64_t want = 2 * kPlanUnits / (tiles > 0 ? tiles : 1), most = kbytes / 1024;
+    const int64_t s = want < most ? want : most;
+    return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+}
+
+template <class M, class Epi>
+hipError_t launch_tile(TileArgs t, const typename Epi::Args &e, int splits, hipStream_t s) {
+    if (splits == 1 && use_persistent_tile(t)) {
+        t.tiles_a = (int)((t.na + 255) / 256);
+        t.tiles_b = (int)((t.nb + 255) / 256);
+        const int64_t tiles = (int64_t)t.tiles_a * t.tiles_b, cus = compute_units();
+        hipLaunchKernelGGL((k_tile_p<M, Epi>), dim3((unsigned)(tiles < cus ? tiles : cus)), dim3(256), 0, s, t, e);
+    } else {
+        t.tiles_a = (int)((t.na + 127) / 128);
+        t.tiles_b = (int)((t.nb + 127) / 128);
+        t.splits = splits;
+        t.split_bytes = ((t.kbytes + splits - 1) / splits + 127) / 128 * 128;
+        const dim3 grid((unsigned)((int64_t)t.tiles_a * t.tiles_b), (unsigned)splits);
+        if (aligned16(t))
+            hipLaunchKernelGGL((k_tile<M, Epi, true>), grid, dim3(256), 0, s, t, e);
+        else
+            hipLaunchKernelGGL((k_tile<M, Epi, false>), grid, dim3(256), 0, s, t, e);
+    }
+    return hipGetLastError();
+}
+
+// Few rows of B (nb <= 64): eight wavefronts where the rows of A give each
+// compute unit few blocks, else four.
+template <class M, class Epi, class Src>
+hipError_t launch_skinny(const TileArgs &t, const typename Epi::Args &e, const typename Src::Args &src, hipStream_t s) {
+    const unsigned grid = (unsigned)((t.na + 15) / 16);
+    auto go = [&](auto kern, int bt, int w, size_t extra) {
+        hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * w), (size_t)w * bt * 1024 + extra, s, t, e, src);
+    };
+    const int bt = (int)((t.nb + 15) / 16);
+    if constexpr (Src::QUANT) {
+        go(k_skinny<M, Epi, 1, 8, Src>, 1, 8, (size_t)t.nb * src.pitch + 4 * (size_t)t.nb);
+    } else {
+        if (bt <= 1)
+            go(k_skinny<M, Epi, 1, 8, Src>, 1, 8, 0);
+        else if (bt == 2)
+            go(k_skinny<M, Epi, 2, 8, Src>, 2, 8, 0);
+        else
+            go(k_skinny<M, Epi, 4, 8, Src>, 4, 8, 0);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace oz2
