@@ -461,6 +461,83 @@ int ozaki2_i8linear_ws(int64_t t, int64_t n, int64_t k, const void *X, int64_t l
                        int64_t ldb, const float *b_scale, const float *bias, void *C, int64_t ldc, int ctype,
                        void *workspace, size_t workspace_bytes, void *stream);
 
+/* ---- Linear cross entropy --------------------------------------------------
+ *
+ * The loss of an output layer without its logits: for T tokens with features X
+ * and a vocabulary of V entries with weights W (both row-major, features
+ * contiguous),
+ *
+ *   z[i][j] = sum_h X[i][h] W[j][h],   lse[i] = log sum_j exp(z[i][j]),
+ *   loss[i] = lse[i] - z[i][targets[i]],  0 where targets[i] == ignore_index.
+ *
+ *   t, v, d   tokens, vocabulary entries, features; t, v < 2^31, d < 2^29;
+ *             v >= 1 unless t == 0.
+ *   X, ldx    DEVICE, element (i, h) at X[i*ldx + h], ldx >= max(1, d).
+ *   W, ldw    DEVICE, element (j, h) at W[j*ldw + h], ldw >= max(1, d).
+ *   type      of X, W and the gradients: OZAKI2_BF16 or OZAKI2_FP16.
+ *   targets   DEVICE int64 [t]. A value outside [0, v) that is not ignore_index
+ *             makes that token's loss NaN (and no memory is read for it).
+ *   loss, lse DEVICE binary32 [t]; lse is written for ignored tokens too.
+ *
+ * z is summed in binary32 on the matrix cores and never stored; maxima, sums of
+ * exponentials and the target's logit are binary32. Results are bitwise
+ * reproducible. Workspace: 8 bytes per token (of at most 16384 at a time) and
+ * 64 vocabulary entries (16 for up to 64 tokens).
+ * ozaki2_xent uses the cached workspace, the _ws form the caller's (256-byte
+ * aligned, capturable into a HIP graph, ordered on one stream if shared).
+ * Returns 0, -1..-12 for an invalid argument (ignore_index is never invalid),
+ * -13 for a workspace that is NULL or misaligned, or an OZAKI2_ERR_* code.
+ */
+int ozaki2_xent(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const void *W, int64_t ldw, int type,
+                const int64_t *targets, int64_t ignore_index, float *loss, float *lse, void *stream);
+size_t ozaki2_xent_workspace_size(int64_t t, int64_t v, int64_t d);
+int ozaki2_xent_ws(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const void *W, int64_t ldw, int type,
+                   const int64_t *targets, int64_t ignore_index, float *loss, float *lse, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/*
+ * The same loss for quantised features and weights (see ozaki2_i8gemm):
+ * z[i][j] = (sum_h A[i][h] B[j][h]) * a_scale[i] * b_scale[j], exact up to the
+ * rounding of the sum and of the two products to binary32. Workspace as
+ * ozaki2_xent (ozaki2_xent_workspace_size), k <= OZAKI2_I8_MAX_K.
+ * Returns as ozaki2_xent: -1..-13 for an argument, -14 for the workspace.
+ */
+int ozaki2_i8xent(int64_t t, int64_t v, int64_t k, const int8_t *A, int64_t lda, const float *a_scale,
+                  const int8_t *B, int64_t ldb, const float *b_scale, const int64_t *targets, int64_t ignore_index,
+                  float *loss, float *lse, void *stream);
+int ozaki2_i8xent_ws(int64_t t, int64_t v, int64_t k, const int8_t *A, int64_t lda, const float *a_scale,
+                     const int8_t *B, int64_t ldb, const float *b_scale, const int64_t *targets, int64_t ignore_index,
+                     float *loss, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of sum_i grad_loss[i] * loss[i]: with
+ * G[i][j] = grad_loss[i] (exp(z[i][j] - lse[i]) - [j == targets[i]]),
+ *   dX[i][h] = sum_j G[i][j] W[j][h],   dW[j][h] = sum_i G[i][j] X[i][h].
+ * The logits are computed again, a piece of the vocabulary at a time, and G is
+ * held in `type` for that piece only (at most 2^28 entries, or t * 256); sums
+ * are binary32, rounded once to `type`. For fp16 G is held relative to the
+ * largest |grad_loss|, so small gradients do not underflow on the way.
+ *   lse       DEVICE binary32 [t] as ozaki2_xent wrote it for the same X, W.
+ *   grad_loss DEVICE binary32 [t].
+ *   dX, lddx  DEVICE output of `type`, or NULL to skip it; lddx >= max(1, d).
+ *   dW, lddw  likewise, v rows.
+ * A token whose target is ignored, or whose grad_loss is 0, contributes
+ * nothing, whatever its row of X holds, and its row of dX is 0. A token whose
+ * target is out of range gives NaN.
+ * Outputs must not overlap the inputs or each other. Bitwise reproducible.
+ * Returns 0, -1..-16 for an invalid argument, -17 for the workspace of the _ws
+ * form (ozaki2_xent_grad_workspace_size bytes with want_dx, want_dw nonzero for
+ * the outputs wanted), or an OZAKI2_ERR_* code. With t == 0 dW is set to zero.
+ */
+int ozaki2_xent_grad(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const void *W, int64_t ldw, int type,
+                     const int64_t *targets, int64_t ignore_index, const float *lse, const float *grad_loss, void *dX,
+                     int64_t lddx, void *dW, int64_t lddw, void *stream);
+size_t ozaki2_xent_grad_workspace_size(int64_t t, int64_t v, int64_t d, int want_dx, int want_dw);
+int ozaki2_xent_grad_ws(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const void *W, int64_t ldw,
+                        int type, const int64_t *targets, int64_t ignore_index, const float *lse,
+                        const float *grad_loss, void *dX, int64_t lddx, void *dW, int64_t lddw, void *workspace,
+                        size_t workspace_bytes, void *stream);
+
 /* Largest supported number of moduli (20). */
 int ozaki2_max_moduli(void);
 

@@ -37,6 +37,8 @@ EXPORTS = (
     "ozaki2_crt_check_debug", "ozaki2_zcrt_debug",
     "ozaki2_quantize_rows", "ozaki2_i8gemm", "ozaki2_i8gemm_ws", "ozaki2_i8gemm_workspace_size",
     "ozaki2_i8linear", "ozaki2_i8linear_ws", "ozaki2_i8linear_workspace_size",
+    "ozaki2_xent", "ozaki2_xent_ws", "ozaki2_xent_workspace_size", "ozaki2_i8xent", "ozaki2_i8xent_ws",
+    "ozaki2_xent_grad", "ozaki2_xent_grad_ws", "ozaki2_xent_grad_workspace_size",
 )
 
 _lib = None
@@ -115,6 +117,22 @@ def lib() -> ctypes.CDLL:
         getattr(L, name + "_ws").restype = i32
         getattr(L, name + "_workspace_size").argtypes = [i64, i64, i64]
         getattr(L, name + "_workspace_size").restype = sz
+    xent = [i64, i64, i64, p, i64, p, i64, i32, p, i64, p, p]
+    L.ozaki2_xent.argtypes = xent + [p]
+    L.ozaki2_xent_ws.argtypes = xent + [p, sz, p]
+    xent = [i64, i64, i64, p, i64, p, p, i64, p, p, i64, p, p]
+    L.ozaki2_i8xent.argtypes = xent + [p]
+    L.ozaki2_i8xent_ws.argtypes = xent + [p, sz, p]
+    xent = [i64, i64, i64, p, i64, p, i64, i32, p, i64, p, p, p, i64, p, i64]
+    L.ozaki2_xent_grad.argtypes = xent + [p]
+    L.ozaki2_xent_grad_ws.argtypes = xent + [p, sz, p]
+    for name in ("ozaki2_xent", "ozaki2_i8xent", "ozaki2_xent_grad"):
+        getattr(L, name).restype = i32
+        getattr(L, name + "_ws").restype = i32
+    L.ozaki2_xent_workspace_size.argtypes = [i64, i64, i64]
+    L.ozaki2_xent_workspace_size.restype = sz
+    L.ozaki2_xent_grad_workspace_size.argtypes = [i64, i64, i64, i32, i32]
+    L.ozaki2_xent_grad_workspace_size.restype = sz
     L.ozaki2_finalize.argtypes = []
     L.ozaki2_finalize.restype = None
     _lib = L
@@ -244,6 +262,46 @@ def ozaki2_i8linear_ws(t, n, k, X, ldx, xtype, B, ldb, b_scale, bias, C, ldc, ct
 
 def ozaki2_i8linear_workspace_size(t, n, k) -> int:
     return lib().ozaki2_i8linear_workspace_size(t, n, k)
+
+
+def ozaki2_xent(t, v, d, X, ldx, W, ldw, type, targets, ignore_index, loss, lse, stream=0) -> int:
+    return lib().ozaki2_xent(t, v, d, X, ldx, W, ldw, type, targets, ignore_index, loss, lse, stream)
+
+
+def ozaki2_xent_ws(t, v, d, X, ldx, W, ldw, type, targets, ignore_index, loss, lse, workspace, workspace_bytes,
+                   stream=0) -> int:
+    return lib().ozaki2_xent_ws(t, v, d, X, ldx, W, ldw, type, targets, ignore_index, loss, lse, workspace,
+                                workspace_bytes, stream)
+
+
+def ozaki2_xent_workspace_size(t, v, d) -> int:
+    return lib().ozaki2_xent_workspace_size(t, v, d)
+
+
+def ozaki2_i8xent(t, v, k, A, lda, a_scale, B, ldb, b_scale, targets, ignore_index, loss, lse, stream=0) -> int:
+    return lib().ozaki2_i8xent(t, v, k, A, lda, a_scale, B, ldb, b_scale, targets, ignore_index, loss, lse, stream)
+
+
+def ozaki2_i8xent_ws(t, v, k, A, lda, a_scale, B, ldb, b_scale, targets, ignore_index, loss, lse, workspace,
+                     workspace_bytes, stream=0) -> int:
+    return lib().ozaki2_i8xent_ws(t, v, k, A, lda, a_scale, B, ldb, b_scale, targets, ignore_index, loss, lse,
+                                  workspace, workspace_bytes, stream)
+
+
+def ozaki2_xent_grad(t, v, d, X, ldx, W, ldw, type, targets, ignore_index, lse, grad_loss, dX, lddx, dW, lddw,
+                     stream=0) -> int:
+    return lib().ozaki2_xent_grad(t, v, d, X, ldx, W, ldw, type, targets, ignore_index, lse, grad_loss, dX, lddx, dW,
+                                  lddw, stream)
+
+
+def ozaki2_xent_grad_ws(t, v, d, X, ldx, W, ldw, type, targets, ignore_index, lse, grad_loss, dX, lddx, dW, lddw,
+                        workspace, workspace_bytes, stream=0) -> int:
+    return lib().ozaki2_xent_grad_ws(t, v, d, X, ldx, W, ldw, type, targets, ignore_index, lse, grad_loss, dX, lddx,
+                                     dW, lddw, workspace, workspace_bytes, stream)
+
+
+def ozaki2_xent_grad_workspace_size(t, v, d, want_dx=True, want_dw=True) -> int:
+    return lib().ozaki2_xent_grad_workspace_size(t, v, d, 1 if want_dx else 0, 1 if want_dw else 0)
 
 
 def ozaki2_crt_debug(m, n, num_moduli, residues, e, f, C, ldc, workspace, workspace_bytes, stream=0) -> int:
@@ -545,3 +603,101 @@ def i8linear(X, B, b_scale, bias=None, out_dtype=None, out=None, workspace=None)
     if st:
         raise Ozaki2Error(st, "ozaki2_i8linear_ws")
     return C
+
+
+# ---- linear cross entropy ----------------------------------------------------
+def _xent_operands(X, W, targets):
+    import torch
+
+    if not X.is_cuda or W.device != X.device or targets.device != X.device:
+        raise TypeError("X, W and targets must be on the same GPU")
+    if targets.dtype != torch.int64:
+        raise TypeError("targets must be int64")
+    X, ldx = _rows(X, "X")
+    W, ldw = _rows(W, "W", X.shape[1])
+    t = X.shape[0]
+    if tuple(targets.shape) != (t,):
+        raise ValueError(f"targets must have shape ({t},)")
+    if t and not W.shape[0]:
+        raise ValueError("W has no rows")
+    return X, ldx, W, ldw, targets if targets.is_contiguous() else targets.contiguous()
+
+
+def _xent_type(X, W):
+    import torch
+
+    if X.dtype not in (torch.bfloat16, torch.float16) or W.dtype != X.dtype:
+        raise TypeError("X and W must both be bfloat16 or both float16")
+    return BF16 if X.dtype == torch.bfloat16 else FP16
+
+
+def xent(X, W, targets, ignore_index=-100, workspace=None):
+    """Per token, the cross entropy of the logits X @ W.T against the target and their log-sum-exp, without storing
+    the logits (ozaki2_xent_ws): (loss, lse), float32. X (t, d) and W (v, d) are bfloat16 or float16, targets (t,)
+    int64. The loss is 0 where the target is ``ignore_index`` and NaN where it is out of range otherwise."""
+    import torch
+
+    kind = _xent_type(X, W)
+    X, ldx, W, ldw, targets = _xent_operands(X, W, targets)
+    t, d = X.shape
+    v = W.shape[0]
+    loss = torch.empty(t, dtype=torch.float32, device=X.device)
+    lse = torch.empty(t, dtype=torch.float32, device=X.device)
+    L = lib()
+    ws, wp, wb = _workspace(L.ozaki2_xent_workspace_size(t, v, d), workspace, X)
+    with _On(X) as stream:
+        st = L.ozaki2_xent_ws(t, v, d, X.data_ptr(), ldx, W.data_ptr(), ldw, kind, targets.data_ptr(), ignore_index,
+                              loss.data_ptr(), lse.data_ptr(), wp, wb, stream)
+    if st:
+        raise Ozaki2Error(st, "ozaki2_xent_ws")
+    return loss, lse
+
+
+def i8xent(A, B, a_scale, b_scale, targets, ignore_index=-100, workspace=None):
+    """xent for quantised features A (t, k) and weights B (v, k), int8 with float32 scales per row: the logits are
+    those of i8gemm in binary32 (ozaki2_i8xent_ws). Returns (loss, lse)."""
+    import torch
+
+    if A.dtype != torch.int8 or B.dtype != torch.int8:
+        raise TypeError("A and B must be int8")
+    A, lda, B, ldb, targets = _xent_operands(A, B, targets)
+    t, k = A.shape
+    v = B.shape[0]
+    a_scale = _vector(a_scale, t, torch.float32, A, "a_scale")
+    b_scale = _vector(b_scale, v, torch.float32, A, "b_scale")
+    loss = torch.empty(t, dtype=torch.float32, device=A.device)
+    lse = torch.empty(t, dtype=torch.float32, device=A.device)
+    L = lib()
+    ws, wp, wb = _workspace(L.ozaki2_xent_workspace_size(t, v, k), workspace, A)
+    with _On(A) as stream:
+        st = L.ozaki2_i8xent_ws(t, v, k, A.data_ptr(), lda, a_scale.data_ptr(), B.data_ptr(), ldb, b_scale.data_ptr(),
+                                targets.data_ptr(), ignore_index, loss.data_ptr(), lse.data_ptr(), wp, wb, stream)
+    if st:
+        raise Ozaki2Error(st, "ozaki2_i8xent_ws")
+    return loss, lse
+
+
+def xent_grad(X, W, targets, lse, grad_loss, ignore_index=-100, want_dx=True, want_dw=True, workspace=None):
+    """(dX, dW), the gradients of sum(grad_loss * loss) for xent's loss, from the lse that xent returned
+    (ozaki2_xent_grad_ws); None for one that is not wanted."""
+    import torch
+
+    kind = _xent_type(X, W)
+    X, ldx, W, ldw, targets = _xent_operands(X, W, targets)
+    t, d = X.shape
+    v = W.shape[0]
+    lse = _vector(lse, t, torch.float32, X, "lse")
+    grad_loss = _vector(grad_loss, t, torch.float32, X, "grad_loss")
+    dX = torch.empty((t, d), dtype=X.dtype, device=X.device) if want_dx else None
+    dW = torch.empty((v, d), dtype=X.dtype, device=X.device) if want_dw else None
+    L = lib()
+    ws, wp, wb = _workspace(L.ozaki2_xent_grad_workspace_size(t, v, d, 1 if want_dx else 0, 1 if want_dw else 0),
+                            workspace, X)
+    with _On(X) as stream:
+        st = L.ozaki2_xent_grad_ws(t, v, d, X.data_ptr(), ldx, W.data_ptr(), ldw, kind, targets.data_ptr(),
+                                   ignore_index, lse.data_ptr(), grad_loss.data_ptr(),
+                                   dX.data_ptr() if want_dx else None, max(d, 1), dW.data_ptr() if want_dw else None,
+                                   max(d, 1), wp, wb, stream)
+    if st:
+        raise Ozaki2Error(st, "ozaki2_xent_grad_ws")
+    return dX, dW

@@ -16,14 +16,6 @@
 namespace oz2 {
 namespace {
 
-#define HIP_TRY(x)                                    \
-    do {                                              \
-        if ((x) != hipSuccess) return OZAKI2_ERR_HIP; \
-    } while (0)
-
-constexpr size_t kAlign = 256;
-size_t up256(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
 // ---- quantisation -------------------------------------------------------------
 // One block per row: the row's values stay in registers between the maximum
 // and the rounding where they fit (NV vectors of 8 per thread), so a row is
@@ -103,7 +95,7 @@ hipError_t launch_quantize_rows(int type, const void *X, int64_t ldx, int64_t t,
 }
 
 // ---- slices of k, joined ---------------------------------------------------------
-// Sums the int32 planes of k_tile<.., EpiRaw> and applies EpiScale's formula;
+// Sums the int32 planes of the slices (EpiRaw) and applies EpiScale's formula;
 // four outputs per thread. Integer sums: the order does not matter.
 template <class OutT>
 __global__ __launch_bounds__(256) void k_join_scale(const int32_t *__restrict__ planes, int splits, int64_t plane,
@@ -122,18 +114,9 @@ __global__ __launch_bounds__(256) void k_join_scale(const int32_t *__restrict__ 
 }
 
 // ---- the product ---------------------------------------------------------------------
-// Up to this many tokens the weights are streamed by k_skinny.
-constexpr int64_t kSkinnyRows = 64;
-
 int splits_of(int64_t t, int64_t n, int64_t k) {
     if (t <= kSkinnyRows) return 1;
-    TileArgs a{};
-    a.na = n;
-    a.nb = t;
-    a.kbytes = k;
-    a.lda = a.ldb = 16;
-    if (use_persistent_tile(a)) return 1;
-    return tile_splits(n, t, k);
+    return use_large_tile(n, t) ? 1 : tile_splits(n, t, k);
 }
 int64_t plane_pitch(int64_t n) { return (n + 3) / 4 * 4; }
 size_t i8gemm_bytes(int64_t t, int64_t n, int64_t k) {
@@ -257,7 +240,7 @@ int front_i8gemm(GemmCall c, bool cached, void *workspace, size_t bytes) {
     const size_t need = i8gemm_bytes(c.t, c.n, c.k);
     if (need == 0) return run_i8gemm(&c, nullptr);
     if (cached) return with_workspace(need, c.s, run_i8gemm, &c);
-    if (workspace == nullptr || ((uintptr_t)workspace & (kAlign - 1)) != 0) return -14;
+    if (workspace == nullptr || ((uintptr_t)workspace & (kWsAlign - 1)) != 0) return -14;
     if (bytes < need) return OZAKI2_ERR_WORKSPACE;
     return run_i8gemm(&c, (char *)workspace);
 }
@@ -318,7 +301,7 @@ int front_i8linear(LinearCall c, bool cached, void *workspace, size_t bytes) {
     const size_t need = i8linear_bytes(c.t, c.n, c.k);
     if (need == 0) return run_i8linear(&c, nullptr);
     if (cached) return with_workspace(need, c.s, run_i8linear, &c);
-    if (workspace == nullptr || ((uintptr_t)workspace & (kAlign - 1)) != 0) return -14;
+    if (workspace == nullptr || ((uintptr_t)workspace & (kWsAlign - 1)) != 0) return -14;
     if (bytes < need) return OZAKI2_ERR_WORKSPACE;
     return run_i8linear(&c, (char *)workspace);
 }

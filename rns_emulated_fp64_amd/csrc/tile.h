@@ -14,8 +14,9 @@
 // 16 x 16 x 64-byte MFMAs: lane L holds row L % 16 and bytes 16 (L / 16) ..
 // + 15 of a 64-byte step of k; in the result lane L holds rows 4 (L / 16) .. + 3
 // of column L % 16):
-//   k_tile_p   256 x 256 tiles, persistent, one wavefront per SIMD: large products
-//   k_tile     128 x 128 tiles, optionally a slice of k per block: the rest
+//   k_tile_p    256 x 256 tiles, persistent, one wavefront per SIMD: large products;
+//               128 x 128 tiles, two blocks per compute unit, with slices of k
+//   k_tile_any  128 x 128 tiles at any alignment
 //   k_skinny   16 to 64 rows of B, weights streamed once from memory: few tokens
 #pragma once
 
@@ -25,6 +26,7 @@
 #include <type_traits>
 
 #include "common.h"
+#include "ozaki2.h"
 
 namespace oz2 {
 
@@ -41,6 +43,16 @@ struct __attribute__((packed, aligned(1))) U8 { uint32_t w[2]; };
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
+#define HIP_TRY(x)                                    \
+    do {                                              \
+        if ((x) != hipSuccess) return OZAKI2_ERR_HIP; \
+    } while (0)
+
+constexpr size_t kWsAlign = 256;  // of workspaces and of the regions in them
+inline size_t up256(size_t v) { return (v + kWsAlign - 1) / kWsAlign * kWsAlign; }
+// Tokens up to which the weights are streamed by k_skinny.
+constexpr int64_t kSkinnyRows = 64;
+
 // ---- element types ---------------------------------------------------------
 // BYTES per element, the MFMA of one 64-byte step of k, and the accumulator
 // bits read as a float.
@@ -54,7 +66,7 @@ struct MmaI8 {
 };
 struct MmaBf16 {
     static constexpr int BYTES = 2;
-    static constexpr bool INT = false;
+    static constexpr bool INT = false, HALF = false;
     typedef __bf16 Elem;
     static __device__ __forceinline__ v4i mma(v4i a, v4i b, v4i c) {
         return __builtin_bit_cast(v4i, __builtin_amdgcn_mfma_f32_16x16x32_bf16(
@@ -65,7 +77,7 @@ struct MmaBf16 {
 };
 struct MmaF16 {
     static constexpr int BYTES = 2;
-    static constexpr bool INT = false;
+    static constexpr bool INT = false, HALF = true;  // HALF: fp16's range
     typedef _Float16 Elem;
     static __device__ __forceinline__ v4i mma(v4i a, v4i b, v4i c) {
         return __builtin_bit_cast(v4i, __builtin_amdgcn_mfma_f32_16x16x32_f16(
@@ -107,7 +119,7 @@ struct TileArgs {
     int64_t na, nb;          // rows
     int64_t kbytes;          // bytes of k per row
     int tiles_a, tiles_b;
-    int splits;              // k_tile: slices of k, one block each
+    int splits;              // 128 x 128 tiles: slices of k, one block each
     int64_t split_bytes;     // bytes of k per slice (a multiple of 128)
 };
 
@@ -183,6 +195,39 @@ __device__ __forceinline__ void store_some(T *dst, U16 u, int64_t left) {
     }
 }
 
+// Where this lane's stores of a pair of tiles begin, from the pair's first a.
+template <class OutT>
+__device__ __forceinline__ int pair_start(int lane) {
+    return sizeof(OutT) == 2 ? 16 * ((lane >> 4) & 1) + 8 * (lane >> 5) : 4 * (lane >> 4);
+}
+
+// Stores a lane's results x of two neighbouring tiles, rounded to OutT. row:
+// where row b of the output begins; a: pair_start's a; EDGE: only below na, and
+// only where b is a row.
+template <class OutT, bool EDGE>
+__device__ __forceinline__ void store_pair(const float (&x)[2][4], OutT *row, int64_t a, int64_t na, bool is_row) {
+    OutT *dst = row + a;
+    if constexpr (sizeof(OutT) == 2) {
+        const uint32_t p[2] = {pack2<OutT>(x[0][0], x[0][1]), pack2<OutT>(x[0][2], x[0][3])};
+        const uint32_t q[2] = {pack2<OutT>(x[1][0], x[1][1]), pack2<OutT>(x[1][2], x[1][3])};
+        const U16 u = trade_pair(p, q);
+        if (!EDGE)
+            *(U16 *)dst = u;
+        else if (is_row)
+            store_some(dst, u, na - a);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const U16 u = {{__float_as_uint(x[h][0]), __float_as_uint(x[h][1]), __float_as_uint(x[h][2]),
+                            __float_as_uint(x[h][3])}};
+            if (!EDGE)
+                *(U16 *)(dst + 16 * h) = u;
+            else if (is_row)
+                store_some(dst + 16 * h, u, na - (a + 16 * h));
+        }
+    }
+}
+
 // R scaled per row of B and per row of A, plus a bias per row of A:
 // out[b][a] = round(R * sb[b] * sa[a] + bias[a]). The int32 sum is rounded to
 // binary32 once, each product once and the sum with the bias once.
@@ -240,8 +285,7 @@ struct EpiScale {
         } else {
         const float *bias = e.bias ? e.bias : e.sa;
         const uint32_t has_bias = e.bias ? 0xffffffffu : 0u;
-        // where this lane's 16-byte stores begin (see trade_pair)
-        const int64_t st0 = w.a0 + (sizeof(OutT) == 2 ? 16 * ((lane >> 4) & 1) + 8 * (lane >> 5) : 4 * (lane >> 4));
+        const int64_t st0 = w.a0 + pair_start<OutT>(lane);
 #pragma unroll
         for (int i = 0; i < RT; i += 2) {
             float sa[2][4], bi[2][4];
@@ -277,26 +321,7 @@ struct EpiScale {
                     for (int v = 0; v < 4; ++v)
                         x[h][v] = fmaf(M::value(acc[i + h][j][v]) * sb[j], sa[h][v], bi[h][v]);
                 const int64_t b = b0 + 16 * j;
-                OutT *dst = e.out + b * e.ldo + st0 + 16 * i;
-                if constexpr (sizeof(OutT) == 2) {
-                    const uint32_t p[2] = {pack2<OutT>(x[0][0], x[0][1]), pack2<OutT>(x[0][2], x[0][3])};
-                    const uint32_t q[2] = {pack2<OutT>(x[1][0], x[1][1]), pack2<OutT>(x[1][2], x[1][3])};
-                    const U16 u = trade_pair(p, q);
-                    if (!EDGE)
-                        *(U16 *)dst = u;
-                    else if (b < e.nb)
-                        store_some(dst, u, e.na - (st0 + 16 * i));
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const U16 u = {{__float_as_uint(x[h][0]), __float_as_uint(x[h][1]), __float_as_uint(x[h][2]),
-                                        __float_as_uint(x[h][3])}};
-                        if (!EDGE)
-                            *(U16 *)(dst + 16 * h) = u;
-                        else if (b < e.nb)
-                            store_some(dst + 16 * h, u, e.na - (st0 + 16 * (i + h)));
-                    }
-                }
+                store_pair<OutT, EDGE>(x, e.out + b * e.ldo, st0 + 16 * i, e.na, b < e.nb);
                 // one pair of tiles at a time, so that the reads of the
                 // accumulators are not hoisted into one register-hungry block
                 __builtin_amdgcn_sched_barrier(0);
@@ -306,7 +331,7 @@ struct EpiScale {
     }
 };
 
-// The accumulators as they are, one plane of 32-bit words per slice of k:
+// The accumulators as they are, one plane of 32-bit words per slice of k,
 // out[split][b][a], joined by the kernels that follow.
 struct EpiRaw {
     struct Args {
@@ -335,8 +360,6 @@ struct EpiRaw {
             }
     }
 };
-
-constexpr int kTileStages = 5;  // LDS ring of k_tile: stages of 64 bytes of k
 
 // ---- persistent kernel ---------------------------------------------------------
 template <int N>
@@ -385,35 +408,56 @@ __device__ __forceinline__ void copies_landed_barrier() {
 //
 // Requires: rows, pitches and kbytes multiples of 16 bytes, lda, ldb < 2^24,
 // na, nb >= 256, 256 <= kbytes < 2^30, tiles < 2^31.
-template <class M, class Epi>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_tile_p(TileArgs ta,
-                                                                                           typename Epi::Args ea) {
-    constexpr int RT = 8, CT = 8, NF = RT + CT, NQ = RT * CT, LPW = 8, UNIT = 32 * 1024;
-    constexpr int PRE = 4, RSTEP = 3, CSTEP = 6;
+template <class M, class Epi, int RT>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(8 / RT, 8 / RT))) void k_tile_p(
+        TileArgs ta, typename Epi::Args ea) {
+    constexpr bool SMALL = RT == 4;
+    constexpr int CT = RT, NF = RT + CT, NQ = RT * CT, LPW = RT, SIDE = 32 * RT, UNIT = SIDE * 128;
+    constexpr int PRE = SMALL ? 1 : 4, RSTEP = SMALL ? 1 : 3, CSTEP = SMALL ? 3 : 6;
     constexpr int STORES = RT * CT / 2 * Epi::STORES;
-    constexpr int LATER = LPW + STORES < 63 ? LPW + STORES : 63;  // vmcnt is 6 bits wide
+    constexpr int LATER = SMALL ? LPW : LPW + STORES < 63 ? LPW + STORES : 63;  // vmcnt is 6 bits wide
     static_assert(PRE + RSTEP * (NF - 1) < NQ && PRE + 1 + CSTEP * (LPW - 1) < NQ, "schedule fits a half");
     __shared__ __attribute__((aligned(1024))) int8_t lds[5 * UNIT];
 
-    const int total = ta.tiles_a * ta.tiles_b;
+    const int tiles = ta.tiles_a * ta.tiles_b, total = SMALL ? tiles * ta.splits : tiles;
     const int G = gridDim.x;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     const int wm = wave >> 1, wn = wave & 1;
     const int kb = (int)ta.kbytes;
-    const int rounds = (kb + 127) / 128;
+    const int rounds = (SMALL ? (int)ta.split_bytes : kb + 127) / 128;
     const uint32_t lda = (uint32_t)ta.lda, ldb = (uint32_t)ta.ldb;
-    auto origin = [&](int b, int &a0, int &b0, int &tile_a) {
+    auto origin = [&](int b, int &a0, int &b0, int &tile_a, int &split) {
         int tb;
-        tile_of(b, total, ta.tiles_a, ta.tiles_b, tile_a, tb);
-        a0 = (int)min((int64_t)tile_a * 256, ta.na - 256);
-        b0 = (int)min((int64_t)tb * 256, ta.nb - 256);
+        tile_of(b, total, ta.tiles_a, ta.tiles_b * (SMALL ? ta.splits : 1), tile_a, tb);
+        split = SMALL ? tb / ta.tiles_b : 0;
+        if (SMALL) tb -= split * ta.tiles_b;
+        a0 = tile_a * SIDE;
+        b0 = tb * SIDE;
+        if (!SMALL) {
+            a0 = (int)min((int64_t)a0, ta.na - SIDE);
+            b0 = (int)min((int64_t)b0, ta.nb - SIDE);
+        }
     };
-    // every wavefront copies 64 rows of each unit, 8 per copy
-    auto source_a = [&](int a0) { return (uint64_t)(uintptr_t)ta.A + (uint64_t)(a0 + wave * 64) * lda; };
-    auto source_b = [&](int b0) { return (uint64_t)(uintptr_t)ta.B + (uint64_t)(b0 + wave * 64) * ldb; };
+    // every wavefront copies SIDE / 4 rows of each unit, 8 per copy. SMALL: rows
+    // past the last one are copies of it, through an offset of their own
+    constexpr int WROWS = SIDE / 4;
+    auto source_a = [&](int a0) { return (uint64_t)(uintptr_t)ta.A + (uint64_t)(a0 + (SMALL ? 0 : wave * WROWS)) * (uint64_t)lda; };
+    auto source_b = [&](int b0) { return (uint64_t)(uintptr_t)ta.B + (uint64_t)(b0 + (SMALL ? 0 : wave * WROWS)) * (uint64_t)ldb; };
     auto rsrc = [&](uint64_t base, uint32_t ld) {
-        return (v4i){(int)(uint32_t)base, (int)((uint32_t)(base >> 32) & 0xffffu), (int)(63u * ld + 128u), 0x00020000};
+        return (v4i){(int)(uint32_t)base, (int)((uint32_t)(base >> 32) & 0xffffu),
+                     (int)((uint32_t)((SMALL ? SIDE : WROWS) - 1) * ld + 128u), 0x00020000};
+    };
+    uint32_t rows_a[SMALL ? LPW : 1], rows_b[SMALL ? LPW : 1];  // SMALL: row offset of each copy
+    auto clamp_rows = [&](int a0, int b0) {
+        if constexpr (SMALL) {
+#pragma unroll
+            for (int q = 0; q < LPW; ++q) {
+                const int64_t r = wave * WROWS + 8 * q + ((threadIdx.x & 63) >> 3);
+                rows_a[q] = (uint32_t)min(r, ta.na - 1 - a0) * lda;
+                rows_b[q] = (uint32_t)min(r, ta.nb - 1 - b0) * ldb;
+            }
+        }
     };
     // this lane's chunk of a copy's row in the even copies; the odd ones (rows 8
     // .. 15 of a fragment) have it ^ 4
@@ -425,12 +469,21 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     // this lane's place in a fragment of step 0; step 1 has it ^ 64
     const uint32_t place = (uint32_t)(lane & 15) * 128u + 16u * ((lane >> 4) ^ ((lane >> 1) & 7));
 
-    int bid = blockIdx.x;
-    int a0, b0, tile_a, na0 = 0, nb0 = 0, ntile_a = 0;
-    origin(bid, a0, b0, tile_a);
-    uint64_t next_a = source_a(a0), next_b = source_b(b0);
-    uint64_t src_a = next_a, src_b = next_b;
     int src_k = 0;  // byte of k at which the copies of a round start
+    // where the lane reads in copy q of the round at src_k
+    auto offset = [&](int q, uint32_t row, const uint32_t *rows) -> uint32_t {
+        const uint32_t c = q & 1 ? chunk ^ 64u : chunk;
+        return src_k < (q & 1 ? k_odd : k_even) ? (SMALL ? rows[q] : row) + c : 0xfffffff0u;
+    };
+
+    int bid = blockIdx.x;
+    int a0, b0, tile_a, split, na0 = 0, nb0 = 0, ntile_a = 0, nsplit = 0;
+    origin(bid, a0, b0, tile_a, split);
+    clamp_rows(a0, b0);
+    int next_k = SMALL ? split * (int)ta.split_bytes : 0;
+    uint64_t next_a = source_a(a0) + (uint32_t)next_k, next_b = source_b(b0) + (uint32_t)next_k;
+    uint64_t src_a = next_a, src_b = next_b;
+    src_k = next_k;
     int nbid = bid + G;
     // the slots of A and B of this round, of the next one, and of A after that
     uint32_t s0 = 0, s1 = UNIT, s2 = 2 * UNIT, s3 = 3 * UNIT, s4 = 4 * UNIT;
@@ -442,13 +495,12 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
         for (int u = 0; u < 2; ++u) {
             const v4i rs = u ? rsrc(src_b, ldb) : rsrc(src_a, lda);
             const uint32_t ld = u ? ldb : lda, row = u ? lane_b : lane_a;
-            const uint32_t even = p * 128 < k_even ? row + chunk : 0xfffffff0u;
-            const uint32_t odd = p * 128 < k_odd ? row + (chunk ^ 64u) : 0xfffffff0u;
 #pragma unroll
             for (int q = 0; q < LPW; ++q)
                 asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds" ::"v"(
-                                 q & 1 ? odd : even),
-                             "s"(rs), "s"((uint32_t)((2 * p + u) * UNIT) + wave_lds + q * 1024u), "s"(8u * q * ld)
+                                 offset(q, row, u ? rows_b : rows_a)),
+                             "s"(rs), "s"((uint32_t)((2 * p + u) * UNIT) + wave_lds + q * 1024u),
+                             "s"(SMALL ? 0u : 8u * q * ld)
                              : "memory");
         }
         src_a += 128;
@@ -458,22 +510,24 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     copies_landed_barrier<2 * LPW>();  // A and B of round 0
     v4i f0[NF], f1[NF];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) f0[r] = *(const v4i *)(lds + wm * 16384 + r * 2048 + place);
+    for (int r = 0; r < RT; ++r) f0[r] = *(const v4i *)(lds + (wm * RT + r) * 2048 + place);
 #pragma unroll
-    for (int r = 0; r < CT; ++r) f0[RT + r] = *(const v4i *)(lds + UNIT + wn * 16384 + r * 2048 + place);
+    for (int r = 0; r < CT; ++r) f0[RT + r] = *(const v4i *)(lds + UNIT + (wn * CT + r) * 2048 + place);
 
     bool later = false;  // a previous tile's stores are in flight
     // Half of a round: MFMAs on fc, reads of the following step into fn (B
     // first) from the slots ra, rb, copies of one unit into the slot cs.
     // SYNC: 0 none, 1 the barrier, 2 the barrier of a tile's first round
     auto half = [&](auto first, auto sync, uint32_t ra, uint32_t rb, uint32_t at, uint64_t src, uint32_t ld, uint32_t row,
-                    uint32_t cs, v4i(&fc)[NF], v4i(&fn)[NF]) {
+                    const uint32_t *rows, uint32_t cs, v4i(&fc)[NF], v4i(&fn)[NF]) {
         constexpr int SYNC = decltype(sync)::value;
-        const int8_t *pa = lds + (ra + (uint32_t)wm * 16384u) + at, *pb = lds + (rb + (uint32_t)wn * 16384u) + at;
+        const int8_t *pa = lds + (ra + (uint32_t)(wm * RT * 2048)) + at,
+                     *pb = lds + (rb + (uint32_t)(wn * CT * 2048)) + at;
         const v4i rs = rsrc(src, ld);
         const uint32_t cbase = cs + wave_lds;
-        const uint32_t even = src_k < k_even ? row + chunk : 0xfffffff0u;
-        const uint32_t odd = src_k < k_odd ? row + (chunk ^ 64u) : 0xfffffff0u;
+        uint32_t off[SMALL ? LPW : 2];
+#pragma unroll
+        for (int q = 0; q < (SMALL ? LPW : 2); ++q) off[q] = offset(q, row, rows);
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
             // a tile's first half starts from zero
@@ -499,8 +553,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
             if (q >= PRE && (q - PRE) % CSTEP == 0 && (q - PRE) / CSTEP < LPW)
                 asm volatile("s_add_i32 m0, %0, %1" ::"s"(cbase), "n"((q - PRE) / CSTEP * 1024) : "memory", "scc");
             if (q > PRE && (q - PRE - 1) % CSTEP == 0 && (q - PRE - 1) / CSTEP < LPW)
-                asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(((q - PRE - 1) / CSTEP) & 1 ? odd : even),
-                             "s"(rs), "s"((uint32_t)((q - PRE - 1) / CSTEP) * 8u * ld)
+                asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(
+                                 off[(q - PRE - 1) / CSTEP & (SMALL ? 3 : 1)]),
+                             "s"(rs), "s"(SMALL ? 0u : (uint32_t)((q - PRE - 1) / CSTEP) * 8u * ld)
                              : "memory");
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -515,16 +570,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
             // on to the next tile (after the last one this tile again: in-bounds
             // copies into slots that nothing reads)
             if (nbid < total) {
-                origin(nbid, na0, nb0, ntile_a);
-                next_a = source_a(na0);
-                next_b = source_b(nb0);
+                origin(nbid, na0, nb0, ntile_a, nsplit);
+                clamp_rows(na0, nb0);
+                next_k = SMALL ? nsplit * (int)ta.split_bytes : 0;
+                next_a = source_a(na0) + (uint32_t)next_k;
+                next_b = source_b(nb0) + (uint32_t)next_k;
             }
             src_a = next_a;
             src_b = next_b;
-            src_k = 0;
+            src_k = next_k;
         }
-        half(first, I0{}, s0, s1, place ^ 64u, src_a, lda, lane_a, s4, f0, f1);
-        half(I0{}, std::integral_constant<int, FIRST ? 2 : 1>{}, s2, s3, place, src_b, ldb, lane_b, s0, f1, f0);
+        half(first, I0{}, s0, s1, place ^ 64u, src_a, lda, lane_a, rows_a, s4, f0, f1);
+        half(I0{}, std::integral_constant<int, FIRST ? 2 : 1>{}, s2, s3, place, src_b, ldb, lane_b, rows_b, s0, f1, f0);
         src_a += 128;
         src_b += 128;
         src_k += 128;
@@ -538,34 +595,35 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 1))) voi
     while (true) {
         round(I1{}, 0);
         for (int p = 1; p < rounds; ++p) round(I0{}, p);
-        const TileWhere w = {(int64_t)a0 + wm * 128, (int64_t)b0 + wn * 128, (int64_t)tile_a * 256, tile_a * 2 + wm, 0};
-        Epi::template run<M, RT, CT, false, true>(acc, w, ea);
+        const TileWhere w = {(int64_t)a0 + wm * (SIDE / 2), (int64_t)b0 + wn * (SIDE / 2), (int64_t)tile_a * SIDE,
+                             tile_a * 2 + wm, split};
+        if (!SMALL || (w.a0 + SIDE / 2 <= ta.na && w.b0 + SIDE / 2 <= ta.nb))
+            Epi::template run<M, RT, CT, false, !SMALL>(acc, w, ea);
+        else if (w.a0 < ta.na && w.b0 < ta.nb)
+            Epi::template run<M, RT, CT, SMALL, !SMALL>(acc, w, ea);
         bid = nbid;
         if (bid >= total) break;
         later = true;
         a0 = na0;
         b0 = nb0;
         tile_a = ntile_a;
+        split = nsplit;
         nbid = bid + G;
     }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the trailing copies land before the block ends
 }
 
-// ---- 128 x 128 tiles -------------------------------------------------------------
-// Four wavefronts of 64 x 64, two blocks per compute unit (80 KiB of LDS each),
-// so one block's epilogue runs beside the other's main loop. Any number of
-// rows: a copy's row is clamped to the last one (its result is not stored).
+// ---- any alignment -----------------------------------------------------------
+// 128 x 128 tiles of four wavefronts for rows or pitches that are not 16-byte
+// aligned, which cannot be copied straight into LDS: each lane loads its 16
+// bytes at any address into registers a stage of 64 bytes of k ahead and writes
+// them to LDS itself, in fragment order. Rows are clamped as in k_tile_p<4>.
 // blockIdx.x: tile, blockIdx.y: slice of k.
-//
-// ALIGNED: rows and pitches are 16-byte aligned, and the stages of 64 bytes go
-// global -> LDS in the ring of k_tile_p. Otherwise each lane loads its 16 bytes at
-// any address into registers a stage ahead and writes them to LDS itself.
-template <class M, class Epi, bool ALIGNED>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_tile(TileArgs ta,
-                                                                                         typename Epi::Args ea) {
+template <class M, class Epi>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_tile_any(TileArgs ta,
+                                                                                             typename Epi::Args ea) {
     constexpr int RT = 4, CT = 4, NF = RT + CT, NQ = RT * CT, LPW = 4, FA = 8, STAGE = 16 * 1024;
-    constexpr int NST = kTileStages;
-    __shared__ __attribute__((aligned(1024))) int8_t lds[NST * STAGE];
+    __shared__ __attribute__((aligned(1024))) int8_t lds[2 * STAGE];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
     const int wm = wave >> 1, wn = wave & 1;
@@ -575,7 +633,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     // this block's slice of k: bytes [k0, k1) of every row
     const int64_t k0 = (int64_t)blockIdx.y * ta.split_bytes;
     const int64_t k1 = min(k0 + ta.split_bytes, ta.kbytes);
-    const int nk = (int)((k1 - k0) >> 7) * 2;
+    const int nk = k1 > k0 ? (int)((k1 - k0) >> 6) : 0;
 
     v4i acc[RT][CT];
 #pragma unroll
@@ -583,57 +641,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 #pragma unroll
         for (int j = 0; j < CT; ++j) acc[i][j] = (v4i){0, 0, 0, 0};
 
-    // copies: wavefronts 0 and 1 take the rows of A, 2 and 3 those of B
-    const bool copies_a = wave < 2;
-    const int8_t *base = copies_a ? ta.A : ta.B;
-    const int64_t ld = copies_a ? ta.lda : ta.ldb, rows = copies_a ? ta.na : ta.nb;
-    const int64_t row0 = (copies_a ? ta0 : tb0) + (wave & 1) * 64;
+    // wavefronts 0 and 1 load the rows of A, 2 and 3 those of B
+    const bool loads_a = wave < 2;
+    const int8_t *base = loads_a ? ta.A : ta.B;
+    const int64_t ld = loads_a ? ta.lda : ta.ldb, rows = loads_a ? ta.na : ta.nb;
+    const int64_t row0 = (loads_a ? ta0 : tb0) + (wave & 1) * 64;
     const int8_t *from[LPW];
 #pragma unroll
     for (int q = 0; q < LPW; ++q) from[q] = base + min(row0 + 16 * q + (lane & 15), rows - 1) * ld + k0 + 16 * (lane >> 4);
-    auto frag = [&](const int8_t *st, int r) {
-        return *(const v4i *)(st + (r < RT ? wm * RT + r : FA + wn * CT + (r - RT)) * 1024 + lane * 16);
-    };
-
-    if constexpr (ALIGNED) {
-        __attribute__((address_space(3))) int8_t *lds3 = (__attribute__((address_space(3))) int8_t *)lds;
-        auto copy = [&](int ks_slot, int q) {
-            // past the last stage: the last one again, into a slot that nothing reads
-            const int ks = ks_slot < nk ? ks_slot : nk - 1;
-            __builtin_amdgcn_global_load_lds(from[q] + (int64_t)ks * 64,
-                                             lds3 + (ks_slot % NST) * STAGE + (wave * LPW + q) * 1024, 16, 0, 0);
-        };
-        if (nk > 0) {
-#pragma unroll
-            for (int st = 0; st < NST - 1; ++st)
-#pragma unroll
-                for (int q = 0; q < LPW; ++q) copy(st, q);
-            copies_landed_barrier<(NST - 3) * LPW>();  // stages 0 and 1
-            v4i f0[NF], f1[NF];
-#pragma unroll
-            for (int r = 0; r < NF; ++r) f0[r] = frag(lds, r);
-            constexpr int SG = NQ / LPW, RG = NF / LPW;
-            auto stage = [&](int ks, v4i(&fc)[NF], v4i(&fn)[NF]) {
-                const int8_t *next = lds + ((ks + 1) % NST) * STAGE;
-#pragma unroll
-                for (int q = 0; q < NQ; ++q) {
-                    acc[q / CT][q % CT] = M::mma(fc[q / CT], fc[RT + q % CT], acc[q / CT][q % CT]);
-                    __builtin_amdgcn_sched_barrier(0);
-                    if ((q % SG) < RG) fn[(q / SG) * RG + (q % SG)] = frag(next, (q / SG) * RG + (q % SG));
-                    if ((q % SG) == SG / 2) copy(ks + NST - 1, q / SG);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-                // the stage after next has landed, and every read of the next one is done
-                // before a later copy refills its slot
-                asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((NST - 3) * LPW) : "memory");
-            };
-            for (int ks = 0; ks < nk; ks += 2) {
-                stage(ks, f0, f1);
-                stage(ks + 1, f1, f0);
-            }
-            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        }
-    } else if (nk > 0) {
+    if (nk > 0) {
         v4i hold[LPW];
 #pragma unroll
         for (int q = 0; q < LPW; ++q) hold[q] = __builtin_bit_cast(v4i, *(const U16 *)from[q]);
@@ -648,14 +664,15 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
             v4i f[NF];
 #pragma unroll
-            for (int r = 0; r < NF; ++r) f[r] = frag(st, r);
+            for (int r = 0; r < NF; ++r)
+                f[r] = *(const v4i *)(st + (r < RT ? wm * RT + r : FA + wn * CT + (r - RT)) * 1024 + lane * 16);
 #pragma unroll
             for (int q = 0; q < NQ; ++q) acc[q / CT][q % CT] = M::mma(f[q / CT], f[RT + q % CT], acc[q / CT][q % CT]);
         }
     }
 
     const TileWhere w = {ta0 + wm * 64, tb0 + wn * 64, ta0, tile_a * 2 + wm, (int)blockIdx.y};
-    for (int64_t k = k0 + (int64_t)nk * 64; k < k1; k += 64) {
+    for (int64_t k = k0 + (int64_t)nk * 64; k < k1; k += 64) {  // the last, partial stage
         const int64_t at = k + 16 * (lane >> 4);
         v4i fb[CT];
 #pragma unroll
@@ -864,45 +881,57 @@ __global__ __launch_bounds__(64 * W) void k_skinny(TileArgs ta, typename Epi::Ar
 constexpr int64_t kPlanUnits = 256;
 
 inline bool aligned16(const TileArgs &t) {
-    return (((uintptr_t)t.A | (uintptr_t)t.B | (uintptr_t)t.lda | (uintptr_t)t.ldb) & 15) == 0;
+    return (((uintptr_t)t.A | (uintptr_t)t.B | (uintptr_t)t.lda | (uintptr_t)t.ldb | (uintptr_t)t.kbytes) & 15) == 0 &&
+           t.lda < (1 << 24) && t.ldb < (1 << 24) && t.kbytes >= 256 && t.kbytes < (1 << 30);
 }
 
-// Whether the persistent kernel takes a product (see k_tile_p): its needs, and
-// enough 256 x 256 tiles to fill most compute units.
-inline bool use_persistent_tile(const TileArgs &t) {
-    if (!aligned16(t) || (t.kbytes & 15) || t.na < 256 || t.nb < 256 || t.kbytes < 256 || t.kbytes >= (1 << 30) || t.lda >= (1 << 24) || t.ldb >= (1 << 24))
-        return false;
-    const int64_t tiles = ((t.na + 255) / 256) * ((t.nb + 255) / 256);
-    return tiles * 4 >= kPlanUnits * 3;
+// Whether k_tile_p runs with 256 x 256 tiles: when they fill most compute
+// units. Else 128 x 128 ones, two blocks per unit.
+inline bool use_large_tile(int64_t na, int64_t nb) {
+    return na >= 256 && nb >= 256 && ((na + 255) / 256) * ((nb + 255) / 256) * 4 >= kPlanUnits * 3;
 }
 
-// Slices of k for k_tile: enough blocks for two per compute unit, at least
-// 1 KiB of k each.
+// Slices of k for the 128 x 128 tiles, with the time that a count of s is
+// expected to take: rounds of 128 bytes of k at 0.25 us (one block per compute
+// unit), and for s > 1 the planes of 32-bit sums, written and read once at 4
+// TB/s, and one more launch.
 inline int tile_splits(int64_t na, int64_t nb, int64_t kbytes) {
     const int64_t tiles = ((na + 127) / 128) * ((nb + 127) / 128);
-    const int64_t want = 2 * kPlanUnits / (tiles > 0 ? tiles : 1), most = kbytes / 1024;
-    const int64_t s = want < most ? want : most;
-    return (int)(s < 1 ? 1 : s > 64 ? 64 : s);
+    const int64_t rounds = (kbytes + 127) / 128;
+    int best = 1;
+    double least = 1e30;
+    for (int s = 1; s <= 64; s *= 2) {
+        if (s > 1 && (tiles * s > 2 * kPlanUnits || rounds < 4 * s)) break;
+        const double per = (double)((rounds + s - 1) / s) * 0.25 * (double)((tiles * s + kPlanUnits - 1) / kPlanUnits);
+        const double us = per + (s > 1 ? 4.0 + (double)s * (double)na * (double)nb * 8.0 / 4e6 : 0.0);
+        if (us < least) {
+            least = us;
+            best = s;
+        }
+    }
+    return best;
 }
+
+// The tile side that launch_tile takes for a product whose k is not sliced.
+inline int tile_side(const TileArgs &t) { return aligned16(t) && use_large_tile(t.na, t.nb) ? 256 : 128; }
 
 template <class M, class Epi>
 hipError_t launch_tile(TileArgs t, const typename Epi::Args &e, int splits, hipStream_t s) {
-    if (splits == 1 && use_persistent_tile(t)) {
-        t.tiles_a = (int)((t.na + 255) / 256);
-        t.tiles_b = (int)((t.nb + 255) / 256);
-        const int64_t tiles = (int64_t)t.tiles_a * t.tiles_b, cus = compute_units();
-        hipLaunchKernelGGL((k_tile_p<M, Epi>), dim3((unsigned)(tiles < cus ? tiles : cus)), dim3(256), 0, s, t, e);
-    } else {
-        t.tiles_a = (int)((t.na + 127) / 128);
-        t.tiles_b = (int)((t.nb + 127) / 128);
-        t.splits = splits;
-        t.split_bytes = ((t.kbytes + splits - 1) / splits + 127) / 128 * 128;
-        const dim3 grid((unsigned)((int64_t)t.tiles_a * t.tiles_b), (unsigned)splits);
-        if (aligned16(t))
-            hipLaunchKernelGGL((k_tile<M, Epi, true>), grid, dim3(256), 0, s, t, e);
-        else
-            hipLaunchKernelGGL((k_tile<M, Epi, false>), grid, dim3(256), 0, s, t, e);
-    }
+    const bool aligned = aligned16(t);
+    const int side = splits == 1 ? tile_side(t) : 128;
+    t.tiles_a = (int)((t.na + side - 1) / side);
+    t.tiles_b = (int)((t.nb + side - 1) / side);
+    t.splits = splits;
+    t.split_bytes = ((t.kbytes + splits - 1) / splits + 127) / 128 * 128;
+    const int64_t total = (int64_t)t.tiles_a * t.tiles_b * splits, cus = compute_units();
+    if (side == 256)
+        hipLaunchKernelGGL((k_tile_p<M, Epi, 8>), dim3((unsigned)(total < cus ? total : cus)), dim3(256), 0, s, t, e);
+    else if (aligned && t.split_bytes >= 256 && total < ((int64_t)1 << 31))
+        hipLaunchKernelGGL((k_tile_p<M, Epi, 4>), dim3((unsigned)(total < 2 * cus ? total : 2 * cus)), dim3(256), 0, s, t,
+                           e);
+    else
+        hipLaunchKernelGGL((k_tile_any<M, Epi>), dim3((unsigned)((int64_t)t.tiles_a * t.tiles_b), (unsigned)splits),
+                           dim3(256), 0, s, t, e);
     return hipGetLastError();
 }
 

@@ -1,0 +1,755 @@
+// xent.hip -- the linear cross entropy and its gradients, through their C
+// entry points (include/ozaki2.h):
+//
+//   z[t][v] = X[t] . W[v],  lse[t] = log sum_v exp(z[t][v]),  loss[t] = lse[t] - z[t][y[t]]
+//   G[t][v] = g[t] (exp(z[t][v] - lse[t]) - [v = y[t]]),  dX = G W,  dW = G^T X
+//
+// The logits never reach memory. Forward: a tile of z stays in the
+// accumulators of tile.h's products, whose epilogue leaves the maximum and the
+// sum of exponentials of each token over the tile's vocabulary entries; one
+// more kernel joins these and computes the target's logit by itself. Backward:
+// z is computed again, a piece of the vocabulary at a time, and its epilogue
+// writes G in 16 bits for that piece alone; G and its transpose then meet the
+// transposes of W and X in two more products. The work is 2 T V d operations
+// forward and 6 T V d backward (4 T V d without the second z), which the matrix
+// cores bound for all but a few tokens; for those it is the reading of W.
+#include <hip/hip_runtime.h>
+
+#include "common.h"
+#include "ozaki2.h"
+#include "tile.h"
+
+namespace oz2 {
+namespace {
+
+// ---- epilogues -------------------------------------------------------------------
+// Softmax statistics of each token over a wavefront's range of the vocabulary:
+// part[w.part][b] = (m, sum exp(z - m)), m the largest z. SCALED: z is an
+// integer sum times sa[a] * sb[b]. A lane holds 4 RT entries of one token, so
+// most of the reduction needs no exchange.
+template <bool SCALED>
+struct EpiLse {
+    struct Args {
+        float2 *part;
+        int64_t ld;            // tokens between parts
+        const float *sa, *sb;  // SCALED
+        int64_t na, nb;
+    };
+    static constexpr int STORES = 0;
+
+    template <class M, int RT, int CT, bool EDGE, bool AGPR = false>
+    static __device__ __forceinline__ void run(v4i (&acc)[RT][CT], const TileWhere &w, const Args &e) {
+        const int lane = fresh_lane();
+        const int64_t a0 = w.a0 + 4 * (lane >> 4);
+        const bool cut = EDGE || w.a0 < w.amin;  // some of the range is not this tile's
+        float sa[SCALED ? RT : 1][4];
+        if constexpr (SCALED) {
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                const int64_t a = a0 + 16 * i;
+                if (!EDGE || a + 4 <= e.na) {
+                    const U16 u = *(const U16 *)(e.sa + a);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) sa[i][v] = __uint_as_float(u.w[v]);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) sa[i][v] = a + v < e.na ? e.sa[a + v] : 0.f;
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+            const int64_t b = w.b0 + 16 * j + (lane & 15);
+            float sb = 1.f;
+            if constexpr (SCALED) sb = e.sb[EDGE && b >= e.nb ? e.nb - 1 : b];
+            float z[RT][4], m = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                keep<AGPR>(acc[i][j]);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) {
+                    z[i][v] = M::value(acc[i][j][v]);
+                    if constexpr (SCALED) z[i][v] = z[i][v] * sb * sa[i][v];
+                }
+            }
+            if (cut) {
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        const int64_t a = a0 + 16 * i + v;
+                        if (a < w.amin || a >= e.na) z[i][v] = -INFINITY;
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) m = fmaxf(m, z[i][v]);
+            m = fmaxf(m, __shfl_xor(m, 16, 64));
+            m = fmaxf(m, __shfl_xor(m, 32, 64));
+            // exp(z - m) as 2^(z log2 e - m log2 e); where every entry is -inf (or cut
+            // off) the sum is 0, not exp(-inf + inf)
+            const float shift = m == -INFINITY ? 0.f : -m * kLog2e;
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int v = 0; v < 4; ++v) s[v] += __builtin_amdgcn_exp2f(fmaf(z[i][v], kLog2e, shift));
+            float sum = (s[0] + s[1]) + (s[2] + s[3]);
+            sum += __shfl_xor(sum, 16, 64);
+            sum += __shfl_xor(sum, 32, 64);
+            if (lane < 16 && (!EDGE || b < e.nb)) e.part[(int64_t)w.part * e.ld + b] = make_float2(m, sum);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+};
+
+// G for a piece of the vocabulary: out[b][a] = g[b] (exp(z - lse[b]) - [v0 + a = y[b]]),
+// rounded to 16 bits (relative error 2^-9 for bf16, 2^-12 for fp16, independent
+// from entry to entry, so the sums over many entries that follow see less of
+// it). A token whose g is 0 gets zeros whatever its logits are.
+template <class T>
+struct EpiProb {
+    struct Args {
+        T *out;
+        int64_t ldo;
+        const float *lse, *g;
+        const int64_t *y;
+        int64_t v0;
+        int64_t na, nb;
+    };
+    static constexpr int STORES = 1;
+
+    template <class M, int RT, int CT, bool EDGE, bool AGPR = false>
+    static __device__ __forceinline__ void run(v4i (&acc)[RT][CT], const TileWhere &w, const Args &e) {
+        const int lane = fresh_lane();
+        const int64_t st0 = w.a0 + pair_start<T>(lane);
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+            const int64_t b = w.b0 + 16 * j + (lane & 15), at = EDGE && b >= e.nb ? e.nb - 1 : b;
+            const float shift = -e.lse[at] * kLog2e, g = e.g[at];
+            // the target's place among this lane's entries, in 16 i + v
+            const int64_t y = e.y[at] - e.v0 - w.a0 - 4 * (lane >> 4);
+            const int hit = y >= 0 && y < 16 * RT && (y & 15) < 4 ? (int)y : -1;
+#pragma unroll
+            for (int i = 0; i < RT; i += 2) {
+                keep<AGPR>(acc[i][j]);
+                keep<AGPR>(acc[i + 1][j]);
+                float x[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {
+                        float p = __builtin_amdgcn_exp2f(fmaf(M::value(acc[i + h][j][v]), kLog2e, shift));
+                        p = hit == 16 * (i + h) + v ? p - 1.f : p;
+                        x[h][v] = g == 0.f ? 0.f : g * p;
+                    }
+                store_pair<T, EDGE>(x, e.out + b * e.ldo, st0 + 16 * i, e.na, b < e.nb);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    }
+};
+
+// out[b][a] = round(R * *unit).
+template <class OutT>
+struct EpiOut {
+    struct Args {
+        OutT *out;
+        int64_t ldo;
+        const float *unit;
+        int64_t na, nb;
+    };
+    static constexpr int STORES = sizeof(OutT) == 2 ? 1 : 2;
+
+    template <class M, int RT, int CT, bool EDGE, bool AGPR = false>
+    static __device__ __forceinline__ void run(v4i (&acc)[RT][CT], const TileWhere &w, const Args &e) {
+        const int lane = fresh_lane();
+        const int64_t st0 = w.a0 + pair_start<OutT>(lane), b0 = w.b0 + (lane & 15);
+        const float unit = *e.unit;
+#pragma unroll
+        for (int i = 0; i < RT; i += 2)
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                keep<AGPR>(acc[i][j]);
+                keep<AGPR>(acc[i + 1][j]);
+                float x[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) x[h][v] = M::value(acc[i + h][j][v]) * unit;
+                const int64_t b = b0 + 16 * j;
+                store_pair<OutT, EDGE>(x, e.out + b * e.ldo, st0 + 16 * i, e.na, b < e.nb);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+    }
+};
+
+// ---- the loss from the statistics ------------------------------------------------
+// Row pairs whose product is the target's logit.
+template <class T>
+struct DotFloat {
+    const T *X, *W;
+    int64_t ldx, ldw, d;
+    // the part of X[t] . W[v] that lane `at` of n sums
+    __device__ __forceinline__ float part(int64_t t, int64_t v, int at, int n) const {
+        float s = 0.f;
+        for (int64_t k = 8 * at; k < d; k += 8 * n) {
+            float x[8], w[8];
+            load8(X + t * ldx, k, d, x);
+            load8(W + v * ldw, k, d, w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s = fmaf(x[i], w[i], s);
+        }
+        return s;
+    }
+    __device__ __forceinline__ float finish(float s, int64_t, int64_t) const { return s; }
+    static __device__ __forceinline__ float add(float a, float b) { return a + b; }
+};
+struct DotInt8 {
+    const int8_t *X, *W;
+    int64_t ldx, ldw, d;
+    const float *sx, *sw;
+    __device__ __forceinline__ float part(int64_t t, int64_t v, int at, int n) const {
+        int s = 0;
+        for (int64_t k = 16 * at; k < d; k += 16 * n) {
+            const v4i x = load_chunk(X + t * ldx, k, d), w = load_chunk(W + v * ldw, k, d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s = __builtin_amdgcn_sdot4(x[i], w[i], s, false);
+        }
+        return __int_as_float(s);
+    }
+    __device__ __forceinline__ float finish(float s, int64_t t, int64_t v) const {
+        return (float)__float_as_int(s) * sx[t] * sw[v];
+    }
+    static __device__ __forceinline__ float add(float a, float b) {
+        return __int_as_float(__float_as_int(a) + __float_as_int(b));
+    }
+};
+
+// (m, s) += (m2, s2), each standing for s * exp(m).
+__device__ __forceinline__ void stat_add(float &m, float &s, float m2, float s2) {
+    const float top = fmaxf(m, m2);
+    const float base = top == -INFINITY ? 0.f : top;
+    // a NaN sum stays one whatever its maximum says
+    s = s * __builtin_amdgcn_exp2f((m - base) * kLog2e) + s2 * __builtin_amdgcn_exp2f((m2 - base) * kLog2e);
+    m = top;
+}
+
+// TB tokens per block, 256 / TB lanes each: joins the parts of each token in a
+// fixed order, and gives loss and lse. A target outside [0, nv) that is not the
+// ignored one makes the loss NaN; no row is read for it.
+template <class Dot, int TB>
+__global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ part, int64_t ld, int nparts, int64_t nt,
+                                                   int64_t nv, const int64_t *__restrict__ y, int64_t ignore, Dot dot,
+                                                   float *__restrict__ loss, float *__restrict__ lse) {
+    constexpr int PL = 256 / TB;
+    __shared__ float sm[256], ss[256];
+    const int tid = threadIdx.x;
+    const int64_t t0 = (int64_t)blockIdx.x * TB;
+    {
+        const int ti = tid % TB, at = tid / TB;
+        float m = -INFINITY, s = 0.f;
+        if (t0 + ti < nt)
+            for (int p = at; p < nparts; p += PL) {
+                const float2 u = part[(int64_t)p * ld + t0 + ti];
+                stat_add(m, s, u.x, u.y);
+            }
+        sm[ti * PL + at] = m;
+        ss[ti * PL + at] = s;
+    }
+    __syncthreads();
+    const int ti = tid / PL, at = tid % PL;
+    const int64_t t = t0 + ti;
+    for (int half = PL / 2; half >= 1; half >>= 1) {
+        if (at < half) {
+            float m = sm[tid], s = ss[tid];
+            stat_add(m, s, sm[tid + half], ss[tid + half]);
+            sm[tid] = m;
+            ss[tid] = s;
+        }
+        __syncthreads();
+    }
+    const float total = ss[ti * PL] == 0.f && sm[ti * PL] == -INFINITY
+                            ? -INFINITY
+                            : fmaf(__builtin_amdgcn_logf(ss[ti * PL]), kLn2, sm[ti * PL]);
+    __syncthreads();
+    const int64_t v = t < nt ? y[t] : ignore;
+    const bool kept = v != ignore, valid = kept && v >= 0 && v < nv;
+    ss[tid] = valid ? dot.part(t, v, at, PL) : 0.f;
+    __syncthreads();
+    for (int half = PL / 2; half >= 1; half >>= 1) {
+        if (at < half) ss[tid] = Dot::add(ss[tid], ss[tid + half]);
+        __syncthreads();
+    }
+    if (at == 0 && t < nt) {
+        lse[t] = total;
+        loss[t] = valid ? total - dot.finish(ss[tid], t, v) : kept ? __uint_as_float(0x7fc00000u) : 0.f;
+    }
+}
+
+// ---- backward: small kernels ---------------------------------------------------------
+// What the products need of each token: its g without the ignored ones, as a
+// multiple of *unit, and its lse (NaN for a target out of range). unit: a power
+// of two near the largest |g|, for fp16, whose range the G of a mean over many
+// tokens would leave; 1 for bf16. One block; NaN and Inf among the g pass
+// through with unit 1.
+__global__ __launch_bounds__(1024) void k_xent_prepare(const float *__restrict__ g, const float *__restrict__ lse,
+                                                       const int64_t *__restrict__ y, int64_t ignore, int64_t nt,
+                                                       int64_t nv, bool rescale, float *__restrict__ g_out,
+                                                       float *__restrict__ lse_out, float *__restrict__ unit) {
+    __shared__ uint32_t top[16];
+    uint32_t m = 0;
+    if (rescale)
+        for (int64_t t = threadIdx.x; t < nt; t += 1024)
+            if (y[t] != ignore) m = max(m, abs_bits(g[t]));
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+    if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) m = max(m, top[i]);
+    // the exponent alone; the smallest and largest binades keep unit 1
+    const uint32_t ex = m & 0x7f800000u;
+    const float u = ex >= 0x01000000u && ex < 0x7e000000u ? __uint_as_float(ex) : 1.f;
+    if (threadIdx.x == 0) *unit = u;
+    const float up = 1.f / u;  // exact
+    for (int64_t t = threadIdx.x; t < nt; t += 1024) {
+        const int64_t v = y[t];
+        g_out[t] = v == ignore ? 0.f : g[t] * up;
+        lse_out[t] = v == ignore || (v >= 0 && v < nv) ? lse[t] : __uint_as_float(0x7fc00000u);
+    }
+}
+
+// out[c][r] = in[r][c] for 16-bit values, through a 64 x 64 tile in LDS.
+// Rows r in [rows, rows8) (rows8: up to the next multiple of 8) come out as
+// zeros, and with PAD the columns [cols, cols8) of `in` are set to zero, so that
+// products over either index may read whole 16-byte chunks. Rows whose g is 0
+// come out as zeros (g may be null). Memory bound.
+template <bool PAD>
+__global__ __launch_bounds__(256) void k_transpose16(uint16_t *in, int64_t ldi, int64_t rows, int64_t cols,
+                                                     uint16_t *__restrict__ out, int64_t ldo,
+                                                     const float *__restrict__ g) {
+    __shared__ uint16_t tile[64][66];  // 33 banks per row: columns are read without conflicts
+    const int64_t c0 = (int64_t)blockIdx.x * 64;
+    const int64_t rows8 = (rows + 7) & ~(int64_t)7, cols8 = (cols + 7) & ~(int64_t)7;
+    const int tid = threadIdx.x, tr = tid >> 3, tc = (tid & 7) * 8;
+    for (int64_t r0 = (int64_t)blockIdx.y * 64; r0 < rows8; r0 += (int64_t)gridDim.y * 64) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t r = r0 + tr + 32 * h, c = c0 + tc;
+            uint16_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if (r < rows && (g == nullptr || g[r] != 0.f)) {
+                if (c + 8 <= cols) {
+                    *(U16 *)e = *(const U16 *)(in + r * ldi + c);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (c + i < cols) e[i] = in[r * ldi + c + i];
+                }
+            }
+            if (PAD && r < rows && c < cols8 && c + 8 > cols)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (c + i >= cols && c + i < cols8) in[r * ldi + c + i] = 0;
+            uint32_t *dst = (uint32_t *)&tile[tr + 32 * h][tc];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) dst[i] = e[2 * i] | ((uint32_t)e[2 * i + 1] << 16);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t c = c0 + tr + 32 * h, r = r0 + tc;
+            if (c < cols && r < rows8) {
+                v4i w;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = tile[tc + 2 * i][tr + 32 * h] | ((int)tile[tc + 2 * i + 1][tr + 32 * h] << 16);
+                *(v4i *)(out + c * ldo + r) = w;  // ldo and r are multiples of 8
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// Sums the planes of a product's slices, and the sum so far if there is one;
+// writes it back, or rounded and times *unit to `out`. Four values per thread,
+// slices in order.
+template <class T>
+__global__ __launch_bounds__(256) void k_join_rows(const float *__restrict__ planes, int splits, int64_t plane,
+                                                   int64_t ldp, float *sum, bool add, T *out, int64_t ldo,
+                                                   const float *__restrict__ unit, int64_t na, int64_t nb) {
+    const int64_t a = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+    if (a >= na) return;
+    for (int64_t b = blockIdx.y; b < nb; b += gridDim.y) {
+        v4f s = *(const v4f *)(planes + b * ldp + a);
+        for (int i = 1; i < splits; ++i) s += *(const v4f *)(planes + i * plane + b * ldp + a);
+        if (add) s += *(const v4f *)(sum + b * ldp + a);
+        if (out == nullptr) {
+            *(v4f *)(sum + b * ldp + a) = s;
+        } else {
+            const float u = *unit;
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                if (a + v < na) out[b * ldo + a + v] = (T)(s[v] * u);
+        }
+    }
+}
+
+__global__ __launch_bounds__(256) void k_zero_rows16(uint16_t *out, int64_t ldo, int64_t rows, int64_t cols) {
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        for (int64_t c = threadIdx.x; c < cols; c += 256) out[r * ldo + c] = 0;
+}
+
+// ---- forward -------------------------------------------------------------------------
+// Tokens are taken in runs, so that the parts (8 bytes per token and 128
+// entries, or fewer for small products) stay small beside W.
+constexpr int64_t kRun = 16384;
+
+// The product of rows of X (tokens of the output) and rows of W, pitches in elements.
+template <int BYTES>
+TileArgs rows_args(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const void *W, int64_t ldw) {
+    TileArgs ta{};
+    ta.A = (const int8_t *)W;
+    ta.B = (const int8_t *)X;
+    ta.lda = ldw * BYTES;
+    ta.ldb = ldx * BYTES;
+    ta.na = v;
+    ta.nb = t;
+    ta.kbytes = d * BYTES;
+    return ta;
+}
+
+int parts_of(const TileArgs &ta) {
+    if (ta.nb <= kSkinnyRows) return (int)((ta.na + 15) / 16);
+    if (tile_side(ta) == 256) return (int)(2 * ((ta.na + 255) / 256));
+    return (int)((ta.na + 63) / 64);
+}
+// Enough for either tile, whatever the alignment of the operands.
+size_t forward_bytes(int64_t t, int64_t v) {
+    const int64_t run = t < kRun ? t : kRun;
+    return up256(8 * (size_t)run * (size_t)(run <= kSkinnyRows ? (v + 15) / 16 : (v + 63) / 64));
+}
+
+template <class M, bool SCALED, class DotOf>
+int forward(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const float *sx, const void *W, int64_t ldw,
+            const float *sw, const int64_t *y, int64_t ignore, float *loss, float *lse, char *ws, DotOf dot_of,
+            hipStream_t s) {
+    float2 *part = (float2 *)ws;
+    for (int64_t t0 = 0; t0 < t; t0 += kRun) {
+        const int64_t nt = t - t0 < kRun ? t - t0 : kRun;
+        const char *x = (const char *)X + t0 * ldx * M::BYTES;
+        const TileArgs ta = rows_args<M::BYTES>(nt, v, d, x, ldx, W, ldw);
+        const typename EpiLse<SCALED>::Args e = {part, nt, sw, sx ? sx + t0 : nullptr, v, nt};
+        if (nt <= kSkinnyRows)
+            HIP_TRY((launch_skinny<M, EpiLse<SCALED>, BRows>(ta, e, {}, s)));
+        else
+            HIP_TRY((launch_tile<M, EpiLse<SCALED>>(ta, e, 1, s)));
+        const auto dot = dot_of(x, t0);
+        typedef std::remove_const_t<decltype(dot)> Dot;
+        const int nparts = parts_of(ta);
+        if (nt <= kSkinnyRows)  // a block each
+            hipLaunchKernelGGL((k_xent_join<Dot, 1>), dim3((unsigned)nt), dim3(256), 0, s, part, nt, nparts, nt, v,
+                               y + t0, ignore, dot, loss + t0, lse + t0);
+        else
+            hipLaunchKernelGGL((k_xent_join<Dot, 8>), dim3((unsigned)((nt + 7) / 8)), dim3(256), 0, s, part, nt, nparts,
+                               nt, v, y + t0, ignore, dot, loss + t0, lse + t0);
+        HIP_TRY(hipGetLastError());
+    }
+    return OZAKI2_SUCCESS;
+}
+
+template <class M>
+int forward16(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const void *W, int64_t ldw, const int64_t *y,
+              int64_t ignore, float *loss, float *lse, char *ws, hipStream_t s) {
+    typedef typename M::Elem T;
+    return forward<M, false>(
+        t, v, d, X, ldx, nullptr, W, ldw, nullptr, y, ignore, loss, lse, ws,
+        [=](const char *x, int64_t) { return DotFloat<T>{(const T *)x, (const T *)W, ldx, ldw, d}; }, s);
+}
+
+// ---- backward ------------------------------------------------------------------------
+// Pitch in 16-bit elements of a workspace matrix: whole cache lines, an odd
+// number of them, so that the rows a tile reads at one k do not all lie in one
+// channel of the memory.
+int64_t pitch16(int64_t n) { return (((n + 63) / 64) | 1) * 64; }
+
+struct GradPlan {
+    int64_t vc;           // vocabulary entries per piece
+    int splits;           // slices of a piece in dX's product
+    int64_t ldp, plane;   // pitch and size of dX's planes
+    size_t g, lse, unit, xt, wt, gm, gt, planes, sum, total;
+};
+// G and its transpose take up to 2^28 entries each: 32768 vocabulary entries
+// at 8192 tokens, enough for the products over them to run at full rate.
+constexpr int64_t kPieceEntries = (int64_t)1 << 28;
+GradPlan plan_grad(int64_t t, int64_t v, int64_t d, bool dx, bool dw) {
+    GradPlan p{};
+    int64_t most = kPieceEntries / (t > 0 ? t : 1) / 256 * 256;
+    if (most < 256) most = 256;
+    const int64_t pieces = (v + most - 1) / most;
+    p.vc = ((v + pieces - 1) / pieces + 255) / 256 * 256;
+    if (p.vc > v) p.vc = v;
+    p.splits = use_large_tile(d, t) ? 1 : tile_splits(d, t, 2 * ((p.vc + 7) / 8 * 8));
+    p.ldp = (d + 3) / 4 * 4;
+    p.plane = t * p.ldp;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += up256(bytes);
+        return at;
+    };
+    const size_t st = (size_t)t, sd = (size_t)d, sv = (size_t)p.vc;
+    p.g = take(4 * st);
+    p.lse = take(4 * st);
+    p.unit = take(4);
+    p.gm = take(2 * st * (size_t)pitch16(p.vc));
+    if (dw) {
+        p.xt = take(2 * sd * (size_t)pitch16(t));
+        p.gt = take(2 * sv * (size_t)pitch16(t));
+    }
+    if (dx) {
+        p.wt = take(2 * sd * (size_t)pitch16(p.vc));
+        p.planes = take(4 * (size_t)p.plane * (size_t)p.splits);
+        p.sum = pieces > 1 ? take(4 * (size_t)p.plane) : 0;
+    }
+    p.total = off;
+    return p;
+}
+
+template <bool PAD>
+hipError_t transpose16(void *in, int64_t ldi, int64_t rows, int64_t cols, void *out, int64_t ldo, const float *g,
+                       hipStream_t s) {
+    const int64_t by = (rows + 63) / 64;
+    hipLaunchKernelGGL((k_transpose16<PAD>), dim3((unsigned)((cols + 63) / 64), (unsigned)(by < 65535 ? by : 65535)),
+                       dim3(256), 0, s, (uint16_t *)in, ldi, rows, cols, (uint16_t *)out, ldo, g);
+    return hipGetLastError();
+}
+
+hipError_t zero_rows16(void *out, int64_t ldo, int64_t rows, int64_t cols, hipStream_t s) {
+    hipLaunchKernelGGL(k_zero_rows16, dim3((unsigned)(rows < 65535 ? rows : 65535)), dim3(256), 0, s, (uint16_t *)out, ldo,
+                       rows, cols);
+    return hipGetLastError();
+}
+
+template <class M>
+int backward(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const void *W, int64_t ldw, const int64_t *y,
+             int64_t ignore, const float *lse, const float *grad, void *dX, int64_t lddx, void *dW, int64_t lddw,
+             char *ws, hipStream_t s) {
+    typedef typename M::Elem T;
+    const GradPlan p = plan_grad(t, v, d, dX != nullptr, dW != nullptr);
+    float *g = (float *)(ws + p.g), *l = (float *)(ws + p.lse), *unit = (float *)(ws + p.unit);
+    T *gm = (T *)(ws + p.gm), *gt = (T *)(ws + p.gt), *xt = (T *)(ws + p.xt), *wt = (T *)(ws + p.wt);
+    float *planes = (float *)(ws + p.planes), *sum = (float *)(ws + p.sum);
+    const int64_t ldg = pitch16(p.vc), ldt = pitch16(t);
+    const int64_t t8 = (t + 7) / 8 * 8;
+    hipLaunchKernelGGL(k_xent_prepare, dim3(1), dim3(1024), 0, s, grad, lse, y, ignore, t, v, M::HALF, g,
+                       l, unit);
+    HIP_TRY(hipGetLastError());
+    if (dW) HIP_TRY(transpose16<false>((void *)X, ldx, t, d, xt, ldt, g, s));
+    for (int64_t v0 = 0; v0 < v; v0 += p.vc) {
+        const int64_t vc = v - v0 < p.vc ? v - v0 : p.vc, v8 = (vc + 7) / 8 * 8;
+        const char *w = (const char *)W + v0 * ldw * 2;
+        HIP_TRY((launch_tile<M, EpiProb<T>>(rows_args<2>(t, vc, d, X, ldx, w, ldw), {gm, ldg, l, g, y, v0, vc, t}, 1,
+                                            s)));
+        if (dW) {
+            HIP_TRY(transpose16<true>(gm, ldg, t, vc, gt, ldt, nullptr, s));
+            HIP_TRY((launch_tile<M, EpiOut<T>>(rows_args<2>(vc, d, t8, gt, ldt, xt, ldt),
+                                               {(T *)dW + v0 * lddw, lddw, unit, d, vc}, 1, s)));
+        }
+        if (dX) {
+            if (!dW && v8 > vc) HIP_TRY(zero_rows16(gm + vc, ldg, t, v8 - vc, s));
+            HIP_TRY(transpose16<false>((void *)w, ldw, vc, d, wt, ldg, nullptr, s));
+            const TileArgs ta = rows_args<2>(t, d, v8, gm, ldg, wt, ldg);
+            const bool first = v0 == 0, last = v0 + vc == v;
+            if (first && last && p.splits == 1) {
+                HIP_TRY((launch_tile<M, EpiOut<T>>(ta, {(T *)dX, lddx, unit, d, t}, 1, s)));
+            } else {
+                HIP_TRY((launch_tile<M, EpiRaw>(ta, {(uint32_t *)planes, p.ldp, p.plane, d, t}, p.splits, s)));
+                hipLaunchKernelGGL((k_join_rows<T>), dim3((unsigned)((d + 1023) / 1024), (unsigned)(t < 65535 ? t : 65535)),
+                                   dim3(256), 0, s, planes, p.splits, p.plane, p.ldp, sum, !first,
+                                   last ? (T *)dX : nullptr, lddx, unit, d, t);
+                HIP_TRY(hipGetLastError());
+            }
+        }
+    }
+    return OZAKI2_SUCCESS;
+}
+
+}  // namespace
+}  // namespace oz2
+
+using namespace oz2;
+
+namespace {
+
+struct XentCall {
+    int64_t t, v, d, ldx, ldw;
+    const void *X, *W;
+    const float *sx, *sw;  // int8 only
+    int type;              // OZAKI2_BF16, OZAKI2_FP16, or -1 for int8
+    const int64_t *y;
+    int64_t ignore;
+    float *loss, *lse;
+    hipStream_t s;
+};
+int run_xent(void *ctx, char *ws) {
+    const XentCall &c = *(const XentCall *)ctx;
+    if (c.type == OZAKI2_BF16)
+        return forward16<MmaBf16>(c.t, c.v, c.d, c.X, c.ldx, c.W, c.ldw, c.y, c.ignore, c.loss, c.lse, ws, c.s);
+    if (c.type == OZAKI2_FP16)
+        return forward16<MmaF16>(c.t, c.v, c.d, c.X, c.ldx, c.W, c.ldw, c.y, c.ignore, c.loss, c.lse, ws, c.s);
+    return forward<MmaI8, true>(
+        c.t, c.v, c.d, c.X, c.ldx, c.sx, c.W, c.ldw, c.sw, c.y, c.ignore, c.loss, c.lse, ws,
+        [&](const char *x, int64_t t0) {
+            return DotInt8{(const int8_t *)x, (const int8_t *)c.W, c.ldx, c.ldw, c.d, c.sx + t0, c.sw};
+        },
+        c.s);
+}
+// After the argument checks; bad_ws: the status of a bad workspace argument.
+int launch(XentCall c, bool cached, void *workspace, size_t bytes, int bad_ws) {
+    const int64_t lim = (int64_t)1 << 31;
+    if (c.t >= lim || c.v >= lim || c.d >= (c.type < 0 ? (int64_t)OZAKI2_I8_MAX_K + 1 : lim / 4)) return OZAKI2_ERR_UNSUPPORTED;
+    if (c.t == 0) return OZAKI2_SUCCESS;
+    const size_t need = forward_bytes(c.t, c.v);
+    if (cached) return with_workspace(need, c.s, run_xent, &c);
+    if (workspace == nullptr || ((uintptr_t)workspace & (kWsAlign - 1)) != 0) return bad_ws;
+    if (bytes < need) return OZAKI2_ERR_WORKSPACE;
+    return run_xent(&c, (char *)workspace);
+}
+int front_xent(const XentCall &c, bool cached, void *workspace, size_t bytes) {
+    const bool any = c.t > 0;
+    const int64_t row = c.d > 1 ? c.d : 1;
+    if (c.t < 0) return -1;
+    if (c.v < 0 || (c.v == 0 && any)) return -2;
+    if (c.d < 0) return -3;
+    if (c.X == nullptr && any && c.d > 0) return -4;
+    if (c.ldx < row) return -5;
+    if (c.W == nullptr && any && c.d > 0) return -6;
+    if (c.ldw < row) return -7;
+    if (c.type != OZAKI2_BF16 && c.type != OZAKI2_FP16) return -8;
+    if (c.y == nullptr && any) return -9;
+    if (c.loss == nullptr && any) return -11;
+    if (c.lse == nullptr && any) return -12;
+    return launch(c, cached, workspace, bytes, -13);
+}
+int front_i8xent(const XentCall &c, bool cached, void *workspace, size_t bytes) {
+    const bool any = c.t > 0;
+    const int64_t row = c.d > 1 ? c.d : 1;
+    if (c.t < 0) return -1;
+    if (c.v < 0 || (c.v == 0 && any)) return -2;
+    if (c.d < 0) return -3;
+    if (c.X == nullptr && any && c.d > 0) return -4;
+    if (c.ldx < row) return -5;
+    if (c.sx == nullptr && any) return -6;
+    if (c.W == nullptr && any && c.d > 0) return -7;
+    if (c.ldw < row) return -8;
+    if (c.sw == nullptr && any) return -9;
+    if (c.y == nullptr && any) return -10;
+    if (c.loss == nullptr && any) return -12;
+    if (c.lse == nullptr && any) return -13;
+    return launch(c, cached, workspace, bytes, -14);
+}
+
+struct GradCall {
+    int64_t t, v, d, ldx, ldw, lddx, lddw;
+    const void *X, *W;
+    int type;
+    const int64_t *y;
+    int64_t ignore;
+    const float *lse, *grad;
+    void *dX, *dW;
+    hipStream_t s;
+};
+int run_grad(void *ctx, char *ws) {
+    const GradCall &c = *(const GradCall *)ctx;
+    return c.type == OZAKI2_BF16 ? backward<MmaBf16>(c.t, c.v, c.d, c.X, c.ldx, c.W, c.ldw, c.y, c.ignore, c.lse, c.grad,
+                                                     c.dX, c.lddx, c.dW, c.lddw, ws, c.s)
+                                 : backward<MmaF16>(c.t, c.v, c.d, c.X, c.ldx, c.W, c.ldw, c.y, c.ignore, c.lse, c.grad,
+                                                    c.dX, c.lddx, c.dW, c.lddw, ws, c.s);
+}
+int front_grad(GradCall c, bool cached, void *workspace, size_t bytes) {
+    const bool any = c.t > 0;
+    const int64_t row = c.d > 1 ? c.d : 1, lim = (int64_t)1 << 31;
+    if (c.t < 0) return -1;
+    if (c.v < 0 || (c.v == 0 && any)) return -2;
+    if (c.d < 0) return -3;
+    if (c.X == nullptr && any && c.d > 0) return -4;
+    if (c.ldx < row) return -5;
+    if (c.W == nullptr && any && c.d > 0) return -6;
+    if (c.ldw < row) return -7;
+    if (c.type != OZAKI2_BF16 && c.type != OZAKI2_FP16) return -8;
+    if (c.y == nullptr && any) return -9;
+    if (c.lse == nullptr && any) return -11;
+    if (c.grad == nullptr && any) return -12;
+    if (c.dX != nullptr && c.lddx < row) return -14;
+    if (c.dW != nullptr && c.lddw < row) return -16;
+    if (c.t >= lim || c.v >= lim || c.d >= lim / 4) return OZAKI2_ERR_UNSUPPORTED;
+    if (c.d == 0 || c.v == 0 || (c.dX == nullptr && c.dW == nullptr)) return OZAKI2_SUCCESS;
+    if (!any) {
+        // no token: nothing flows into W
+        if (c.dW) HIP_TRY(zero_rows16(c.dW, c.lddw, c.v, c.d, c.s));
+        return OZAKI2_SUCCESS;
+    }
+    const size_t need = plan_grad(c.t, c.v, c.d, c.dX != nullptr, c.dW != nullptr).total;
+    if (cached) return with_workspace(need, c.s, run_grad, &c);
+    if (workspace == nullptr || ((uintptr_t)workspace & (kWsAlign - 1)) != 0) return -17;
+    if (bytes < need) return OZAKI2_ERR_WORKSPACE;
+    return run_grad(&c, (char *)workspace);
+}
+
+bool sizes_fit(int64_t t, int64_t v, int64_t d) {
+    const int64_t lim = (int64_t)1 << 31;
+    return t > 0 && v > 0 && d >= 0 && t < lim && v < lim && d < lim / 4;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ozaki2_xent(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const void *W, int64_t ldw, int type,
+                const int64_t *targets, int64_t ignore_index, float *loss, float *lse, void *stream) {
+    return front_xent({t, v, d, ldx, ldw, X, W, nullptr, nullptr, type, targets, ignore_index, loss, lse,
+                       (hipStream_t)stream}, true, nullptr, 0);
+}
+int ozaki2_xent_ws(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const void *W, int64_t ldw, int type,
+                   const int64_t *targets, int64_t ignore_index, float *loss, float *lse, void *workspace,
+                   size_t workspace_bytes, void *stream) {
+    return front_xent({t, v, d, ldx, ldw, X, W, nullptr, nullptr, type, targets, ignore_index, loss, lse,
+                       (hipStream_t)stream}, false, workspace, workspace_bytes);
+}
+size_t ozaki2_xent_workspace_size(int64_t t, int64_t v, int64_t d) {
+    return sizes_fit(t, v, d) ? forward_bytes(t, v) : 0;
+}
+
+int ozaki2_i8xent(int64_t t, int64_t v, int64_t k, const int8_t *A, int64_t lda, const float *a_scale, const int8_t *B,
+                  int64_t ldb, const float *b_scale, const int64_t *targets, int64_t ignore_index, float *loss,
+                  float *lse, void *stream) {
+    return front_i8xent({t, v, k, lda, ldb, A, B, a_scale, b_scale, -1, targets, ignore_index, loss, lse,
+                         (hipStream_t)stream}, true, nullptr, 0);
+}
+int ozaki2_i8xent_ws(int64_t t, int64_t v, int64_t k, const int8_t *A, int64_t lda, const float *a_scale,
+                     const int8_t *B, int64_t ldb, const float *b_scale, const int64_t *targets, int64_t ignore_index,
+                     float *loss, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+    return front_i8xent({t, v, k, lda, ldb, A, B, a_scale, b_scale, -1, targets, ignore_index, loss, lse,
+                         (hipStream_t)stream}, false, workspace, workspace_bytes);
+}
+
+int ozaki2_xent_grad(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const void *W, int64_t ldw, int type,
+                     const int64_t *targets, int64_t ignore_index, const float *lse, const float *grad_loss, void *dX,
+                     int64_t lddx, void *dW, int64_t lddw, void *stream) {
+    return front_grad({t, v, d, ldx, ldw, lddx, lddw, X, W, type, targets, ignore_index, lse, grad_loss, dX, dW,
+                       (hipStream_t)stream}, true, nullptr, 0);
+}
+int ozaki2_xent_grad_ws(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const void *W, int64_t ldw,
+                        int type, const int64_t *targets, int64_t ignore_index, const float *lse,
+                        const float *grad_loss, void *dX, int64_t lddx, void *dW, int64_t lddw, void *workspace,
+                        size_t workspace_bytes, void *stream) {
+    return front_grad({t, v, d, ldx, ldw, lddx, lddw, X, W, type, targets, ignore_index, lse, grad_loss, dX, dW,
+                       (hipStream_t)stream}, false, workspace, workspace_bytes);
+}
+size_t ozaki2_xent_grad_workspace_size(int64_t t, int64_t v, int64_t d, int want_dx, int want_dw) {
+    return sizes_fit(t, v, d) && d > 0 && (want_dx || want_dw) ? plan_grad(t, v, d, want_dx != 0, want_dw != 0).total : 0;
+}
+
+}  // extern "C"
