@@ -417,9 +417,9 @@ enum ozaki2_type {
 
 /*
  * Rows of X (type xtype, element (i, h) at X[i*ldx + h]) as int8 with a scale
- * each: amax = max_h |X[i][h]|, scale[i] = amax / 127 and
- * Q[i][h] = rint(X[i][h] * (127 / amax)), in binary32 with ties to even, for
- * Q[i*ldq + h]. A row of zeros gets scale 0 and zeros; one whose amax is below
+ * each: amax = max_h |X[i][h]|, scale[i] = amax * (1/127) and
+ * Q[i*ldq + h] = rint(X[i][h] * ((1/amax) * 127)), every operation rounded to
+ * binary32 to nearest, ties to even. A row of zeros gets scale 0 and zeros; one whose amax is below
  * 2^-120 gets zeros; one that holds Inf or NaN gets zeros and a NaN scale, so
  * products with it are NaN. Returns 0, -1..-8 for an invalid argument,
  * OZAKI2_ERR_UNSUPPORTED (t or k >= 2^31) or OZAKI2_ERR_HIP. Capturable.
@@ -516,7 +516,8 @@ int ozaki2_i8xent_ws(int64_t t, int64_t v, int64_t k, const int8_t *A, int64_t l
  * The logits are computed again, a piece of the vocabulary at a time, and G is
  * held in `type` for that piece only (at most 2^28 entries, or t * 256); sums
  * are binary32, rounded once to `type`. For fp16 G is held relative to the
- * largest |grad_loss|, so small gradients do not underflow on the way.
+ * largest |grad_loss|, so small gradients do not underflow on the way; below
+ * 2^-126 the matrix cores and the exponential give zeros.
  *   lse       DEVICE binary32 [t] as ozaki2_xent wrote it for the same X, W.
  *   grad_loss DEVICE binary32 [t].
  *   dX, lddx  DEVICE output of `type`, or NULL to skip it; lddx >= max(1, d).

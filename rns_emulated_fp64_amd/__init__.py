@@ -465,83 +465,80 @@ def _type_of(dtype, what):
         raise TypeError(f"{what} must be bfloat16, float16 or float32, not {dtype}") from None
 
 
-def _rows(x, what, cols=None):
-    """A 2-D tensor with unit stride along its rows (a copy if it has none) and its pitch."""
-    if x.dim() != 2 or (cols is not None and x.shape[1] != cols):
-        raise ValueError(f"{what} must be a matrix" + (f" with {cols} columns" if cols is not None else ""))
-    if x.shape[1] > 1 and x.stride(1) != 1 or x.shape[0] > 1 and x.stride(0) < x.shape[1]:
-        x = x.contiguous()
-    return x, max(x.stride(0) if x.shape[0] > 1 else x.shape[1], 1)
+def _rows(x, what):
+    """A matrix whose rows are contiguous (a copy if they are not), and its pitch."""
+    if x.dim() != 2:
+        raise ValueError(f"{what} must be a matrix")
+    (t, k), (pitch, step) = x.shape, x.stride()
+    if step == 1 and pitch >= k > 0:
+        return x, pitch
+    if k > 1 and step != 1 or t > 1 and pitch < k:
+        return x.contiguous(), max(k, 1)
+    return x, max(pitch if t > 1 else k, 1)
 
 
-def _vector(x, n, dtype, like, what):
-    """A contiguous vector of n values on the device of `like`."""
-    if x.dtype != dtype or x.device != like.device or x.numel() != n:
-        raise ValueError(f"{what} must hold {n} {dtype} values on {like.device}")
+def _vector(x, n, dtype, device, what):
+    """A contiguous vector of n values on a device."""
+    if x.dtype != dtype or x.device != device or x.numel() != n:
+        raise ValueError(f"{what} must hold {n} {dtype} values on {device}")
     return x if x.is_contiguous() else x.contiguous()
 
 
-class _On:
-    """The library launches on the current device: makes it the operands' one, and gives their current stream."""
+def _call(fn, name, device, *args):
+    """fn(*args, stream) on the current stream of a device, which the library needs to be the current one."""
+    import torch
 
-    def __init__(self, x):
-        import torch
-
-        self._device = x.device.index
-        self._other = None if torch.cuda.current_device() == self._device else torch.cuda.device(x.device)
-        self._stream = torch.cuda.current_stream
-
-    def __enter__(self):
-        if self._other is not None:
-            self._other.__enter__()
-        return self._stream(self._device).cuda_stream
-
-    def __exit__(self, *exc):
-        if self._other is not None:
-            self._other.__exit__(*exc)
+    index = device.index
+    if index == torch.cuda.current_device():
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if st:
+        raise Ozaki2Error(st, name)
 
 
-def _workspace(size, given, like):
-    """Pointer and bytes of the caller's workspace, or of a new one from torch's allocator (which may be captured)."""
+def _workspace(size, given, device):
+    """The caller's workspace or a new one from torch's allocator (which may be captured), its pointer and bytes."""
     import torch
 
     if given is not None:
-        if given.device != like.device:
-            raise ValueError(f"workspace must be a tensor on {like.device}")
+        if given.device != device:
+            raise ValueError(f"workspace must be a tensor on {device}")
         return given, given.data_ptr(), given.numel() * given.element_size()
     if size == 0:
         return None, None, 0
-    ws = torch.empty(size, dtype=torch.uint8, device=like.device)
+    ws = torch.empty(size, dtype=torch.uint8, device=device)
     return ws, ws.data_ptr(), size
 
 
-def _product_out(t, n, dtype, out, like):
+def _product_out(t, n, dtype, out, device):
     import torch
 
     if out is None:
-        return torch.empty((t, n), dtype=dtype, device=like.device)
-    if out.dtype != dtype or out.device != like.device or tuple(out.shape) != (t, n) or n > 1 and out.stride(1) != 1 \
+        return torch.empty((t, n), dtype=dtype, device=device), max(n, 1)
+    if out.dtype != dtype or out.device != device or tuple(out.shape) != (t, n) or n > 1 and out.stride(1) != 1 \
             or t > 1 and out.stride(0) < n:
-        raise ValueError(f"out must be a ({t}, {n}) {dtype} tensor on {like.device} with contiguous rows")
-    return out
+        raise ValueError(f"out must be a ({t}, {n}) {dtype} tensor on {device} with contiguous rows")
+    return out, max(out.stride(0) if t > 1 else n, 1)
 
 
 def quantize_rows(X):
     """Rows of X (float32, float16 or bfloat16) as int8 with a binary32 scale each: (q, scale) with
-    scale = max|x| / 127 and q = rint(x * (127 / max|x|)) (ozaki2_quantize_rows)."""
+    scale = max|x| / 127 and q = rint(x / scale), with the binary32 roundings that include/ozaki2.h states
+    (ozaki2_quantize_rows)."""
     import torch
 
     xtype = _type_of(X.dtype, "X")
-    if not X.is_cuda:
+    device = X.device
+    if device.type != "cuda":
         raise TypeError("X must be on a GPU")
     X, ldx = _rows(X, "X")
     t, k = X.shape
-    q = torch.empty((t, k), dtype=torch.int8, device=X.device)
-    scale = torch.empty(t, dtype=torch.float32, device=X.device)
-    with _On(X) as stream:
-        st = lib().ozaki2_quantize_rows(t, k, X.data_ptr(), ldx, xtype, q.data_ptr(), max(k, 1), scale.data_ptr(), stream)
-    if st:
-        raise Ozaki2Error(st, "ozaki2_quantize_rows")
+    q = torch.empty((t, k), dtype=torch.int8, device=device)
+    scale = torch.empty(t, dtype=torch.float32, device=device)
+    _call(lib().ozaki2_quantize_rows, "ozaki2_quantize_rows", device, t, k, X.data_ptr(), ldx, xtype, q.data_ptr(),
+          max(k, 1), scale.data_ptr())
     return q, scale
 
 
@@ -553,25 +550,24 @@ def i8gemm(A, B, a_scale, b_scale, bias=None, out_dtype=None, out=None, workspac
 
     dt = out_dtype if out_dtype is not None else out.dtype if out is not None else torch.bfloat16
     ctype = _type_of(dt, "out_dtype")
-    if A.dtype != torch.int8 or B.dtype != torch.int8 or not A.is_cuda or A.device != B.device:
+    device = A.device
+    if A.dtype != torch.int8 or B.dtype != torch.int8 or device.type != "cuda" or B.device != device:
         raise TypeError("A and B must be int8 tensors on the same GPU")
     A, lda = _rows(A, "A")
+    B, ldb = _rows(B, "B")
     t, k = A.shape
-    B, ldb = _rows(B, "B", k)
     n = B.shape[0]
-    a_scale = _vector(a_scale, t, torch.float32, A, "a_scale")
-    b_scale = _vector(b_scale, n, torch.float32, A, "b_scale")
+    if B.shape[1] != k:
+        raise ValueError("A and B must have the same number of columns")
+    a_scale = _vector(a_scale, t, torch.float32, device, "a_scale")
+    b_scale = _vector(b_scale, n, torch.float32, device, "b_scale")
     if bias is not None:
-        bias = _vector(bias, n, torch.float32, A, "bias")
-    C = _product_out(t, n, dt, out, A)
+        bias = _vector(bias, n, torch.float32, device, "bias")
+    C, ldc = _product_out(t, n, dt, out, device)
     L = lib()
-    ws, wp, wb = _workspace(L.ozaki2_i8gemm_workspace_size(t, n, k), workspace, A)
-    with _On(A) as stream:
-        st = L.ozaki2_i8gemm_ws(t, n, k, A.data_ptr(), lda, a_scale.data_ptr(), B.data_ptr(), ldb, b_scale.data_ptr(),
-                                None if bias is None else bias.data_ptr(), C.data_ptr(),
-                                max(C.stride(0) if t > 1 else n, 1), ctype, wp, wb, stream)
-    if st:
-        raise Ozaki2Error(st, "ozaki2_i8gemm_ws")
+    ws, wp, wb = _workspace(L.ozaki2_i8gemm_workspace_size(t, n, k), workspace, device)
+    _call(L.ozaki2_i8gemm_ws, "ozaki2_i8gemm_ws", device, t, n, k, A.data_ptr(), lda, a_scale.data_ptr(), B.data_ptr(),
+          ldb, b_scale.data_ptr(), None if bias is None else bias.data_ptr(), C.data_ptr(), ldc, ctype, wp, wb)
     return C
 
 
@@ -584,24 +580,23 @@ def i8linear(X, B, b_scale, bias=None, out_dtype=None, out=None, workspace=None)
     xtype = _type_of(X.dtype, "X")
     dt = out_dtype if out_dtype is not None else out.dtype if out is not None else X.dtype
     ctype = _type_of(dt, "out_dtype")
-    if B.dtype != torch.int8 or not X.is_cuda or X.device != B.device:
+    device = X.device
+    if B.dtype != torch.int8 or device.type != "cuda" or B.device != device:
         raise TypeError("X and int8 B must be on the same GPU")
     X, ldx = _rows(X, "X")
+    B, ldb = _rows(B, "B")
     t, k = X.shape
-    B, ldb = _rows(B, "B", k)
     n = B.shape[0]
-    b_scale = _vector(b_scale, n, torch.float32, X, "b_scale")
+    if B.shape[1] != k:
+        raise ValueError("X and B must have the same number of columns")
+    b_scale = _vector(b_scale, n, torch.float32, device, "b_scale")
     if bias is not None:
-        bias = _vector(bias, n, torch.float32, X, "bias")
-    C = _product_out(t, n, dt, out, X)
+        bias = _vector(bias, n, torch.float32, device, "bias")
+    C, ldc = _product_out(t, n, dt, out, device)
     L = lib()
-    ws, wp, wb = _workspace(L.ozaki2_i8linear_workspace_size(t, n, k), workspace, X)
-    with _On(X) as stream:
-        st = L.ozaki2_i8linear_ws(t, n, k, X.data_ptr(), ldx, xtype, B.data_ptr(), ldb, b_scale.data_ptr(),
-                                  None if bias is None else bias.data_ptr(), C.data_ptr(),
-                                  max(C.stride(0) if t > 1 else n, 1), ctype, wp, wb, stream)
-    if st:
-        raise Ozaki2Error(st, "ozaki2_i8linear_ws")
+    ws, wp, wb = _workspace(L.ozaki2_i8linear_workspace_size(t, n, k), workspace, device)
+    _call(L.ozaki2_i8linear_ws, "ozaki2_i8linear_ws", device, t, n, k, X.data_ptr(), ldx, xtype, B.data_ptr(), ldb,
+          b_scale.data_ptr(), None if bias is None else bias.data_ptr(), C.data_ptr(), ldc, ctype, wp, wb)
     return C
 
 
@@ -609,18 +604,22 @@ def i8linear(X, B, b_scale, bias=None, out_dtype=None, out=None, workspace=None)
 def _xent_operands(X, W, targets):
     import torch
 
-    if not X.is_cuda or W.device != X.device or targets.device != X.device:
+    device = X.device
+    if device.type != "cuda" or W.device != device or targets.device != device:
         raise TypeError("X, W and targets must be on the same GPU")
     if targets.dtype != torch.int64:
         raise TypeError("targets must be int64")
     X, ldx = _rows(X, "X")
-    W, ldw = _rows(W, "W", X.shape[1])
-    t = X.shape[0]
-    if tuple(targets.shape) != (t,):
+    W, ldw = _rows(W, "W")
+    t, d = X.shape
+    v = W.shape[0]
+    if W.shape[1] != d:
+        raise ValueError("X and W must have the same number of columns")
+    if targets.dim() != 1 or targets.shape[0] != t:
         raise ValueError(f"targets must have shape ({t},)")
-    if t and not W.shape[0]:
+    if t and not v:
         raise ValueError("W has no rows")
-    return X, ldx, W, ldw, targets if targets.is_contiguous() else targets.contiguous()
+    return device, t, v, d, X, ldx, W, ldw, targets if targets.is_contiguous() else targets.contiguous()
 
 
 def _xent_type(X, W):
@@ -638,18 +637,13 @@ def xent(X, W, targets, ignore_index=-100, workspace=None):
     import torch
 
     kind = _xent_type(X, W)
-    X, ldx, W, ldw, targets = _xent_operands(X, W, targets)
-    t, d = X.shape
-    v = W.shape[0]
-    loss = torch.empty(t, dtype=torch.float32, device=X.device)
-    lse = torch.empty(t, dtype=torch.float32, device=X.device)
+    device, t, v, d, X, ldx, W, ldw, targets = _xent_operands(X, W, targets)
+    loss = torch.empty(t, dtype=torch.float32, device=device)
+    lse = torch.empty(t, dtype=torch.float32, device=device)
     L = lib()
-    ws, wp, wb = _workspace(L.ozaki2_xent_workspace_size(t, v, d), workspace, X)
-    with _On(X) as stream:
-        st = L.ozaki2_xent_ws(t, v, d, X.data_ptr(), ldx, W.data_ptr(), ldw, kind, targets.data_ptr(), ignore_index,
-                              loss.data_ptr(), lse.data_ptr(), wp, wb, stream)
-    if st:
-        raise Ozaki2Error(st, "ozaki2_xent_ws")
+    ws, wp, wb = _workspace(L.ozaki2_xent_workspace_size(t, v, d), workspace, device)
+    _call(L.ozaki2_xent_ws, "ozaki2_xent_ws", device, t, v, d, X.data_ptr(), ldx, W.data_ptr(), ldw, kind,
+          targets.data_ptr(), ignore_index, loss.data_ptr(), lse.data_ptr(), wp, wb)
     return loss, lse
 
 
@@ -660,20 +654,15 @@ def i8xent(A, B, a_scale, b_scale, targets, ignore_index=-100, workspace=None):
 
     if A.dtype != torch.int8 or B.dtype != torch.int8:
         raise TypeError("A and B must be int8")
-    A, lda, B, ldb, targets = _xent_operands(A, B, targets)
-    t, k = A.shape
-    v = B.shape[0]
-    a_scale = _vector(a_scale, t, torch.float32, A, "a_scale")
-    b_scale = _vector(b_scale, v, torch.float32, A, "b_scale")
-    loss = torch.empty(t, dtype=torch.float32, device=A.device)
-    lse = torch.empty(t, dtype=torch.float32, device=A.device)
+    device, t, v, k, A, lda, B, ldb, targets = _xent_operands(A, B, targets)
+    a_scale = _vector(a_scale, t, torch.float32, device, "a_scale")
+    b_scale = _vector(b_scale, v, torch.float32, device, "b_scale")
+    loss = torch.empty(t, dtype=torch.float32, device=device)
+    lse = torch.empty(t, dtype=torch.float32, device=device)
     L = lib()
-    ws, wp, wb = _workspace(L.ozaki2_xent_workspace_size(t, v, k), workspace, A)
-    with _On(A) as stream:
-        st = L.ozaki2_i8xent_ws(t, v, k, A.data_ptr(), lda, a_scale.data_ptr(), B.data_ptr(), ldb, b_scale.data_ptr(),
-                                targets.data_ptr(), ignore_index, loss.data_ptr(), lse.data_ptr(), wp, wb, stream)
-    if st:
-        raise Ozaki2Error(st, "ozaki2_i8xent_ws")
+    ws, wp, wb = _workspace(L.ozaki2_xent_workspace_size(t, v, k), workspace, device)
+    _call(L.ozaki2_i8xent_ws, "ozaki2_i8xent_ws", device, t, v, k, A.data_ptr(), lda, a_scale.data_ptr(), B.data_ptr(),
+          ldb, b_scale.data_ptr(), targets.data_ptr(), ignore_index, loss.data_ptr(), lse.data_ptr(), wp, wb)
     return loss, lse
 
 
@@ -683,21 +672,15 @@ def xent_grad(X, W, targets, lse, grad_loss, ignore_index=-100, want_dx=True, wa
     import torch
 
     kind = _xent_type(X, W)
-    X, ldx, W, ldw, targets = _xent_operands(X, W, targets)
-    t, d = X.shape
-    v = W.shape[0]
-    lse = _vector(lse, t, torch.float32, X, "lse")
-    grad_loss = _vector(grad_loss, t, torch.float32, X, "grad_loss")
-    dX = torch.empty((t, d), dtype=X.dtype, device=X.device) if want_dx else None
-    dW = torch.empty((v, d), dtype=X.dtype, device=X.device) if want_dw else None
+    device, t, v, d, X, ldx, W, ldw, targets = _xent_operands(X, W, targets)
+    lse = _vector(lse, t, torch.float32, device, "lse")
+    grad_loss = _vector(grad_loss, t, torch.float32, device, "grad_loss")
+    dX = torch.empty((t, d), dtype=X.dtype, device=device) if want_dx else None
+    dW = torch.empty((v, d), dtype=X.dtype, device=device) if want_dw else None
     L = lib()
     ws, wp, wb = _workspace(L.ozaki2_xent_grad_workspace_size(t, v, d, 1 if want_dx else 0, 1 if want_dw else 0),
-                            workspace, X)
-    with _On(X) as stream:
-        st = L.ozaki2_xent_grad_ws(t, v, d, X.data_ptr(), ldx, W.data_ptr(), ldw, kind, targets.data_ptr(),
-                                   ignore_index, lse.data_ptr(), grad_loss.data_ptr(),
-                                   dX.data_ptr() if want_dx else None, max(d, 1), dW.data_ptr() if want_dw else None,
-                                   max(d, 1), wp, wb, stream)
-    if st:
-        raise Ozaki2Error(st, "ozaki2_xent_grad_ws")
+                            workspace, device)
+    _call(L.ozaki2_xent_grad_ws, "ozaki2_xent_grad_ws", device, t, v, d, X.data_ptr(), ldx, W.data_ptr(), ldw, kind,
+          targets.data_ptr(), ignore_index, lse.data_ptr(), grad_loss.data_ptr(),
+          dX.data_ptr() if want_dx else None, max(d, 1), dW.data_ptr() if want_dw else None, max(d, 1), wp, wb)
     return dX, dW

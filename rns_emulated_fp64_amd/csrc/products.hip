@@ -109,14 +109,19 @@ __global__ __launch_bounds__(256) void k_join_scale(const int32_t *__restrict__ 
 #pragma unroll
         for (int v = 0; v < 4; ++v)
             if (a + v < e.na)
-                e.out[b * e.ldo + a + v] = (OutT)fmaf((float)sum[v] * sb, e.sa[a + v], e.bias ? e.bias[a + v] : 0.f);
+                e.out[b * e.ldo + a + v] =
+                    rounded<OutT>(fmaf((float)sum[v] * sb, e.sa[a + v], e.bias ? e.bias[a + v] : 0.f));
     }
 }
 
 // ---- the product ---------------------------------------------------------------------
+// Slices of k, from the sizes alone: operands that are not aligned take as many.
 int splits_of(int64_t t, int64_t n, int64_t k) {
-    if (t <= kSkinnyRows) return 1;
-    return use_large_tile(n, t) ? 1 : tile_splits(n, t, k);
+    TileArgs ta{};
+    ta.na = n;
+    ta.nb = t;
+    ta.kbytes = k >= 256 ? (k + 15) / 16 * 16 : k;
+    return tile_splits(choose_tile(ta, false), n, t, ta.kbytes);
 }
 int64_t plane_pitch(int64_t n) { return (n + 3) / 4 * 4; }
 size_t i8gemm_bytes(int64_t t, int64_t n, int64_t k) {
@@ -124,9 +129,9 @@ size_t i8gemm_bytes(int64_t t, int64_t n, int64_t k) {
     return s > 1 ? (size_t)s * (size_t)t * (size_t)plane_pitch(n) * 4 : 0;
 }
 
-// Activations that the skinny kernel quantises itself: a few rows that fit LDS
-// beside its sums.
-constexpr int64_t kQuantRows = 4, kQuantLds = 48 * 1024;
+// Activations that the skinny kernel quantises itself: rows that fit LDS beside
+// its sums.
+constexpr int64_t kQuantRows = 8, kQuantLds = 46 * 1024;
 int64_t quant_pitch(int64_t k) { return (k + 63) / 64 * 64 + 16; }
 bool quantises_in_product(int64_t t, int64_t k) { return t <= kQuantRows && t * (quant_pitch(k) + 4) <= kQuantLds; }
 
@@ -142,17 +147,14 @@ int product_t(int64_t t, int64_t n, int64_t k, const int8_t *A, int64_t lda, con
     ta.nb = t;
     ta.kbytes = k;
     const typename EpiScale<OutT>::Args e = {(OutT *)C, ldc, b_scale, a_scale, bias, n, t};
-    if (t <= kSkinnyRows) {
-        HIP_TRY((launch_skinny<MmaI8, EpiScale<OutT>, BRows>(ta, e, {}, s)));
-        return OZAKI2_SUCCESS;
-    }
-    const int splits = splits_of(t, n, k);
+    const Tile tile = choose_tile(ta, false);
+    const int splits = tile == Tile::skinny ? 1 : splits_of(t, n, k);
     if (splits == 1) {
-        HIP_TRY((launch_tile<MmaI8, EpiScale<OutT>>(ta, e, 1, s)));
+        HIP_TRY((launch_tile<MmaI8, EpiScale<OutT>, false>(ta, e, tile, 1, s)));
         return OZAKI2_SUCCESS;
     }
     const int64_t ldp = plane_pitch(n), plane = t * ldp;
-    HIP_TRY((launch_tile<MmaI8, EpiRaw>(ta, {(uint32_t *)ws, ldp, plane, n, t}, splits, s)));
+    HIP_TRY((launch_tile<MmaI8, EpiRaw, false>(ta, {(uint32_t *)ws, ldp, plane, n, t}, tile, splits, s)));
     const dim3 grid((unsigned)((n + 1023) / 1024), (unsigned)(t < 65535 ? t : 65535));
     hipLaunchKernelGGL((k_join_scale<OutT>), grid, dim3(256), 0, s, (const int32_t *)ws, splits, plane, ldp, e);
     HIP_TRY(hipGetLastError());

@@ -10,19 +10,23 @@
 // probabilities. "a" is the operand whose index is contiguous in the output
 // (weight channels, vocabulary entries), "b" the other one (tokens).
 //
-// Three kernels share the fragment layout (the operand order of the
+// Four kernels share the fragment layout (the operand order of the
 // 16 x 16 x 64-byte MFMAs: lane L holds row L % 16 and bytes 16 (L / 16) ..
 // + 15 of a 64-byte step of k; in the result lane L holds rows 4 (L / 16) .. + 3
 // of column L % 16):
 //   k_tile_p    256 x 256 tiles, persistent, one wavefront per SIMD: large products;
 //               128 x 128 tiles, two blocks per compute unit, with slices of k
 //   k_tile_any  128 x 128 tiles at any alignment
-//   k_skinny   16 to 64 rows of B, weights streamed once from memory: few tokens
+//   k_tile_s    smaller tiles with a deeper ring: few rows
+//   k_skinny    up to 64 rows of B at any alignment, without LDS copies
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+#include <stdlib.h>
+#include <string.h>
 
+#include <initializer_list>
 #include <type_traits>
 
 #include "common.h"
@@ -87,11 +91,20 @@ struct MmaF16 {
     static __device__ __forceinline__ float value(int bits) { return __int_as_float(bits); }
 };
 
-// Two floats rounded to nearest even as packed 16-bit values.
+// x rounded to nearest even in T. For fp16 x is made opaque first: the compiler
+// would fold a multiply-add before it into one that rounds to fp16 directly,
+// and only some of the kernels' forms of the same formula allow that, so their
+// results would differ in the last bit.
+template <class T>
+__device__ __forceinline__ T rounded(float x) {
+    if constexpr (std::is_same_v<T, _Float16>) asm("" : "+v"(x));
+    return (T)x;
+}
+// Two floats rounded, packed.
 template <class T>
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
     typedef T v2 __attribute__((ext_vector_type(2)));
-    const v2 p = {(T)x, (T)y};
+    const v2 p = {rounded<T>(x), rounded<T>(y)};
     return __builtin_bit_cast(uint32_t, p);
 }
 
@@ -278,7 +291,7 @@ struct EpiScale {
                 } else {
 #pragma unroll
                     for (int v = 0; v < 4; ++v)
-                        if (a0 + v < e.na) dst[v] = (OutT)x[v];
+                        if (a0 + v < e.na) dst[v] = rounded<OutT>(x[v]);
                 }
             }
             return;
@@ -613,6 +626,125 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(8 / RT, 8 /
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the trailing copies land before the block ends
 }
 
+// ---- small tiles -----------------------------------------------------------------
+// 32 RT x 32 CT tiles, one per block: four wavefronts of 16 RT x 16 CT, and a
+// ring of NR rounds of 128 bytes of k, NR - 1 ahead, so that a block keeps most
+// of its LDS in flight; that, not the matrix cores, bounds products with few
+// rows. Copies, their order in LDS, the halves of a round and the edges of k are
+// those of k_tile_p (its ring of units would waste LDS on tiles that are not
+// square); the slot of round p - 1 is refilled during round p, whose
+// predecessor's barrier has seen its last reads done. Rows past the last one
+// are copies of it. blockIdx.y: slice of k.
+template <class M, class Epi, int RT, int CT, int NR>
+__global__ __launch_bounds__(256) void k_tile_s(TileArgs ta, typename Epi::Args ea) {
+    constexpr int NF = RT + CT, UA = RT * 4096, SLOT = (RT + CT) * 4096;
+    static_assert(NR * SLOT <= 160 * 1024 && NR >= 3, "the ring fits LDS");
+    __shared__ __attribute__((aligned(1024))) int8_t lds[NR * SLOT];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    const int wm = wave >> 1, wn = wave & 1;
+    const uint32_t lda = (uint32_t)ta.lda, ldb = (uint32_t)ta.ldb;
+    int tile_a, tile_b;
+    tile_of(blockIdx.x, ta.tiles_a * ta.tiles_b, ta.tiles_a, ta.tiles_b, tile_a, tile_b);
+    const int64_t a0 = (int64_t)tile_a * (32 * RT), b0 = (int64_t)tile_b * (32 * CT);
+    const int k0 = (int)(blockIdx.y * ta.split_bytes);
+    const int k1 = (int)min((int64_t)k0 + ta.split_bytes, ta.kbytes);
+    const int rounds = k1 > k0 ? (k1 - k0 + 127) / 128 : 0;
+
+    const uint32_t chunk = 16u * ((lane & 7) ^ (lane >> 4));
+    uint32_t off_a[RT], off_b[CT];  // of this wavefront's copies, rows wave * 8 RT + 8 q ..
+#pragma unroll
+    for (int q = 0; q < RT; ++q) {
+        const int c = wave * RT + q;
+        off_a[q] = (uint32_t)min((int64_t)(8 * c + (lane >> 3)), ta.na - 1 - a0) * lda + (c & 1 ? chunk ^ 64u : chunk);
+    }
+#pragma unroll
+    for (int q = 0; q < CT; ++q) {
+        const int c = wave * CT + q;
+        off_b[q] = (uint32_t)min((int64_t)(8 * c + (lane >> 3)), ta.nb - 1 - b0) * ldb + (c & 1 ? chunk ^ 64u : chunk);
+    }
+    auto rsrc = [&](uint64_t base, uint32_t ld, uint32_t rows) {
+        return (v4i){(int)(uint32_t)base, (int)((uint32_t)(base >> 32) & 0xffffu), (int)((rows - 1) * ld + 128u), 0x00020000};
+    };
+    const uint64_t base_a = (uint64_t)(uintptr_t)ta.A + (uint64_t)a0 * lda, base_b = (uint64_t)(uintptr_t)ta.B + (uint64_t)b0 * ldb;
+    const uint32_t lds0 = (uint32_t)(uintptr_t)((__attribute__((address_space(3))) int8_t *)lds);
+    // the copies of round p of one operand into the slot at `at`
+    auto copy_a = [&](int p, uint32_t at) {
+        const int k = k0 + p * 128;
+        const v4i rs = rsrc(base_a + (uint32_t)k, lda, 32 * RT);
+#pragma unroll
+        for (int q = 0; q < RT; ++q) {
+            const int c = wave * RT + q;
+            const int left = k1 - k - (int)(c & 1 ? chunk ^ 64u : chunk);
+            asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(
+                             left > 0 ? off_a[q] : 0xfffffff0u),
+                         "s"(rs), "s"(lds0 + at + (uint32_t)c * 1024u)
+                         : "memory");
+        }
+    };
+    auto copy_b = [&](int p, uint32_t at) {
+        const int k = k0 + p * 128;
+        const v4i rs = rsrc(base_b + (uint32_t)k, ldb, 32 * CT);
+#pragma unroll
+        for (int q = 0; q < CT; ++q) {
+            const int c = wave * CT + q;
+            const int left = k1 - k - (int)(c & 1 ? chunk ^ 64u : chunk);
+            asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds" ::"v"(
+                             left > 0 ? off_b[q] : 0xfffffff0u),
+                         "s"(rs), "s"(lds0 + at + (uint32_t)(UA + c * 1024))
+                         : "memory");
+        }
+    };
+    const uint32_t place = (uint32_t)(lane & 15) * 128u + 16u * ((lane >> 4) ^ ((lane >> 1) & 7));
+    auto read = [&](uint32_t at, uint32_t step, v4i(&f)[NF]) {
+        const int8_t *pa = lds + at + (uint32_t)(wm * RT * 2048) + (place ^ step), *pb = lds + at + (uint32_t)(UA + wn * CT * 2048) + (place ^ step);
+#pragma unroll
+        for (int r = 0; r < CT; ++r) f[RT + r] = *(const v4i *)(pb + r * 2048);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) f[r] = *(const v4i *)(pa + r * 2048);
+    };
+
+    v4i acc[RT][CT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < CT; ++j) acc[i][j] = (v4i){0, 0, 0, 0};
+    if (rounds > 0) {
+        // rounds past the last one copy nothing (every lane is past the end of k),
+        // but count
+#pragma unroll
+        for (int p = 0; p < NR - 1; ++p) {
+            copy_a(p, (uint32_t)(p * SLOT));
+            copy_b(p, (uint32_t)(p * SLOT));
+        }
+        copies_landed_barrier<(NR - 2) * NF>();  // round 0
+        v4i f0[NF], f1[NF];
+        read(0, 0, f0);
+        uint32_t at = 0, last = (NR - 1) * SLOT;  // slots of round p and p - 1
+        for (int p = 0; p < rounds; ++p) {
+            const uint32_t next = at == (NR - 1) * SLOT ? 0u : at + SLOT;
+            read(at, 64u, f1);
+            copy_a(p + NR - 1, last);
+#pragma unroll
+            for (int q = 0; q < RT * CT; ++q) acc[q / CT][q % CT] = M::mma(f0[q / CT], f0[RT + q % CT], acc[q / CT][q % CT]);
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            copies_landed_barrier<(NR - 3) * NF + RT>();  // round p + 1
+            read(next, 0, f0);
+            copy_b(p + NR - 1, last);
+#pragma unroll
+            for (int q = 0; q < RT * CT; ++q) acc[q / CT][q % CT] = M::mma(f1[q / CT], f1[RT + q % CT], acc[q / CT][q % CT]);
+            last = at;
+            at = next;
+        }
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // the trailing copies land before the block ends
+    }
+    const TileWhere w = {a0 + wm * (16 * RT), b0 + wn * (16 * CT), a0, tile_a * 2 + wm, (int)blockIdx.y};
+    if (RT > 1 && w.a0 + 16 * RT <= ta.na && w.b0 + 16 * CT <= ta.nb)
+        Epi::template run<M, RT, CT, RT == 1>(acc, w, ea);
+    else if (w.a0 < ta.na && w.b0 < ta.nb)
+        Epi::template run<M, RT, CT, true>(acc, w, ea);
+}
+
 // ---- any alignment -----------------------------------------------------------
 // 128 x 128 tiles of four wavefronts for rows or pitches that are not 16-byte
 // aligned, which cannot be copied straight into LDS: each lane loads its 16
@@ -700,8 +832,6 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
 //
 // Src says where fragments of B come from: BRows (memory) or BQuant (quantised
 // by the block itself from 16- or 32-bit activations).
-constexpr int kSkinnySteps = 8;
-
 struct BRows {
     struct Args {};
     static constexpr bool QUANT = false;
@@ -710,18 +840,18 @@ struct BRows {
 // Largest magnitude as ordered bits (NaN above infinity above every number).
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-// The step and its inverse for a row whose largest magnitude has these bits:
-// s = amax / 127, up = 127 / amax. A row with Inf or NaN gets a NaN scale and
-// zeros (its outputs are NaN); below 2^-120, where 127 / amax nears the end of
-// binary32, a row becomes zeros.
+// The step of a row and its inverse, from the bits of its largest magnitude:
+// s = amax * RN(1 / 127), up = RN(1 / amax) * 127, each rounded to binary32. A
+// row with Inf or NaN gets a NaN scale and zeros (its outputs are NaN); below
+// 2^-120, where 127 / amax nears the end of binary32, a row becomes zeros.
 __device__ __forceinline__ void row_scale(uint32_t bits, float &s, float &up) {
     const float amax = __uint_as_float(bits);
     if (bits >= 0x7f800000u) {
         s = __uint_as_float(0x7fc00000u);
         up = 0.f;
     } else {
-        s = amax / 127.0f;
-        up = amax >= 0x1p-120f ? 127.0f / amax : 0.f;
+        s = amax * (1.0f / 127.0f);
+        up = amax >= 0x1p-120f ? (1.0f / amax) * 127.0f : 0.f;
     }
 }
 __device__ __forceinline__ int quantised(float x, float up) { return up == 0.f ? 0 : (int)rintf(x * up); }
@@ -760,22 +890,25 @@ struct BQuant {
     static constexpr bool QUANT = true;
 };
 
-template <class M, class Epi, int BT, int W, class Src>
+template <class M, class Epi, int RT, int BT, int W, int U, class Src>
 __global__ __launch_bounds__(64 * W) void k_skinny(TileArgs ta, typename Epi::Args ea, typename Src::Args sa) {
     extern __shared__ __attribute__((aligned(16))) int8_t dyn[];
     v4i *sums = (v4i *)dyn;  // [W][BT][64]
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int lane = threadIdx.x & 63;
-    const int64_t a0 = (int64_t)blockIdx.x * 16;
-    const int8_t *arow = ta.A + min(a0 + (lane & 15), ta.na - 1) * ta.lda + 16 * (lane >> 4);
+    const int64_t a0 = (int64_t)blockIdx.x * (16 * RT);
+    const int8_t *arow[RT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i) arow[i] = ta.A + min(a0 + 16 * i + (lane & 15), ta.na - 1) * ta.lda + 16 * (lane >> 4);
     const int steps = (int)(ta.kbytes >> 6);  // whole steps
-    constexpr int U = kSkinnySteps;
-    v4i fa[U];
+    v4i fa[RT][U];
     auto load_a = [&](int s0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int s = s0 + u * W;
-            if (s < steps) fa[u] = __builtin_bit_cast(v4i, *(const U16 *)(arow + (int64_t)s * 64));
+            if (s < steps)
+#pragma unroll
+                for (int i = 0; i < RT; ++i) fa[i][u] = __builtin_bit_cast(v4i, *(const U16 *)(arow[i] + (int64_t)s * 64));
         }
     };
     load_a(wave);  // on their way while the block quantises
@@ -783,12 +916,17 @@ __global__ __launch_bounds__(64 * W) void k_skinny(TileArgs ta, typename Epi::Ar
     const int8_t *brow[BT];
     int8_t *rows = dyn + W * BT * 1024;
     if constexpr (Src::QUANT) {
+        // the wavefronts split into groups, one per row
         __shared__ uint32_t top[W];
         float *scale = (float *)(rows + ta.nb * sa.pitch);
-        for (int64_t r = 0; r < ta.nb; ++r) {
-            const auto *x = sa.X + r * sa.ldx;
+        int per = W;  // wavefronts per row
+        while (per > 1 && W / per < ta.nb) per >>= 1;
+        const int first = 8 * ((wave % per) * 64 + lane), step = 8 * 64 * per;
+        for (int64_t r0 = 0; r0 < ta.nb; r0 += W / per) {
+            const int64_t r = r0 + wave / per;
+            const auto *x = sa.X + (r < ta.nb ? r : ta.nb - 1) * sa.ldx;
             uint32_t m = 0;
-            for (int64_t k = 8 * threadIdx.x; k < ta.kbytes; k += 8 * 64 * W) {
+            for (int64_t k = first; k < ta.kbytes; k += step) {
                 float e[8];
                 load8(x, k, ta.kbytes, e);
 #pragma unroll
@@ -796,18 +934,21 @@ __global__ __launch_bounds__(64 * W) void k_skinny(TileArgs ta, typename Epi::Ar
             }
 #pragma unroll
             for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
-            __syncthreads();  // top is free again
-            if (lane == 0) top[wave] = m;
-            __syncthreads();
-#pragma unroll
-            for (int i = 0; i < W; ++i) m = max(m, top[i]);
-            float s, up;
-            row_scale(m, s, up);
-            if (threadIdx.x == 0) scale[r] = s;
-            for (int64_t k = 8 * threadIdx.x; k < ((ta.kbytes + 63) & ~(int64_t)63); k += 8 * 64 * W) {
-                float e[8];
-                load8(x, k, ta.kbytes, e);
-                *(U8 *)(rows + r * sa.pitch + k) = quantised8(e, up);
+            if (per > 1) {
+                __syncthreads();  // top is free again
+                if (lane == 0) top[wave] = m;
+                __syncthreads();
+                for (int i = 0; i < per; ++i) m = max(m, top[wave / per * per + i]);
+            }
+            if (r < ta.nb) {
+                float s, up;
+                row_scale(m, s, up);
+                if (lane == 0 && wave % per == 0) scale[r] = s;
+                for (int64_t k = first; k < ((ta.kbytes + 63) & ~(int64_t)63); k += step) {
+                    float e[8];
+                    load8(x, k, ta.kbytes, e);
+                    *(U8 *)(rows + r * sa.pitch + k) = quantised8(e, up);
+                }
             }
         }
         __syncthreads();
@@ -826,9 +967,11 @@ __global__ __launch_bounds__(64 * W) void k_skinny(TileArgs ta, typename Epi::Ar
             return __builtin_bit_cast(v4i, *(const U16 *)(brow[j] + (int64_t)s * 64));
     };
 
-    v4i acc[BT];
+    v4i acc[RT][BT];
 #pragma unroll
-    for (int j = 0; j < BT; ++j) acc[j] = (v4i){0, 0, 0, 0};
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < BT; ++j) acc[i][j] = (v4i){0, 0, 0, 0};
     for (int s0 = wave; s0 < steps; s0 += U * W) {
         if (s0 > wave) load_a(s0);
         v4i fb[BT][U];
@@ -841,38 +984,81 @@ __global__ __launch_bounds__(64 * W) void k_skinny(TileArgs ta, typename Epi::Ar
         for (int u = 0; u < U; ++u)
             if (s0 + u * W < steps)
 #pragma unroll
-                for (int j = 0; j < BT; ++j) acc[j] = M::mma(fa[u], fb[j][u], acc[j]);
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int j = 0; j < BT; ++j) acc[i][j] = M::mma(fa[i][u], fb[j][u], acc[i][j]);
     }
     if ((ta.kbytes & 63) && wave == steps % W) {  // the last, partial step
         const int64_t at = (int64_t)steps * 64 + 16 * (lane >> 4);
-        const v4i a = load_chunk(arow - 16 * (lane >> 4), at, ta.kbytes);
+        v4i b[BT];
 #pragma unroll
         for (int j = 0; j < BT; ++j) {
-            v4i b;
             if constexpr (Src::QUANT)
-                b = load_b(j, steps);
+                b[j] = load_b(j, steps);
             else
-                b = load_chunk(brow[j] - 16 * (lane >> 4), at, ta.kbytes);
-            acc[j] = M::mma(a, b, acc[j]);
+                b[j] = load_chunk(brow[j] - 16 * (lane >> 4), at, ta.kbytes);
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            const v4i a = load_chunk(arow[i] - 16 * (lane >> 4), at, ta.kbytes);
+#pragma unroll
+            for (int j = 0; j < BT; ++j) acc[i][j] = M::mma(a, b[j], acc[i][j]);
         }
     }
 #pragma unroll
-    for (int j = 0; j < BT; ++j) sums[(wave * BT + j) * 64 + lane] = acc[j];
-    __syncthreads();
-    for (int j = wave; j < BT; j += W) {
-        v4i t[1][1];
-        t[0][0] = sums[j * 64 + lane];
+    for (int i = 0; i < RT; ++i) {
+        if (i > 0) __syncthreads();  // the sums of the previous 16 rows have been read
 #pragma unroll
-        for (int i = 1; i < W; ++i) {
-            const v4i o = sums[(i * BT + j) * 64 + lane];
-            if constexpr (M::INT)
-                t[0][0] += o;
-            else
-                t[0][0] = __builtin_bit_cast(v4i, __builtin_bit_cast(v4f, t[0][0]) + __builtin_bit_cast(v4f, o));
+        for (int j = 0; j < BT; ++j) sums[(wave * BT + j) * 64 + lane] = acc[i][j];
+        __syncthreads();
+        for (int j = wave; j < BT; j += W) {
+            v4i t[1][1];
+            t[0][0] = sums[j * 64 + lane];
+#pragma unroll
+            for (int q = 1; q < W; ++q) {
+                const v4i o = sums[(q * BT + j) * 64 + lane];
+                if constexpr (M::INT)
+                    t[0][0] += o;
+                else
+                    t[0][0] = __builtin_bit_cast(v4i, __builtin_bit_cast(v4f, t[0][0]) + __builtin_bit_cast(v4f, o));
+            }
+            const TileWhere w = {a0 + 16 * i, 16 * j, a0, (int)blockIdx.x * RT + i, 0};
+            if (w.a0 < ta.na) Epi::template run<M, 1, 1, true>(t, w, ea);
         }
-        const TileWhere w = {a0, 16 * j, a0, (int)blockIdx.x, 0};
-        Epi::template run<M, 1, 1, true>(t, w, ea);
     }
+}
+
+// Wavefronts and steps in flight as measured (int8 unless noted, weights from
+// memory): 4096 x 4096, 1 row: 16 wavefronts 5.4 us, 8 7.2, 4 7.7; bf16 32000 x 4096,
+// 1 row: 4 wavefronts of 4 steps 49.5 us (5.3 TB/s), 8 of 8 steps 70 (too few
+// blocks fit).
+template <class M, class Epi, class Src>
+hipError_t launch_skinny(const TileArgs &t, const typename Epi::Args &e, const typename Src::Args &src, hipStream_t s) {
+    const int bt = (int)((t.nb + 15) / 16);
+    const bool few = t.na <= 512 * 16;
+    auto go = [&](auto kern, int rt, int b, int w, size_t extra) {
+        hipLaunchKernelGGL(kern, dim3((unsigned)((t.na + 16 * rt - 1) / (16 * rt))), dim3(64 * w),
+                           (size_t)w * b * 1024 + extra, s, t, e, src);
+    };
+    if constexpr (Src::QUANT) {
+        const size_t own = (size_t)t.nb * src.pitch + 4 * (size_t)t.nb;
+        if (few)
+            go(k_skinny<M, Epi, 1, 1, 16, 4, Src>, 1, 1, 16, own);
+        else
+            go(k_skinny<M, Epi, 1, 1, 4, 4, Src>, 1, 1, 4, own);
+    } else {
+        if (bt <= 1) {
+            if (few)
+                go(k_skinny<M, Epi, 1, 1, 16, 4, Src>, 1, 1, 16, 0);
+            else
+                go(k_skinny<M, Epi, 1, 1, 4, 4, Src>, 1, 1, 4, 0);
+        } else if (bt == 2) {
+            go(k_skinny<M, Epi, 1, 2, 8, 4, Src>, 1, 2, 8, 0);
+        } else {
+            go(k_skinny<M, Epi, 1, 4, 8, 4, Src>, 1, 4, 8, 0);
+        }
+    }
+    return hipGetLastError();
 }
 
 // ---- choice of kernel -------------------------------------------------------------
@@ -885,25 +1071,110 @@ inline bool aligned16(const TileArgs &t) {
            t.lda < (1 << 24) && t.ldb < (1 << 24) && t.kbytes >= 256 && t.kbytes < (1 << 30);
 }
 
-// Whether k_tile_p runs with 256 x 256 tiles: when they fill most compute
-// units. Else 128 x 128 ones, two blocks per unit.
-inline bool use_large_tile(int64_t na, int64_t nb) {
-    return na >= 256 && nb >= 256 && ((na + 255) / 256) * ((nb + 255) / 256) * 4 >= kPlanUnits * 3;
+enum class Tile { skinny, s11, s21, s22, s42, p4, p8, any };
+struct TileShape {
+    int a, b;     // sides
+    int part;     // rows of A that one wavefront's epilogue covers
+};
+inline TileShape shape_of(Tile t) {
+    switch (t) {
+    case Tile::skinny: return {16, 64, 16};
+    case Tile::s11: return {32, 32, 16};
+    case Tile::s21: return {64, 32, 32};
+    case Tile::s22: return {64, 64, 32};
+    case Tile::s42: return {128, 64, 64};
+    case Tile::p8: return {256, 256, 128};
+    default: return {128, 128, 64};
+    }
+}
+inline int64_t tiles_of(Tile t, int64_t na, int64_t nb) {
+    const TileShape s = shape_of(t);
+    return ((na + s.a - 1) / s.a) * ((nb + s.b - 1) / s.b);
 }
 
-// Slices of k for the 128 x 128 tiles, with the time that a count of s is
-// expected to take: rounds of 128 bytes of k at 0.25 us (one block per compute
-// unit), and for s > 1 the planes of 32-bit sums, written and read once at 4
-// TB/s, and one more launch.
-inline int tile_splits(int64_t na, int64_t nb, int64_t kbytes) {
-    const int64_t tiles = ((na + 127) / 128) * ((nb + 127) / 128);
-    const int64_t rounds = (kbytes + 127) / 128;
+// Microseconds per round of 128 bytes of k that all tiles of a product take
+// side by side, without the start and the end of a block (measured, random
+// int8). The small tiles: latency, at most one block per compute unit. 128 x
+// 128: one block per unit, or two and then in proportion; 256 x 256: one.
+inline double round_us(Tile tile, int64_t blocks) {
+    switch (tile) {
+    case Tile::s11: return 0.14;
+    case Tile::s21: return 0.17;
+    case Tile::s22: return 0.22;
+    case Tile::s42: return 0.32;
+    case Tile::p8:
+        return (2 * blocks <= kPlanUnits ? 1.3 : 1.55) * (double)((blocks + kPlanUnits - 1) / kPlanUnits);
+    default: {
+        const double c = 0.58 * (double)blocks / (double)kPlanUnits;
+        return blocks <= kPlanUnits ? 0.62 : c > 0.9 ? c : 0.9;
+    }
+    }
+}
+// Whether 256 x 256 tiles beat 128 x 128 ones (11008 x 4096, 1024 rows: 51.8 against
+// 56.8 us; 1536 rows, 258 tiles: 88.5 against 81.8).
+inline bool use_large_tile(int64_t na, int64_t nb) {
+    if (na < 256 || nb < 256) return false;
+    return round_us(Tile::p8, tiles_of(Tile::p8, na, nb)) <= round_us(Tile::p4, tiles_of(Tile::p4, na, nb));
+}
+
+// The kernel for a product whose k is not sliced. pairs: the epilogue needs two
+// neighbouring 16-row tiles in a wavefront.
+//   - at most 16 rows of B and at most 512 blocks: k_skinny, whose 16 wavefronts
+//     per block start all loads at once (int8, 4096 x 4096, 1 row: 5.4 us against
+//     6.9 with s11);
+//   - else the smallest tile that gives at most one block per compute unit: more
+//     would queue, and larger ones leave units idle (int8, 11008 x 4096, 64 rows:
+//     s21 17.6, s22 13.8, s42 18.7, p4 22.1 us; 4096 x 4096, 512 rows: s22 14.7, s42
+//     12.8, p4 18.0);
+//   - where even s42 gives more: with up to 64 rows of B the tile that covers them,
+//     so A is read once (bf16, 32000 x 4096, 1 row: 49.0 us or 5.3 TB/s; 64 rows: 54.8,
+//     against 61.2 with p4); else 128 x 128 or 256 x 256.
+// OZ2_LINEAR_TILE=skinny, s11, s21, s22, s42, p4, p8 or any forces one where the
+// product allows it; results of int8 products do not depend on it.
+inline Tile choose_tile(const TileArgs &t, bool pairs) {
+    const bool aligned = aligned16(t);
+    const bool can_skinny = t.nb <= kSkinnyRows && !pairs;
+    if (const char *force = getenv("OZ2_LINEAR_TILE")) {
+        if (!strcmp(force, "any")) return Tile::any;
+        if (!strcmp(force, "skinny") && can_skinny) return Tile::skinny;
+        if (aligned) {
+            if (!strcmp(force, "s11") && !pairs) return Tile::s11;
+            if (!strcmp(force, "s21")) return Tile::s21;
+            if (!strcmp(force, "s22")) return Tile::s22;
+            if (!strcmp(force, "s42")) return Tile::s42;
+            if (!strcmp(force, "p4")) return Tile::p4;
+            if (!strcmp(force, "p8") && t.na >= 256 && t.nb >= 256) return Tile::p8;
+        }
+    }
+    if (!aligned) return can_skinny ? Tile::skinny : Tile::any;
+    if (can_skinny && t.nb <= 16 && t.na <= 512 * 16) return Tile::skinny;
+    if (!pairs && tiles_of(Tile::s11, t.na, t.nb) <= kPlanUnits) return Tile::s11;
+    for (Tile c : {Tile::s21, Tile::s22, Tile::s42})
+        if (tiles_of(c, t.na, t.nb) <= kPlanUnits) return c;
+    if (t.nb <= 32) return Tile::s21;
+    if (t.nb <= 64) return Tile::s22;
+    return use_large_tile(t.na, t.nb) ? Tile::p8 : Tile::p4;
+}
+// Wavefront ranges of A that an epilogue of this tile reports on.
+inline int tile_parts(Tile tile, int64_t na) {
+    const TileShape s = shape_of(tile);
+    // 256 x 256 tiles are moved back at the edge, so all their wavefronts report
+    return tile == Tile::p8 ? (int)(2 * ((na + 255) / 256)) : (int)((na + s.part - 1) / s.part);
+}
+
+// Slices of k for a tile, by the time that a count of s is expected to take:
+// round_us, and for s > 1 the planes of 32-bit sums, written and read once at 4
+// TB/s, and one more launch. Slices fill compute units that the tiles leave idle.
+inline int tile_splits(Tile tile, int64_t na, int64_t nb, int64_t kbytes) {
+    if (tile == Tile::skinny || tile == Tile::any || tile == Tile::p8) return 1;
+    const int64_t tiles = tiles_of(tile, na, nb), rounds = (kbytes + 127) / 128;
+    const int64_t most = tile == Tile::p4 ? 2 * kPlanUnits : kPlanUnits;
     int best = 1;
     double least = 1e30;
     for (int s = 1; s <= 64; s *= 2) {
-        if (s > 1 && (tiles * s > 2 * kPlanUnits || rounds < 4 * s)) break;
-        const double per = (double)((rounds + s - 1) / s) * 0.25 * (double)((tiles * s + kPlanUnits - 1) / kPlanUnits);
-        const double us = per + (s > 1 ? 4.0 + (double)s * (double)na * (double)nb * 8.0 / 4e6 : 0.0);
+        if (s > 1 && (tiles * s > most || rounds < 4 * s)) break;
+        const double us = (double)((rounds + s - 1) / s) * round_us(tile, tiles * s) +
+                          (s > 1 ? 4.0 + (double)s * (double)na * (double)nb * 8.0 / 4e6 : 0.0);
         if (us < least) {
             least = us;
             best = s;
@@ -912,47 +1183,38 @@ inline int tile_splits(int64_t na, int64_t nb, int64_t kbytes) {
     return best;
 }
 
-// The tile side that launch_tile takes for a product whose k is not sliced.
-inline int tile_side(const TileArgs &t) { return aligned16(t) && use_large_tile(t.na, t.nb) ? 256 : 128; }
-
-template <class M, class Epi>
-hipError_t launch_tile(TileArgs t, const typename Epi::Args &e, int splits, hipStream_t s) {
-    const bool aligned = aligned16(t);
-    const int side = splits == 1 ? tile_side(t) : 128;
-    t.tiles_a = (int)((t.na + side - 1) / side);
-    t.tiles_b = (int)((t.nb + side - 1) / side);
+// PAIRS: as choose_tile's, and then the kernels that cannot have pairs are not built.
+template <class M, class Epi, bool PAIRS>
+hipError_t launch_tile(TileArgs t, const typename Epi::Args &e, Tile tile, int splits, hipStream_t s) {
+    const TileShape shape = shape_of(tile);
+    t.tiles_a = (int)((t.na + shape.a - 1) / shape.a);
+    t.tiles_b = (int)((t.nb + shape.b - 1) / shape.b);
     t.splits = splits;
     t.split_bytes = ((t.kbytes + splits - 1) / splits + 127) / 128 * 128;
-    const int64_t total = (int64_t)t.tiles_a * t.tiles_b * splits, cus = compute_units();
-    if (side == 256)
+    const int64_t total = (int64_t)t.tiles_a * t.tiles_b, cus = compute_units();
+    const dim3 grid((unsigned)total, (unsigned)splits);
+    if (tile == Tile::p4 && t.split_bytes < 256) tile = Tile::any;
+    switch (tile) {
+    case Tile::p8:
         hipLaunchKernelGGL((k_tile_p<M, Epi, 8>), dim3((unsigned)(total < cus ? total : cus)), dim3(256), 0, s, t, e);
-    else if (aligned && t.split_bytes >= 256 && total < ((int64_t)1 << 31))
-        hipLaunchKernelGGL((k_tile_p<M, Epi, 4>), dim3((unsigned)(total < 2 * cus ? total : 2 * cus)), dim3(256), 0, s, t,
-                           e);
-    else
-        hipLaunchKernelGGL((k_tile_any<M, Epi>), dim3((unsigned)((int64_t)t.tiles_a * t.tiles_b), (unsigned)splits),
-                           dim3(256), 0, s, t, e);
-    return hipGetLastError();
-}
-
-// Few rows of B (nb <= 64): eight wavefronts where the rows of A give each
-// compute unit few blocks, else four.
-template <class M, class Epi, class Src>
-hipError_t launch_skinny(const TileArgs &t, const typename Epi::Args &e, const typename Src::Args &src, hipStream_t s) {
-    const unsigned grid = (unsigned)((t.na + 15) / 16);
-    auto go = [&](auto kern, int bt, int w, size_t extra) {
-        hipLaunchKernelGGL(kern, dim3(grid), dim3(64 * w), (size_t)w * bt * 1024 + extra, s, t, e, src);
-    };
-    const int bt = (int)((t.nb + 15) / 16);
-    if constexpr (Src::QUANT) {
-        go(k_skinny<M, Epi, 1, 8, Src>, 1, 8, (size_t)t.nb * src.pitch + 4 * (size_t)t.nb);
-    } else {
-        if (bt <= 1)
-            go(k_skinny<M, Epi, 1, 8, Src>, 1, 8, 0);
-        else if (bt == 2)
-            go(k_skinny<M, Epi, 2, 8, Src>, 2, 8, 0);
-        else
-            go(k_skinny<M, Epi, 4, 8, Src>, 4, 8, 0);
+        break;
+    case Tile::p4: {
+        const int64_t blocks = total * splits;
+        hipLaunchKernelGGL((k_tile_p<M, Epi, 4>), dim3((unsigned)(blocks < 2 * cus ? blocks : 2 * cus)), dim3(256), 0, s,
+                           t, e);
+        break;
+    }
+    case Tile::s42: hipLaunchKernelGGL((k_tile_s<M, Epi, 4, 2, 6>), grid, dim3(256), 0, s, t, e); break;
+    case Tile::s22: hipLaunchKernelGGL((k_tile_s<M, Epi, 2, 2, 5>), grid, dim3(256), 0, s, t, e); break;
+    case Tile::s21: hipLaunchKernelGGL((k_tile_s<M, Epi, 2, 1, 6>), grid, dim3(256), 0, s, t, e); break;
+    case Tile::any: hipLaunchKernelGGL((k_tile_any<M, Epi>), grid, dim3(256), 0, s, t, e); break;
+    default:
+        if constexpr (!PAIRS) {
+            if (tile == Tile::s11)
+                hipLaunchKernelGGL((k_tile_s<M, Epi, 1, 1, 5>), grid, dim3(256), 0, s, t, e);
+            else
+                return launch_skinny<M, Epi, BRows>(t, e, {}, s);
+        }
     }
     return hipGetLastError();
 }

@@ -60,8 +60,15 @@ struct EpiLse {
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
             const int64_t b = w.b0 + 16 * j + (lane & 15);
-            float sb = 1.f;
-            if constexpr (SCALED) sb = e.sb[EDGE && b >= e.nb ? e.nb - 1 : b];
+            // SCALED: z = (sum * sa) * sb; the entries are kept as sum * sa, with the
+            // sign of sb, and |sb| goes into the exponentials' factor
+            float unit = 1.f;
+            bool flip = false;
+            if constexpr (SCALED) {
+                const float sb = e.sb[EDGE && b >= e.nb ? e.nb - 1 : b];
+                unit = fabsf(sb);
+                flip = sb < 0.f;
+            }
             float z[RT][4], m = -INFINITY;
 #pragma unroll
             for (int i = 0; i < RT; ++i) {
@@ -69,8 +76,14 @@ struct EpiLse {
 #pragma unroll
                 for (int v = 0; v < 4; ++v) {
                     z[i][v] = M::value(acc[i][j][v]);
-                    if constexpr (SCALED) z[i][v] = z[i][v] * sb * sa[i][v];
+                    if constexpr (SCALED) z[i][v] *= sa[i][v];
                 }
+            }
+            if (SCALED && __any(flip)) {
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) z[i][v] = flip ? -z[i][v] : z[i][v];
             }
             if (cut) {
 #pragma unroll
@@ -89,16 +102,17 @@ struct EpiLse {
             m = fmaxf(m, __shfl_xor(m, 32, 64));
             // exp(z - m) as 2^(z log2 e - m log2 e); where every entry is -inf (or cut
             // off) the sum is 0, not exp(-inf + inf)
-            const float shift = m == -INFINITY ? 0.f : -m * kLog2e;
+            const float factor = unit * kLog2e;
+            const float shift = m == -INFINITY ? 0.f : -m * factor;
             float s[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < RT; ++i)
 #pragma unroll
-                for (int v = 0; v < 4; ++v) s[v] += __builtin_amdgcn_exp2f(fmaf(z[i][v], kLog2e, shift));
+                for (int v = 0; v < 4; ++v) s[v] += __builtin_amdgcn_exp2f(fmaf(z[i][v], factor, shift));
             float sum = (s[0] + s[1]) + (s[2] + s[3]);
             sum += __shfl_xor(sum, 16, 64);
             sum += __shfl_xor(sum, 32, 64);
-            if (lane < 16 && (!EDGE || b < e.nb)) e.part[(int64_t)w.part * e.ld + b] = make_float2(m, sum);
+            if (lane < 16 && (!EDGE || b < e.nb)) e.part[(int64_t)w.part * e.ld + b] = make_float2(SCALED ? m * unit : m, sum);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
@@ -247,20 +261,34 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
     __shared__ float sm[256], ss[256];
     const int tid = threadIdx.x;
     const int64_t t0 = (int64_t)blockIdx.x * TB;
+    const int ti = tid / PL, at = tid % PL;
+    const int64_t t = t0 + ti;
+    // the target's logit first: its loads and those of the parts overlap
+    const int64_t v = t < nt ? y[t] : ignore;
+    const bool kept = v != ignore, valid = kept && v >= 0 && v < nv;
+    const float mine = valid ? dot.part(t, v, at, PL) : 0.f;
     {
         const int ti = tid % TB, at = tid / TB;
         float m = -INFINITY, s = 0.f;
-        if (t0 + ti < nt)
-            for (int p = at; p < nparts; p += PL) {
-                const float2 u = part[(int64_t)p * ld + t0 + ti];
+        if (t0 + ti < nt) {
+            const float2 *from = part + t0 + ti;
+            int p = at;
+            for (; p + 3 * PL < nparts; p += 4 * PL) {
+                float2 u[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) u[i] = from[(int64_t)(p + i * PL) * ld];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) stat_add(m, s, u[i].x, u[i].y);
+            }
+            for (; p < nparts; p += PL) {
+                const float2 u = from[(int64_t)p * ld];
                 stat_add(m, s, u.x, u.y);
             }
+        }
         sm[ti * PL + at] = m;
         ss[ti * PL + at] = s;
     }
     __syncthreads();
-    const int ti = tid / PL, at = tid % PL;
-    const int64_t t = t0 + ti;
     for (int half = PL / 2; half >= 1; half >>= 1) {
         if (at < half) {
             float m = sm[tid], s = ss[tid];
@@ -274,9 +302,7 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
                             ? -INFINITY
                             : fmaf(__builtin_amdgcn_logf(ss[ti * PL]), kLn2, sm[ti * PL]);
     __syncthreads();
-    const int64_t v = t < nt ? y[t] : ignore;
-    const bool kept = v != ignore, valid = kept && v >= 0 && v < nv;
-    ss[tid] = valid ? dot.part(t, v, at, PL) : 0.f;
+    ss[tid] = mine;
     __syncthreads();
     for (int half = PL / 2; half >= 1; half >>= 1) {
         if (at < half) ss[tid] = Dot::add(ss[tid], ss[tid + half]);
@@ -391,7 +417,7 @@ __global__ __launch_bounds__(256) void k_join_rows(const float *__restrict__ pla
             const float u = *unit;
 #pragma unroll
             for (int v = 0; v < 4; ++v)
-                if (a + v < na) out[b * ldo + a + v] = (T)(s[v] * u);
+                if (a + v < na) out[b * ldo + a + v] = rounded<T>(s[v] * u);
         }
     }
 }
@@ -420,15 +446,11 @@ TileArgs rows_args(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, 
     return ta;
 }
 
-int parts_of(const TileArgs &ta) {
-    if (ta.nb <= kSkinnyRows) return (int)((ta.na + 15) / 16);
-    if (tile_side(ta) == 256) return (int)(2 * ((ta.na + 255) / 256));
-    return (int)((ta.na + 63) / 64);
-}
-// Enough for either tile, whatever the alignment of the operands.
+// Enough for any tile: parts of 16 entries for up to 64 tokens and for small
+// products, of at least 32 beyond.
 size_t forward_bytes(int64_t t, int64_t v) {
     const int64_t run = t < kRun ? t : kRun;
-    return up256(8 * (size_t)run * (size_t)(run <= kSkinnyRows ? (v + 15) / 16 : (v + 63) / 64));
+    return up256(8 * (size_t)run * (size_t)((v + 15) / 16 < 1024 || run <= kSkinnyRows ? (v + 15) / 16 : (v + 63) / 64));
 }
 
 template <class M, bool SCALED, class DotOf>
@@ -441,13 +463,13 @@ int forward(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const f
         const char *x = (const char *)X + t0 * ldx * M::BYTES;
         const TileArgs ta = rows_args<M::BYTES>(nt, v, d, x, ldx, W, ldw);
         const typename EpiLse<SCALED>::Args e = {part, nt, sw, sx ? sx + t0 : nullptr, v, nt};
-        if (nt <= kSkinnyRows)
-            HIP_TRY((launch_skinny<M, EpiLse<SCALED>, BRows>(ta, e, {}, s)));
-        else
-            HIP_TRY((launch_tile<M, EpiLse<SCALED>>(ta, e, 1, s)));
+        Tile tile = choose_tile(ta, false);
+        // (a forced tile may have more parts than the workspace)
+        if (8 * (size_t)nt * (size_t)tile_parts(tile, v) > forward_bytes(t, v)) tile = aligned16(ta) ? Tile::p4 : Tile::any;
+        HIP_TRY((launch_tile<M, EpiLse<SCALED>, false>(ta, e, tile, 1, s)));
         const auto dot = dot_of(x, t0);
         typedef std::remove_const_t<decltype(dot)> Dot;
-        const int nparts = parts_of(ta);
+        const int nparts = tile_parts(tile, v);
         if (nt <= kSkinnyRows)  // a block each
             hipLaunchKernelGGL((k_xent_join<Dot, 1>), dim3((unsigned)nt), dim3(256), 0, s, part, nt, nparts, nt, v,
                                y + t0, ignore, dot, loss + t0, lse + t0);
@@ -490,7 +512,7 @@ GradPlan plan_grad(int64_t t, int64_t v, int64_t d, bool dx, bool dw) {
     const int64_t pieces = (v + most - 1) / most;
     p.vc = ((v + pieces - 1) / pieces + 255) / 256 * 256;
     if (p.vc > v) p.vc = v;
-    p.splits = use_large_tile(d, t) ? 1 : tile_splits(d, t, 2 * ((p.vc + 7) / 8 * 8));
+    p.splits = use_large_tile(d, t) ? 1 : tile_splits(Tile::p4, d, t, 2 * ((p.vc + 7) / 8 * 8));
     p.ldp = (d + 3) / 4 * 4;
     p.plane = t * p.ldp;
     size_t off = 0;
@@ -532,6 +554,12 @@ hipError_t zero_rows16(void *out, int64_t ldo, int64_t rows, int64_t cols, hipSt
     return hipGetLastError();
 }
 
+// A product whose k is not sliced, for an epilogue that takes pairs of tiles.
+template <class M, class Epi>
+hipError_t launch_whole(const TileArgs &ta, const typename Epi::Args &e, hipStream_t s) {
+    return launch_tile<M, Epi, true>(ta, e, choose_tile(ta, true), 1, s);
+}
+
 template <class M>
 int backward(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const void *W, int64_t ldw, const int64_t *y,
              int64_t ignore, const float *lse, const float *grad, void *dX, int64_t lddx, void *dW, int64_t lddw,
@@ -550,12 +578,11 @@ int backward(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const 
     for (int64_t v0 = 0; v0 < v; v0 += p.vc) {
         const int64_t vc = v - v0 < p.vc ? v - v0 : p.vc, v8 = (vc + 7) / 8 * 8;
         const char *w = (const char *)W + v0 * ldw * 2;
-        HIP_TRY((launch_tile<M, EpiProb<T>>(rows_args<2>(t, vc, d, X, ldx, w, ldw), {gm, ldg, l, g, y, v0, vc, t}, 1,
-                                            s)));
+        HIP_TRY((launch_whole<M, EpiProb<T>>(rows_args<2>(t, vc, d, X, ldx, w, ldw), {gm, ldg, l, g, y, v0, vc, t}, s)));
         if (dW) {
             HIP_TRY(transpose16<true>(gm, ldg, t, vc, gt, ldt, nullptr, s));
-            HIP_TRY((launch_tile<M, EpiOut<T>>(rows_args<2>(vc, d, t8, gt, ldt, xt, ldt),
-                                               {(T *)dW + v0 * lddw, lddw, unit, d, vc}, 1, s)));
+            HIP_TRY((launch_whole<M, EpiOut<T>>(rows_args<2>(vc, d, t8, gt, ldt, xt, ldt),
+                                                {(T *)dW + v0 * lddw, lddw, unit, d, vc}, s)));
         }
         if (dX) {
             if (!dW && v8 > vc) HIP_TRY(zero_rows16(gm + vc, ldg, t, v8 - vc, s));
@@ -563,9 +590,10 @@ int backward(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const 
             const TileArgs ta = rows_args<2>(t, d, v8, gm, ldg, wt, ldg);
             const bool first = v0 == 0, last = v0 + vc == v;
             if (first && last && p.splits == 1) {
-                HIP_TRY((launch_tile<M, EpiOut<T>>(ta, {(T *)dX, lddx, unit, d, t}, 1, s)));
+                HIP_TRY((launch_whole<M, EpiOut<T>>(ta, {(T *)dX, lddx, unit, d, t}, s)));
             } else {
-                HIP_TRY((launch_tile<M, EpiRaw>(ta, {(uint32_t *)planes, p.ldp, p.plane, d, t}, p.splits, s)));
+                HIP_TRY((launch_tile<M, EpiRaw, true>(ta, {(uint32_t *)planes, p.ldp, p.plane, d, t},
+                                                      p.splits > 1 ? Tile::p4 : choose_tile(ta, true), p.splits, s)));
                 hipLaunchKernelGGL((k_join_rows<T>), dim3((unsigned)((d + 1023) / 1024), (unsigned)(t < 65535 ? t : 65535)),
                                    dim3(256), 0, s, planes, p.splits, p.plane, p.ldp, sum, !first,
                                    last ? (T *)dX : nullptr, lddx, unit, d, t);
