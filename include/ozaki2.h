@@ -429,8 +429,9 @@ int ozaki2_quantize_rows(int64_t t, int64_t k, const void *X, int64_t ldx, int x
 
 /*
  * The product of quantised operands. ozaki2_i8gemm uses the cached workspace
- * (only sizes whose tiles would leave most compute units idle need any, and a
- * call that needs none neither takes nor waits for it); the _ws form takes one
+ * (needed where a long k is cut into slices, and for aligned copies where k is
+ * no multiple of 16 and t > 16; a call that needs none neither takes nor waits
+ * for it); the _ws form takes one
  * of ozaki2_i8gemm_workspace_size bytes (0: may be NULL), 256-byte aligned, and
  * only enqueues kernels, so it can be captured into a HIP graph. Calls that
  * share a workspace must be ordered on one stream.
@@ -482,7 +483,9 @@ int ozaki2_i8linear_ws(int64_t t, int64_t n, int64_t k, const void *X, int64_t l
  * z is summed in binary32 on the matrix cores and never stored; maxima, sums of
  * exponentials and the target's logit are binary32. Results are bitwise
  * reproducible. Workspace: 8 bytes per token (of at most 16384 at a time) and
- * 64 vocabulary entries (16 for up to 64 tokens).
+ * 64 vocabulary entries (16 for up to 64 tokens and for small vocabularies); where
+ * rows are not whole multiples of 16 bytes, aligned copies of the rows of X and
+ * of at most 96 MiB of those of W as well.
  * ozaki2_xent uses the cached workspace, the _ws form the caller's (256-byte
  * aligned, capturable into a HIP graph, ordered on one stream if shared).
  * Returns 0, -1..-12 for an invalid argument (ignore_index is never invalid),
@@ -498,13 +501,14 @@ int ozaki2_xent_ws(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, 
 /*
  * The same loss for quantised features and weights (see ozaki2_i8gemm):
  * z[i][j] = (sum_h A[i][h] B[j][h]) * a_scale[i] * b_scale[j], exact up to the
- * rounding of the sum and of the two products to binary32. Workspace as
- * ozaki2_xent (ozaki2_xent_workspace_size), k <= OZAKI2_I8_MAX_K.
+ * rounding of the sum and of the two products to binary32. Scales of either
+ * sign. Workspace as ozaki2_xent, k <= OZAKI2_I8_MAX_K.
  * Returns as ozaki2_xent: -1..-13 for an argument, -14 for the workspace.
  */
 int ozaki2_i8xent(int64_t t, int64_t v, int64_t k, const int8_t *A, int64_t lda, const float *a_scale,
                   const int8_t *B, int64_t ldb, const float *b_scale, const int64_t *targets, int64_t ignore_index,
                   float *loss, float *lse, void *stream);
+size_t ozaki2_i8xent_workspace_size(int64_t t, int64_t v, int64_t k);
 int ozaki2_i8xent_ws(int64_t t, int64_t v, int64_t k, const int8_t *A, int64_t lda, const float *a_scale,
                      const int8_t *B, int64_t ldb, const float *b_scale, const int64_t *targets, int64_t ignore_index,
                      float *loss, float *lse, void *workspace, size_t workspace_bytes, void *stream);

@@ -38,6 +38,7 @@ EXPORTS = (
     "ozaki2_quantize_rows", "ozaki2_i8gemm", "ozaki2_i8gemm_ws", "ozaki2_i8gemm_workspace_size",
     "ozaki2_i8linear", "ozaki2_i8linear_ws", "ozaki2_i8linear_workspace_size",
     "ozaki2_xent", "ozaki2_xent_ws", "ozaki2_xent_workspace_size", "ozaki2_i8xent", "ozaki2_i8xent_ws",
+    "ozaki2_i8xent_workspace_size",
     "ozaki2_xent_grad", "ozaki2_xent_grad_ws", "ozaki2_xent_grad_workspace_size",
 )
 
@@ -131,6 +132,8 @@ def lib() -> ctypes.CDLL:
         getattr(L, name + "_ws").restype = i32
     L.ozaki2_xent_workspace_size.argtypes = [i64, i64, i64]
     L.ozaki2_xent_workspace_size.restype = sz
+    L.ozaki2_i8xent_workspace_size.argtypes = [i64, i64, i64]
+    L.ozaki2_i8xent_workspace_size.restype = sz
     L.ozaki2_xent_grad_workspace_size.argtypes = [i64, i64, i64, i32, i32]
     L.ozaki2_xent_grad_workspace_size.restype = sz
     L.ozaki2_finalize.argtypes = []
@@ -286,6 +289,10 @@ def ozaki2_i8xent_ws(t, v, k, A, lda, a_scale, B, ldb, b_scale, targets, ignore_
                      workspace_bytes, stream=0) -> int:
     return lib().ozaki2_i8xent_ws(t, v, k, A, lda, a_scale, B, ldb, b_scale, targets, ignore_index, loss, lse,
                                   workspace, workspace_bytes, stream)
+
+
+def ozaki2_i8xent_workspace_size(t, v, k) -> int:
+    return lib().ozaki2_i8xent_workspace_size(t, v, k)
 
 
 def ozaki2_xent_grad(t, v, d, X, ldx, W, ldw, type, targets, ignore_index, lse, grad_loss, dX, lddx, dW, lddw,
@@ -660,7 +667,7 @@ def i8xent(A, B, a_scale, b_scale, targets, ignore_index=-100, workspace=None):
     loss = torch.empty(t, dtype=torch.float32, device=device)
     lse = torch.empty(t, dtype=torch.float32, device=device)
     L = lib()
-    ws, wp, wb = _workspace(L.ozaki2_xent_workspace_size(t, v, k), workspace, device)
+    ws, wp, wb = _workspace(L.ozaki2_i8xent_workspace_size(t, v, k), workspace, device)
     _call(L.ozaki2_i8xent_ws, "ozaki2_i8xent_ws", device, t, v, k, A.data_ptr(), lda, a_scale.data_ptr(), B.data_ptr(),
           ldb, b_scale.data_ptr(), targets.data_ptr(), ignore_index, loss.data_ptr(), lse.data_ptr(), wp, wb)
     return loss, lse

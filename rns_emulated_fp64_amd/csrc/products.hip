@@ -124,9 +124,17 @@ int splits_of(int64_t t, int64_t n, int64_t k) {
     return tile_splits(choose_tile(ta, false), n, t, ta.kbytes);
 }
 int64_t plane_pitch(int64_t n) { return (n + 3) / 4 * 4; }
-size_t i8gemm_bytes(int64_t t, int64_t n, int64_t k) {
+size_t plane_bytes(int64_t t, int64_t n, int64_t k) {
     const int s = splits_of(t, n, k);
-    return s > 1 ? (size_t)s * (size_t)t * (size_t)plane_pitch(n) * 4 : 0;
+    return s > 1 ? up256((size_t)s * (size_t)t * (size_t)plane_pitch(n) * 4) : 0;
+}
+// Workspace of a product: packed rows of A (unless they are the library's own)
+// and of a run of B, and the planes.
+size_t product_bytes(int64_t t, int64_t n, int64_t k, bool own_a) {
+    if (!needs_pack(k, t)) return plane_bytes(t, n, k);
+    const int64_t run = pack_rows(n, k);
+    return (own_a ? 0 : up256((size_t)t * (size_t)pack_pitch(k))) + up256((size_t)run * (size_t)pack_pitch(k)) +
+           plane_bytes(t, run, k);
 }
 
 // Activations that the skinny kernel quantises itself: rows that fit LDS beside
@@ -135,39 +143,76 @@ constexpr int64_t kQuantRows = 8, kQuantLds = 46 * 1024;
 int64_t quant_pitch(int64_t k) { return (k + 63) / 64 * 64 + 16; }
 bool quantises_in_product(int64_t t, int64_t k) { return t <= kQuantRows && t * (quant_pitch(k) + 4) <= kQuantLds; }
 
+struct Product {
+    int64_t t, n, k;
+    const int8_t *A;
+    int64_t lda;
+    const float *a_scale;
+    const int8_t *B;
+    int64_t ldb;
+    const float *b_scale, *bias;
+    void *C;
+    int64_t ldc;
+};
+
 template <class OutT>
-int product_t(int64_t t, int64_t n, int64_t k, const int8_t *A, int64_t lda, const float *a_scale, const int8_t *B,
-              int64_t ldb, const float *b_scale, const float *bias, void *C, int64_t ldc, char *ws, hipStream_t s) {
+int product_rows(const Product &p, char *ws, hipStream_t s) {
     TileArgs ta{};
-    ta.A = B;  // the weights' index is contiguous in C
-    ta.B = A;
-    ta.lda = ldb;
-    ta.ldb = lda;
-    ta.na = n;
-    ta.nb = t;
-    ta.kbytes = k;
-    const typename EpiScale<OutT>::Args e = {(OutT *)C, ldc, b_scale, a_scale, bias, n, t};
+    ta.A = p.B;  // the weights' index is contiguous in C
+    ta.B = p.A;
+    ta.lda = p.ldb;
+    ta.ldb = p.lda;
+    ta.na = p.n;
+    ta.nb = p.t;
+    ta.kbytes = p.k;
+    const typename EpiScale<OutT>::Args e = {(OutT *)p.C, p.ldc, p.b_scale, p.a_scale, p.bias, p.n, p.t};
     const Tile tile = choose_tile(ta, false);
-    const int splits = tile == Tile::skinny ? 1 : splits_of(t, n, k);
+    const int splits = tile == Tile::skinny ? 1 : splits_of(p.t, p.n, p.k);
     if (splits == 1) {
         HIP_TRY((launch_tile<MmaI8, EpiScale<OutT>, false>(ta, e, tile, 1, s)));
         return OZAKI2_SUCCESS;
     }
-    const int64_t ldp = plane_pitch(n), plane = t * ldp;
-    HIP_TRY((launch_tile<MmaI8, EpiRaw, false>(ta, {(uint32_t *)ws, ldp, plane, n, t}, tile, splits, s)));
-    const dim3 grid((unsigned)((n + 1023) / 1024), (unsigned)(t < 65535 ? t : 65535));
+    const int64_t ldp = plane_pitch(p.n), plane = p.t * ldp;
+    HIP_TRY((launch_tile<MmaI8, EpiRaw, false>(ta, {(uint32_t *)ws, ldp, plane, p.n, p.t}, tile, splits, s)));
+    const dim3 grid((unsigned)((p.n + 1023) / 1024), (unsigned)(p.t < 65535 ? p.t : 65535));
     hipLaunchKernelGGL((k_join_scale<OutT>), grid, dim3(256), 0, s, (const int32_t *)ws, splits, plane, ldp, e);
     HIP_TRY(hipGetLastError());
     return OZAKI2_SUCCESS;
 }
 
-int product(int64_t t, int64_t n, int64_t k, const int8_t *A, int64_t lda, const float *a_scale, const int8_t *B,
-            int64_t ldb, const float *b_scale, const float *bias, void *C, int64_t ldc, int ctype, char *ws,
-            hipStream_t s) {
-    if (ctype == OZAKI2_BF16) return product_t<__bf16>(t, n, k, A, lda, a_scale, B, ldb, b_scale, bias, C, ldc, ws, s);
-    if (ctype == OZAKI2_FP16)
-        return product_t<_Float16>(t, n, k, A, lda, a_scale, B, ldb, b_scale, bias, C, ldc, ws, s);
-    return product_t<float>(t, n, k, A, lda, a_scale, B, ldb, b_scale, bias, C, ldc, ws, s);
+// own_a: the rows of A are the library's own, with an aligned pitch and any
+// bytes (which meet zeros of B) up to the next 16.
+template <class OutT>
+int product_t(Product p, bool own_a, char *ws, hipStream_t s) {
+    if (!needs_pack(p.k, p.t)) return product_rows<OutT>(p, ws, s);
+    const int64_t pitch = pack_pitch(p.k), run = pack_rows(p.n, p.k), k16 = (p.k + 15) / 16 * 16;
+    if (!own_a) {
+        HIP_TRY(launch_pack_rows(p.A, p.lda, p.t, p.k, ws, pitch, nullptr, s));
+        p.A = (const int8_t *)ws;
+        p.lda = pitch;
+        ws += up256((size_t)p.t * (size_t)pitch);
+    }
+    char *planes = ws + up256((size_t)run * (size_t)pitch);
+    for (int64_t n0 = 0; n0 < p.n; n0 += run) {
+        Product q = p;
+        q.n = p.n - n0 < run ? p.n - n0 : run;
+        q.k = k16;
+        q.B = (const int8_t *)ws;
+        q.ldb = pitch;
+        q.b_scale += n0;
+        if (q.bias) q.bias += n0;
+        q.C = (OutT *)p.C + n0;
+        HIP_TRY(launch_pack_rows(p.B + n0 * p.ldb, p.ldb, q.n, p.k, ws, pitch, nullptr, s));
+        const int st = product_rows<OutT>(q, planes, s);
+        if (st) return st;
+    }
+    return OZAKI2_SUCCESS;
+}
+
+int product(const Product &p, bool own_a, int ctype, char *ws, hipStream_t s) {
+    if (ctype == OZAKI2_BF16) return product_t<__bf16>(p, own_a, ws, s);
+    if (ctype == OZAKI2_FP16) return product_t<_Float16>(p, own_a, ws, s);
+    return product_t<float>(p, own_a, ws, s);
 }
 
 template <class XT, class OutT>
@@ -232,14 +277,15 @@ struct GemmCall {
 };
 int run_i8gemm(void *ctx, char *ws) {
     const GemmCall &c = *(const GemmCall *)ctx;
-    return product(c.t, c.n, c.k, c.A, c.lda, c.a_scale, c.B, c.ldb, c.b_scale, c.bias, c.C, c.ldc, c.ctype, ws, c.s);
+    return product({c.t, c.n, c.k, c.A, c.lda, c.a_scale, c.B, c.ldb, c.b_scale, c.bias, c.C, c.ldc}, false, c.ctype, ws,
+                   c.s);
 }
 int front_i8gemm(GemmCall c, bool cached, void *workspace, size_t bytes) {
     const int st = check_i8gemm(c.t, c.n, c.k, c.A, c.lda, c.a_scale, c.B, c.ldb, c.b_scale, c.C, c.ldc, c.ctype);
     if (st) return st;
     if (!fits(c.t, c.n, c.k)) return OZAKI2_ERR_UNSUPPORTED;
     if (c.t == 0 || c.n == 0) return OZAKI2_SUCCESS;
-    const size_t need = i8gemm_bytes(c.t, c.n, c.k);
+    const size_t need = product_bytes(c.t, c.n, c.k, false);
     if (need == 0) return run_i8gemm(&c, nullptr);
     if (cached) return with_workspace(need, c.s, run_i8gemm, &c);
     if (workspace == nullptr || ((uintptr_t)workspace & (kWsAlign - 1)) != 0) return -14;
@@ -274,14 +320,12 @@ struct LinearCall {
     int xtype, ctype;
     hipStream_t s;
 };
-// Workspace of ozaki2_i8linear: the quantised rows (pitch a multiple of 128, so
-// the product takes its aligned path on this side whatever k is), their
-// scales, the product's own.
-int64_t q_pitch(int64_t k) { return (k + 127) / 128 * 128; }
-size_t q_bytes(int64_t t, int64_t k) { return up256((size_t)t * (size_t)(q_pitch(k) > 0 ? q_pitch(k) : 128)); }
+// Workspace of ozaki2_i8linear: the quantised rows, their scales, the product's own.
+int64_t q_pitch(int64_t k) { return pack_pitch(k); }
+size_t q_bytes(int64_t t, int64_t k) { return up256((size_t)t * (size_t)q_pitch(k)); }
 size_t i8linear_bytes(int64_t t, int64_t n, int64_t k) {
     if (quantises_in_product(t, k)) return 0;
-    return q_bytes(t, k) + up256(4 * (size_t)t) + i8gemm_bytes(t, n, k);
+    return q_bytes(t, k) + up256(4 * (size_t)t) + product_bytes(t, n, k, true);
 }
 int run_i8linear(void *ctx, char *ws) {
     const LinearCall &c = *(const LinearCall *)ctx;
@@ -293,7 +337,8 @@ int run_i8linear(void *ctx, char *ws) {
     float *scale = (float *)(ws + q_bytes(c.t, c.k));
     char *rest = ws + q_bytes(c.t, c.k) + up256(4 * (size_t)c.t);
     HIP_TRY(launch_quantize_rows(c.xtype, c.X, c.ldx, c.t, c.k, q, q_pitch(c.k), scale, c.s));
-    return product(c.t, c.n, c.k, q, q_pitch(c.k), scale, c.B, c.ldb, c.b_scale, c.bias, c.C, c.ldc, c.ctype, rest, c.s);
+    return product({c.t, c.n, c.k, q, q_pitch(c.k), scale, c.B, c.ldb, c.b_scale, c.bias, c.C, c.ldc}, true, c.ctype, rest,
+                   c.s);
 }
 int front_i8linear(LinearCall c, bool cached, void *workspace, size_t bytes) {
     const int st = check_i8linear(c.t, c.n, c.k, c.X, c.ldx, c.xtype, c.B, c.ldb, c.b_scale, c.C, c.ldc, c.ctype);
@@ -339,7 +384,7 @@ int ozaki2_i8gemm(int64_t t, int64_t n, int64_t k, const int8_t *A, int64_t lda,
 
 size_t ozaki2_i8gemm_workspace_size(int64_t t, int64_t n, int64_t k) {
     if (t <= 0 || n <= 0 || k < 0 || !fits(t, n, k)) return 0;
-    return i8gemm_bytes(t, n, k);
+    return product_bytes(t, n, k, false);
 }
 
 int ozaki2_i8gemm_ws(int64_t t, int64_t n, int64_t k, const int8_t *A, int64_t lda, const float *a_scale,

@@ -420,7 +420,7 @@ __device__ __forceinline__ void copies_landed_barrier() {
 // such loads return zeros.
 //
 // Requires: rows, pitches and kbytes multiples of 16 bytes, lda, ldb < 2^24,
-// na, nb >= 256, 256 <= kbytes < 2^30, tiles < 2^31.
+// na, nb >= 256, 0 < kbytes < 2^30, tiles < 2^31; slices of k of at least 256 bytes.
 template <class M, class Epi, int RT>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(8 / RT, 8 / RT))) void k_tile_p(
         TileArgs ta, typename Epi::Args ea) {
@@ -438,7 +438,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(8 / RT, 8 /
     const int lane = threadIdx.x & 63;
     const int wm = wave >> 1, wn = wave & 1;
     const int kb = (int)ta.kbytes;
-    const int rounds = (SMALL ? (int)ta.split_bytes : kb + 127) / 128;
+    // at least two, the second of them all past the end of a short k
+    const int rounds = max(2, (SMALL ? (int)ta.split_bytes : kb + 127) / 128);
     const uint32_t lda = (uint32_t)ta.lda, ldb = (uint32_t)ta.ldb;
     auto origin = [&](int b, int &a0, int &b0, int &tile_a, int &split) {
         int tb;
@@ -1061,6 +1062,41 @@ hipError_t launch_skinny(const TileArgs &t, const typename Epi::Args &e, const t
     return hipGetLastError();
 }
 
+// ---- rows whose length is not a multiple of 16 bytes ------------------------------
+// They cannot be copied into LDS directly, and loads at odd addresses are slow
+// (bf16, 1024 tokens, 32000 x 1025: 413 us through k_tile_any against 68 for 32000 x
+// 1024), so beyond a few rows of B the operands are first copied to rows that
+// are: whole cache lines, an odd number of them (rows at a power of two apart would meet in
+// one memory channel), zeros up to the next 16 bytes. Weights go in runs that
+// stay in the last-level cache until the product reads them.
+constexpr int64_t kPackRun = (int64_t)96 << 20;
+inline int64_t pack_pitch(int64_t kbytes) { return (((kbytes + 127) / 128) | 1) * 128; }
+inline int64_t pack_rows(int64_t rows, int64_t kbytes) {
+    const int64_t run = kPackRun / pack_pitch(kbytes) / 256 * 256;
+    return rows < run ? rows : run < 256 ? 256 : run;
+}
+inline bool needs_pack(int64_t kbytes, int64_t nb) { return (kbytes & 15) != 0 && nb > 16; }
+
+// out[r][0 .. kbytes) = in[r], zeros to the next 16 bytes. Rows whose g is 0 are
+// zeros (g may be null). 16 bytes per lane and step, a wavefront per row.
+__global__ __launch_bounds__(256) static void k_pack_rows(const int8_t *__restrict__ in, int64_t ldi, int64_t rows,
+                                                          int64_t kbytes, int8_t *__restrict__ out, int64_t ldo,
+                                                          const float *__restrict__ g) {
+    const int lane = threadIdx.x & 63;
+    for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < rows; r += (int64_t)gridDim.x * 4) {
+        const bool zero = g != nullptr && g[r] == 0.f;
+        for (int64_t k = 16 * lane; k < kbytes; k += 1024)
+            *(v4i *)(out + r * ldo + k) = zero ? (v4i){0, 0, 0, 0} : load_chunk(in + r * ldi, k, kbytes);
+    }
+}
+inline hipError_t launch_pack_rows(const void *in, int64_t ldi, int64_t rows, int64_t kbytes, void *out, int64_t ldo,
+                                   const float *g, hipStream_t s) {
+    const int64_t blocks = (rows + 3) / 4;
+    hipLaunchKernelGGL(k_pack_rows, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, s, (const int8_t *)in, ldi,
+                       rows, kbytes, (int8_t *)out, ldo, g);
+    return hipGetLastError();
+}
+
 // ---- choice of kernel -------------------------------------------------------------
 // Compute units that the choices below plan for (a whole MI355X), so that a
 // workspace size depends on the problem alone.
@@ -1068,7 +1104,7 @@ constexpr int64_t kPlanUnits = 256;
 
 inline bool aligned16(const TileArgs &t) {
     return (((uintptr_t)t.A | (uintptr_t)t.B | (uintptr_t)t.lda | (uintptr_t)t.ldb | (uintptr_t)t.kbytes) & 15) == 0 &&
-           t.lda < (1 << 24) && t.ldb < (1 << 24) && t.kbytes >= 256 && t.kbytes < (1 << 30);
+           t.lda < (1 << 24) && t.ldb < (1 << 24) && t.kbytes > 0 && t.kbytes < (1 << 30);
 }
 
 enum class Tile { skinny, s11, s21, s22, s42, p4, p8, any };
@@ -1193,7 +1229,7 @@ hipError_t launch_tile(TileArgs t, const typename Epi::Args &e, Tile tile, int s
     t.split_bytes = ((t.kbytes + splits - 1) / splits + 127) / 128 * 128;
     const int64_t total = (int64_t)t.tiles_a * t.tiles_b, cus = compute_units();
     const dim3 grid((unsigned)total, (unsigned)splits);
-    if (tile == Tile::p4 && t.split_bytes < 256) tile = Tile::any;
+    if (tile == Tile::p4 && splits > 1 && t.split_bytes < 256) tile = Tile::any;
     switch (tile) {
     case Tile::p8:
         hipLaunchKernelGGL((k_tile_p<M, Epi, 8>), dim3((unsigned)(total < cus ? total : cus)), dim3(256), 0, s, t, e);

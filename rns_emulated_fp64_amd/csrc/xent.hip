@@ -448,28 +448,59 @@ TileArgs rows_args(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, 
 
 // Enough for any tile: parts of 16 entries for up to 64 tokens and for small
 // products, of at least 32 beyond.
-size_t forward_bytes(int64_t t, int64_t v) {
-    const int64_t run = t < kRun ? t : kRun;
-    return up256(8 * (size_t)run * (size_t)((v + 15) / 16 < 1024 || run <= kSkinnyRows ? (v + 15) / 16 : (v + 63) / 64));
+int64_t most_parts(int64_t nt, int64_t v) {
+    return (v + 15) / 16 < 1024 || nt <= kSkinnyRows ? (v + 15) / 16 : (v + 63) / 64;
+}
+struct ForwardPlan {
+    int64_t run;  // vocabulary entries per product
+    size_t part, x, w, total;
+};
+ForwardPlan plan_forward(int64_t t, int64_t v, int64_t kbytes) {
+    ForwardPlan p{};
+    const int64_t nt = t < kRun ? t : kRun;
+    const bool pack = needs_pack(kbytes, nt);
+    p.run = pack ? pack_rows(v, kbytes) : v;
+    // a last, short run may take narrower parts than the others
+    p.x = up256(8 * (size_t)nt * (size_t)(v / p.run * most_parts(nt, p.run) + most_parts(nt, v % p.run)));
+    p.w = p.x + (pack ? up256((size_t)nt * (size_t)pack_pitch(kbytes)) : 0);
+    p.total = p.w + (pack ? up256((size_t)p.run * (size_t)pack_pitch(kbytes)) : 0);
+    return p;
 }
 
 template <class M, bool SCALED, class DotOf>
 int forward(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const float *sx, const void *W, int64_t ldw,
             const float *sw, const int64_t *y, int64_t ignore, float *loss, float *lse, char *ws, DotOf dot_of,
             hipStream_t s) {
+    const ForwardPlan plan = plan_forward(t, v, d * M::BYTES);
     float2 *part = (float2 *)ws;
     for (int64_t t0 = 0; t0 < t; t0 += kRun) {
         const int64_t nt = t - t0 < kRun ? t - t0 : kRun;
         const char *x = (const char *)X + t0 * ldx * M::BYTES;
-        const TileArgs ta = rows_args<M::BYTES>(nt, v, d, x, ldx, W, ldw);
-        const typename EpiLse<SCALED>::Args e = {part, nt, sw, sx ? sx + t0 : nullptr, v, nt};
-        Tile tile = choose_tile(ta, false);
-        // (a forced tile may have more parts than the workspace)
-        if (8 * (size_t)nt * (size_t)tile_parts(tile, v) > forward_bytes(t, v)) tile = aligned16(ta) ? Tile::p4 : Tile::any;
-        HIP_TRY((launch_tile<M, EpiLse<SCALED>, false>(ta, e, tile, 1, s)));
+        const bool pack = needs_pack(d * M::BYTES, nt);
+        const int64_t pitch = pack_pitch(d * M::BYTES), run = pack ? plan.run : v;
+        if (pack) HIP_TRY(launch_pack_rows(x, ldx * M::BYTES, nt, d * M::BYTES, ws + plan.x, pitch, nullptr, s));
+        int nparts = 0;
+        for (int64_t v0 = 0; v0 < v; v0 += run) {
+            const int64_t nv = v - v0 < run ? v - v0 : run;
+            const char *w = (const char *)W + v0 * ldw * M::BYTES;
+            TileArgs ta = rows_args<M::BYTES>(nt, nv, d, x, ldx, w, ldw);
+            if (pack) {
+                HIP_TRY(launch_pack_rows(w, ldw * M::BYTES, nv, d * M::BYTES, ws + plan.w, pitch, nullptr, s));
+                ta.A = (const int8_t *)ws + plan.w;
+                ta.B = (const int8_t *)ws + plan.x;
+                ta.lda = ta.ldb = pitch;
+                ta.kbytes = (ta.kbytes + 15) / 16 * 16;
+            }
+            Tile tile = choose_tile(ta, false);
+            // (a forced tile may have more parts than the workspace)
+            if (tile_parts(tile, nv) > most_parts(nt, nv)) tile = aligned16(ta) ? Tile::p4 : Tile::any;
+            const typename EpiLse<SCALED>::Args e = {part + (int64_t)nparts * nt, nt, sw ? sw + v0 : nullptr,
+                                                     sx ? sx + t0 : nullptr, nv, nt};
+            HIP_TRY((launch_tile<M, EpiLse<SCALED>, false>(ta, e, tile, 1, s)));
+            nparts += tile_parts(tile, nv);
+        }
         const auto dot = dot_of(x, t0);
         typedef std::remove_const_t<decltype(dot)> Dot;
-        const int nparts = tile_parts(tile, v);
         if (nt <= kSkinnyRows)  // a block each
             hipLaunchKernelGGL((k_xent_join<Dot, 1>), dim3((unsigned)nt), dim3(256), 0, s, part, nt, nparts, nt, v,
                                y + t0, ignore, dot, loss + t0, lse + t0);
@@ -639,7 +670,7 @@ int launch(XentCall c, bool cached, void *workspace, size_t bytes, int bad_ws) {
     const int64_t lim = (int64_t)1 << 31;
     if (c.t >= lim || c.v >= lim || c.d >= (c.type < 0 ? (int64_t)OZAKI2_I8_MAX_K + 1 : lim / 4)) return OZAKI2_ERR_UNSUPPORTED;
     if (c.t == 0) return OZAKI2_SUCCESS;
-    const size_t need = forward_bytes(c.t, c.v);
+    const size_t need = plan_forward(c.t, c.v, c.type < 0 ? c.d : 2 * c.d).total;
     if (cached) return with_workspace(need, c.s, run_xent, &c);
     if (workspace == nullptr || ((uintptr_t)workspace & (kWsAlign - 1)) != 0) return bad_ws;
     if (bytes < need) return OZAKI2_ERR_WORKSPACE;
@@ -747,7 +778,10 @@ int ozaki2_xent_ws(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, 
                        (hipStream_t)stream}, false, workspace, workspace_bytes);
 }
 size_t ozaki2_xent_workspace_size(int64_t t, int64_t v, int64_t d) {
-    return sizes_fit(t, v, d) ? forward_bytes(t, v) : 0;
+    return sizes_fit(t, v, d) ? plan_forward(t, v, 2 * d).total : 0;
+}
+size_t ozaki2_i8xent_workspace_size(int64_t t, int64_t v, int64_t k) {
+    return sizes_fit(t, v, k) && k <= OZAKI2_I8_MAX_K ? plan_forward(t, v, k).total : 0;
 }
 
 int ozaki2_i8xent(int64_t t, int64_t v, int64_t k, const int8_t *A, int64_t lda, const float *a_scale, const int8_t *B,

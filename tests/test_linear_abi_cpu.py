@@ -84,7 +84,7 @@ def test_i8xent_refusals():
     for i, bad in [(0, -1), (1, 0), (2, -1), (3, 0), (4, 15), (5, 0), (6, 0), (7, 15), (8, 0), (9, 0), (11, 0), (12, 0)]:
         assert oz.ozaki2_i8xent(*with_arg(good, i, bad)) == -(i + 1), i
         assert oz.ozaki2_i8xent_ws(*with_arg(good, i, bad), P, 1 << 30) == -(i + 1), i
-    need = oz.ozaki2_xent_workspace_size(5, 9, 16)
+    need = oz.ozaki2_i8xent_workspace_size(5, 9, 16)
     assert oz.ozaki2_i8xent_ws(*good, 0, need) == -14
     assert oz.ozaki2_i8xent_ws(*good, P, need - 1) == 2
     k = 1 << 17
