@@ -35,7 +35,10 @@
 namespace oz2 {
 
 typedef int v4i __attribute__((ext_vector_type(4)));
+typedef int v2i __attribute__((ext_vector_type(2)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef short v4s __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) v4s lds_v4s;
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
@@ -131,6 +134,7 @@ struct TileArgs {
     int64_t lda, ldb;        // bytes between rows
     int64_t na, nb;          // rows
     int64_t kbytes;          // bytes of k per row
+    int krows;               // K-major operands: rows of k (zeros beyond)
     int tiles_a, tiles_b;
     int splits;              // 128 x 128 tiles: slices of k, one block each
     int64_t split_bytes;     // bytes of k per slice (a multiple of 128)
@@ -254,6 +258,7 @@ struct EpiScale {
         int64_t na, nb;
     };
     static constexpr int STORES = sizeof(OutT) == 2 ? 1 : 2;  // 16-byte stores per two 16 x 16 tiles
+    static constexpr bool PADDED = false;  // whether the output may be written up to the next multiple of 8 of a
 
     template <class M, int RT, int CT, bool EDGE, bool AGPR = false>
     static __device__ __forceinline__ void run(v4i (&acc)[RT][CT], const TileWhere &w, const Args &e) {
@@ -353,6 +358,7 @@ struct EpiRaw {
         int64_t na, nb;
     };
     static constexpr int STORES = 2;
+    static constexpr bool PADDED = true;  // ldo is a multiple of 8 with K-major operands
     template <class M, int RT, int CT, bool EDGE, bool AGPR = false>
     static __device__ __forceinline__ void run(v4i (&acc)[RT][CT], const TileWhere &w, const Args &e) {
         const int lane = fresh_lane();
@@ -412,24 +418,42 @@ __device__ __forceinline__ void copies_landed_barrier() {
 // stores, all of them unconditional (EDGE = false), lie between the two and are
 // allowed as well.
 //
+// KA, KB: the operand is stored with k as its row index instead, element (k, a)
+// at A + k lda + 2 a (16-bit types): products over the other index of a matrix
+// without transposing it first. A unit is then 64 rows of k, and a fragment is put
+// together by two transposing LDS reads (16 lanes turn 4 rows of 16 values into
+// 16 columns of 4).
+//
 // Edges: a last tile that would reach past na or nb is moved back to end
-// there (na, nb >= 256), so every access is in bounds and no store is
-// conditional; rows that two tiles cover get the same values twice (or the
+// there (na, nb >= 256), so every access is in bounds and (but for K-major operands,
+// which it is moved in steps of 8) no store is conditional; rows that two tiles cover get the same values twice (or the
 // epilogue looks at amin). k is padded to whole rounds: a lane whose 16 bytes
 // lie past the end of the row asks for an offset outside the copy's buffer, and
 // such loads return zeros.
 //
 // Requires: rows, pitches and kbytes multiples of 16 bytes, lda, ldb < 2^24,
-// na, nb >= 256, 0 < kbytes < 2^30, tiles < 2^31; slices of k of at least 256 bytes.
-template <class M, class Epi, int RT>
+// na, nb >= 256, 0 < kbytes < 2^30, tiles < 2^31; slices of k of at least 256 bytes;
+// K-major operands: pointer and pitch multiples of 16 bytes, and na (nb) of 8 or
+// rows padded to that.
+template <class M, class Epi, int RT, bool KA = false, bool KB = false>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(8 / RT, 8 / RT))) void k_tile_p(
         TileArgs ta, typename Epi::Args ea) {
     constexpr bool SMALL = RT == 4;
     constexpr int CT = RT, NF = RT + CT, NQ = RT * CT, LPW = RT, SIDE = 32 * RT, UNIT = SIDE * 128;
     constexpr int PRE = SMALL ? 1 : 4, RSTEP = SMALL ? 1 : 3, CSTEP = SMALL ? 3 : 6;
     constexpr int STORES = RT * CT / 2 * Epi::STORES;
-    constexpr int LATER = SMALL ? LPW : LPW + STORES < 63 ? LPW + STORES : 63;  // vmcnt is 6 bits wide
+    // stores that may be left out are not counted; vmcnt is 6 bits wide
+    constexpr int LATER = SMALL || ((KA || KB) && !Epi::PADDED) ? LPW : LPW + STORES < 63 ? LPW + STORES : 63;
+    // a K-major operand takes two reads per fragment
+    constexpr int NA = KA ? 2 * RT : RT, NB = KB ? 2 * CT : CT, NREAD = NA + NB;
+    constexpr int ROWB = SIDE * 2, LPR = ROWB / 16, RPC = 1024 / ROWB;  // K-major: bytes and lanes per row of k, rows per copy
+    static_assert(!(KA || KB) || M::BYTES == 2, "16-bit transposing reads");
     static_assert(PRE + RSTEP * (NF - 1) < NQ && PRE + 1 + CSTEP * (LPW - 1) < NQ, "schedule fits a half");
+    // reads issued up to MFMA q
+    constexpr auto reads_by = [](int q) {
+        const int n = NREAD == NF ? (q - PRE) / RSTEP + 1 : ((q - PRE + 1) * NREAD + NQ - PRE - 1) / (NQ - PRE);
+        return q < PRE ? 0 : n < NREAD ? n : NREAD;
+    };
     __shared__ __attribute__((aligned(1024))) int8_t lds[5 * UNIT];
 
     const int tiles = ta.tiles_a * ta.tiles_b, total = SMALL ? tiles * ta.splits : tiles;
@@ -449,29 +473,58 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(8 / RT, 8 /
         a0 = tile_a * SIDE;
         b0 = tb * SIDE;
         if (!SMALL) {
-            a0 = (int)min((int64_t)a0, ta.na - SIDE);
-            b0 = (int)min((int64_t)b0, ta.nb - SIDE);
+            // (K-major: back to a multiple of 8, which keeps 16-byte accesses aligned)
+            a0 = (int)min((int64_t)a0, (KA ? (ta.na + 7) & ~(int64_t)7 : ta.na) - SIDE);
+            b0 = (int)min((int64_t)b0, (KB ? (ta.nb + 7) & ~(int64_t)7 : ta.nb) - SIDE);
         }
     };
     // every wavefront copies SIDE / 4 rows of each unit, 8 per copy. SMALL: rows
     // past the last one are copies of it, through an offset of their own
     constexpr int WROWS = SIDE / 4;
-    auto source_a = [&](int a0) { return (uint64_t)(uintptr_t)ta.A + (uint64_t)(a0 + (SMALL ? 0 : wave * WROWS)) * (uint64_t)lda; };
-    auto source_b = [&](int b0) { return (uint64_t)(uintptr_t)ta.B + (uint64_t)(b0 + (SMALL ? 0 : wave * WROWS)) * (uint64_t)ldb; };
-    auto rsrc = [&](uint64_t base, uint32_t ld) {
-        return (v4i){(int)(uint32_t)base, (int)((uint32_t)(base >> 32) & 0xffffu),
-                     (int)((uint32_t)((SMALL ? SIDE : WROWS) - 1) * ld + 128u), 0x00020000};
+    // where the copies of a tile begin at byte k of its slice (K-major: 2 bytes
+    // per row of k, every wavefront copies 16 rows of the round's 64)
+    auto source = [&](auto kmajor, const int8_t *p, int row, uint32_t ld, int k) {
+        if constexpr (decltype(kmajor)::value)
+            return (uint64_t)(uintptr_t)p + (uint64_t)(k / 2 + wave * 16) * (uint64_t)ld + (uint64_t)row * 2u;
+        else
+            return (uint64_t)(uintptr_t)p + (uint64_t)(row + (SMALL ? 0 : wave * WROWS)) * (uint64_t)ld + (uint32_t)k;
     };
-    uint32_t rows_a[SMALL ? LPW : 1], rows_b[SMALL ? LPW : 1];  // SMALL: row offset of each copy
-    auto clamp_rows = [&](int a0, int b0) {
-        if constexpr (SMALL) {
+    const std::integral_constant<bool, KA> kind_a;
+    const std::integral_constant<bool, KB> kind_b;
+    const uint64_t step_a = KA ? 64 * (uint64_t)lda : 128, step_b = KB ? 64 * (uint64_t)ldb : 128;
+    auto rsrc = [&](auto kmajor, uint64_t base, uint32_t ld) {
+        const uint32_t bytes = decltype(kmajor)::value ? 15u * ld + (uint32_t)ROWB
+                                                       : (uint32_t)((SMALL ? SIDE : WROWS) - 1) * ld + 128u;
+        return (v4i){(int)(uint32_t)base, (int)((uint32_t)(base >> 32) & 0xffffu), (int)bytes, 0x00020000};
+    };
+    // Offsets of a lane's copies that depend on the tile. SMALL: the row of each copy.
+    // K-major: the lane's 16 bytes of a row of k, whose 32-byte pieces are permuted
+    // by f(k) = (k & 3) + 4 (k >> 3 & 1), so that the rows a transposing read takes (four
+    // consecutive ones from each of 0, 8, 16, 24) meet all banks; VAR values of f
+    // from copy to copy, and columns past the operand's end out of the buffer.
+    constexpr int VAR = SMALL ? 2 : 4;
+    auto variant = [](int q) { return SMALL ? q >> 1 : (q & 1) | (q >> 2) << 1; };
+    constexpr int OA = KA ? VAR : SMALL ? LPW : 1, OB = KB ? VAR : SMALL ? LPW : 1;
+    uint32_t rows_a[OA], rows_b[OB];
+    auto place_copies = [&](auto kmajor, uint32_t *rows, int row0, int64_t n, uint32_t ld) {
+        const int ln = threadIdx.x & 63;
+        if constexpr (decltype(kmajor)::value) {
+            const int kl = ln / LPR, idx = ln % LPR;
 #pragma unroll
-            for (int q = 0; q < LPW; ++q) {
-                const int64_t r = wave * WROWS + 8 * q + ((threadIdx.x & 63) >> 3);
-                rows_a[q] = (uint32_t)min(r, ta.na - 1 - a0) * lda;
-                rows_b[q] = (uint32_t)min(r, ta.nb - 1 - b0) * ldb;
+            for (int v = 0; v < VAR; ++v) {
+                const int f = SMALL ? (kl & 3) | v << 2 : (v & 1) << 1 | kl | (v >> 1) << 2;
+                const int c = ((idx >> 1) ^ f) * 32 + (idx & 1) * 16;
+                rows[v] = (int64_t)row0 + c / 2 < ((n + 7) & ~(int64_t)7) ? (uint32_t)kl * ld + (uint32_t)c : 0xfffffff0u;
             }
+        } else if constexpr (SMALL) {
+#pragma unroll
+            for (int q = 0; q < LPW; ++q)
+                rows[q] = (uint32_t)min((int64_t)(wave * WROWS + 8 * q + (ln >> 3)), n - 1 - row0) * ld;
         }
+    };
+    auto clamp_rows = [&](int a0, int b0) {
+        place_copies(kind_a, rows_a, a0, ta.na, lda);
+        place_copies(kind_b, rows_b, b0, ta.nb, ldb);
     };
     // this lane's chunk of a copy's row in the even copies; the odd ones (rows 8
     // .. 15 of a fragment) have it ^ 4
@@ -485,7 +538,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(8 / RT, 8 /
 
     int src_k = 0;  // byte of k at which the copies of a round start
     // where the lane reads in copy q of the round at src_k
-    auto offset = [&](int q, uint32_t row, const uint32_t *rows) -> uint32_t {
+    auto offset = [&](auto kmajor, int q, uint32_t row, const uint32_t *rows) -> uint32_t {
+        if constexpr (decltype(kmajor)::value)
+            return q * RPC < ta.krows - src_k / 2 - wave * 16 - lane / LPR ? rows[variant(q)] : 0xfffffff0u;
         const uint32_t c = q & 1 ? chunk ^ 64u : chunk;
         return src_k < (q & 1 ? k_odd : k_even) ? (SMALL ? rows[q] : row) + c : 0xfffffff0u;
     };
@@ -495,7 +550,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(8 / RT, 8 /
     origin(bid, a0, b0, tile_a, split);
     clamp_rows(a0, b0);
     int next_k = SMALL ? split * (int)ta.split_bytes : 0;
-    uint64_t next_a = source_a(a0) + (uint32_t)next_k, next_b = source_b(b0) + (uint32_t)next_k;
+    uint64_t next_a = source(kind_a, ta.A, a0, lda, next_k), next_b = source(kind_b, ta.B, b0, ldb, next_k);
     uint64_t src_a = next_a, src_b = next_b;
     src_k = next_k;
     int nbid = bid + G;
@@ -505,43 +560,73 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(8 / RT, 8 /
     v4i acc[RT][CT];
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
+        auto copy = [&](auto kmajor, uint64_t src, uint32_t ld, uint32_t row, const uint32_t *rows, uint32_t at) {
+            constexpr bool KM = decltype(kmajor)::value;
+            const v4i rs = rsrc(kmajor, src, ld);
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const v4i rs = u ? rsrc(src_b, ldb) : rsrc(src_a, lda);
-            const uint32_t ld = u ? ldb : lda, row = u ? lane_b : lane_a;
-#pragma unroll
-            for (int q = 0; q < LPW; ++q)
-                asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds" ::"v"(
-                                 offset(q, row, u ? rows_b : rows_a)),
-                             "s"(rs), "s"((uint32_t)((2 * p + u) * UNIT) + wave_lds + q * 1024u),
-                             "s"(SMALL ? 0u : 8u * q * ld)
+            for (int q = 0; q < LPW; ++q) {
+                const uint32_t from = offset(kmajor, q, row, rows), to = at + wave_lds + q * 1024u;
+                const uint32_t more = KM ? (uint32_t)(RPC * q) * ld : SMALL ? 0u : 8u * q * ld;
+                asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds" ::"v"(from),
+                             "s"(rs), "s"(to), "s"(more)
                              : "memory");
-        }
-        src_a += 128;
-        src_b += 128;
+            }
+        };
+        copy(kind_a, src_a, lda, lane_a, rows_a, (uint32_t)(2 * p * UNIT));
+        copy(kind_b, src_b, ldb, lane_b, rows_b, (uint32_t)((2 * p + 1) * UNIT));
+        src_a += step_a;
+        src_b += step_b;
         src_k += 128;
     }
     copies_landed_barrier<2 * LPW>();  // A and B of round 0
     v4i f0[NF], f1[NF];
+    // K-major: this lane's part of fragment r, step 0, first four of its eight k
+    uint32_t tr_a[KA ? RT : 1], tr_b[KB ? CT : 1];
+    {
+        const int c = lane >> 4, kr = (lane & 15) >> 2, f = kr | (c & 1) << 2;
+        const uint32_t base = (uint32_t)(8 * c + kr) * ROWB + (uint32_t)(lane & 3) * 8u;
+        if constexpr (KA)
 #pragma unroll
-    for (int r = 0; r < RT; ++r) f0[r] = *(const v4i *)(lds + (wm * RT + r) * 2048 + place);
+            for (int r = 0; r < RT; ++r) tr_a[r] = base + (uint32_t)(((wm * RT + r) ^ f) * 32);
+        if constexpr (KB)
 #pragma unroll
-    for (int r = 0; r < CT; ++r) f0[RT + r] = *(const v4i *)(lds + UNIT + (wn * CT + r) * 2048 + place);
+            for (int r = 0; r < CT; ++r) tr_b[r] = base + (uint32_t)(((wn * CT + r) ^ f) * 32);
+    }
+    // read i of the following step's fragments (B first) from the slots ra and rb
+    auto read = [&](auto step, int i, uint32_t ra, uint32_t rb, v4i(&f)[NF]) {
+        constexpr uint32_t S = decltype(step)::value;
+        const bool is_b = i < NB;
+        const int n = is_b ? i : i - NB;
+        if (is_b ? KB : KA) {
+            const int r = n >> 1, h = n & 1;
+            const int8_t *p = lds + ((is_b ? rb : ra) + (is_b ? tr_b[KB ? r : 0] : tr_a[KA ? r : 0])) + (S * 32 + h * 4) * ROWB;
+            const v2i t = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)p));
+            f[(is_b ? RT : 0) + r][2 * h] = t[0];
+            f[(is_b ? RT : 0) + r][2 * h + 1] = t[1];
+        } else {
+            const int8_t *p = lds + (is_b ? rb + (uint32_t)(wn * CT * 2048) : ra + (uint32_t)(wm * RT * 2048)) + (place ^ (S * 64u));
+            f[(is_b ? RT : 0) + n] = *(const v4i *)(p + n * 2048);
+        }
+    };
+    typedef std::integral_constant<uint32_t, 0> Step0;
+    typedef std::integral_constant<uint32_t, 1> Step1;
+#pragma unroll
+    for (int i = 0; i < NREAD; ++i) read(Step0{}, i, 0, UNIT, f0);
 
     bool later = false;  // a previous tile's stores are in flight
     // Half of a round: MFMAs on fc, reads of the following step into fn (B
     // first) from the slots ra, rb, copies of one unit into the slot cs.
     // SYNC: 0 none, 1 the barrier, 2 the barrier of a tile's first round
-    auto half = [&](auto first, auto sync, uint32_t ra, uint32_t rb, uint32_t at, uint64_t src, uint32_t ld, uint32_t row,
-                    const uint32_t *rows, uint32_t cs, v4i(&fc)[NF], v4i(&fn)[NF]) {
+    auto half = [&](auto first, auto sync, uint32_t ra, uint32_t rb, auto step, auto kmajor, uint64_t src, uint32_t ld,
+                    uint32_t row, const uint32_t *rows, uint32_t cs, v4i(&fc)[NF], v4i(&fn)[NF]) {
         constexpr int SYNC = decltype(sync)::value;
-        const int8_t *pa = lds + (ra + (uint32_t)(wm * RT * 2048)) + at,
-                     *pb = lds + (rb + (uint32_t)(wn * CT * 2048)) + at;
-        const v4i rs = rsrc(src, ld);
+        constexpr bool KM = decltype(kmajor)::value;
+        const v4i rs = rsrc(kmajor, src, ld);
         const uint32_t cbase = cs + wave_lds;
-        uint32_t off[SMALL ? LPW : 2];
+        constexpr int NOFF = KM || SMALL ? LPW : 2;
+        uint32_t off[NOFF];
 #pragma unroll
-        for (int q = 0; q < (SMALL ? LPW : 2); ++q) off[q] = offset(q, row, rows);
+        for (int q = 0; q < NOFF; ++q) off[q] = offset(kmajor, q, row, rows);
 #pragma unroll
         for (int q = 0; q < NQ; ++q) {
             // a tile's first half starts from zero
@@ -557,19 +642,14 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(8 / RT, 8 /
                         copies_landed_barrier<LPW>();
                 }
             }
-            if (q >= PRE && (q - PRE) % RSTEP == 0 && (q - PRE) / RSTEP < NF) {
-                const int i = (q - PRE) / RSTEP;
-                if (i < CT)
-                    fn[RT + i] = *(const v4i *)(pb + i * 2048);
-                else
-                    fn[i - CT] = *(const v4i *)(pa + (i - CT) * 2048);
-            }
+            if (q >= PRE && reads_by(q) > reads_by(q - 1)) read(step, reads_by(q - 1), ra, rb, fn);
+            if (q >= PRE && reads_by(q) > reads_by(q - 1) + 1) read(step, reads_by(q - 1) + 1, ra, rb, fn);
             if (q >= PRE && (q - PRE) % CSTEP == 0 && (q - PRE) / CSTEP < LPW)
                 asm volatile("s_add_i32 m0, %0, %1" ::"s"(cbase), "n"((q - PRE) / CSTEP * 1024) : "memory", "scc");
             if (q > PRE && (q - PRE - 1) % CSTEP == 0 && (q - PRE - 1) / CSTEP < LPW)
                 asm volatile("buffer_load_dwordx4 %0, %1, %2 offen lds" ::"v"(
-                                 off[(q - PRE - 1) / CSTEP & (SMALL ? 3 : 1)]),
-                             "s"(rs), "s"(SMALL ? 0u : (uint32_t)((q - PRE - 1) / CSTEP) * 8u * ld)
+                                 off[(q - PRE - 1) / CSTEP & (NOFF - 1)]),
+                             "s"(rs), "s"((uint32_t)((q - PRE - 1) / CSTEP) * (KM ? (uint32_t)RPC * ld : SMALL ? 0u : 8u * ld))
                              : "memory");
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -587,17 +667,18 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(8 / RT, 8 /
                 origin(nbid, na0, nb0, ntile_a, nsplit);
                 clamp_rows(na0, nb0);
                 next_k = SMALL ? nsplit * (int)ta.split_bytes : 0;
-                next_a = source_a(na0) + (uint32_t)next_k;
-                next_b = source_b(nb0) + (uint32_t)next_k;
+                next_a = source(kind_a, ta.A, na0, lda, next_k);
+                next_b = source(kind_b, ta.B, nb0, ldb, next_k);
             }
             src_a = next_a;
             src_b = next_b;
             src_k = next_k;
         }
-        half(first, I0{}, s0, s1, place ^ 64u, src_a, lda, lane_a, rows_a, s4, f0, f1);
-        half(I0{}, std::integral_constant<int, FIRST ? 2 : 1>{}, s2, s3, place, src_b, ldb, lane_b, rows_b, s0, f1, f0);
-        src_a += 128;
-        src_b += 128;
+        half(first, I0{}, s0, s1, Step1{}, kind_a, src_a, lda, lane_a, rows_a, s4, f0, f1);
+        half(I0{}, std::integral_constant<int, FIRST ? 2 : 1>{}, s2, s3, Step0{}, kind_b, src_b, ldb, lane_b, rows_b, s0, f1,
+             f0);
+        src_a += step_a;
+        src_b += step_b;
         src_k += 128;
         const uint32_t t0 = s0, t1 = s1;
         s0 = s2;
@@ -611,10 +692,11 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(8 / RT, 8 /
         for (int p = 1; p < rounds; ++p) round(I0{}, p);
         const TileWhere w = {(int64_t)a0 + wm * (SIDE / 2), (int64_t)b0 + wn * (SIDE / 2), (int64_t)tile_a * SIDE,
                              tile_a * 2 + wm, split};
-        if (!SMALL || (w.a0 + SIDE / 2 <= ta.na && w.b0 + SIDE / 2 <= ta.nb))
+        constexpr bool CUT = SMALL || ((KA || KB) && !Epi::PADDED);  // tiles may reach past the edges
+        if (!CUT || (w.a0 + SIDE / 2 <= ta.na && w.b0 + SIDE / 2 <= ta.nb))
             Epi::template run<M, RT, CT, false, !SMALL>(acc, w, ea);
         else if (w.a0 < ta.na && w.b0 < ta.nb)
-            Epi::template run<M, RT, CT, SMALL, !SMALL>(acc, w, ea);
+            Epi::template run<M, RT, CT, CUT, !SMALL>(acc, w, ea);
         bid = nbid;
         if (bid >= total) break;
         later = true;
@@ -1217,6 +1299,25 @@ inline int tile_splits(Tile tile, int64_t na, int64_t nb, int64_t kbytes) {
         }
     }
     return best;
+}
+
+// A product with K-major operands (see k_tile_p): no slices with p8.
+template <class M, class Epi, bool KA, bool KB>
+hipError_t launch_kmajor(TileArgs t, const typename Epi::Args &e, int splits, hipStream_t s) {
+    const bool large = splits == 1 && use_large_tile(t.na, t.nb);
+    const int side = large ? 256 : 128;
+    t.tiles_a = (int)((t.na + side - 1) / side);
+    t.tiles_b = (int)((t.nb + side - 1) / side);
+    t.splits = splits;
+    t.split_bytes = ((t.kbytes + splits - 1) / splits + 127) / 128 * 128;
+    const int64_t total = (int64_t)t.tiles_a * t.tiles_b * splits, cus = compute_units();
+    if (large)
+        hipLaunchKernelGGL((k_tile_p<M, Epi, 8, KA, KB>), dim3((unsigned)(total < cus ? total : cus)), dim3(256), 0, s, t,
+                           e);
+    else
+        hipLaunchKernelGGL((k_tile_p<M, Epi, 4, KA, KB>), dim3((unsigned)(total < 2 * cus ? total : 2 * cus)), dim3(256), 0,
+                           s, t, e);
+    return hipGetLastError();
 }
 
 // PAIRS: as choose_tile's, and then the kernels that cannot have pairs are not built.

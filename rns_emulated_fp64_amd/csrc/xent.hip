@@ -9,8 +9,8 @@
 // sum of exponentials of each token over the tile's vocabulary entries; one
 // more kernel joins these and computes the target's logit by itself. Backward:
 // z is computed again, a piece of the vocabulary at a time, and its epilogue
-// writes G in 16 bits for that piece alone; G and its transpose then meet the
-// transposes of W and X in two more products. The work is 2 T V d operations
+// writes G in 16 bits for that piece alone, which two more products take with W
+// and with X, read across their rows (k_tile_p's K-major operands). The work is 2 T V d operations
 // forward and 6 T V d backward (4 T V d without the second z), which the matrix
 // cores bound for all but a few tokens; for those it is the reading of W.
 #include <hip/hip_runtime.h>
@@ -36,6 +36,7 @@ struct EpiLse {
         int64_t na, nb;
     };
     static constexpr int STORES = 0;
+    static constexpr bool PADDED = false;
 
     template <class M, int RT, int CT, bool EDGE, bool AGPR = false>
     static __device__ __forceinline__ void run(v4i (&acc)[RT][CT], const TileWhere &w, const Args &e) {
@@ -133,6 +134,7 @@ struct EpiProb {
         int64_t na, nb;
     };
     static constexpr int STORES = 1;
+    static constexpr bool PADDED = false;
 
     template <class M, int RT, int CT, bool EDGE, bool AGPR = false>
     static __device__ __forceinline__ void run(v4i (&acc)[RT][CT], const TileWhere &w, const Args &e) {
@@ -175,6 +177,7 @@ struct EpiOut {
         int64_t na, nb;
     };
     static constexpr int STORES = sizeof(OutT) == 2 ? 1 : 2;
+    static constexpr bool PADDED = false;
 
     template <class M, int RT, int CT, bool EDGE, bool AGPR = false>
     static __device__ __forceinline__ void run(v4i (&acc)[RT][CT], const TileWhere &w, const Args &e) {
@@ -347,57 +350,6 @@ __global__ __launch_bounds__(1024) void k_xent_prepare(const float *__restrict__
     }
 }
 
-// out[c][r] = in[r][c] for 16-bit values, through a 64 x 64 tile in LDS.
-// Rows r in [rows, rows8) (rows8: up to the next multiple of 8) come out as
-// zeros, and with PAD the columns [cols, cols8) of `in` are set to zero, so that
-// products over either index may read whole 16-byte chunks. Rows whose g is 0
-// come out as zeros (g may be null). Memory bound.
-template <bool PAD>
-__global__ __launch_bounds__(256) void k_transpose16(uint16_t *in, int64_t ldi, int64_t rows, int64_t cols,
-                                                     uint16_t *__restrict__ out, int64_t ldo,
-                                                     const float *__restrict__ g) {
-    __shared__ uint16_t tile[64][66];  // 33 banks per row: columns are read without conflicts
-    const int64_t c0 = (int64_t)blockIdx.x * 64;
-    const int64_t rows8 = (rows + 7) & ~(int64_t)7, cols8 = (cols + 7) & ~(int64_t)7;
-    const int tid = threadIdx.x, tr = tid >> 3, tc = (tid & 7) * 8;
-    for (int64_t r0 = (int64_t)blockIdx.y * 64; r0 < rows8; r0 += (int64_t)gridDim.y * 64) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t r = r0 + tr + 32 * h, c = c0 + tc;
-            uint16_t e[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (r < rows && (g == nullptr || g[r] != 0.f)) {
-                if (c + 8 <= cols) {
-                    *(U16 *)e = *(const U16 *)(in + r * ldi + c);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (c + i < cols) e[i] = in[r * ldi + c + i];
-                }
-            }
-            if (PAD && r < rows && c < cols8 && c + 8 > cols)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (c + i >= cols && c + i < cols8) in[r * ldi + c + i] = 0;
-            uint32_t *dst = (uint32_t *)&tile[tr + 32 * h][tc];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) dst[i] = e[2 * i] | ((uint32_t)e[2 * i + 1] << 16);
-        }
-        __syncthreads();
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t c = c0 + tr + 32 * h, r = r0 + tc;
-            if (c < cols && r < rows8) {
-                v4i w;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    w[i] = tile[tc + 2 * i][tr + 32 * h] | ((int)tile[tc + 2 * i + 1][tr + 32 * h] << 16);
-                *(v4i *)(out + c * ldo + r) = w;  // ldo and r are multiples of 8
-            }
-        }
-        __syncthreads();
-    }
-}
-
 // Sums the planes of a product's slices, and the sum so far if there is one;
 // writes it back, or rounded and times *unit to `out`. Four values per thread,
 // slices in order.
@@ -522,29 +474,29 @@ int forward16(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const
 }
 
 // ---- backward ------------------------------------------------------------------------
-// Pitch in 16-bit elements of a workspace matrix: whole cache lines, an odd
-// number of them, so that the rows a tile reads at one k do not all lie in one
-// channel of the memory.
-int64_t pitch16(int64_t n) { return (((n + 63) / 64) | 1) * 64; }
+// Pitch in 16-bit elements of a workspace matrix (see pack_pitch).
+int64_t pitch16(int64_t n) { return pack_pitch(2 * n) / 2; }
 
 struct GradPlan {
     int64_t vc;           // vocabulary entries per piece
     int splits;           // slices of a piece in dX's product
     int64_t ldp, plane;   // pitch and size of dX's planes
-    size_t g, lse, unit, xt, wt, gm, gt, planes, sum, total;
+    size_t g, lse, unit, x, w, gm, planes, sum, total;
 };
-// G and its transpose take up to 2^28 entries each: 32768 vocabulary entries
-// at 8192 tokens, enough for the products over them to run at full rate.
+// G takes up to 2^28 entries: 32768 vocabulary entries at 8192 tokens, enough for
+// the products over them to run at full rate.
 constexpr int64_t kPieceEntries = (int64_t)1 << 28;
-GradPlan plan_grad(int64_t t, int64_t v, int64_t d, bool dx, bool dw) {
+constexpr int64_t kPieceMost = (int64_t)1 << 22;  // rows of G stay below 2^24 bytes
+GradPlan plan_grad(int64_t t, int64_t v, int64_t d, bool dx) {
     GradPlan p{};
     int64_t most = kPieceEntries / (t > 0 ? t : 1) / 256 * 256;
     if (most < 256) most = 256;
+    if (most > kPieceMost) most = kPieceMost;
     const int64_t pieces = (v + most - 1) / most;
     p.vc = ((v + pieces - 1) / pieces + 255) / 256 * 256;
     if (p.vc > v) p.vc = v;
     p.splits = use_large_tile(d, t) ? 1 : tile_splits(Tile::p4, d, t, 2 * ((p.vc + 7) / 8 * 8));
-    p.ldp = (d + 3) / 4 * 4;
+    p.ldp = (d + 7) / 8 * 8;
     p.plane = t * p.ldp;
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -552,31 +504,19 @@ GradPlan plan_grad(int64_t t, int64_t v, int64_t d, bool dx, bool dw) {
         off += up256(bytes);
         return at;
     };
-    const size_t st = (size_t)t, sd = (size_t)d, sv = (size_t)p.vc;
+    const size_t st = (size_t)t, sv = (size_t)p.vc;
     p.g = take(4 * st);
     p.lse = take(4 * st);
     p.unit = take(4);
     p.gm = take(2 * st * (size_t)pitch16(p.vc));
-    if (dw) {
-        p.xt = take(2 * sd * (size_t)pitch16(t));
-        p.gt = take(2 * sv * (size_t)pitch16(t));
-    }
+    p.x = take(2 * st * (size_t)pitch16(d));
+    p.w = take(2 * sv * (size_t)pitch16(d));  // for W in rows that are not aligned
     if (dx) {
-        p.wt = take(2 * sd * (size_t)pitch16(p.vc));
         p.planes = take(4 * (size_t)p.plane * (size_t)p.splits);
         p.sum = pieces > 1 ? take(4 * (size_t)p.plane) : 0;
     }
     p.total = off;
     return p;
-}
-
-template <bool PAD>
-hipError_t transpose16(void *in, int64_t ldi, int64_t rows, int64_t cols, void *out, int64_t ldo, const float *g,
-                       hipStream_t s) {
-    const int64_t by = (rows + 63) / 64;
-    hipLaunchKernelGGL((k_transpose16<PAD>), dim3((unsigned)((cols + 63) / 64), (unsigned)(by < 65535 ? by : 65535)),
-                       dim3(256), 0, s, (uint16_t *)in, ldi, rows, cols, (uint16_t *)out, ldo, g);
-    return hipGetLastError();
 }
 
 hipError_t zero_rows16(void *out, int64_t ldo, int64_t rows, int64_t cols, hipStream_t s) {
@@ -585,49 +525,55 @@ hipError_t zero_rows16(void *out, int64_t ldo, int64_t rows, int64_t cols, hipSt
     return hipGetLastError();
 }
 
-// A product whose k is not sliced, for an epilogue that takes pairs of tiles.
-template <class M, class Epi>
-hipError_t launch_whole(const TileArgs &ta, const typename Epi::Args &e, hipStream_t s) {
-    return launch_tile<M, Epi, true>(ta, e, choose_tile(ta, true), 1, s);
-}
-
 template <class M>
 int backward(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const void *W, int64_t ldw, const int64_t *y,
              int64_t ignore, const float *lse, const float *grad, void *dX, int64_t lddx, void *dW, int64_t lddw,
              char *ws, hipStream_t s) {
     typedef typename M::Elem T;
-    const GradPlan p = plan_grad(t, v, d, dX != nullptr, dW != nullptr);
+    const GradPlan p = plan_grad(t, v, d, dX != nullptr);
     float *g = (float *)(ws + p.g), *l = (float *)(ws + p.lse), *unit = (float *)(ws + p.unit);
-    T *gm = (T *)(ws + p.gm), *gt = (T *)(ws + p.gt), *xt = (T *)(ws + p.xt), *wt = (T *)(ws + p.wt);
+    T *gm = (T *)(ws + p.gm), *x = (T *)(ws + p.x);
     float *planes = (float *)(ws + p.planes), *sum = (float *)(ws + p.sum);
-    const int64_t ldg = pitch16(p.vc), ldt = pitch16(t);
-    const int64_t t8 = (t + 7) / 8 * 8;
-    hipLaunchKernelGGL(k_xent_prepare, dim3(1), dim3(1024), 0, s, grad, lse, y, ignore, t, v, M::HALF, g,
-                       l, unit);
+    const int64_t ldg = pitch16(p.vc), ldp = pitch16(d), d8 = (d + 7) / 8 * 8;
+    const bool aligned = (((uintptr_t)W | (uintptr_t)(2 * ldw) | (uintptr_t)(2 * d)) & 15) == 0 && 2 * ldw < (1 << 24);
+    hipLaunchKernelGGL(k_xent_prepare, dim3(1), dim3(1024), 0, s, grad, lse, y, ignore, t, v, M::HALF, g, l, unit);
     HIP_TRY(hipGetLastError());
-    if (dW) HIP_TRY(transpose16<false>((void *)X, ldx, t, d, xt, ldt, g, s));
+    // the rows of X, zeros for the tokens that take no part: what theirs hold must
+    // not meet the zeros of G
+    HIP_TRY(launch_pack_rows(X, 2 * ldx, t, 2 * d, x, 2 * ldp, g, s));
     for (int64_t v0 = 0; v0 < v; v0 += p.vc) {
         const int64_t vc = v - v0 < p.vc ? v - v0 : p.vc, v8 = (vc + 7) / 8 * 8;
-        const char *w = (const char *)W + v0 * ldw * 2;
-        HIP_TRY((launch_whole<M, EpiProb<T>>(rows_args<2>(t, vc, d, X, ldx, w, ldw), {gm, ldg, l, g, y, v0, vc, t}, s)));
+        const void *w = (const char *)W + v0 * ldw * 2;
+        int64_t ldv = ldw;
+        if (!aligned) {
+            HIP_TRY(launch_pack_rows(w, 2 * ldw, vc, 2 * d, ws + p.w, 2 * ldp, nullptr, s));
+            w = ws + p.w;
+            ldv = ldp;
+        }
+        TileArgs ta = rows_args<2>(t, vc, d8, x, ldp, w, ldv);
+        HIP_TRY((launch_tile<M, EpiProb<T>, true>(ta, {gm, ldg, l, g, y, v0, vc, t}, choose_tile(ta, true), 1, s)));
         if (dW) {
-            HIP_TRY(transpose16<true>(gm, ldg, t, vc, gt, ldt, nullptr, s));
-            HIP_TRY((launch_whole<M, EpiOut<T>>(rows_args<2>(vc, d, t8, gt, ldt, xt, ldt),
-                                                {(T *)dW + v0 * lddw, lddw, unit, d, vc}, s)));
+            // rows of X and of G as the rows of k
+            ta = rows_args<2>(vc, d, t, gm, ldg, x, ldp);
+            ta.krows = (int)t;
+            HIP_TRY((launch_kmajor<M, EpiOut<T>, true, true>(ta, {(T *)dW + v0 * lddw, lddw, unit, d, vc}, 1, s)));
         }
         if (dX) {
-            if (!dW && v8 > vc) HIP_TRY(zero_rows16(gm + vc, ldg, t, v8 - vc, s));
-            HIP_TRY(transpose16<false>((void *)w, ldw, vc, d, wt, ldg, nullptr, s));
-            const TileArgs ta = rows_args<2>(t, d, v8, gm, ldg, wt, ldg);
+            // rows of W as the rows of k; G's columns up to v8 meet zeros
+            if (v8 > vc) HIP_TRY(zero_rows16(gm + vc, ldg, t, v8 - vc, s));
+            ta = rows_args<2>(t, d, v8, gm, ldg, w, ldv);
+            ta.krows = (int)vc;
             const bool first = v0 == 0, last = v0 + vc == v;
             if (first && last && p.splits == 1) {
-                HIP_TRY((launch_whole<M, EpiOut<T>>(ta, {(T *)dX, lddx, unit, d, t}, s)));
+                HIP_TRY((launch_kmajor<M, EpiOut<T>, true, false>(ta, {(T *)dX, lddx, unit, d, t}, 1, s)));
             } else {
-                HIP_TRY((launch_tile<M, EpiRaw, true>(ta, {(uint32_t *)planes, p.ldp, p.plane, d, t},
-                                                      p.splits > 1 ? Tile::p4 : choose_tile(ta, true), p.splits, s)));
+                // (a short last piece has fewer slices: the rest of its planes are not read)
+                int splits = p.splits;
+                while (splits > 1 && v8 * 2 / splits < 512) splits /= 2;
+                HIP_TRY((launch_kmajor<M, EpiRaw, true, false>(ta, {(uint32_t *)planes, p.ldp, p.plane, d, t}, splits, s)));
                 hipLaunchKernelGGL((k_join_rows<T>), dim3((unsigned)((d + 1023) / 1024), (unsigned)(t < 65535 ? t : 65535)),
-                                   dim3(256), 0, s, planes, p.splits, p.plane, p.ldp, sum, !first,
-                                   last ? (T *)dX : nullptr, lddx, unit, d, t);
+                                   dim3(256), 0, s, planes, splits, p.plane, p.ldp, sum, !first, last ? (T *)dX : nullptr,
+                                   lddx, unit, d, t);
                 HIP_TRY(hipGetLastError());
             }
         }
@@ -743,14 +689,14 @@ int front_grad(GradCall c, bool cached, void *workspace, size_t bytes) {
     if (c.grad == nullptr && any) return -12;
     if (c.dX != nullptr && c.lddx < row) return -14;
     if (c.dW != nullptr && c.lddw < row) return -16;
-    if (c.t >= lim || c.v >= lim || c.d >= lim / 4) return OZAKI2_ERR_UNSUPPORTED;
+    if (c.t >= lim || c.v >= lim || c.d >= (int64_t)1 << 22) return OZAKI2_ERR_UNSUPPORTED;
     if (c.d == 0 || c.v == 0 || (c.dX == nullptr && c.dW == nullptr)) return OZAKI2_SUCCESS;
     if (!any) {
         // no token: nothing flows into W
         if (c.dW) HIP_TRY(zero_rows16(c.dW, c.lddw, c.v, c.d, c.s));
         return OZAKI2_SUCCESS;
     }
-    const size_t need = plan_grad(c.t, c.v, c.d, c.dX != nullptr, c.dW != nullptr).total;
+    const size_t need = plan_grad(c.t, c.v, c.d, c.dX != nullptr).total;
     if (cached) return with_workspace(need, c.s, run_grad, &c);
     if (workspace == nullptr || ((uintptr_t)workspace & (kWsAlign - 1)) != 0) return -17;
     if (bytes < need) return OZAKI2_ERR_WORKSPACE;
@@ -811,7 +757,7 @@ int ozaki2_xent_grad_ws(int64_t t, int64_t v, int64_t d, const void *X, int64_t 
                        (hipStream_t)stream}, false, workspace, workspace_bytes);
 }
 size_t ozaki2_xent_grad_workspace_size(int64_t t, int64_t v, int64_t d, int want_dx, int want_dw) {
-    return sizes_fit(t, v, d) && d > 0 && (want_dx || want_dw) ? plan_grad(t, v, d, want_dx != 0, want_dw != 0).total : 0;
+    return sizes_fit(t, v, d) && d > 0 && (want_dx || want_dw) ? plan_grad(t, v, d, want_dx != 0).total : 0;
 }
 
 }  // extern "C"

@@ -99,7 +99,7 @@ def test_xent_grad_refusals():
         assert oz.ozaki2_xent_grad(*with_arg(good, i, bad)) == -(i + 1), i
         assert oz.ozaki2_xent_grad_ws(*with_arg(good, i, bad), P, 1 << 40) == -(i + 1), i
     need = oz.ozaki2_xent_grad_workspace_size(5, 9, 16)
-    assert need > oz.ozaki2_xent_grad_workspace_size(5, 9, 16, want_dw=False) > 0
+    assert need > oz.ozaki2_xent_grad_workspace_size(5, 9, 16, want_dx=False) > 0
     assert oz.ozaki2_xent_grad_workspace_size(5, 9, 16, False, False) == 0
     assert oz.ozaki2_xent_grad_ws(*good, 0, need) == -17
     assert oz.ozaki2_xent_grad_ws(*good, P + 16, need) == -17
