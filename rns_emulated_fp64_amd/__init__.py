@@ -462,14 +462,24 @@ def _gemm(A, B, num_moduli, mode, out, workspace, kind):
 
 # ---- INT8 products with scales -----------------------------------------------
 BF16, FP16, FP32 = 0, 1, 2  # enum ozaki2_type
-_TYPES = {"torch.bfloat16": BF16, "torch.float16": FP16, "torch.float32": FP32}
+_types = {}  # torch dtype -> enum ozaki2_type, filled on the first call
+_torch = None
+
+
+def _load_torch():
+    global _torch
+    import torch
+
+    _types.update({torch.bfloat16: BF16, torch.float16: FP16, torch.float32: FP32})
+    _torch = torch
+    return torch
 
 
 def _type_of(dtype, what):
-    try:
-        return _TYPES[str(dtype)]
-    except KeyError:
-        raise TypeError(f"{what} must be bfloat16, float16 or float32, not {dtype}") from None
+    kind = _types.get(dtype)
+    if kind is None:
+        raise TypeError(f"{what} must be bfloat16, float16 or float32, not {dtype}")
+    return kind
 
 
 def _rows(x, what):
@@ -493,22 +503,19 @@ def _vector(x, n, dtype, device, what):
 
 def _call(fn, name, device, *args):
     """fn(*args, stream) on the current stream of a device, which the library needs to be the current one."""
-    import torch
-
     index = device.index
-    if index == torch.cuda.current_device():
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if index == _torch._C._cuda_getDevice():
+        st = fn(*args, _torch._C._cuda_getCurrentRawStream(index))
     else:
-        with torch.cuda.device(device):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+        with _torch.cuda.device(device):
+            st = fn(*args, _torch._C._cuda_getCurrentRawStream(index))
     if st:
         raise Ozaki2Error(st, name)
 
 
 def _workspace(size, given, device):
     """The caller's workspace or a new one from torch's allocator (which may be captured), its pointer and bytes."""
-    import torch
-
+    torch = _torch or _load_torch()
     if given is not None:
         if given.device != device:
             raise ValueError(f"workspace must be a tensor on {device}")
@@ -520,8 +527,7 @@ def _workspace(size, given, device):
 
 
 def _product_out(t, n, dtype, out, device):
-    import torch
-
+    torch = _torch or _load_torch()
     if out is None:
         return torch.empty((t, n), dtype=dtype, device=device), max(n, 1)
     if out.dtype != dtype or out.device != device or tuple(out.shape) != (t, n) or n > 1 and out.stride(1) != 1 \
@@ -534,8 +540,7 @@ def quantize_rows(X):
     """Rows of X (float32, float16 or bfloat16) as int8 with a binary32 scale each: (q, scale) with
     scale = max|x| / 127 and q = rint(x / scale), with the binary32 roundings that include/ozaki2.h states
     (ozaki2_quantize_rows)."""
-    import torch
-
+    torch = _torch or _load_torch()
     xtype = _type_of(X.dtype, "X")
     device = X.device
     if device.type != "cuda":
@@ -553,8 +558,7 @@ def i8gemm(A, B, a_scale, b_scale, bias=None, out_dtype=None, out=None, workspac
     """C[t, n] = (sum_k A[t, k] B[n, k]) * a_scale[t] * b_scale[n] + bias[n] for int8 A (t, k) and B (n, k), the
     layout of a linear layer (ozaki2_i8gemm_ws). The scales and the bias are float32; ``out_dtype`` is bfloat16
     (default), float16 or float32; ``workspace`` (optional) a tensor of ``ozaki2_i8gemm_workspace_size`` bytes."""
-    import torch
-
+    torch = _torch or _load_torch()
     dt = out_dtype if out_dtype is not None else out.dtype if out is not None else torch.bfloat16
     ctype = _type_of(dt, "out_dtype")
     device = A.device
@@ -582,8 +586,7 @@ def i8linear(X, B, b_scale, bias=None, out_dtype=None, out=None, workspace=None)
     """A linear layer with int8 weights B (n, k) and a scale per channel: the rows of X (t, k; bfloat16, float16 or
     float32) are quantised as quantize_rows does and multiplied as i8gemm does, bit for bit (ozaki2_i8linear_ws).
     The result has X's dtype unless ``out_dtype`` or ``out`` says otherwise."""
-    import torch
-
+    torch = _torch or _load_torch()
     xtype = _type_of(X.dtype, "X")
     dt = out_dtype if out_dtype is not None else out.dtype if out is not None else X.dtype
     ctype = _type_of(dt, "out_dtype")
@@ -609,8 +612,7 @@ def i8linear(X, B, b_scale, bias=None, out_dtype=None, out=None, workspace=None)
 
 # ---- linear cross entropy ----------------------------------------------------
 def _xent_operands(X, W, targets):
-    import torch
-
+    torch = _torch or _load_torch()
     device = X.device
     if device.type != "cuda" or W.device != device or targets.device != device:
         raise TypeError("X, W and targets must be on the same GPU")
@@ -630,8 +632,7 @@ def _xent_operands(X, W, targets):
 
 
 def _xent_type(X, W):
-    import torch
-
+    torch = _torch or _load_torch()
     if X.dtype not in (torch.bfloat16, torch.float16) or W.dtype != X.dtype:
         raise TypeError("X and W must both be bfloat16 or both float16")
     return BF16 if X.dtype == torch.bfloat16 else FP16
@@ -641,8 +642,7 @@ def xent(X, W, targets, ignore_index=-100, workspace=None):
     """Per token, the cross entropy of the logits X @ W.T against the target and their log-sum-exp, without storing
     the logits (ozaki2_xent_ws): (loss, lse), float32. X (t, d) and W (v, d) are bfloat16 or float16, targets (t,)
     int64. The loss is 0 where the target is ``ignore_index`` and NaN where it is out of range otherwise."""
-    import torch
-
+    torch = _torch or _load_torch()
     kind = _xent_type(X, W)
     device, t, v, d, X, ldx, W, ldw, targets = _xent_operands(X, W, targets)
     loss = torch.empty(t, dtype=torch.float32, device=device)
@@ -657,8 +657,7 @@ def xent(X, W, targets, ignore_index=-100, workspace=None):
 def i8xent(A, B, a_scale, b_scale, targets, ignore_index=-100, workspace=None):
     """xent for quantised features A (t, k) and weights B (v, k), int8 with float32 scales per row: the logits are
     those of i8gemm in binary32 (ozaki2_i8xent_ws). Returns (loss, lse)."""
-    import torch
-
+    torch = _torch or _load_torch()
     if A.dtype != torch.int8 or B.dtype != torch.int8:
         raise TypeError("A and B must be int8")
     device, t, v, k, A, lda, B, ldb, targets = _xent_operands(A, B, targets)
@@ -676,8 +675,7 @@ def i8xent(A, B, a_scale, b_scale, targets, ignore_index=-100, workspace=None):
 def xent_grad(X, W, targets, lse, grad_loss, ignore_index=-100, want_dx=True, want_dw=True, workspace=None):
     """(dX, dW), the gradients of sum(grad_loss * loss) for xent's loss, from the lse that xent returned
     (ozaki2_xent_grad_ws); None for one that is not wanted."""
-    import torch
-
+    torch = _torch or _load_torch()
     kind = _xent_type(X, W)
     device, t, v, d, X, ldx, W, ldw, targets = _xent_operands(X, W, targets)
     lse = _vector(lse, t, torch.float32, device, "lse")

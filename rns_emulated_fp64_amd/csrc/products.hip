@@ -103,8 +103,17 @@ __global__ __launch_bounds__(256) void k_join_scale(const int32_t *__restrict__ 
     const int64_t a = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
     if (a >= e.na) return;
     for (int64_t b = blockIdx.y; b < e.nb; b += gridDim.y) {
+        const int32_t *from = planes + b * ldp + a;
         v4i sum = {0, 0, 0, 0};
-        for (int i = 0; i < splits; ++i) sum += *(const v4i *)(planes + i * plane + b * ldp + a);
+        int i = 0;
+        for (; i + 4 <= splits; i += 4) {  // four loads on their way at a time
+            v4i o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = *(const v4i *)(from + (i + j) * plane);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sum += o[j];
+        }
+        for (; i < splits; ++i) sum += *(const v4i *)(from + i * plane);
         const float sb = e.sb[b];
 #pragma unroll
         for (int v = 0; v < 4; ++v)

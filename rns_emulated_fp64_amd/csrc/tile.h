@@ -136,6 +136,7 @@ struct TileArgs {
     int64_t kbytes;          // bytes of k per row
     int krows;               // K-major operands: rows of k (zeros beyond)
     int tiles_a, tiles_b;
+    int group;               // tiles of a per group (group_of)
     int splits;              // 128 x 128 tiles: slices of k, one block each
     int64_t split_bytes;     // bytes of k per slice (a multiple of 128)
 };
@@ -150,17 +151,25 @@ struct TileWhere {
 };
 
 // Block order: consecutive block ids go round-robin over the 8 XCDs; each XCD
-// gets one contiguous range of the logical order (groups of 4 tiles of a, all
-// tiles of b), so its L2 serves the panels its blocks share.
-__device__ __forceinline__ void tile_of(int bid, int total, int tiles_a, int tiles_b, int &ta, int &tb) {
+// gets one contiguous range of the logical order (groups of `group` tiles of a,
+// all tiles of b), so its L2 serves the panels its blocks share.
+__device__ __forceinline__ void tile_of(int bid, int total, int tiles_a, int tiles_b, int per_group, int &ta, int &tb) {
     const int per = total >> 3, rem = total & 7, x = bid & 7;
     const int lid = x * per + min(x, rem) + (bid >> 3);
-    const int group = 4 * tiles_b;
-    const int g = lid / group, first = 4 * g;
-    const int size = min(tiles_a - first, 4);
+    const int group = per_group * tiles_b;
+    const int g = lid / group, first = per_group * g;
+    const int size = min(tiles_a - first, per_group);
     const int in = lid - g * group;
     ta = first + in % size;
     tb = in / size;
+}
+// Tiles of a per group: 4 beside 8 or more tiles of b (about 32 blocks run on an
+// XCD); more beside fewer, which spreads what an XCD reads at a time over the
+// columns of K-major operands: rows a power of two apart put one tile's columns
+// in one channel of the L2 (dX of one token, W 32000 x 4096: 98 us with groups of 4).
+inline int group_of(int tiles_a, int tiles_b) {
+    const int g = 32 / tiles_b;
+    return g < 4 ? 4 : g < tiles_a ? g : tiles_a < 4 ? 4 : tiles_a;
 }
 
 // 16 bytes of a row from byte k on, zero from byte kb (the row's end) on. Any
@@ -467,7 +476,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(8 / RT, 8 /
     const uint32_t lda = (uint32_t)ta.lda, ldb = (uint32_t)ta.ldb;
     auto origin = [&](int b, int &a0, int &b0, int &tile_a, int &split) {
         int tb;
-        tile_of(b, total, ta.tiles_a, ta.tiles_b * (SMALL ? ta.splits : 1), tile_a, tb);
+        tile_of(b, total, ta.tiles_a, ta.tiles_b * (SMALL ? ta.splits : 1), ta.group, tile_a, tb);
         split = SMALL ? tb / ta.tiles_b : 0;
         if (SMALL) tb -= split * ta.tiles_b;
         a0 = tile_a * SIDE;
@@ -632,6 +641,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(8 / RT, 8 /
             // a tile's first half starts from zero
             acc[q / CT][q % CT] = M::mma(fc[q / CT], fc[RT + q % CT],
                                          decltype(first)::value ? (v4i){0, 0, 0, 0} : acc[q / CT][q % CT]);
+            if constexpr (decltype(first)::value) keep<!SMALL>(acc[q / CT][q % CT]);
             __builtin_amdgcn_sched_barrier(0);
             if (q == PRE - 1) {
                 if constexpr (SYNC == 1) copies_landed_barrier<LPW>();
@@ -728,7 +738,7 @@ __global__ __launch_bounds__(256) void k_tile_s(TileArgs ta, typename Epi::Args 
     const int wm = wave >> 1, wn = wave & 1;
     const uint32_t lda = (uint32_t)ta.lda, ldb = (uint32_t)ta.ldb;
     int tile_a, tile_b;
-    tile_of(blockIdx.x, ta.tiles_a * ta.tiles_b, ta.tiles_a, ta.tiles_b, tile_a, tile_b);
+    tile_of(blockIdx.x, ta.tiles_a * ta.tiles_b, ta.tiles_a, ta.tiles_b, ta.group, tile_a, tile_b);
     const int64_t a0 = (int64_t)tile_a * (32 * RT), b0 = (int64_t)tile_b * (32 * CT);
     const int k0 = (int)(blockIdx.y * ta.split_bytes);
     const int k1 = (int)min((int64_t)k0 + ta.split_bytes, ta.kbytes);
@@ -843,7 +853,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
     const int lane = threadIdx.x & 63;
     const int wm = wave >> 1, wn = wave & 1;
     int tile_a, tile_b;
-    tile_of(blockIdx.x, ta.tiles_a * ta.tiles_b, ta.tiles_a, ta.tiles_b, tile_a, tile_b);
+    tile_of(blockIdx.x, ta.tiles_a * ta.tiles_b, ta.tiles_a, ta.tiles_b, ta.group, tile_a, tile_b);
     const int64_t ta0 = (int64_t)tile_a * 128, tb0 = (int64_t)tile_b * 128;
     // this block's slice of k: bytes [k0, k1) of every row
     const int64_t k0 = (int64_t)blockIdx.y * ta.split_bytes;
@@ -1308,6 +1318,7 @@ hipError_t launch_kmajor(TileArgs t, const typename Epi::Args &e, int splits, hi
     const int side = large ? 256 : 128;
     t.tiles_a = (int)((t.na + side - 1) / side);
     t.tiles_b = (int)((t.nb + side - 1) / side);
+    t.group = group_of(t.tiles_a, t.tiles_b);
     t.splits = splits;
     t.split_bytes = ((t.kbytes + splits - 1) / splits + 127) / 128 * 128;
     const int64_t total = (int64_t)t.tiles_a * t.tiles_b * splits, cus = compute_units();
@@ -1326,6 +1337,7 @@ hipError_t launch_tile(TileArgs t, const typename Epi::Args &e, Tile tile, int s
     const TileShape shape = shape_of(tile);
     t.tiles_a = (int)((t.na + shape.a - 1) / shape.a);
     t.tiles_b = (int)((t.nb + shape.b - 1) / shape.b);
+    t.group = group_of(t.tiles_a, t.tiles_b);
     t.splits = splits;
     t.split_bytes = ((t.kbytes + splits - 1) / splits + 127) / 128 * 128;
     const int64_t total = (int64_t)t.tiles_a * t.tiles_b, cus = compute_units();

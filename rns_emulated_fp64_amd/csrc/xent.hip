@@ -211,7 +211,20 @@ struct DotFloat {
     // the part of X[t] . W[v] that lane `at` of n sums
     __device__ __forceinline__ float part(int64_t t, int64_t v, int at, int n) const {
         float s = 0.f;
-        for (int64_t k = 8 * at; k < d; k += 8 * n) {
+        int64_t k = 8 * at;
+        for (; k + 24 * n + 8 <= d; k += 32 * n) {  // eight loads on their way at a time
+            float x[4][8], w[4][8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                load8(X + t * ldx, k + 8 * n * j, d, x[j]);
+                load8(W + v * ldw, k + 8 * n * j, d, w[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s = fmaf(x[j][i], w[j][i], s);
+        }
+        for (; k < d; k += 8 * n) {
             float x[8], w[8];
             load8(X + t * ldx, k, d, x);
             load8(W + v * ldw, k, d, w);
@@ -320,30 +333,33 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
 // ---- backward: small kernels ---------------------------------------------------------
 // What the products need of each token: its g without the ignored ones, as a
 // multiple of *unit, and its lse (NaN for a target out of range). unit: a power
-// of two near the largest |g|, for fp16, whose range the G of a mean over many
-// tokens would leave; 1 for bf16. One block; NaN and Inf among the g pass
-// through with unit 1.
-__global__ __launch_bounds__(1024) void k_xent_prepare(const float *__restrict__ g, const float *__restrict__ lse,
-                                                       const int64_t *__restrict__ y, int64_t ignore, int64_t nt,
-                                                       int64_t nv, bool rescale, float *__restrict__ g_out,
-                                                       float *__restrict__ lse_out, float *__restrict__ unit) {
-    __shared__ uint32_t top[16];
-    uint32_t m = 0;
-    if (rescale)
-        for (int64_t t = threadIdx.x; t < nt; t += 1024)
+// of two near the largest |g|, for fp16 (RESCALE), whose range the G of a mean
+// over many tokens would leave; 1 for bf16. Every block finds that maximum for
+// itself, over all tokens: 12 bytes each, from the L2, against one more launch.
+template <bool RESCALE>
+__global__ __launch_bounds__(256) void k_xent_prepare(const float *__restrict__ g, const float *__restrict__ lse,
+                                                      const int64_t *__restrict__ y, int64_t ignore, int64_t nt,
+                                                      int64_t nv, float *__restrict__ g_out,
+                                                      float *__restrict__ lse_out, float *__restrict__ unit) {
+    float u = 1.f;
+    if constexpr (RESCALE) {
+        __shared__ uint32_t top[4];
+        uint32_t m = 0;
+        for (int64_t t = threadIdx.x; t < nt; t += 256)
             if (y[t] != ignore) m = max(m, abs_bits(g[t]));
 #pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
-    if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = m;
-    __syncthreads();
+        for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+        if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = m;
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = max(m, top[i]);
-    // the exponent alone; the smallest and largest binades keep unit 1
-    const uint32_t ex = m & 0x7f800000u;
-    const float u = ex >= 0x01000000u && ex < 0x7e000000u ? __uint_as_float(ex) : 1.f;
-    if (threadIdx.x == 0) *unit = u;
+        for (int i = 0; i < 4; ++i) m = max(m, top[i]);
+        // the exponent alone; the smallest and largest binades, Inf and NaN keep unit 1
+        const uint32_t ex = m & 0x7f800000u;
+        if (ex >= 0x01000000u && ex < 0x7e000000u) u = __uint_as_float(ex);
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *unit = u;
     const float up = 1.f / u;  // exact
-    for (int64_t t = threadIdx.x; t < nt; t += 1024) {
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < nt; t += (int64_t)gridDim.x * 256) {
         const int64_t v = y[t];
         g_out[t] = v == ignore ? 0.f : g[t] * up;
         lse_out[t] = v == ignore || (v >= 0 && v < nv) ? lse[t] : __uint_as_float(0x7fc00000u);
@@ -360,8 +376,17 @@ __global__ __launch_bounds__(256) void k_join_rows(const float *__restrict__ pla
     const int64_t a = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
     if (a >= na) return;
     for (int64_t b = blockIdx.y; b < nb; b += gridDim.y) {
-        v4f s = *(const v4f *)(planes + b * ldp + a);
-        for (int i = 1; i < splits; ++i) s += *(const v4f *)(planes + i * plane + b * ldp + a);
+        const float *from = planes + b * ldp + a;
+        v4f s = *(const v4f *)from;
+        int i = 1;
+        for (; i + 4 <= splits; i += 4) {  // four loads on their way at a time
+            v4f o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = *(const v4f *)(from + (i + j) * plane);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s += o[j];
+        }
+        for (; i < splits; ++i) s += *(const v4f *)(from + i * plane);
         if (add) s += *(const v4f *)(sum + b * ldp + a);
         if (out == nullptr) {
             *(v4f *)(sum + b * ldp + a) = s;
@@ -374,9 +399,10 @@ __global__ __launch_bounds__(256) void k_join_rows(const float *__restrict__ pla
     }
 }
 
+// A row per 8 lanes.
 __global__ __launch_bounds__(256) void k_zero_rows16(uint16_t *out, int64_t ldo, int64_t rows, int64_t cols) {
-    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
-        for (int64_t c = threadIdx.x; c < cols; c += 256) out[r * ldo + c] = 0;
+    for (int64_t r = (int64_t)blockIdx.x * 32 + (threadIdx.x >> 3); r < rows; r += (int64_t)gridDim.x * 32)
+        for (int64_t c = threadIdx.x & 7; c < cols; c += 8) out[r * ldo + c] = 0;
 }
 
 // ---- forward -------------------------------------------------------------------------
@@ -520,8 +546,8 @@ GradPlan plan_grad(int64_t t, int64_t v, int64_t d, bool dx) {
 }
 
 hipError_t zero_rows16(void *out, int64_t ldo, int64_t rows, int64_t cols, hipStream_t s) {
-    hipLaunchKernelGGL(k_zero_rows16, dim3((unsigned)(rows < 65535 ? rows : 65535)), dim3(256), 0, s, (uint16_t *)out, ldo,
-                       rows, cols);
+    hipLaunchKernelGGL(k_zero_rows16, dim3((unsigned)((rows + 31) / 32 < 65535 ? (rows + 31) / 32 : 65535)), dim3(256), 0, s,
+                       (uint16_t *)out, ldo, rows, cols);
     return hipGetLastError();
 }
 
@@ -536,7 +562,8 @@ int backward(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const 
     float *planes = (float *)(ws + p.planes), *sum = (float *)(ws + p.sum);
     const int64_t ldg = pitch16(p.vc), ldp = pitch16(d), d8 = (d + 7) / 8 * 8;
     const bool aligned = (((uintptr_t)W | (uintptr_t)(2 * ldw) | (uintptr_t)(2 * d)) & 15) == 0 && 2 * ldw < (1 << 24);
-    hipLaunchKernelGGL(k_xent_prepare, dim3(1), dim3(1024), 0, s, grad, lse, y, ignore, t, v, M::HALF, g, l, unit);
+    const unsigned blocks = (unsigned)((t + 255) / 256 < 32 ? (t + 255) / 256 : 32);
+    hipLaunchKernelGGL((k_xent_prepare<M::HALF>), dim3(blocks), dim3(256), 0, s, grad, lse, y, ignore, t, v, g, l, unit);
     HIP_TRY(hipGetLastError());
     // the rows of X, zeros for the tokens that take no part: what theirs hold must
     // not meet the zeros of G
