@@ -1169,23 +1169,26 @@ inline int64_t pack_rows(int64_t rows, int64_t kbytes) {
 }
 inline bool needs_pack(int64_t kbytes, int64_t nb) { return (kbytes & 15) != 0 && nb > 16; }
 
-// out[r][0 .. kbytes) = in[r], zeros to the next 16 bytes. Rows whose g is 0 are
-// zeros (g may be null). 16 bytes per lane and step, a wavefront per row.
+// out[r][0 .. kbytes) = in[r], zeros to the next 16 bytes; `copies` times, one after
+// another. Rows whose g is 0 are zeros (g may be null). 16 bytes per lane and
+// step, a wavefront per row.
 __global__ __launch_bounds__(256) static void k_pack_rows(const int8_t *__restrict__ in, int64_t ldi, int64_t rows,
                                                           int64_t kbytes, int8_t *__restrict__ out, int64_t ldo,
-                                                          const float *__restrict__ g) {
+                                                          const float *__restrict__ g, int copies) {
     const int lane = threadIdx.x & 63;
     for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < rows; r += (int64_t)gridDim.x * 4) {
         const bool zero = g != nullptr && g[r] == 0.f;
-        for (int64_t k = 16 * lane; k < kbytes; k += 1024)
-            *(v4i *)(out + r * ldo + k) = zero ? (v4i){0, 0, 0, 0} : load_chunk(in + r * ldi, k, kbytes);
+        for (int64_t k = 16 * lane; k < kbytes; k += 1024) {
+            const v4i e = zero ? (v4i){0, 0, 0, 0} : load_chunk(in + r * ldi, k, kbytes);
+            for (int c = 0; c < copies; ++c) *(v4i *)(out + (c * rows + r) * ldo + k) = e;
+        }
     }
 }
 inline hipError_t launch_pack_rows(const void *in, int64_t ldi, int64_t rows, int64_t kbytes, void *out, int64_t ldo,
-                                   const float *g, hipStream_t s) {
+                                   const float *g, hipStream_t s, int copies = 1) {
     const int64_t blocks = (rows + 3) / 4;
     hipLaunchKernelGGL(k_pack_rows, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, s, (const int8_t *)in, ldi,
-                       rows, kbytes, (int8_t *)out, ldo, g);
+                       rows, kbytes, (int8_t *)out, ldo, g, copies);
     return hipGetLastError();
 }
 
@@ -1253,10 +1256,10 @@ inline bool use_large_tile(int64_t na, int64_t nb) {
 //   - else the smallest tile that gives at most one block per compute unit: more
 //     would queue, and larger ones leave units idle (int8, 11008 x 4096, 64 rows:
 //     s21 17.6, s22 13.8, s42 18.7, p4 22.1 us; 4096 x 4096, 512 rows: s22 14.7, s42
-//     12.8, p4 18.0);
-//   - where even s42 gives more: with up to 64 rows of B the tile that covers them,
-//     so A is read once (bf16, 32000 x 4096, 1 row: 49.0 us or 5.3 TB/s; 64 rows: 54.8,
-//     against 61.2 with p4); else 128 x 128 or 256 x 256.
+//     12.8, p4 18.0); but no larger than covers up to 64 rows of B, so that A is
+//     read once by small blocks (bf16, 32000 x 4096, 1 row: s21 49.0 us or 5.3 TB/s,
+//     s42 57.8; 64 rows: s22 54.8, p4 61.2);
+//   - else 128 x 128 or 256 x 256.
 // OZ2_LINEAR_TILE=skinny, s11, s21, s22, s42, p4, p8 or any forces one where the
 // product allows it; results of int8 products do not depend on it.
 inline Tile choose_tile(const TileArgs &t, bool pairs) {
@@ -1277,10 +1280,9 @@ inline Tile choose_tile(const TileArgs &t, bool pairs) {
     if (!aligned) return can_skinny ? Tile::skinny : Tile::any;
     if (can_skinny && t.nb <= 16 && t.na <= 512 * 16) return Tile::skinny;
     if (!pairs && tiles_of(Tile::s11, t.na, t.nb) <= kPlanUnits) return Tile::s11;
-    for (Tile c : {Tile::s21, Tile::s22, Tile::s42})
-        if (tiles_of(c, t.na, t.nb) <= kPlanUnits) return c;
-    if (t.nb <= 32) return Tile::s21;
-    if (t.nb <= 64) return Tile::s22;
+    if (t.nb <= 32 || tiles_of(Tile::s21, t.na, t.nb) <= kPlanUnits) return Tile::s21;
+    if (t.nb <= 64 || tiles_of(Tile::s22, t.na, t.nb) <= kPlanUnits) return Tile::s22;
+    if (tiles_of(Tile::s42, t.na, t.nb) <= kPlanUnits) return Tile::s42;
     return use_large_tile(t.na, t.nb) ? Tile::p8 : Tile::p4;
 }
 // Wavefront ranges of A that an epilogue of this tile reports on.

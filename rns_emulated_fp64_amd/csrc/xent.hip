@@ -120,10 +120,12 @@ struct EpiLse {
 };
 
 // G for a piece of the vocabulary: out[b][a] = g[b] (exp(z - lse[b]) - [v0 + a = y[b]]),
-// rounded to 16 bits (relative error 2^-9 for bf16, 2^-12 for fp16, independent
-// from entry to entry, so the sums over many entries that follow see less of
-// it). A token whose g is 0 gets zeros whatever its logits are.
-template <class T>
+// rounded to 16 bits (half a step relative, independent from entry to entry, so
+// the sums over many entries that follow see less of it). A token whose g is 0
+// gets zeros. TWO: with few tokens a sum has few large entries and would show their
+// roundings, so what the rounding left follows in rows nb .. 2 nb - 1, in 16 bits
+// of its own.
+template <class T, bool TWO>
 struct EpiProb {
     struct Args {
         T *out;
@@ -143,10 +145,13 @@ struct EpiProb {
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
             const int64_t b = w.b0 + 16 * j + (lane & 15), at = EDGE && b >= e.nb ? e.nb - 1 : b;
-            const float shift = -e.lse[at] * kLog2e, g = e.g[at];
+            const float g = e.g[at];
+            // (exp2 of -inf is 0 for a token without a gradient)
+            const float shift = g == 0.f ? -INFINITY : -e.lse[at] * kLog2e;
             // the target's place among this lane's entries, in 16 i + v
             const int64_t y = e.y[at] - e.v0 - w.a0 - 4 * (lane >> 4);
-            const int hit = y >= 0 && y < 16 * RT && (y & 15) < 4 ? (int)y : -1;
+            int hit = y >= 0 && y < 16 * RT && (y & 15) < 4 ? (int)y : -1;
+            asm("" : "+v"(hit));  // 32-bit comparisons
 #pragma unroll
             for (int i = 0; i < RT; i += 2) {
                 keep<AGPR>(acc[i][j]);
@@ -158,9 +163,17 @@ struct EpiProb {
                     for (int v = 0; v < 4; ++v) {
                         float p = __builtin_amdgcn_exp2f(fmaf(M::value(acc[i + h][j][v]), kLog2e, shift));
                         p = hit == 16 * (i + h) + v ? p - 1.f : p;
-                        x[h][v] = g == 0.f ? 0.f : g * p;
+                        x[h][v] = g * p;
                     }
-                store_pair<T, EDGE>(x, e.out + b * e.ldo, st0 + 16 * i, e.na, b < e.nb);
+                T *row = e.out + b * e.ldo;
+                store_pair<T, EDGE>(x, row, st0 + 16 * i, e.na, b < e.nb);
+                if constexpr (TWO) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) x[h][v] -= (float)rounded<T>(x[h][v]);
+                    store_pair<T, EDGE>(x, row + e.nb * e.ldo, st0 + 16 * i, e.na, b < e.nb);
+                }
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
@@ -340,7 +353,8 @@ template <bool RESCALE>
 __global__ __launch_bounds__(256) void k_xent_prepare(const float *__restrict__ g, const float *__restrict__ lse,
                                                       const int64_t *__restrict__ y, int64_t ignore, int64_t nt,
                                                       int64_t nv, float *__restrict__ g_out,
-                                                      float *__restrict__ lse_out, float *__restrict__ unit) {
+                                                      float *__restrict__ lse_out, float *__restrict__ unit,
+                                                      uint16_t *__restrict__ pad, int64_t ldg, int cols, int64_t rows) {
     float u = 1.f;
     if constexpr (RESCALE) {
         __shared__ uint32_t top[4];
@@ -364,9 +378,13 @@ __global__ __launch_bounds__(256) void k_xent_prepare(const float *__restrict__ 
         g_out[t] = v == ignore ? 0.f : g[t] * up;
         lse_out[t] = v == ignore || (v >= 0 && v < nv) ? lse[t] : __uint_as_float(0x7fc00000u);
     }
+    // columns of G past its entries, up to the next multiple of 8
+    for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < rows; r += (int64_t)gridDim.x * 256)
+        for (int c = 0; c < cols; ++c) pad[r * ldg + c] = 0;
 }
 
-// Sums the planes of a product's slices, and the sum so far if there is one;
+// Sums the planes of a product's slices (and the parts of G, whose rows follow one
+// another in a plane), and the sum so far if there is one;
 // writes it back, or rounded and times *unit to `out`. Four values per thread,
 // slices in order.
 template <class T>
@@ -505,10 +523,14 @@ int64_t pitch16(int64_t n) { return pack_pitch(2 * n) / 2; }
 
 struct GradPlan {
     int64_t vc;           // vocabulary entries per piece
+    int parts;            // 16-bit values that hold an entry of G
     int splits;           // slices of a piece in dX's product
     int64_t ldp, plane;   // pitch and size of dX's planes
     size_t g, lse, unit, x, w, gm, planes, sum, total;
 };
+// Up to this many tokens G is held in two 16-bit parts. Memory bounds the products
+// there, so the second part costs little.
+constexpr int64_t kTwoParts = 64;
 // G takes up to 2^28 entries: 32768 vocabulary entries at 8192 tokens, enough for
 // the products over them to run at full rate.
 constexpr int64_t kPieceEntries = (int64_t)1 << 28;
@@ -521,9 +543,10 @@ GradPlan plan_grad(int64_t t, int64_t v, int64_t d, bool dx) {
     const int64_t pieces = (v + most - 1) / most;
     p.vc = ((v + pieces - 1) / pieces + 255) / 256 * 256;
     if (p.vc > v) p.vc = v;
-    p.splits = use_large_tile(d, t) ? 1 : tile_splits(Tile::p4, d, t, 2 * ((p.vc + 7) / 8 * 8));
+    p.parts = t <= kTwoParts ? 2 : 1;
+    p.splits = use_large_tile(d, p.parts * t) ? 1 : tile_splits(Tile::p4, d, p.parts * t, 2 * ((p.vc + 7) / 8 * 8));
     p.ldp = (d + 7) / 8 * 8;
-    p.plane = t * p.ldp;
+    p.plane = p.parts * t * p.ldp;
     size_t off = 0;
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -534,12 +557,12 @@ GradPlan plan_grad(int64_t t, int64_t v, int64_t d, bool dx) {
     p.g = take(4 * st);
     p.lse = take(4 * st);
     p.unit = take(4);
-    p.gm = take(2 * st * (size_t)pitch16(p.vc));
-    p.x = take(2 * st * (size_t)pitch16(d));
+    p.gm = take(2 * p.parts * st * (size_t)pitch16(p.vc));
+    p.x = take(2 * p.parts * st * (size_t)pitch16(d));
     p.w = take(2 * sv * (size_t)pitch16(d));  // for W in rows that are not aligned
     if (dx) {
         p.planes = take(4 * (size_t)p.plane * (size_t)p.splits);
-        p.sum = pieces > 1 ? take(4 * (size_t)p.plane) : 0;
+        p.sum = pieces > 1 ? take(4 * st * (size_t)p.ldp) : 0;
     }
     p.total = off;
     return p;
@@ -562,12 +585,15 @@ int backward(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const 
     float *planes = (float *)(ws + p.planes), *sum = (float *)(ws + p.sum);
     const int64_t ldg = pitch16(p.vc), ldp = pitch16(d), d8 = (d + 7) / 8 * 8;
     const bool aligned = (((uintptr_t)W | (uintptr_t)(2 * ldw) | (uintptr_t)(2 * d)) & 15) == 0 && 2 * ldw < (1 << 24);
+    const bool two = p.parts == 2;
+    const int64_t rows = p.parts * t;  // of G
     const unsigned blocks = (unsigned)((t + 255) / 256 < 32 ? (t + 255) / 256 : 32);
-    hipLaunchKernelGGL((k_xent_prepare<M::HALF>), dim3(blocks), dim3(256), 0, s, grad, lse, y, ignore, t, v, g, l, unit);
+    hipLaunchKernelGGL((k_xent_prepare<M::HALF>), dim3(blocks), dim3(256), 0, s, grad, lse, y, ignore, t, v, g, l, unit,
+                       (uint16_t *)gm + v, ldg, (int)((v + 7) / 8 * 8 - v), dX != nullptr && p.vc == v ? rows : 0);
     HIP_TRY(hipGetLastError());
     // the rows of X, zeros for the tokens that take no part: what theirs hold must
-    // not meet the zeros of G
-    HIP_TRY(launch_pack_rows(X, 2 * ldx, t, 2 * d, x, 2 * ldp, g, s));
+    // not meet the zeros of G; once for each part of G
+    HIP_TRY(launch_pack_rows(X, 2 * ldx, t, 2 * d, x, 2 * ldp, g, s, p.parts));
     for (int64_t v0 = 0; v0 < v; v0 += p.vc) {
         const int64_t vc = v - v0 < p.vc ? v - v0 : p.vc, v8 = (vc + 7) / 8 * 8;
         const void *w = (const char *)W + v0 * ldw * 2;
@@ -578,29 +604,34 @@ int backward(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const 
             ldv = ldp;
         }
         TileArgs ta = rows_args<2>(t, vc, d8, x, ldp, w, ldv);
-        HIP_TRY((launch_tile<M, EpiProb<T>, true>(ta, {gm, ldg, l, g, y, v0, vc, t}, choose_tile(ta, true), 1, s)));
+        if (two)
+            HIP_TRY((launch_tile<M, EpiProb<T, true>, true>(ta, {gm, ldg, l, g, y, v0, vc, t}, choose_tile(ta, true), 1, s)));
+        else
+            HIP_TRY((launch_tile<M, EpiProb<T, false>, true>(ta, {gm, ldg, l, g, y, v0, vc, t}, choose_tile(ta, true), 1,
+                                                             s)));
         if (dW) {
             // rows of X and of G as the rows of k
-            ta = rows_args<2>(vc, d, t, gm, ldg, x, ldp);
-            ta.krows = (int)t;
+            ta = rows_args<2>(vc, d, rows, gm, ldg, x, ldp);
+            ta.krows = (int)rows;
             HIP_TRY((launch_kmajor<M, EpiOut<T>, true, true>(ta, {(T *)dW + v0 * lddw, lddw, unit, d, vc}, 1, s)));
         }
         if (dX) {
             // rows of W as the rows of k; G's columns up to v8 meet zeros
-            if (v8 > vc) HIP_TRY(zero_rows16(gm + vc, ldg, t, v8 - vc, s));
-            ta = rows_args<2>(t, d, v8, gm, ldg, w, ldv);
+            if (v8 > vc && vc < v) HIP_TRY(zero_rows16(gm + vc, ldg, rows, v8 - vc, s));
+            ta = rows_args<2>(rows, d, v8, gm, ldg, w, ldv);
             ta.krows = (int)vc;
             const bool first = v0 == 0, last = v0 + vc == v;
-            if (first && last && p.splits == 1) {
+            if (first && last && p.splits == 1 && !two) {
                 HIP_TRY((launch_kmajor<M, EpiOut<T>, true, false>(ta, {(T *)dX, lddx, unit, d, t}, 1, s)));
             } else {
                 // (a short last piece has fewer slices: the rest of its planes are not read)
                 int splits = p.splits;
                 while (splits > 1 && v8 * 2 / splits < 512) splits /= 2;
-                HIP_TRY((launch_kmajor<M, EpiRaw, true, false>(ta, {(uint32_t *)planes, p.ldp, p.plane, d, t}, splits, s)));
+                HIP_TRY((launch_kmajor<M, EpiRaw, true, false>(ta, {(uint32_t *)planes, p.ldp, p.plane, d, rows}, splits,
+                                                               s)));
                 hipLaunchKernelGGL((k_join_rows<T>), dim3((unsigned)((d + 1023) / 1024), (unsigned)(t < 65535 ? t : 65535)),
-                                   dim3(256), 0, s, planes, splits, p.plane, p.ldp, sum, !first, last ? (T *)dX : nullptr,
-                                   lddx, unit, d, t);
+                                   dim3(256), 0, s, planes, p.parts * splits, t * p.ldp, p.ldp, sum, !first,
+                                   last ? (T *)dX : nullptr, lddx, unit, d, t);
                 HIP_TRY(hipGetLastError());
             }
         }
