@@ -166,9 +166,11 @@ __device__ __forceinline__ void tile_of(int bid, int total, int tiles_a, int til
 // Tiles of a per group: 4 beside 8 or more tiles of b (about 32 blocks run on an
 // XCD); more beside fewer, which spreads what an XCD reads at a time over the
 // columns of K-major operands: rows a power of two apart put one tile's columns
-// in one channel of the L2 (dX of one token, W 32000 x 4096: 98 us with groups of 4).
-inline int group_of(int tiles_a, int tiles_b) {
-    const int g = 32 / tiles_b;
+// in one channel of the L2 (dX of one token, W 32000 x 4096: 98 us with groups of 4,
+// 90 with 32). So do those of the output, which is most of what a short k moves (dW of
+// one token, 128000 x 4096: 503 us against 570).
+inline int group_of(int tiles_a, int tiles_b, int64_t kbytes) {
+    const int g = kbytes <= 256 ? 32 : 32 / tiles_b;
     return g < 4 ? 4 : g < tiles_a ? g : tiles_a < 4 ? 4 : tiles_a;
 }
 
@@ -1226,18 +1228,21 @@ inline int64_t tiles_of(Tile t, int64_t na, int64_t nb) {
 // Microseconds per round of 128 bytes of k that all tiles of a product take
 // side by side, without the start and the end of a block (measured, random
 // int8). The small tiles: latency, at most one block per compute unit. 128 x
-// 128: one block per unit, or two and then in proportion; 256 x 256: one.
+// 128: turns of two blocks per unit, 256 x 256: of one; a turn that is not full
+// costs less.
 inline double round_us(Tile tile, int64_t blocks) {
     switch (tile) {
     case Tile::s11: return 0.14;
     case Tile::s21: return 0.17;
     case Tile::s22: return 0.22;
     case Tile::s42: return 0.32;
-    case Tile::p8:
-        return (2 * blocks <= kPlanUnits ? 1.3 : 1.55) * (double)((blocks + kPlanUnits - 1) / kPlanUnits);
+    case Tile::p8: {
+        const int64_t rest = blocks % kPlanUnits;
+        return 1.55 * (double)(blocks / kPlanUnits) + (rest ? 1.25 + 0.3 * (double)rest / (double)kPlanUnits : 0.0);
+    }
     default: {
-        const double c = 0.58 * (double)blocks / (double)kPlanUnits;
-        return blocks <= kPlanUnits ? 0.62 : c > 0.9 ? c : 0.9;
+        const int64_t rest = blocks % (2 * kPlanUnits);
+        return 0.92 * (double)(blocks / (2 * kPlanUnits)) + (rest > kPlanUnits ? 0.92 : rest ? 0.68 : 0.0);
     }
     }
 }
@@ -1245,7 +1250,7 @@ inline double round_us(Tile tile, int64_t blocks) {
 // 56.8 us; 1536 rows, 258 tiles: 88.5 against 81.8).
 inline bool use_large_tile(int64_t na, int64_t nb) {
     if (na < 256 || nb < 256) return false;
-    return round_us(Tile::p8, tiles_of(Tile::p8, na, nb)) <= round_us(Tile::p4, tiles_of(Tile::p4, na, nb));
+    return round_us(Tile::p8, tiles_of(Tile::p8, na, nb)) <= 1.02 * round_us(Tile::p4, tiles_of(Tile::p4, na, nb));
 }
 
 // The kernel for a product whose k is not sliced. pairs: the epilogue needs two
@@ -1316,11 +1321,15 @@ inline int tile_splits(Tile tile, int64_t na, int64_t nb, int64_t kbytes) {
 // A product with K-major operands (see k_tile_p): no slices with p8.
 template <class M, class Epi, bool KA, bool KB>
 hipError_t launch_kmajor(TileArgs t, const typename Epi::Args &e, int splits, hipStream_t s) {
-    const bool large = splits == 1 && use_large_tile(t.na, t.nb);
+    bool large = splits == 1 && use_large_tile(t.na, t.nb);
+    if (const char *force = getenv("OZ2_LINEAR_TILE")) {
+        if (!strcmp(force, "p4")) large = false;
+        if (!strcmp(force, "p8") && splits == 1 && t.na >= 256 && t.nb >= 256) large = true;
+    }
     const int side = large ? 256 : 128;
     t.tiles_a = (int)((t.na + side - 1) / side);
     t.tiles_b = (int)((t.nb + side - 1) / side);
-    t.group = group_of(t.tiles_a, t.tiles_b);
+    t.group = group_of(t.tiles_a, t.tiles_b, t.kbytes);
     t.splits = splits;
     t.split_bytes = ((t.kbytes + splits - 1) / splits + 127) / 128 * 128;
     const int64_t total = (int64_t)t.tiles_a * t.tiles_b * splits, cus = compute_units();
@@ -1339,7 +1348,7 @@ hipError_t launch_tile(TileArgs t, const typename Epi::Args &e, Tile tile, int s
     const TileShape shape = shape_of(tile);
     t.tiles_a = (int)((t.na + shape.a - 1) / shape.a);
     t.tiles_b = (int)((t.nb + shape.b - 1) / shape.b);
-    t.group = group_of(t.tiles_a, t.tiles_b);
+    t.group = group_of(t.tiles_a, t.tiles_b, t.kbytes);
     t.splits = splits;
     t.split_bytes = ((t.kbytes + splits - 1) / splits + 127) / 128 * 128;
     const int64_t total = (int64_t)t.tiles_a * t.tiles_b, cus = compute_units();
