@@ -389,8 +389,8 @@ size_t ozaki2_debug_workspace_size(int64_t m, int64_t n, int64_t k, int num_modu
  *   C[i][j] = (sum_h A[i][h] B[j][h]) * a_scale[i] * b_scale[j] + bias[j]
  *
  *   t, n, k   rows of A (tokens), rows of B (channels), inner dimension; each
- *             >= 0, t and n < 2^31, k <= OZAKI2_I8_MAX_K (so that every int32
- *             sum is exact).
+ *             >= 0, t < 2^29, n < 2^23, k <= OZAKI2_I8_MAX_K (so that every
+ *             int32 sum is exact).
  *   A, lda    DEVICE int8, element (i, h) at A[i*lda + h], lda >= max(1, k).
  *   B, ldb    DEVICE int8, element (j, h) at B[j*ldb + h], ldb >= max(1, k).
  *   a_scale, b_scale   DEVICE binary32 [t], [n].
@@ -419,9 +419,9 @@ enum ozaki2_type {
  * Rows of X (type xtype, element (i, h) at X[i*ldx + h]) as int8 with a scale
  * each: amax = max_h |X[i][h]|, scale[i] = amax * (1/127) and
  * Q[i*ldq + h] = rint(X[i][h] * ((1/amax) * 127)), every operation rounded to
- * binary32 to nearest, ties to even. A row of zeros gets scale 0 and zeros; one whose amax is below
- * 2^-120 gets zeros; one that holds Inf or NaN gets zeros and a NaN scale, so
- * products with it are NaN. Returns 0, -1..-8 for an invalid argument,
+ * binary32 to nearest, ties to even. A row of zeros gets scale 0 and zeros; one
+ * whose amax is below 2^-120 gets zeros; one that holds Inf or NaN gets zeros
+ * and a NaN scale, so products with it are NaN. Returns 0, -1..-8 for an invalid argument,
  * OZAKI2_ERR_UNSUPPORTED (t or k >= 2^31) or OZAKI2_ERR_HIP. Capturable.
  */
 int ozaki2_quantize_rows(int64_t t, int64_t k, const void *X, int64_t ldx, int xtype, int8_t *Q, int64_t ldq,
@@ -471,8 +471,8 @@ int ozaki2_i8linear_ws(int64_t t, int64_t n, int64_t k, const void *X, int64_t l
  *   z[i][j] = sum_h X[i][h] W[j][h],   lse[i] = log sum_j exp(z[i][j]),
  *   loss[i] = lse[i] - z[i][targets[i]],  0 where targets[i] == ignore_index.
  *
- *   t, v, d   tokens, vocabulary entries, features; t, v < 2^31, d < 2^29;
- *             v >= 1 unless t == 0.
+ *   t, v, d   tokens, vocabulary entries, features; t < 2^31, v < 2^23, d < 2^29
+ *             (gradients: t < 2^29, d < 2^22); v >= 1 unless t == 0.
  *   X, ldx    DEVICE, element (i, h) at X[i*ldx + h], ldx >= max(1, d).
  *   W, ldw    DEVICE, element (j, h) at W[j*ldw + h], ldw >= max(1, d).
  *   type      of X, W and the gradients: OZAKI2_BF16 or OZAKI2_FP16.

@@ -22,68 +22,73 @@ namespace {
 // read once; longer rows are read twice, the second time mostly from the L2.
 // Memory bound.
 constexpr int kQuantThreads = 256;
+constexpr int64_t kQuantBlocks = (int64_t)1 << 20;
 template <class T, int NV>
-__global__ __launch_bounds__(kQuantThreads) void k_quantize_rows(const T *__restrict__ X, int64_t ldx, int64_t k,
+__global__ __launch_bounds__(kQuantThreads) void k_quantize_rows(const T *__restrict__ X, int64_t ldx,
+                                                                 int64_t rows, int64_t k,
                                                                  int8_t *__restrict__ Q, int64_t ldq,
                                                                  float *__restrict__ scale) {
     __shared__ uint32_t top[kQuantThreads / 64];
-    const int64_t r = blockIdx.x;
-    const T *x = X + r * ldx;
-    int8_t *q = Q + r * ldq;
     const int t = threadIdx.x;
     constexpr int64_t STEP = 8 * kQuantThreads;
-    float keep[NV][8];
-    uint32_t m = 0;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
+        const T *x = X + r * ldx;
+        int8_t *q = Q + r * ldq;
+        float keep[NV][8];
+        uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) load8(x, 8 * t + i * STEP, k, keep[i]);
+        for (int i = 0; i < NV; ++i) load8(x, 8 * t + i * STEP, k, keep[i]);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(keep[i][j]));
-    for (int64_t at = 8 * t + NV * STEP; at < k; at += STEP) {
-        float e[8];
-        load8(x, at, k, e);
+            for (int j = 0; j < 8; ++j) m = max(m, abs_bits(keep[i][j]));
+        for (int64_t at = 8 * t + NV * STEP; at < k; at += STEP) {
+            float e[8];
+            load8(x, at, k, e);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m = max(m, abs_bits(e[j]));
-    }
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
-    if ((t & 63) == 0) top[t >> 6] = m;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kQuantThreads / 64; ++i) m = max(m, top[i]);
-    float s, up;
-    row_scale(m, s, up);
-    if (t == 0) scale[r] = s;
-    auto put = [&](int64_t at, const float(&e)[8]) {
-        const U8 u = quantised8(e, up);
-        if (at + 8 <= k) {
-            *(U8 *)(q + at) = u;
-        } else {
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (at + j < k) q[at + j] = (int8_t)(u.w[j >> 2] >> (8 * (j & 3)));
+            for (int j = 0; j < 8; ++j) m = max(m, abs_bits(e[j]));
         }
-    };
 #pragma unroll
-    for (int i = 0; i < NV; ++i) put(8 * t + i * STEP, keep[i]);
-    for (int64_t at = 8 * t + NV * STEP; at < k; at += STEP) {
-        float e[8];
-        load8(x, at, k, e);
-        put(at, e);
+        for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+        if (r != blockIdx.x) __syncthreads();  // the maxima of the row before have been read
+        if ((t & 63) == 0) top[t >> 6] = m;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kQuantThreads / 64; ++i) m = max(m, top[i]);
+        float s, up;
+        row_scale(m, s, up);
+        if (t == 0) scale[r] = s;
+        auto put = [&](int64_t at, const float(&e)[8]) {
+            const U8 u = quantised8(e, up);
+            if (at + 8 <= k) {
+                *(U8 *)(q + at) = u;
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (at + j < k) q[at + j] = (int8_t)(u.w[j >> 2] >> (8 * (j & 3)));
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < NV; ++i) put(8 * t + i * STEP, keep[i]);
+        for (int64_t at = 8 * t + NV * STEP; at < k; at += STEP) {
+            float e[8];
+            load8(x, at, k, e);
+            put(at, e);
+        }
     }
 }
 
 template <class T>
 hipError_t launch_quantize_rows_t(const T *X, int64_t ldx, int64_t t, int64_t k, int8_t *Q, int64_t ldq, float *scale,
                                   hipStream_t s) {
-    // a grid's x dimension holds 2^31 - 1 blocks, so one launch takes every row
+    // (a launch holds less than 2^32 threads)
+    const dim3 grid((unsigned)(t < kQuantBlocks ? t : kQuantBlocks));
     if (k <= 8 * kQuantThreads)
-        hipLaunchKernelGGL((k_quantize_rows<T, 1>), dim3((unsigned)t), dim3(kQuantThreads), 0, s, X, ldx, k, Q, ldq, scale);
+        hipLaunchKernelGGL((k_quantize_rows<T, 1>), grid, dim3(kQuantThreads), 0, s, X, ldx, t, k, Q, ldq, scale);
     else if (k <= 2 * 8 * kQuantThreads)
-        hipLaunchKernelGGL((k_quantize_rows<T, 2>), dim3((unsigned)t), dim3(kQuantThreads), 0, s, X, ldx, k, Q, ldq, scale);
+        hipLaunchKernelGGL((k_quantize_rows<T, 2>), grid, dim3(kQuantThreads), 0, s, X, ldx, t, k, Q, ldq, scale);
     else
-        hipLaunchKernelGGL((k_quantize_rows<T, 4>), dim3((unsigned)t), dim3(kQuantThreads), 0, s, X, ldx, k, Q, ldq, scale);
+        hipLaunchKernelGGL((k_quantize_rows<T, 4>), grid, dim3(kQuantThreads), 0, s, X, ldx, t, k, Q, ldq, scale);
     return hipGetLastError();
 }
 
@@ -253,8 +258,7 @@ hipError_t few_rows(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx,
 // ---- checks ---------------------------------------------------------------------------
 bool is_type(int type) { return type == OZAKI2_BF16 || type == OZAKI2_FP16 || type == OZAKI2_FP32; }
 bool fits(int64_t t, int64_t n, int64_t k) {
-    const int64_t lim = (int64_t)1 << 31;
-    return t < lim && n < lim && k <= OZAKI2_I8_MAX_K;
+    return t < kMostTokens && n < kMostChannels && k <= OZAKI2_I8_MAX_K;
 }
 
 // Argument checks of ozaki2_i8gemm in signature order.

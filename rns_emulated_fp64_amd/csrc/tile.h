@@ -60,6 +60,12 @@ inline size_t up256(size_t v) { return (v + kWsAlign - 1) / kWsAlign * kWsAlign;
 // Tokens up to which the weights are streamed by k_skinny.
 constexpr int64_t kSkinnyRows = 64;
 
+// Rows of A (channels, vocabulary entries) and of B (tokens) stay below these, so
+// that row numbers are ints and a launch has less than 2^32 threads whatever its
+// tile: a result of t x n entries that fits 288 GB has fewer than 2^24 tiles of 128 x
+// 128, and so have the runs of 16384 tokens whose results are not stored.
+constexpr int64_t kMostChannels = (int64_t)1 << 23, kMostTokens = (int64_t)1 << 29;
+
 // ---- element types ---------------------------------------------------------
 // BYTES per element, the MFMA of one 64-byte step of k, and the accumulator
 // bits read as a float.
@@ -436,11 +442,12 @@ __device__ __forceinline__ void copies_landed_barrier() {
 // 16 columns of 4).
 //
 // Edges: a last tile that would reach past na or nb is moved back to end
-// there (na, nb >= 256), so every access is in bounds and (but for K-major operands,
-// which it is moved in steps of 8) no store is conditional; rows that two tiles cover get the same values twice (or the
-// epilogue looks at amin). k is padded to whole rounds: a lane whose 16 bytes
-// lie past the end of the row asks for an offset outside the copy's buffer, and
-// such loads return zeros.
+// there (na, nb >= 256), so every access is in bounds and no store is conditional
+// (with K-major operands it is moved back by a multiple of 8, and what still reaches
+// past the edge is not stored); rows that two tiles cover get the same values twice
+// (or the epilogue looks at amin). k is padded to whole rounds: a lane whose 16
+// bytes lie past the end of the row asks for an offset outside the copy's buffer,
+// and such loads return zeros.
 //
 // Requires: rows, pitches and kbytes multiples of 16 bytes, lda, ldb < 2^24,
 // na, nb >= 256, 0 < kbytes < 2^30, tiles < 2^31; slices of k of at least 256 bytes;

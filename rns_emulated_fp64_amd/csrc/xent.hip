@@ -62,13 +62,14 @@ struct EpiLse {
         for (int j = 0; j < CT; ++j) {
             const int64_t b = w.b0 + 16 * j + (lane & 15);
             // SCALED: z = (sum * sa) * sb; the entries are kept as sum * sa, with the
-            // sign of sb, and |sb| goes into the exponentials' factor
-            float unit = 1.f;
-            bool flip = false;
+            // sign of sb, and |sb| goes into the exponentials' factor. For sb = 0 they
+            // are zeros in units of 1 (a factor of 0 would make NaN of the -inf of
+            // entries that are cut off)
+            float unit = 1.f, sign = 1.f;
             if constexpr (SCALED) {
                 const float sb = e.sb[EDGE && b >= e.nb ? e.nb - 1 : b];
-                unit = fabsf(sb);
-                flip = sb < 0.f;
+                unit = sb == 0.f ? 1.f : fabsf(sb);
+                sign = sb == 0.f ? 0.f : sb < 0.f ? -1.f : 1.f;
             }
             float z[RT][4], m = -INFINITY;
 #pragma unroll
@@ -80,11 +81,11 @@ struct EpiLse {
                     if constexpr (SCALED) z[i][v] *= sa[i][v];
                 }
             }
-            if (SCALED && __any(flip)) {
+            if (SCALED && __any(sign != 1.f)) {
 #pragma unroll
                 for (int i = 0; i < RT; ++i)
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) z[i][v] = flip ? -z[i][v] : z[i][v];
+                    for (int v = 0; v < 4; ++v) z[i][v] *= sign;
             }
             if (cut) {
 #pragma unroll
@@ -672,7 +673,8 @@ int run_xent(void *ctx, char *ws) {
 // After the argument checks; bad_ws: the status of a bad workspace argument.
 int launch(XentCall c, bool cached, void *workspace, size_t bytes, int bad_ws) {
     const int64_t lim = (int64_t)1 << 31;
-    if (c.t >= lim || c.v >= lim || c.d >= (c.type < 0 ? (int64_t)OZAKI2_I8_MAX_K + 1 : lim / 4)) return OZAKI2_ERR_UNSUPPORTED;
+    if (c.t >= lim || c.v >= kMostChannels || c.d >= (c.type < 0 ? (int64_t)OZAKI2_I8_MAX_K + 1 : lim / 4))
+        return OZAKI2_ERR_UNSUPPORTED;
     if (c.t == 0) return OZAKI2_SUCCESS;
     const size_t need = plan_forward(c.t, c.v, c.type < 0 ? c.d : 2 * c.d).total;
     if (cached) return with_workspace(need, c.s, run_xent, &c);
@@ -714,6 +716,11 @@ int front_i8xent(const XentCall &c, bool cached, void *workspace, size_t bytes) 
     return launch(c, cached, workspace, bytes, -14);
 }
 
+// Rows of X and W in the workspace of less than 2^24 bytes, G of less than 2^30.
+bool grad_fits(int64_t t, int64_t v, int64_t d) {
+    return t < kMostTokens && v < kMostChannels && d < (int64_t)1 << 22;
+}
+
 struct GradCall {
     int64_t t, v, d, ldx, ldw, lddx, lddw;
     const void *X, *W;
@@ -733,7 +740,7 @@ int run_grad(void *ctx, char *ws) {
 }
 int front_grad(GradCall c, bool cached, void *workspace, size_t bytes) {
     const bool any = c.t > 0;
-    const int64_t row = c.d > 1 ? c.d : 1, lim = (int64_t)1 << 31;
+    const int64_t row = c.d > 1 ? c.d : 1;
     if (c.t < 0) return -1;
     if (c.v < 0 || (c.v == 0 && any)) return -2;
     if (c.d < 0) return -3;
@@ -747,7 +754,7 @@ int front_grad(GradCall c, bool cached, void *workspace, size_t bytes) {
     if (c.grad == nullptr && any) return -12;
     if (c.dX != nullptr && c.lddx < row) return -14;
     if (c.dW != nullptr && c.lddw < row) return -16;
-    if (c.t >= lim || c.v >= lim || c.d >= (int64_t)1 << 22) return OZAKI2_ERR_UNSUPPORTED;
+    if (!grad_fits(c.t, c.v, c.d)) return OZAKI2_ERR_UNSUPPORTED;
     if (c.d == 0 || c.v == 0 || (c.dX == nullptr && c.dW == nullptr)) return OZAKI2_SUCCESS;
     if (!any) {
         // no token: nothing flows into W
@@ -763,7 +770,7 @@ int front_grad(GradCall c, bool cached, void *workspace, size_t bytes) {
 
 bool sizes_fit(int64_t t, int64_t v, int64_t d) {
     const int64_t lim = (int64_t)1 << 31;
-    return t > 0 && v > 0 && d >= 0 && t < lim && v < lim && d < lim / 4;
+    return t > 0 && v > 0 && d >= 0 && t < lim && v < kMostChannels && d < lim / 4;
 }
 
 }  // namespace
@@ -815,7 +822,7 @@ int ozaki2_xent_grad_ws(int64_t t, int64_t v, int64_t d, const void *X, int64_t 
                        (hipStream_t)stream}, false, workspace, workspace_bytes);
 }
 size_t ozaki2_xent_grad_workspace_size(int64_t t, int64_t v, int64_t d, int want_dx, int want_dw) {
-    return sizes_fit(t, v, d) && d > 0 && (want_dx || want_dw) ? plan_grad(t, v, d, want_dx != 0).total : 0;
+    return sizes_fit(t, v, d) && grad_fits(t, v, d) && d > 0 && (want_dx || want_dw) ? plan_grad(t, v, d, want_dx != 0).total : 0;
 }
 
 }  // extern "C"

@@ -149,7 +149,8 @@ def quantised(x):
     return torch.round(x * up[:, None]).to(torch.int8), scale
 
 
-@pytest.mark.parametrize("t,k", [(1, 1), (3, 7), (5, 64), (2, 4096), (17, 2049), (4, 8193), (3, 20000), (1000, 512)])
+@pytest.mark.parametrize("t,k", [(1, 1), (3, 7), (5, 64), (2, 4096), (17, 2049), (4, 8193), (3, 20000), (1000, 512),
+                                 ((1 << 20) + 300, 5)])  # the last: more rows than blocks
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.float16])
 def test_quantize_rows(t, k, dtype):
     x = (torch.randn(t, k + 3, generator=gen(t + k), device="cuda") * torch.rand(t, 1, generator=gen(1), device="cuda")).to(dtype)

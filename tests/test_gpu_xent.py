@@ -149,6 +149,24 @@ def test_int8_loss(t, v, k):
     near(loss, e["loss"], 2 * e["tol"], "loss")
 
 
+@pytest.mark.parametrize("tile", ("",) + TILES)
+@pytest.mark.parametrize("t,v", [(3, 37), (40, 300), (300, 557), (300, 700)])
+def test_int8_rows_of_scale_zero(t, v, tile, monkeypatch):
+    # a row of zeros is quantised with scale 0 (and -0 is one too): its logits are all 0, so its loss is log v,
+    # beside tiles that reach past the vocabulary's end
+    X, W, y, _ = operands(t, v, 64, torch.bfloat16, t, skip=0)
+    X[::2] = 0
+    A, sa = oz.quantize_rows(X)
+    B, sb = oz.quantize_rows(W)
+    A[2::4] = 1  # values that the scale alone takes away
+    sa[2::4] = -0.0
+    e = exact(A, B, y, None, sa, sb)
+    monkeypatch.setenv("OZ2_LINEAR_TILE", tile)
+    loss, lse = oz.i8xent(A, B, sa, sb, y)
+    near(lse, e["lse"], e["tol"], "lse")
+    near(loss, e["loss"], 2 * e["tol"], "loss")
+
+
 def test_loss_chain_of_quantised_layers():
     # as they are used together: a quantised layer, then the loss of an output layer and its gradients, and the
     # quantised form of that layer

@@ -108,6 +108,23 @@ def test_xent_grad_refusals():
     assert oz.ozaki2_xent_grad(*good[:12], 0, 0, 0, 0) == 0
 
 
+def test_limits():
+    # sizes whose launches or row numbers would leave their range are refused, with workspaces of 0 bytes
+    t, n = 1 << 29, 1 << 23
+    gemm = (P, 16, P, P, 16, P, 0, P)
+    assert oz.ozaki2_i8gemm(t, 6, 16, *gemm, 6, oz.BF16) == 3
+    assert oz.ozaki2_i8gemm(4, n, 16, *gemm, n, oz.BF16) == 3
+    assert oz.ozaki2_i8linear(t, 6, 16, P, 16, oz.BF16, *gemm[3:], 6, oz.BF16) == 3
+    assert oz.ozaki2_i8linear(4, n, 16, P, 16, oz.BF16, *gemm[3:], n, oz.BF16) == 3
+    assert oz.ozaki2_xent(5, n, 16, P, 16, P, 16, oz.BF16, P, -100, P, P) == 3
+    assert oz.ozaki2_i8xent(5, n, 16, P, 16, P, P, 16, P, P, -100, P, P) == 3
+    for a, b, d in ((t, 9, 16), (5, n, 16), (5, 9, 1 << 22)):
+        assert oz.ozaki2_xent_grad(a, b, d, P, d, P, d, oz.FP16, P, -100, P, P, P, d, P, d) == 3
+        assert oz.ozaki2_xent_grad_workspace_size(a, b, d) == 0
+    assert oz.ozaki2_i8gemm_workspace_size(t, 6, 15) == oz.ozaki2_i8linear_workspace_size(9, n, 16) == 0
+    assert oz.ozaki2_xent_workspace_size(5, n, 16) == oz.ozaki2_i8xent_workspace_size(5, n, 16) == 0
+
+
 def test_workspace_sizes():
     # sizes grow with the problem, stay small beside the logits, and are 0 for what is refused
     big = oz.ozaki2_xent_workspace_size(8192, 128000, 4096)
