@@ -201,7 +201,7 @@ int product_t(Product p, bool own_a, char *ws, hipStream_t s) {
     if (!needs_pack(p.k, p.t)) return product_rows<OutT>(p, ws, s);
     const int64_t pitch = pack_pitch(p.k), run = pack_rows(p.n, p.k), k16 = (p.k + 15) / 16 * 16;
     if (!own_a) {
-        HIP_TRY(launch_pack_rows(p.A, p.lda, p.t, p.k, ws, pitch, nullptr, s));
+        HIP_TRY(launch_pack_rows(p.A, p.lda, p.t, p.k, ws, pitch, s));
         p.A = (const int8_t *)ws;
         p.lda = pitch;
         ws += up256((size_t)p.t * (size_t)pitch);
@@ -216,7 +216,7 @@ int product_t(Product p, bool own_a, char *ws, hipStream_t s) {
         q.b_scale += n0;
         if (q.bias) q.bias += n0;
         q.C = (OutT *)p.C + n0;
-        HIP_TRY(launch_pack_rows(p.B + n0 * p.ldb, p.ldb, q.n, p.k, ws, pitch, nullptr, s));
+        HIP_TRY(launch_pack_rows(p.B + n0 * p.ldb, p.ldb, q.n, p.k, ws, pitch, s));
         const int st = product_rows<OutT>(q, planes, s);
         if (st) return st;
     }

@@ -10,7 +10,7 @@
 // probabilities. "a" is the operand whose index is contiguous in the output
 // (weight channels, vocabulary entries), "b" the other one (tokens).
 //
-// Four kernels share the fragment layout (the operand order of the
+// Five kernels share the fragment layout (the operand order of the
 // 16 x 16 x 64-byte MFMAs: lane L holds row L % 16 and bytes 16 (L / 16) ..
 // + 15 of a 64-byte step of k; in the result lane L holds rows 4 (L / 16) .. + 3
 // of column L % 16):
@@ -18,6 +18,7 @@
 //               128 x 128 tiles, two blocks per compute unit, with slices of k
 //   k_tile_any  128 x 128 tiles at any alignment
 //   k_tile_s    smaller tiles with a deeper ring: few rows
+//   k_tile_short  128 x 128 tiles of K-major operands with few rows of k
 //   k_skinny    up to 64 rows of B at any alignment, without LDS copies
 #pragma once
 
@@ -847,6 +848,82 @@ __global__ __launch_bounds__(256) void k_tile_s(TileArgs ta, typename Epi::Args 
         Epi::template run<M, RT, CT, true>(acc, w, ea);
 }
 
+// ---- K-major operands with few rows of k ------------------------------------------
+// One 128 x 128 tile per block, for outer products of few rows (a gradient of
+// weights from few tokens), which the stores of R bound: k_tile_p's ring would make
+// a tile's first copies wait for the stores of the tile before, with two blocks per
+// compute unit. Here four blocks fit, and each ends with its stores on their way
+// (dW, bf16, 32000 x 4096: one token 42 us or 6.2 TB/s, 16 tokens 54, against 68 with
+// k_tile_p). 64 rows of k at a time pass through registers into LDS, in
+// k_tile_p's K-major order, and are read as there.
+template <class M, class Epi>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4, 4))) void k_tile_short(TileArgs ta,
+                                                                                               typename Epi::Args ea) {
+    constexpr int RT = 4, CT = 4, ROWB = 256, UNIT = 64 * ROWB;
+    __shared__ __attribute__((aligned(1024))) int8_t lds[2 * UNIT];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int lane = threadIdx.x & 63;
+    const int wm = wave >> 1, wn = wave & 1;
+    int tile_a, tile_b;
+    tile_of(blockIdx.x, ta.tiles_a * ta.tiles_b, ta.tiles_a, ta.tiles_b, ta.group, tile_a, tile_b);
+    const int64_t a0 = (int64_t)tile_a * 128, b0 = (int64_t)tile_b * 128;
+    // this thread's 16 bytes of every 16th row
+    const int kr = threadIdx.x >> 4, idx = threadIdx.x & 15;
+    const bool in_a = a0 + 8 * idx < ta.na, in_b = b0 + 8 * idx < ta.nb;
+    const int8_t *pa = ta.A + kr * ta.lda + 2 * a0 + 16 * idx, *pb = ta.B + kr * ta.ldb + 2 * b0 + 16 * idx;
+    const int c = lane >> 4, r4 = (lane & 15) >> 2, f = r4 | (c & 1) << 2;
+    const uint32_t base = (uint32_t)((8 * c + r4) * ROWB + (lane & 3) * 8);
+    v4i acc[RT][CT];
+#pragma unroll
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < CT; ++j) acc[i][j] = (v4i){0, 0, 0, 0};
+    for (int k0 = 0; k0 < ta.krows; k0 += 64) {
+        const int rows = min(64, ta.krows - k0);
+        const int steps = rows <= 32 ? 1 : 2;
+        v4i ea4[4], eb4[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const bool in = kr + 16 * q < rows;
+            ea4[q] = in && in_a ? *(const v4i *)(pa + (int64_t)(k0 + 16 * q) * ta.lda) : (v4i){0, 0, 0, 0};
+            eb4[q] = in && in_b ? *(const v4i *)(pb + (int64_t)(k0 + 16 * q) * ta.ldb) : (v4i){0, 0, 0, 0};
+        }
+        if (k0 > 0) __syncthreads();  // the previous rows have been read
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int k = kr + 16 * q;
+            const int at = k * ROWB + ((idx >> 1) ^ ((k & 3) | (k >> 3 & 1) << 2)) * 32 + (idx & 1) * 16;
+            if (16 * q < 32 * steps) {
+                *(v4i *)(lds + at) = ea4[q];
+                *(v4i *)(lds + UNIT + at) = eb4[q];
+            }
+        }
+        __syncthreads();
+        for (int s = 0; s < steps; ++s) {
+            auto frag = [&](int unit, int n) {
+                const int8_t *p = lds + unit * UNIT + base + (uint32_t)((n ^ f) * 32) + s * 32 * ROWB;
+                const v2i lo = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)p));
+                const v2i hi = __builtin_bit_cast(v2i, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4s *)(p + 4 * ROWB)));
+                return (v4i){lo[0], lo[1], hi[0], hi[1]};
+            };
+            v4i fb[CT];
+#pragma unroll
+            for (int j = 0; j < CT; ++j) fb[j] = frag(1, wn * CT + j);
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                const v4i fa = frag(0, wm * RT + i);
+#pragma unroll
+                for (int j = 0; j < CT; ++j) acc[i][j] = M::mma(fa, fb[j], acc[i][j]);
+            }
+        }
+    }
+    const TileWhere w = {a0 + wm * 64, b0 + wn * 64, a0, tile_a * 2 + wm, 0};
+    if (w.a0 + 64 <= ta.na && w.b0 + 64 <= ta.nb)
+        Epi::template run<M, RT, CT, false>(acc, w, ea);
+    else if (w.a0 < ta.na && w.b0 < ta.nb)
+        Epi::template run<M, RT, CT, true>(acc, w, ea);
+}
+
 // ---- any alignment -----------------------------------------------------------
 // 128 x 128 tiles of four wavefronts for rows or pitches that are not 16-byte
 // aligned, which cannot be copied straight into LDS: each lane loads its 16
@@ -1178,26 +1255,19 @@ inline int64_t pack_rows(int64_t rows, int64_t kbytes) {
 }
 inline bool needs_pack(int64_t kbytes, int64_t nb) { return (kbytes & 15) != 0 && nb > 16; }
 
-// out[r][0 .. kbytes) = in[r], zeros to the next 16 bytes; `copies` times, one after
-// another. Rows whose g is 0 are zeros (g may be null). 16 bytes per lane and
-// step, a wavefront per row.
+// out[r][0 .. kbytes) = in[r], zeros to the next 16 bytes. 16 bytes per lane and step, a
+// wavefront per row.
 __global__ __launch_bounds__(256) static void k_pack_rows(const int8_t *__restrict__ in, int64_t ldi, int64_t rows,
-                                                          int64_t kbytes, int8_t *__restrict__ out, int64_t ldo,
-                                                          const float *__restrict__ g, int copies) {
+                                                          int64_t kbytes, int8_t *__restrict__ out, int64_t ldo) {
     const int lane = threadIdx.x & 63;
-    for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < rows; r += (int64_t)gridDim.x * 4) {
-        const bool zero = g != nullptr && g[r] == 0.f;
-        for (int64_t k = 16 * lane; k < kbytes; k += 1024) {
-            const v4i e = zero ? (v4i){0, 0, 0, 0} : load_chunk(in + r * ldi, k, kbytes);
-            for (int c = 0; c < copies; ++c) *(v4i *)(out + (c * rows + r) * ldo + k) = e;
-        }
-    }
+    for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < rows; r += (int64_t)gridDim.x * 4)
+        for (int64_t k = 16 * lane; k < kbytes; k += 1024) *(v4i *)(out + r * ldo + k) = load_chunk(in + r * ldi, k, kbytes);
 }
 inline hipError_t launch_pack_rows(const void *in, int64_t ldi, int64_t rows, int64_t kbytes, void *out, int64_t ldo,
-                                   const float *g, hipStream_t s, int copies = 1) {
+                                   hipStream_t s) {
     const int64_t blocks = (rows + 3) / 4;
     hipLaunchKernelGGL(k_pack_rows, dim3((unsigned)(blocks < 8192 ? blocks : 8192)), dim3(256), 0, s, (const int8_t *)in, ldi,
-                       rows, kbytes, (int8_t *)out, ldo, g, copies);
+                       rows, kbytes, (int8_t *)out, ldo);
     return hipGetLastError();
 }
 
@@ -1325,21 +1395,30 @@ inline int tile_splits(Tile tile, int64_t na, int64_t nb, int64_t kbytes) {
     return best;
 }
 
-// A product with K-major operands (see k_tile_p): no slices with p8.
+// A product with K-major operands (see k_tile_p): no slices with p8. Up to 128 rows of
+// k both operands' tiles go through k_tile_short (gradients of bf16, 32000 x 4096: 16
+// tokens 183 us against 202, 64 tokens in two parts 220 against 226; 250 rows in it 292
+// against 294, 500 447 against 420).
+constexpr int kShortRows = 128;
 template <class M, class Epi, bool KA, bool KB>
 hipError_t launch_kmajor(TileArgs t, const typename Epi::Args &e, int splits, hipStream_t s) {
-    bool large = splits == 1 && use_large_tile(t.na, t.nb);
+    bool large = splits == 1 && use_large_tile(t.na, t.nb), few = KA && KB && t.krows <= kShortRows;
     if (const char *force = getenv("OZ2_LINEAR_TILE")) {
-        if (!strcmp(force, "p4")) large = false;
-        if (!strcmp(force, "p8") && splits == 1 && t.na >= 256 && t.nb >= 256) large = true;
+        if (!strcmp(force, "p4")) large = few = false;
+        if (!strcmp(force, "p8") && splits == 1 && t.na >= 256 && t.nb >= 256) large = true, few = false;
     }
-    const int side = large ? 256 : 128;
+    const int side = large && !few ? 256 : 128;
     t.tiles_a = (int)((t.na + side - 1) / side);
     t.tiles_b = (int)((t.nb + side - 1) / side);
     t.group = group_of(t.tiles_a, t.tiles_b, t.kbytes);
     t.splits = splits;
     t.split_bytes = ((t.kbytes + splits - 1) / splits + 127) / 128 * 128;
     const int64_t total = (int64_t)t.tiles_a * t.tiles_b * splits, cus = compute_units();
+    if constexpr (KA && KB)
+        if (few) {
+            hipLaunchKernelGGL((k_tile_short<M, Epi>), dim3((unsigned)total), dim3(256), 0, s, t, e);
+            return hipGetLastError();
+        }
     if (large)
         hipLaunchKernelGGL((k_tile_p<M, Epi, 8, KA, KB>), dim3((unsigned)(total < cus ? total : cus)), dim3(256), 0, s, t,
                            e);

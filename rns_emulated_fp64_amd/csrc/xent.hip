@@ -346,22 +346,35 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
 
 // ---- backward: small kernels ---------------------------------------------------------
 // What the products need of each token: its g without the ignored ones, as a
-// multiple of *unit, and its lse (NaN for a target out of range). unit: a power
-// of two near the largest |g|, for fp16 (RESCALE), whose range the G of a mean
-// over many tokens would leave; 1 for bf16. Every block finds that maximum for
-// itself, over all tokens: 12 bytes each, from the L2, against one more launch.
+// multiple of *unit; its lse (NaN for a target out of range); and its row of X in
+// aligned rows, `copies` times, zeros for a token that takes no part (what its row
+// holds must not meet the zeros of G). unit: a power of two near the largest |g|, for
+// fp16 (RESCALE), whose range the G of a mean over many tokens would leave; 1 for
+// bf16. Every block finds that maximum for itself, over all tokens: 12 bytes each,
+// from the L2, against one more launch (about 5 us). pad: columns of G past
+// its entries, up to the next multiple of 8. A block per token.
+struct PrepareArgs {
+    const float *g, *lse;
+    const int64_t *y;
+    int64_t ignore, nt, nv;
+    float *g_out, *lse_out, *unit;
+    const int8_t *X;
+    int64_t ldx, bytes;  // of a row
+    int8_t *x_out;
+    int64_t ldx_out;
+    int copies;
+    uint16_t *pad;  // or null
+    int64_t ldg;
+    int cols;
+};
 template <bool RESCALE>
-__global__ __launch_bounds__(256) void k_xent_prepare(const float *__restrict__ g, const float *__restrict__ lse,
-                                                      const int64_t *__restrict__ y, int64_t ignore, int64_t nt,
-                                                      int64_t nv, float *__restrict__ g_out,
-                                                      float *__restrict__ lse_out, float *__restrict__ unit,
-                                                      uint16_t *__restrict__ pad, int64_t ldg, int cols, int64_t rows) {
+__global__ __launch_bounds__(256) void k_xent_prepare(PrepareArgs p) {
     float u = 1.f;
     if constexpr (RESCALE) {
         __shared__ uint32_t top[4];
         uint32_t m = 0;
-        for (int64_t t = threadIdx.x; t < nt; t += 256)
-            if (y[t] != ignore) m = max(m, abs_bits(g[t]));
+        for (int64_t t = threadIdx.x; t < p.nt; t += 256)
+            if (p.y[t] != p.ignore) m = max(m, abs_bits(p.g[t]));
 #pragma unroll
         for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
         if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = m;
@@ -372,16 +385,23 @@ __global__ __launch_bounds__(256) void k_xent_prepare(const float *__restrict__ 
         const uint32_t ex = m & 0x7f800000u;
         if (ex >= 0x01000000u && ex < 0x7e000000u) u = __uint_as_float(ex);
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) *unit = u;
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.unit = u;
     const float up = 1.f / u;  // exact
-    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < nt; t += (int64_t)gridDim.x * 256) {
-        const int64_t v = y[t];
-        g_out[t] = v == ignore ? 0.f : g[t] * up;
-        lse_out[t] = v == ignore || (v >= 0 && v < nv) ? lse[t] : __uint_as_float(0x7fc00000u);
+    const int i = threadIdx.x;
+    for (int64_t t = blockIdx.x; t < p.nt; t += gridDim.x) {
+        const int64_t v = p.y[t];
+        const float g = v == p.ignore ? 0.f : p.g[t] * up;
+        if (i == 0) {
+            p.g_out[t] = g;
+            p.lse_out[t] = v == p.ignore || (v >= 0 && v < p.nv) ? p.lse[t] : __uint_as_float(0x7fc00000u);
+        }
+        for (int64_t k = 16 * i; k < p.bytes; k += 4096) {
+            const v4i e = g == 0.f ? (v4i){0, 0, 0, 0} : load_chunk(p.X + t * p.ldx, k, p.bytes);
+            for (int c = 0; c < p.copies; ++c) *(v4i *)(p.x_out + (c * p.nt + t) * p.ldx_out + k) = e;
+        }
+        if (p.pad != nullptr && i < p.cols)
+            for (int c = 0; c < p.copies; ++c) p.pad[(c * p.nt + t) * p.ldg + i] = 0;
     }
-    // columns of G past its entries, up to the next multiple of 8
-    for (int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x; r < rows; r += (int64_t)gridDim.x * 256)
-        for (int c = 0; c < cols; ++c) pad[r * ldg + c] = 0;
 }
 
 // Sums the planes of a product's slices (and the parts of G, whose rows follow one
@@ -398,7 +418,14 @@ __global__ __launch_bounds__(256) void k_join_rows(const float *__restrict__ pla
         const float *from = planes + b * ldp + a;
         v4f s = *(const v4f *)from;
         int i = 1;
-        for (; i + 4 <= splits; i += 4) {  // four loads on their way at a time
+        for (; i + 16 <= splits; i += 16) {  // sixteen loads on their way at a time (128 planes of one row: 8 us against 14 with four)
+            v4f o[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = *(const v4f *)(from + (i + j) * plane);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) s += o[j];
+        }
+        for (; i + 4 <= splits; i += 4) {
             v4f o[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) o[j] = *(const v4f *)(from + (i + j) * plane);
@@ -475,14 +502,14 @@ int forward(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const f
         const char *x = (const char *)X + t0 * ldx * M::BYTES;
         const bool pack = needs_pack(d * M::BYTES, nt);
         const int64_t pitch = pack_pitch(d * M::BYTES), run = pack ? plan.run : v;
-        if (pack) HIP_TRY(launch_pack_rows(x, ldx * M::BYTES, nt, d * M::BYTES, ws + plan.x, pitch, nullptr, s));
+        if (pack) HIP_TRY(launch_pack_rows(x, ldx * M::BYTES, nt, d * M::BYTES, ws + plan.x, pitch, s));
         int nparts = 0;
         for (int64_t v0 = 0; v0 < v; v0 += run) {
             const int64_t nv = v - v0 < run ? v - v0 : run;
             const char *w = (const char *)W + v0 * ldw * M::BYTES;
             TileArgs ta = rows_args<M::BYTES>(nt, nv, d, x, ldx, w, ldw);
             if (pack) {
-                HIP_TRY(launch_pack_rows(w, ldw * M::BYTES, nv, d * M::BYTES, ws + plan.w, pitch, nullptr, s));
+                HIP_TRY(launch_pack_rows(w, ldw * M::BYTES, nv, d * M::BYTES, ws + plan.w, pitch, s));
                 ta.A = (const int8_t *)ws + plan.w;
                 ta.B = (const int8_t *)ws + plan.x;
                 ta.lda = ta.ldb = pitch;
@@ -588,19 +615,18 @@ int backward(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const 
     const bool aligned = (((uintptr_t)W | (uintptr_t)(2 * ldw) | (uintptr_t)(2 * d)) & 15) == 0 && 2 * ldw < (1 << 24);
     const bool two = p.parts == 2;
     const int64_t rows = p.parts * t;  // of G
-    const unsigned blocks = (unsigned)((t + 255) / 256 < 32 ? (t + 255) / 256 : 32);
-    hipLaunchKernelGGL((k_xent_prepare<M::HALF>), dim3(blocks), dim3(256), 0, s, grad, lse, y, ignore, t, v, g, l, unit,
-                       (uint16_t *)gm + v, ldg, (int)((v + 7) / 8 * 8 - v), dX != nullptr && p.vc == v ? rows : 0);
+    const int64_t most = M::HALF ? 512 : 8192, blocks = t < most ? t : most;
+    const bool pad = dX != nullptr && p.vc == v;
+    hipLaunchKernelGGL((k_xent_prepare<M::HALF>), dim3((unsigned)blocks), dim3(256), 0, s,
+                       PrepareArgs{grad, lse, y, ignore, t, v, g, l, unit, (const int8_t *)X, 2 * ldx, 2 * d, (int8_t *)x,
+                                   2 * ldp, p.parts, pad ? (uint16_t *)gm + v : nullptr, ldg, (int)((v + 7) / 8 * 8 - v)});
     HIP_TRY(hipGetLastError());
-    // the rows of X, zeros for the tokens that take no part: what theirs hold must
-    // not meet the zeros of G; once for each part of G
-    HIP_TRY(launch_pack_rows(X, 2 * ldx, t, 2 * d, x, 2 * ldp, g, s, p.parts));
     for (int64_t v0 = 0; v0 < v; v0 += p.vc) {
         const int64_t vc = v - v0 < p.vc ? v - v0 : p.vc, v8 = (vc + 7) / 8 * 8;
         const void *w = (const char *)W + v0 * ldw * 2;
         int64_t ldv = ldw;
         if (!aligned) {
-            HIP_TRY(launch_pack_rows(w, 2 * ldw, vc, 2 * d, ws + p.w, 2 * ldp, nullptr, s));
+            HIP_TRY(launch_pack_rows(w, 2 * ldw, vc, 2 * d, ws + p.w, 2 * ldp, s));
             w = ws + p.w;
             ldv = ldp;
         }
