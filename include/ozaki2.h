@@ -1,6 +1,8 @@
 /*
  * ozaki2.h -- C ABI of libozaki2.so: FP64 matrix products emulated with
- * Ozaki Scheme II on INT8 matrix cores of AMD Instinct MI355X (gfx950).
+ * Ozaki Scheme II on INT8 matrix cores of AMD Instinct MI355X (gfx950), and
+ * operators of language models on the same cores: INT8 products with scales
+ * and the linear cross entropy (sections of their own below).
  *
  * Pages this interface follows:
  *   [Q] "8ビットの整数で53ビットの倍精度を組み立てる。中国剰余定理をGPUに載せた
@@ -53,11 +55,14 @@
  * on any of these settings. OZ2_CRT=fma reconstructs real products
  * with 17 to 20 moduli, and complex products with any number, with FP64 FMAs
  * on 40-bit pieces instead of digit sums on the matrix cores (the same
- * results).
+ * results). OZ2_LINEAR_TILE=skinny, s11, s21, s22, s42, p4, p8 or any forces
+ * the tile of the INT8 products with scales and of the linear cross entropy
+ * where their sizes and alignment allow it (for tests; a workspace must be
+ * sized and used under the same setting).
  *
  * Memory ownership: A, B, C and any workspace belong to the caller. The
- * library keeps one cached workspace per device for ozaki2_dgemm (freed by
- * ozaki2_finalize) and small per-device constant tables.
+ * library keeps one cached workspace per device for the entry points without a
+ * workspace argument (freed by ozaki2_finalize) and small per-device constant tables.
  *
  * Status codes: 0 success; -i the i-th argument (1-based, in signature order)
  * is invalid, as in BLAS xerbla; positive codes are the OZAKI2_ERR_* values.

@@ -616,7 +616,8 @@ const char *ozaki2_status_string(int status) {
         return "product needs more workspace than the static scratch of ozaki2_dgemm_noalloc "
                "(OZAKI2_NOALLOC_MAX_WORKSPACE bytes); use ozaki2_dgemm_ws";
     case OZAKI2_ERR_UNSUPPORTED:
-        return "unsupported size (k <= 2^22 - 1, or 2^19 - 1 in accurate mode; m, n < 2^31; raw products need k < 2^17)";
+        return "unsupported size (k <= 2^22 - 1, or 2^19 - 1 in accurate mode; m, n < 2^31; raw products need k < 2^17; "
+               "INT8 products with scales and the linear cross entropy have limits of their own)";
     default: break;
     }
     if (status < 0) return "invalid argument (status is minus its 1-based position)";
