@@ -114,7 +114,7 @@ int product_ws(Elem el, int64_t m, int64_t n, int64_t k, const void *A, int64_t 
 int with_workspace(size_t bytes, hipStream_t s, int (*fn)(void *ctx, char *ws), void *ctx);
 
 // Compute units of the current device (kernels.hip).
-int compute_units();
+int device_units();
 
 // ---- kernel launchers (kernels.hip). Each returns hipGetLastError(). ----
 // cplx: interleaved complex operands (A, B, C hold (re, im) pairs; leading

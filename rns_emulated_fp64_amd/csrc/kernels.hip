@@ -2231,7 +2231,7 @@ hipError_t launch_quantize(Elem el, const void *A, int64_t m, int64_t lda, const
 // or 256 in the environment forces a shape; the results do not depend on it
 // (the tests run both shapes at every size).
 // Compute units of the current device (cached per device).
-int compute_units() {
+static int compute_units() {
     static std::atomic<int> cu_count[64];
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) dev = 0;
@@ -2493,5 +2493,7 @@ hipError_t launch_copy_planes_i32(const int32_t *raw, int nmod, int64_t m, int64
     hipLaunchKernelGGL(k_copy_planes_i32, grid, dim3(256), 0, s, raw, m, L.m_pad, L.m_pad * L.n_pad, n, out);
     return hipGetLastError();
 }
+
+int device_units() { return compute_units(); }
 
 }  // namespace oz2

@@ -1413,7 +1413,7 @@ hipError_t launch_kmajor(TileArgs t, const typename Epi::Args &e, int splits, hi
     t.group = group_of(t.tiles_a, t.tiles_b, t.kbytes);
     t.splits = splits;
     t.split_bytes = ((t.kbytes + splits - 1) / splits + 127) / 128 * 128;
-    const int64_t total = (int64_t)t.tiles_a * t.tiles_b * splits, cus = compute_units();
+    const int64_t total = (int64_t)t.tiles_a * t.tiles_b * splits, cus = device_units();
     if constexpr (KA && KB)
         if (few) {
             hipLaunchKernelGGL((k_tile_short<M, Epi>), dim3((unsigned)total), dim3(256), 0, s, t, e);
@@ -1437,7 +1437,7 @@ hipError_t launch_tile(TileArgs t, const typename Epi::Args &e, Tile tile, int s
     t.group = group_of(t.tiles_a, t.tiles_b, t.kbytes);
     t.splits = splits;
     t.split_bytes = ((t.kbytes + splits - 1) / splits + 127) / 128 * 128;
-    const int64_t total = (int64_t)t.tiles_a * t.tiles_b, cus = compute_units();
+    const int64_t total = (int64_t)t.tiles_a * t.tiles_b, cus = device_units();
     const dim3 grid((unsigned)total, (unsigned)splits);
     if (tile == Tile::p4 && splits > 1 && t.split_bytes < 256) tile = Tile::any;
     switch (tile) {
