@@ -523,8 +523,11 @@ int ozaki2_i8xent_ws(int64_t t, int64_t v, int64_t k, const int8_t *A, int64_t l
  * G[i][j] = grad_loss[i] (exp(z[i][j] - lse[i]) - [j == targets[i]]),
  *   dX[i][h] = sum_j G[i][j] W[j][h],   dW[j][h] = sum_i G[i][j] X[i][h].
  * The logits are computed again, a piece of the vocabulary at a time, and G is
- * held in `type` for that piece only (at most 2^28 entries, or t * 256); sums
- * are binary32, rounded once to `type`. For fp16 G is held relative to the
+ * held in `type` for that piece only (at most 2^28 entries, or t * 256; twice for
+ * t <= 64, the second time what rounding the first left); sums are binary32,
+ * rounded once to `type`. The workspace has room for that piece, for the rows of
+ * X (twice for t <= 64), for 256 MiB (or 256 rows) of aligned copies of rows of W,
+ * used where those are not multiples of 16 bytes, and for sums of dX. For fp16 G is held relative to the
  * largest |grad_loss|, so small gradients do not underflow on the way; below
  * 2^-126 the matrix cores and the exponential give zeros.
  *   lse       DEVICE binary32 [t] as ozaki2_xent wrote it for the same X, W.

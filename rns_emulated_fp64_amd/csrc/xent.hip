@@ -551,6 +551,7 @@ int64_t pitch16(int64_t n) { return pack_pitch(2 * n) / 2; }
 
 struct GradPlan {
     int64_t vc;           // vocabulary entries per piece
+    int64_t vw;           // the same where W is copied to aligned rows
     int parts;            // 16-bit values that hold an entry of G
     int splits;           // slices of a piece in dX's product
     int64_t ldp, plane;   // pitch and size of dX's planes
@@ -562,6 +563,10 @@ constexpr int64_t kTwoParts = 64;
 // G takes up to 2^28 entries: 32768 vocabulary entries at 8192 tokens, enough for
 // the products over them to run at full rate.
 constexpr int64_t kPieceEntries = (int64_t)1 << 28;
+// W in rows that are not aligned is copied a piece of 256 MiB at a time, for the two
+// products that read it (bf16, 128000 x 4097, 1024 tokens: 4.08 ms, 4.29 with 128 MiB, 4.24
+// with all of W at once; 128000 x 2050, 200 tokens: 0.95, 1.04, 0.92).
+constexpr int64_t kCopyBytes = (int64_t)1 << 28;
 constexpr int64_t kPieceMost = (int64_t)1 << 22;  // rows of G stay below 2^24 bytes
 GradPlan plan_grad(int64_t t, int64_t v, int64_t d, bool dx) {
     GradPlan p{};
@@ -571,6 +576,9 @@ GradPlan plan_grad(int64_t t, int64_t v, int64_t d, bool dx) {
     const int64_t pieces = (v + most - 1) / most;
     p.vc = ((v + pieces - 1) / pieces + 255) / 256 * 256;
     if (p.vc > v) p.vc = v;
+    const int64_t run = kCopyBytes / (2 * pitch16(d)) / 256 * 256;
+    p.vw = run < 256 ? 256 : run;
+    if (p.vw > p.vc) p.vw = p.vc;
     p.parts = t <= kTwoParts ? 2 : 1;
     p.splits = use_large_tile(d, p.parts * t) ? 1 : tile_splits(Tile::p4, d, p.parts * t, 2 * ((p.vc + 7) / 8 * 8));
     p.ldp = (d + 7) / 8 * 8;
@@ -581,16 +589,16 @@ GradPlan plan_grad(int64_t t, int64_t v, int64_t d, bool dx) {
         off += up256(bytes);
         return at;
     };
-    const size_t st = (size_t)t, sv = (size_t)p.vc;
+    const size_t st = (size_t)t;
     p.g = take(4 * st);
     p.lse = take(4 * st);
     p.unit = take(4);
     p.gm = take(2 * p.parts * st * (size_t)pitch16(p.vc));
     p.x = take(2 * p.parts * st * (size_t)pitch16(d));
-    p.w = take(2 * sv * (size_t)pitch16(d));  // for W in rows that are not aligned
+    p.w = take(2 * (size_t)p.vw * (size_t)pitch16(d));  // (sizes alone do not say whether W is aligned)
     if (dx) {
         p.planes = take(4 * (size_t)p.plane * (size_t)p.splits);
-        p.sum = pieces > 1 ? take(4 * st * (size_t)p.ldp) : 0;
+        p.sum = p.vw < v ? take(4 * st * (size_t)p.ldp) : 0;
     }
     p.total = off;
     return p;
@@ -613,16 +621,17 @@ int backward(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, const 
     float *planes = (float *)(ws + p.planes), *sum = (float *)(ws + p.sum);
     const int64_t ldg = pitch16(p.vc), ldp = pitch16(d), d8 = (d + 7) / 8 * 8;
     const bool aligned = (((uintptr_t)W | (uintptr_t)(2 * ldw) | (uintptr_t)(2 * d)) & 15) == 0 && 2 * ldw < (1 << 24);
+    const int64_t piece = aligned ? p.vc : p.vw;
     const bool two = p.parts == 2;
     const int64_t rows = p.parts * t;  // of G
     const int64_t most = M::HALF ? 512 : 8192, blocks = t < most ? t : most;
-    const bool pad = dX != nullptr && p.vc == v;
+    const bool pad = dX != nullptr && piece == v;
     hipLaunchKernelGGL((k_xent_prepare<M::HALF>), dim3((unsigned)blocks), dim3(256), 0, s,
                        PrepareArgs{grad, lse, y, ignore, t, v, g, l, unit, (const int8_t *)X, 2 * ldx, 2 * d, (int8_t *)x,
                                    2 * ldp, p.parts, pad ? (uint16_t *)gm + v : nullptr, ldg, (int)((v + 7) / 8 * 8 - v)});
     HIP_TRY(hipGetLastError());
-    for (int64_t v0 = 0; v0 < v; v0 += p.vc) {
-        const int64_t vc = v - v0 < p.vc ? v - v0 : p.vc, v8 = (vc + 7) / 8 * 8;
+    for (int64_t v0 = 0; v0 < v; v0 += piece) {
+        const int64_t vc = v - v0 < piece ? v - v0 : piece, v8 = (vc + 7) / 8 * 8;
         const void *w = (const char *)W + v0 * ldw * 2;
         int64_t ldv = ldw;
         if (!aligned) {

@@ -347,6 +347,15 @@ def test_pieces_of_the_vocabulary():
         assert ((dW[at].double() - want).abs() <= tol).all()
 
 
+def test_pieces_of_rows_that_are_copied():
+    # rows of W that are not aligned, more than one copy holds
+    t, v, d = 6, 33000, 4104
+    X, W, y, grad = operands(t, v, d, torch.bfloat16, 16, pad=1)
+    size = oz.ozaki2_xent_grad_workspace_size(t, v, d)
+    assert 1 << 28 < size < 3 << 27
+    check(X, W, y, grad)
+
+
 def test_streams_and_graph():
     X, W, y, grad = operands(80, 3001, 256, torch.bfloat16, 13)
     A, sa = oz.quantize_rows(X)
