@@ -356,6 +356,45 @@ def test_pieces_of_rows_that_are_copied():
     check(X, W, y, grad)
 
 
+@pytest.mark.parametrize("t", [3, 40, 300])
+def test_weights_past_32_bits(t):
+    # more than 2^32 bytes of W and of dW; 64 bits a slab at a time, with the docstring's bounds
+    v, d = 540000, 4096
+    W = torch.empty(v, d, dtype=torch.bfloat16, device="cuda")
+    g = gen(17)
+    for at in range(0, v, 60000):
+        W[at:at + 60000] = torch.randn(60000, d, generator=g, device="cuda") * (1.5 / d ** 0.5)
+    X = torch.randn(t, d, generator=g, device="cuda").bfloat16()
+    y = torch.randint(v, (t,), generator=g, device="cuda")
+    y[0] = v - 1
+    grad = torch.rand(t, generator=g, device="cuda") / t
+    loss, lse = oz.xent(X, W, y)
+    dX, dW = oz.xent_grad(X, W, y, lse, grad)
+    x = X.double()
+    zs = [x @ W[at:at + 60000].double().t().contiguous() for at in range(0, v, 60000)]
+    most = max(z.abs().max().item() for z in zs)
+    sums = (x.abs().sum(1) * W.abs().max().double()).max().item()  # at least sum |x w|
+    want = torch.logsumexp(torch.stack([torch.logsumexp(z, 1) for z in zs]), 0)
+    tol = d * U * sums + 2.0 ** -15 + 8 * U * most
+    assert ((lse.double() - want).abs() <= tol).all()
+    E, h = 2 * (d * U * sums + 8 * U * most) + 2.0 ** -15, STEP[torch.bfloat16]
+    sx, sx_abs = torch.zeros_like(x), torch.zeros_like(x)
+    for i, z in enumerate(zs):
+        slab = W[i * 60000:(i + 1) * 60000].double()
+        G = torch.exp(z - want[:, None])
+        mine = (y >= i * 60000) & (y < (i + 1) * 60000)
+        G[mine, y[mine] - i * 60000] -= 1
+        G *= grad.double()[:, None]
+        P = G.abs() + (G + grad.double()[:, None] * (G < 0)).abs()  # |G| and the probability's own part of the target's
+        sx += G @ slab
+        sx_abs += P @ slab.abs()
+        got = dW[i * 60000:(i + 1) * 60000].double()
+        ref = G.t().contiguous() @ x
+        bound = (h + 2 * E + t * U) * (P.t().contiguous() @ x.abs()) + h * ref.abs() + 2.0 ** -126
+        assert ((got - ref).abs() <= bound).all(), i
+    assert ((dX.double() - sx).abs() <= (h + 2 * E + v * U) * sx_abs + h * sx.abs() + 2.0 ** -126).all()
+
+
 def test_streams_and_graph():
     X, W, y, grad = operands(80, 3001, 256, torch.bfloat16, 13)
     A, sa = oz.quantize_rows(X)
