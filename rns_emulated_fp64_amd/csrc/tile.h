@@ -1341,6 +1341,10 @@ inline bool use_large_tile(int64_t na, int64_t nb) {
 //     12.8, p4 18.0); but no larger than covers up to 64 rows of B, so that A is
 //     read once by small blocks (bf16, 32000 x 4096, 1 row: s21 49.0 us or 5.3 TB/s,
 //     s42 57.8; 64 rows: s22 54.8, p4 61.2);
+//   - with a short k, up to two 128 x 64 blocks per compute unit, whose starts and ends
+//     overlap (257 to 440 tiles, k of 768 to 2048 bytes, int8 and statistics: 1.00 to 1.16
+//     times as fast as p4; with a k of 1040, whose rows share cache lines with their
+//     neighbours so that the smaller tile's copies cost more, 0.87 to 1.04);
 //   - else 128 x 128 or 256 x 256.
 // OZ2_LINEAR_TILE=skinny, s11, s21, s22, s42, p4, p8 or any forces one where the
 // product allows it; results of int8 products do not depend on it.
@@ -1364,7 +1368,8 @@ inline Tile choose_tile(const TileArgs &t, bool pairs) {
     if (!pairs && tiles_of(Tile::s11, t.na, t.nb) <= kPlanUnits) return Tile::s11;
     if (t.nb <= 32 || tiles_of(Tile::s21, t.na, t.nb) <= kPlanUnits) return Tile::s21;
     if (t.nb <= 64 || tiles_of(Tile::s22, t.na, t.nb) <= kPlanUnits) return Tile::s22;
-    if (tiles_of(Tile::s42, t.na, t.nb) <= kPlanUnits) return Tile::s42;
+    const bool two = t.kbytes <= 2048 && ((t.lda | t.ldb) & 127) == 0;
+    if (tiles_of(Tile::s42, t.na, t.nb) <= (two ? 2 : 1) * kPlanUnits) return Tile::s42;
     return use_large_tile(t.na, t.nb) ? Tile::p8 : Tile::p4;
 }
 // Wavefront ranges of A that an epilogue of this tile reports on.
@@ -1450,7 +1455,12 @@ hipError_t launch_tile(TileArgs t, const typename Epi::Args &e, Tile tile, int s
                            t, e);
         break;
     }
-    case Tile::s42: hipLaunchKernelGGL((k_tile_s<M, Epi, 4, 2, 6>), grid, dim3(256), 0, s, t, e); break;
+    case Tile::s42:
+        if (total > kPlanUnits)  // a ring that leaves room for a second block
+            hipLaunchKernelGGL((k_tile_s<M, Epi, 4, 2, 3>), grid, dim3(256), 0, s, t, e);
+        else
+            hipLaunchKernelGGL((k_tile_s<M, Epi, 4, 2, 6>), grid, dim3(256), 0, s, t, e);
+        break;
     case Tile::s22: hipLaunchKernelGGL((k_tile_s<M, Epi, 2, 2, 5>), grid, dim3(256), 0, s, t, e); break;
     case Tile::s21: hipLaunchKernelGGL((k_tile_s<M, Epi, 2, 1, 6>), grid, dim3(256), 0, s, t, e); break;
     case Tile::any: hipLaunchKernelGGL((k_tile_any<M, Epi>), grid, dim3(256), 0, s, t, e); break;

@@ -55,7 +55,7 @@ def check(C, S, sa, sb, bias):
 
 SHAPES = [(1, 1, 1), (1, 1, 5), (3, 17, 15), (1, 4096, 256), (2, 33, 64), (16, 100, 300), (17, 333, 77), (31, 65, 272),
           (33, 129, 1000), (64, 257, 1024), (65, 65, 65), (100, 200, 304), (129, 127, 1040), (256, 256, 256),
-          (257, 300, 400), (300, 511, 2047)]
+          (257, 300, 400), (300, 511, 2047), (700, 3001, 384), (700, 3000, 400)]
 
 
 @pytest.mark.parametrize("t,n,k", SHAPES)

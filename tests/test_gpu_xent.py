@@ -107,7 +107,7 @@ def check(X, W, y, grad, e=None):
 
 SHAPES = [(1, 1, 1), (1, 2, 3), (1, 17, 8), (2, 100, 64), (5, 33, 130), (16, 1000, 100), (17, 333, 129), (40, 5000, 77),
           (64, 2000, 256), (65, 130, 64), (100, 1000, 128), (130, 257, 1024), (129, 4097, 136), (300, 3001, 200),
-          (520, 1037, 512)]
+          (520, 1037, 512), (610, 3501, 128)]
 
 
 @pytest.mark.parametrize("dtype", BOTH)
