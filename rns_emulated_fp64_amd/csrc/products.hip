@@ -143,12 +143,15 @@ size_t plane_bytes(int64_t t, int64_t n, int64_t k) {
     return s > 1 ? up256((size_t)s * (size_t)t * (size_t)plane_pitch(n) * 4) : 0;
 }
 // Workspace of a product: packed rows of A (unless they are the library's own)
-// and of a run of B, and the planes.
+// and of a run of B, and the planes. The last run has fewer channels than the
+// others, and with them more slices, whose planes can be the larger ones (256 x
+// 12100 x 8193: 1 slice of 12032 channels, 8 slices of 68).
 size_t product_bytes(int64_t t, int64_t n, int64_t k, bool own_a) {
     if (!needs_pack(k, t)) return plane_bytes(t, n, k);
-    const int64_t run = pack_rows(n, k);
+    const int64_t run = pack_rows(n, k), rest = n % run;
+    const size_t full = plane_bytes(t, run, k), last = rest ? plane_bytes(t, rest, k) : 0;
     return (own_a ? 0 : up256((size_t)t * (size_t)pack_pitch(k))) + up256((size_t)run * (size_t)pack_pitch(k)) +
-           plane_bytes(t, run, k);
+           (full > last ? full : last);
 }
 
 // Activations that the skinny kernel quantises itself: rows that fit LDS beside
