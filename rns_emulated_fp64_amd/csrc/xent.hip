@@ -121,8 +121,9 @@ struct EpiLse {
 };
 
 // G for a piece of the vocabulary: out[b][a] = g[b] (exp(z - lse[b]) - [v0 + a = y[b]]),
-// rounded to 16 bits (half a step relative, independent from entry to entry, so
-// the sums over many entries that follow see less of it). A token whose g is 0
+// rounded to 16 bits: half a step relative, independent from entry to entry, so
+// the sums over many entries that follow see less of it; fp16 also 2^-25 of the unit
+// that k_xent_prepare gives it, at most 2^-39 of the largest |g|. A token whose g is 0
 // gets zeros. TWO: with few tokens a sum has few large entries and would show their
 // roundings, so what the rounding left follows in rows nb .. 2 nb - 1, in 16 bits
 // of its own.
@@ -348,9 +349,11 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
 // What the products need of each token: its g without the ignored ones, as a
 // multiple of *unit; its lse (NaN for a target out of range); and its row of X in
 // aligned rows, `copies` times, zeros for a token that takes no part (what its row
-// holds must not meet the zeros of G). unit: a power of two near the largest |g|, for
-// fp16 (RESCALE), whose range the G of a mean over many tokens would leave; 1 for
-// bf16. Every block finds that maximum for itself, over all tokens: 12 bytes each,
+// holds must not meet the zeros of G). unit: for fp16 (RESCALE), whose range G would
+// leave at both ends, 2^-14 of the power of two at the largest |g|, which puts the largest
+// entries of G below 2^15 and the smallest probabilities as far above fp16's end as
+// they can be (a mean one of 128000 entries is 2^-17; with the power of two itself
+// everything below 2^-14 was subnormal and below 2^-25 zero); 1 for bf16. Every block finds that maximum for itself, over all tokens: 12 bytes each,
 // from the L2, against one more launch (about 5 us). pad: columns of G past
 // its entries, up to the next multiple of 8. A block per token.
 struct PrepareArgs {
@@ -381,9 +384,10 @@ __global__ __launch_bounds__(256) void k_xent_prepare(PrepareArgs p) {
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 4; ++i) m = max(m, top[i]);
-        // the exponent alone; the smallest and largest binades, Inf and NaN keep unit 1
+        // the exponent alone, less 14, so that unit and its inverse are normal numbers
+        // (from 2^-126, for the smallest g, to 2^113); all zeros, Inf and NaN keep unit 1
         const uint32_t ex = m & 0x7f800000u;
-        if (ex >= 0x01000000u && ex < 0x7e000000u) u = __uint_as_float(ex);
+        if (m != 0 && ex < 0x7f800000u) u = __uint_as_float(max(ex, 0x07800000u) - 0x07000000u);
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.unit = u;
     const float up = 1.f / u;  // exact
