@@ -528,8 +528,9 @@ int ozaki2_i8xent_ws(int64_t t, int64_t v, int64_t k, const int8_t *A, int64_t l
  * rounded once to `type`. The workspace has room for that piece, for the rows of
  * X (twice for t <= 64), for 256 MiB (or 256 rows) of aligned copies of rows of W,
  * used where those are not multiples of 16 bytes, and for sums of dX. For fp16 G is held relative to
- * 2^-14 of the power of two at the largest |grad_loss|: an entry is off by half a
- * step of fp16, or by 2^-39 of the largest |grad_loss| where that is more; below
+ * 2^-14 of the power of two at the largest finite |grad_loss| of a token with a
+ * target in range: an entry is off by half a step of fp16, or by 2^-39 of that
+ * |grad_loss| where that is more; below
  * 2^-126 the matrix cores and the exponential give zeros.
  *   lse       DEVICE binary32 [t] as ozaki2_xent wrote it for the same X, W.
  *   grad_loss DEVICE binary32 [t].

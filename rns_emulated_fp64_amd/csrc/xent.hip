@@ -350,7 +350,7 @@ __global__ __launch_bounds__(256) void k_xent_join(const float2 *__restrict__ pa
 // multiple of *unit; its lse (NaN for a target out of range); and its row of X in
 // aligned rows, `copies` times, zeros for a token that takes no part (what its row
 // holds must not meet the zeros of G). unit: for fp16 (RESCALE), whose range G would
-// leave at both ends, 2^-14 of the power of two at the largest |g|, which puts the largest
+// leave at both ends, 2^-14 of the power of two at the largest finite |g|, which puts the largest
 // entries of G below 2^15 and the smallest probabilities as far above fp16's end as
 // they can be (a mean one of 128000 entries is 2^-17; with the power of two itself
 // everything below 2^-14 was subnormal and below 2^-25 zero); 1 for bf16. Every block finds that maximum for itself, over all tokens: 12 bytes each,
@@ -376,8 +376,12 @@ __global__ __launch_bounds__(256) void k_xent_prepare(PrepareArgs p) {
     if constexpr (RESCALE) {
         __shared__ uint32_t top[4];
         uint32_t m = 0;
-        for (int64_t t = threadIdx.x; t < p.nt; t += 256)
-            if (p.y[t] != p.ignore) m = max(m, abs_bits(p.g[t]));
+        for (int64_t t = threadIdx.x; t < p.nt; t += 256) {
+            // (a token whose own result is NaN does not set the unit of the others)
+            const int64_t v = p.y[t];
+            const uint32_t g = abs_bits(p.g[t]);
+            if (v != p.ignore && v >= 0 && v < p.nv && g < 0x7f800000u) m = max(m, g);
+        }
 #pragma unroll
         for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
         if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = m;
@@ -385,9 +389,8 @@ __global__ __launch_bounds__(256) void k_xent_prepare(PrepareArgs p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) m = max(m, top[i]);
         // the exponent alone, less 14, so that unit and its inverse are normal numbers
-        // (from 2^-126, for the smallest g, to 2^113); all zeros, Inf and NaN keep unit 1
-        const uint32_t ex = m & 0x7f800000u;
-        if (m != 0 && ex < 0x7f800000u) u = __uint_as_float(max(ex, 0x07800000u) - 0x07000000u);
+        // (from 2^-126, for the smallest g, to 2^113)
+        if (m != 0) u = __uint_as_float(max(m & 0x7f800000u, 0x07800000u) - 0x07000000u);
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.unit = u;
     const float up = 1.f / u;  // exact
