@@ -537,8 +537,9 @@ int ozaki2_i8xent_ws(int64_t t, int64_t v, int64_t k, const int8_t *A, int64_t l
  *   dX, lddx  DEVICE output of `type`, or NULL to skip it; lddx >= max(1, d).
  *   dW, lddw  likewise, v rows.
  * A token whose target is ignored, or whose grad_loss is 0, contributes
- * nothing, whatever its row of X holds, and its row of dX is 0. A token whose
- * target is out of range gives NaN.
+ * nothing to dW, whatever its row of X and W hold, and its row of dX is 0 (but
+ * NaN at a feature for which W holds Inf or NaN, as that feature is in every row).
+ * A token whose target is out of range gives NaN.
  * Outputs must not overlap the inputs or each other. Bitwise reproducible.
  * Returns 0, -1..-16 for an invalid argument, -17 for the workspace of the _ws
  * form (ozaki2_xent_grad_workspace_size bytes with want_dx, want_dw nonzero for

@@ -148,8 +148,10 @@ struct EpiProb {
         for (int j = 0; j < CT; ++j) {
             const int64_t b = w.b0 + 16 * j + (lane & 15), at = EDGE && b >= e.nb ? e.nb - 1 : b;
             const float g = e.g[at];
-            // (exp2 of -inf is 0 for a token without a gradient)
-            const float shift = g == 0.f ? -INFINITY : -e.lse[at] * kLog2e;
+            // zeros for a token without a gradient, whatever its lse and the weights hold (0 times an
+            // infinite weight is NaN)
+            const bool none = g == 0.f;
+            const float shift = -e.lse[at] * kLog2e;
             // the target's place among this lane's entries, in 16 i + v
             const int64_t y = e.y[at] - e.v0 - w.a0 - 4 * (lane >> 4);
             int hit = y >= 0 && y < 16 * RT && (y & 15) < 4 ? (int)y : -1;
@@ -165,7 +167,7 @@ struct EpiProb {
                     for (int v = 0; v < 4; ++v) {
                         float p = __builtin_amdgcn_exp2f(fmaf(M::value(acc[i + h][j][v]), kLog2e, shift));
                         p = hit == 16 * (i + h) + v ? p - 1.f : p;
-                        x[h][v] = g * p;
+                        x[h][v] = none ? 0.f : g * p;
                     }
                 T *row = e.out + b * e.ldo;
                 store_pair<T, EDGE>(x, row, st0 + 16 * i, e.na, b < e.nb);

@@ -44,3 +44,39 @@ def test_a_token_that_is_not_a_number_leaves_the_others(t, bad, dtype):
     assert want[rest].isfinite().all() and (want[rest] != 0).float().mean() > 0.9
     assert torch.equal(dX[rest], want[rest])
     assert not dX[at].isfinite().any() and not dW.isfinite().any()
+
+
+@pytest.mark.parametrize("dtype", BOTH)
+@pytest.mark.parametrize("t,v", [(6, 300), (100, 300), (300, 700), (600, 3000)])
+def test_tokens_without_a_loss_beside_infinite_weights(t, v, dtype):
+    # entries that a weight of -inf takes out of the vocabulary (their feature is 1 in every token): their rows of dW are 0
+    # and their other features add nothing to dX, with ignored tokens and tokens of weight 0 beside the others
+    X, W, y = operands(t, v, 64, dtype, t)
+    X[:, 3] = 1
+    keep = torch.ones(v, dtype=torch.bool, device="cuda")
+    keep[5:v // 2] = False
+    W[~keep, 3] = float("-inf")
+    y %= 5
+    grad = torch.rand(t, generator=gen(7), device="cuda") + 0.5
+    y[::3] = -100
+    grad[1::3] = 0
+    _, lse = oz.xent(X, W, y)
+    dX, dW = oz.xent_grad(X, W, y, lse, grad)
+    assert not dW[~keep].any()
+    assert dW[keep].isfinite().all()
+    assert not dX[grad == 0][:, 4:].any() and not dX[y == -100][:, 4:].any()
+    Wk = W[keep].contiguous()
+    kX, kW = oz.xent_grad(X, Wk, y, oz.xent(X, Wk, y)[1], grad)
+    # the same products from sums in another order: G and the sums agree to a step of the type, and so do the results
+    # within two steps of each, relative to the magnitudes that they are sums of
+    x, w, n = X.double(), Wk.double(), keep.sum()
+    z = x @ w.t().contiguous()
+    G = torch.exp(z - torch.logsumexp(z, 1, keepdim=True))
+    G[torch.arange(t, device="cuda"), y.clamp(min=0)] += 1
+    G *= torch.where(y != -100, grad, torch.zeros_like(grad)).double()[:, None]
+    step = torch.finfo(dtype).eps
+    tol = 4 * step * (G @ w.abs()) + 2.0 ** -24
+    cols = torch.arange(64, device="cuda") != 3
+    assert ((dX.double() - kX.double()).abs() <= tol)[:, cols].all()
+    tol = 4 * step * (G.t().contiguous() @ x.abs()) + 2.0 ** -24
+    assert ((dW[keep].double() - kW.double()).abs() <= tol).all()
