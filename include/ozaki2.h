@@ -506,8 +506,8 @@ int ozaki2_xent_ws(int64_t t, int64_t v, int64_t d, const void *X, int64_t ldx, 
 /*
  * The same loss for quantised features and weights (see ozaki2_i8gemm):
  * z[i][j] = (sum_h A[i][h] B[j][h]) * a_scale[i] * b_scale[j], exact up to the
- * rounding of the sum and of the two products to binary32. Scales of either
- * sign. Workspace as ozaki2_xent, k <= OZAKI2_I8_MAX_K.
+ * rounding of the sum and of the two products to binary32 (b_scale first, where
+ * ozaki2_i8gemm takes a_scale first). Scales of either sign. Workspace as ozaki2_xent, k <= OZAKI2_I8_MAX_K.
  * Returns as ozaki2_xent: -1..-13 for an argument, -14 for the workspace.
  */
 int ozaki2_i8xent(int64_t t, int64_t v, int64_t k, const int8_t *A, int64_t lda, const float *a_scale,

@@ -641,7 +641,8 @@ def _xent_type(X, W):
 def xent(X, W, targets, ignore_index=-100, workspace=None):
     """Per token, the cross entropy of the logits X @ W.T against the target and their log-sum-exp, without storing
     the logits (ozaki2_xent_ws): (loss, lse), float32. X (t, d) and W (v, d) are bfloat16 or float16, targets (t,)
-    int64. The loss is 0 where the target is ``ignore_index`` and NaN where it is out of range otherwise."""
+    int64. The loss is 0 where the target is ``ignore_index`` and NaN where it is out of range otherwise. Autograd does
+    not see the call (the results require no gradient): xent_grad gives the gradients."""
     torch = _torch or _load_torch()
     kind = _xent_type(X, W)
     device, t, v, d, X, ldx, W, ldw, targets = _xent_operands(X, W, targets)
@@ -656,7 +657,8 @@ def xent(X, W, targets, ignore_index=-100, workspace=None):
 
 def i8xent(A, B, a_scale, b_scale, targets, ignore_index=-100, workspace=None):
     """xent for quantised features A (t, k) and weights B (v, k), int8 with float32 scales per row: the logits are
-    those of i8gemm in binary32 (ozaki2_i8xent_ws). Returns (loss, lse)."""
+    i8gemm's products in binary32, but with the sum times b_scale rounded first, so not always its bits
+    (ozaki2_i8xent_ws). Returns (loss, lse)."""
     torch = _torch or _load_torch()
     if A.dtype != torch.int8 or B.dtype != torch.int8:
         raise TypeError("A and B must be int8")

@@ -1,7 +1,8 @@
 // products.hip -- INT8 products with scales, through their C entry points
 // (include/ozaki2.h):
 //
-//   ozaki2_quantize_rows  s[t] = max_k |x[t][k]| / 127, q = rint(x * (127 / max))
+//   ozaki2_quantize_rows  s[t] = max_k |x[t][k]| / 127, q = rint(x * 127 / max), in
+//                         the binary32 operations of row_scale
 //   ozaki2_i8gemm         C[t][n] = (sum_k A[t][k] B[n][k]) sa[t] sb[n] + bias[n]
 //   ozaki2_i8linear       both: activations quantised row by row, then the product
 //
