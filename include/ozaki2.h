@@ -467,6 +467,32 @@ int ozaki2_i8linear_ws(int64_t t, int64_t n, int64_t k, const void *X, int64_t l
                        int64_t ldb, const float *b_scale, const float *bias, void *C, int64_t ldc, int ctype,
                        void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * The norm in front of a quantised layer: with h = X[i] + residual[i] (binary32, one rounding),
+ *
+ *   y[h] = h * w[h] / sqrt(mean_h h^2 + eps),
+ *
+ * squares, their sum and y in binary64, y rounded once to binary32, and y as int8 with a
+ * scale per row as ozaki2_quantize_rows has it, so that Q and scale are the operands of
+ * ozaki2_i8gemm and do not depend on how a row is spread over threads.
+ *   t, k      rows (tokens), elements of a row, each < 2^31.
+ *   X, ldx    DEVICE, of `type`, element (i, h) at X[i*ldx + h], ldx >= max(1, k).
+ *   residual, ldr   likewise, or NULL for none (ldr is then not looked at).
+ *   weight    DEVICE binary32 [k], or NULL for ones.
+ *   eps       >= 0 and finite. With eps = 0 a row of zeros gives zeros.
+ *   Q, ldq, scale   as ozaki2_quantize_rows: a row that holds Inf or NaN, or whose sum or y overflows binary32, gets zeros
+ *             and a NaN scale.
+ *   sum, lds  DEVICE output, h rounded to `type` (the norm is that of h before this rounding), or
+ *             NULL to skip it. It may be X or residual themselves (same pointer and pitch);
+ *             outputs must not overlap inputs or each other otherwise.
+ * Any alignment; multiples of 16 bytes are fastest. Returns 0, -1..-14 for an invalid argument
+ * (a NULL residual, weight or sum is none), OZAKI2_ERR_UNSUPPORTED or OZAKI2_ERR_HIP. No
+ * workspace; capturable.
+ */
+int ozaki2_rmsnorm_quantize(int64_t t, int64_t k, const void *X, int64_t ldx, int type, const void *residual, int64_t ldr,
+                            const float *weight, double eps, int8_t *Q, int64_t ldq, float *scale, void *sum, int64_t lds,
+                            void *stream);
+
 /* ---- Linear cross entropy --------------------------------------------------
  *
  * The loss of an output layer without its logits: for T tokens with features X

@@ -40,6 +40,7 @@ EXPORTS = (
     "ozaki2_xent", "ozaki2_xent_ws", "ozaki2_xent_workspace_size", "ozaki2_i8xent", "ozaki2_i8xent_ws",
     "ozaki2_i8xent_workspace_size",
     "ozaki2_xent_grad", "ozaki2_xent_grad_ws", "ozaki2_xent_grad_workspace_size",
+    "ozaki2_rmsnorm_quantize",
 )
 
 _lib = None
@@ -59,7 +60,7 @@ def lib() -> ctypes.CDLL:
     if not os.path.exists(LIB_PATH):
         raise RuntimeError(f"{LIB_PATH} is missing: build it with `python -m rns_emulated_fp64_amd.build`")
     L = ctypes.CDLL(LIB_PATH)
-    i64, p, i32, sz = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    i64, p, i32, sz, f64 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_double
     prod = [i64, i64, i64, p, i64, p, i64, p, i64, i32, i32]
     L.ozaki2_dgemm.argtypes = prod + [p]
     L.ozaki2_dgemm.restype = i32
@@ -136,6 +137,8 @@ def lib() -> ctypes.CDLL:
     L.ozaki2_i8xent_workspace_size.restype = sz
     L.ozaki2_xent_grad_workspace_size.argtypes = [i64, i64, i64, i32, i32]
     L.ozaki2_xent_grad_workspace_size.restype = sz
+    L.ozaki2_rmsnorm_quantize.argtypes = [i64, i64, p, i64, i32, p, i64, p, f64, p, i64, p, p, i64, p]
+    L.ozaki2_rmsnorm_quantize.restype = i32
     L.ozaki2_finalize.argtypes = []
     L.ozaki2_finalize.restype = None
     _lib = L
@@ -309,6 +312,10 @@ def ozaki2_xent_grad_ws(t, v, d, X, ldx, W, ldw, type, targets, ignore_index, ls
 
 def ozaki2_xent_grad_workspace_size(t, v, d, want_dx=True, want_dw=True) -> int:
     return lib().ozaki2_xent_grad_workspace_size(t, v, d, 1 if want_dx else 0, 1 if want_dw else 0)
+
+
+def ozaki2_rmsnorm_quantize(t, k, X, ldx, type, residual, ldr, weight, eps, Q, ldq, scale, sum, lds, stream=0) -> int:
+    return lib().ozaki2_rmsnorm_quantize(t, k, X, ldx, type, residual, ldr, weight, eps, Q, ldq, scale, sum, lds, stream)
 
 
 def ozaki2_crt_debug(m, n, num_moduli, residues, e, f, C, ldc, workspace, workspace_bytes, stream=0) -> int:
@@ -536,6 +543,17 @@ def _product_out(t, n, dtype, out, device):
     return out, max(out.stride(0) if t > 1 else n, 1)
 
 
+def _overlap(a, b):
+    """Whether the memory that two matrices reach from first to last element overlaps."""
+    def span(x):
+        last = sum((n - 1) * s for n, s in zip(x.shape, x.stride()))
+        return x.data_ptr(), x.data_ptr() + (last + 1) * x.element_size()
+    if not a.numel() or not b.numel():
+        return False
+    (a0, a1), (b0, b1) = span(a), span(b)
+    return a0 < b1 and b0 < a1
+
+
 def quantize_rows(X):
     """Rows of X (float32, float16 or bfloat16) as int8 with a binary32 scale each: (q, scale) with
     scale = max|x| / 127 and q = rint(x / scale), with the binary32 roundings that include/ozaki2.h states
@@ -608,6 +626,45 @@ def i8linear(X, B, b_scale, bias=None, out_dtype=None, out=None, workspace=None)
     _call(L.ozaki2_i8linear_ws, "ozaki2_i8linear_ws", device, t, n, k, X.data_ptr(), ldx, xtype, B.data_ptr(), ldb,
           b_scale.data_ptr(), None if bias is None else bias.data_ptr(), C.data_ptr(), ldc, ctype, wp, wb)
     return C
+
+
+def rmsnorm_quantize(X, weight=None, residual=None, eps=1e-6, sum_out=None):
+    """The root-mean-square norm in front of a quantised layer, with the residual's addition (ozaki2_rmsnorm_quantize):
+    (q, scale, sum) with h = X + residual, y = h / sqrt(mean(h^2) + eps) * weight, and y as int8 with a float32 scale per
+    row as quantize_rows gives it, the operands of i8gemm. ``weight`` is float32 (k,), ones if None. ``sum`` is h in X's
+    dtype, or None without a residual; ``sum_out`` (optional) the tensor it is written to, which may be ``residual`` or
+    ``X`` itself. Autograd does not see the call."""
+    torch = _torch or _load_torch()
+    xtype = _type_of(X.dtype, "X")
+    device = X.device
+    if device.type != "cuda":
+        raise TypeError("X must be on a GPU")
+    given_x, given_r = X, residual
+    X, ldx = _rows(X, "X")
+    t, k = X.shape
+    if weight is not None:
+        weight = _vector(weight, k, torch.float32, device, "weight")
+    ldr = lds = 0
+    if residual is not None:
+        if residual.dtype != X.dtype or residual.device != device or residual.shape != X.shape:
+            raise ValueError(f"residual must be a ({t}, {k}) {X.dtype} tensor on {device}")
+        residual, ldr = _rows(residual, "residual")
+    total = None
+    if residual is not None or sum_out is not None:
+        total, lds = _product_out(t, k, X.dtype, sum_out, device)
+        if sum_out is not None:
+            # element for element over an input, or apart from it (a row that stands for several cannot be written)
+            for x in (given_x, given_r):
+                if x is not None and _overlap(total, x) and (
+                        total.data_ptr() != x.data_ptr()
+                        or any(n > 1 and a != b for n, a, b in zip(x.shape, x.stride(), total.stride()))):
+                    raise ValueError("sum_out must be X or residual itself or not overlap them")
+    q = torch.empty((t, k), dtype=torch.int8, device=device)
+    scale = torch.empty(t, dtype=torch.float32, device=device)
+    _call(lib().ozaki2_rmsnorm_quantize, "ozaki2_rmsnorm_quantize", device, t, k, X.data_ptr(), ldx, xtype,
+          None if residual is None else residual.data_ptr(), ldr, None if weight is None else weight.data_ptr(), eps,
+          q.data_ptr(), max(k, 1), scale.data_ptr(), None if total is None else total.data_ptr(), lds)
+    return q, scale, total
 
 
 # ---- linear cross entropy ----------------------------------------------------
