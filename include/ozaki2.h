@@ -468,6 +468,40 @@ int ozaki2_i8linear_ws(int64_t t, int64_t n, int64_t k, const void *X, int64_t l
                        void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * ozaki2_i8gemm and ozaki2_i8linear with what follows a layer's product,
+ *
+ *   C[i][j] = act((sum_h A[i][h] B[j][h]) * a_scale[i] * b_scale[j] + bias[j]) + residual[i][j]
+ *
+ * in binary32, rounded once to ctype: the activation is taken of the value that
+ * ozaki2_i8gemm would round, so results do not depend on kernel, tile or slices either.
+ *   activation   an ozaki2_activation.
+ *   residual, ldr   DEVICE of type ctype, element (i, j) at residual[i*ldr + j], ldr >= max(1, n), or NULL for none (ldr is
+ *             then not looked at). It must not share memory with C (refused, from the first byte of each to its last).
+ * Workspaces: those of ozaki2_i8gemm_workspace_size and ozaki2_i8linear_workspace_size.
+ * Returns as ozaki2_i8gemm and ozaki2_i8linear with three more arguments: -1..-16 (the bias is never
+ * invalid; -12 for a residual that shares memory with C), -17 for the workspace.
+ */
+enum ozaki2_activation {
+    OZAKI2_ACT_NONE = 0,
+    OZAKI2_ACT_RELU = 1,      /* max(z, 0) */
+    OZAKI2_ACT_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2, the factor of z off by 4e-7 at most */
+    OZAKI2_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+    OZAKI2_ACT_SILU = 4       /* z / (1 + exp(-z)) */
+};                            /* (the last three give NaN for -inf) */
+int ozaki2_i8gemm_act(int64_t t, int64_t n, int64_t k, const int8_t *A, int64_t lda, const float *a_scale, const int8_t *B,
+                      int64_t ldb, const float *b_scale, const float *bias, int activation, const void *residual, int64_t ldr,
+                      void *C, int64_t ldc, int ctype, void *stream);
+int ozaki2_i8gemm_act_ws(int64_t t, int64_t n, int64_t k, const int8_t *A, int64_t lda, const float *a_scale, const int8_t *B,
+                         int64_t ldb, const float *b_scale, const float *bias, int activation, const void *residual,
+                         int64_t ldr, void *C, int64_t ldc, int ctype, void *workspace, size_t workspace_bytes, void *stream);
+int ozaki2_i8linear_act(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, int xtype, const int8_t *B, int64_t ldb,
+                        const float *b_scale, const float *bias, int activation, const void *residual, int64_t ldr, void *C,
+                        int64_t ldc, int ctype, void *stream);
+int ozaki2_i8linear_act_ws(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, int xtype, const int8_t *B, int64_t ldb,
+                           const float *b_scale, const float *bias, int activation, const void *residual, int64_t ldr, void *C,
+                           int64_t ldc, int ctype, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * The norm in front of a quantised layer: with h = X[i] + residual[i] (binary32, one rounding),
  *
  *   y[h] = h * w[h] / sqrt(mean_h h^2 + eps),
@@ -492,6 +526,67 @@ int ozaki2_i8linear_ws(int64_t t, int64_t n, int64_t k, const void *X, int64_t l
 int ozaki2_rmsnorm_quantize(int64_t t, int64_t k, const void *X, int64_t ldx, int type, const void *residual, int64_t ldr,
                             const float *weight, double eps, int8_t *Q, int64_t ldq, float *scale, void *sum, int64_t lds,
                             void *stream);
+
+/* ---- 16-bit layers and their gradients ------------------------------------
+ *
+ * A layer of 16-bit weights, row-major with the inner dimension contiguous in both operands:
+ *
+ *   Z[i][j] = sum_h X[i][h] W[j][h] + bias[j],   Y[i][j] = act(Z[i][j]) + residual[i][j]
+ *
+ * summed and finished in binary32, Z and Y rounded once each (act is taken of Z before its rounding).
+ *   t, n, k   rows of X (tokens), rows of W (channels), inner dimension; t < 2^29, n < 2^23, k < 2^29.
+ *   X, ldx    DEVICE, of `type`, element (i, h) at X[i*ldx + h], ldx >= max(1, k).
+ *   W, ldw    DEVICE, of `type`, element (j, h) at W[j*ldw + h], ldw >= max(1, k).
+ *   type      OZAKI2_BF16 or OZAKI2_FP16.
+ *   bias      DEVICE binary32 [n], or NULL for none.
+ *   activation   an ozaki2_activation.
+ *   residual, ldr   DEVICE of ytype, element (i, j) at residual[i*ldr + j], ldr >= max(1, n), or NULL for none. It must
+ *             not share memory with Y (refused, from the first byte of each to its last).
+ *   Y, ldy    DEVICE output of ytype, which is `type` or OZAKI2_FP32, ldy >= max(1, n).
+ *   Z, ldz    DEVICE output of `type`, ldz >= max(1, n), or NULL to skip it: what ozaki2_linear_grad needs.
+ * Outputs must not overlap the inputs or each other; elements between their rows are left as they were. Bitwise
+ * reproducible. Any alignment; multiples of 16 bytes are fastest. The workspace holds the sums of slices of a long k
+ * (for few tiles), and aligned copies of X and of at most 96 MiB of W where a row is no multiple of 16 bytes and t > 16.
+ * ozaki2_linear uses the cached workspace where it needs one, the _ws form the caller's (256-byte aligned, may be NULL if
+ * the size is 0; capturable into a HIP graph; calls that share one must be ordered on one stream).
+ * Returns 0, -1..-17 for an invalid argument (the bias is never invalid; -11 for a residual that shares memory with
+ * Y), -18 for a workspace that is NULL while needed or misaligned, or an OZAKI2_ERR_* code. t == 0 or n == 0 returns
+ * at once; k == 0 gives act(bias) + residual.
+ */
+int ozaki2_linear(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, const void *W, int64_t ldw, int type,
+                  const float *bias, int activation, const void *residual, int64_t ldr, void *Y, int64_t ldy, int ytype, void *Z,
+                  int64_t ldz, void *stream);
+size_t ozaki2_linear_workspace_size(int64_t t, int64_t n, int64_t k);
+int ozaki2_linear_ws(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, const void *W, int64_t ldw, int type,
+                     const float *bias, int activation, const void *residual, int64_t ldr, void *Y, int64_t ldy, int ytype,
+                     void *Z, int64_t ldz, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of that layer from the gradient dY of Y (of `type`; the residual's own gradient is dY): with
+ * G[i][j] = dY[i][j] act'(Z[i][j]),
+ *   dX[i][h] = sum_j G[i][j] W[j][h],  dW[j][h] = sum_i G[i][j] X[i][h],  dbias[j] = sum_i G[i][j].
+ * G is rounded once to `type` for the two products (without an activation it is dY itself) and not for dbias; sums are
+ * binary32, rounded once to `type`. act'(0) = 0 for relu; a Z that overflowed its type has the slope of its infinity.
+ *   t, n, k   as for ozaki2_linear, with n, k < 2^22.
+ *   dY, lddy  DEVICE, of `type`, lddy >= max(1, n).
+ *   Z, ldz    DEVICE, of `type`, as ozaki2_linear wrote it; not looked at with OZAKI2_ACT_NONE.
+ *   dX, lddx  DEVICE output of `type`, t rows of k, or NULL to skip it (W is then not read); lddx >= max(1, k).
+ *   dW, lddw  likewise, n rows of k (X is not read without it).
+ *   dbias     DEVICE output, binary32 [n], or NULL.
+ * Outputs must not overlap the inputs or each other. Bitwise reproducible. The workspace has room for G, for aligned
+ * copies of X and W (used where pointer, pitch or row are no multiples of 16 bytes) and for sums of slices.
+ * Returns 0, -1..-17 for an invalid argument, -19 for the workspace of the _ws form
+ * (ozaki2_linear_grad_workspace_size bytes with want_* nonzero for the outputs wanted), or an OZAKI2_ERR_* code. With
+ * t == 0 dW and dbias are set to zero, with n == 0 dX.
+ */
+int ozaki2_linear_grad(int64_t t, int64_t n, int64_t k, const void *dY, int64_t lddy, const void *X, int64_t ldx, const void *W,
+                       int64_t ldw, int type, int activation, const void *Z, int64_t ldz, void *dX, int64_t lddx, void *dW,
+                       int64_t lddw, float *dbias, void *stream);
+size_t ozaki2_linear_grad_workspace_size(int64_t t, int64_t n, int64_t k, int want_dx, int want_dw, int want_dbias);
+int ozaki2_linear_grad_ws(int64_t t, int64_t n, int64_t k, const void *dY, int64_t lddy, const void *X, int64_t ldx,
+                          const void *W, int64_t ldw, int type, int activation, const void *Z, int64_t ldz, void *dX,
+                          int64_t lddx, void *dW, int64_t lddw, float *dbias, void *workspace, size_t workspace_bytes,
+                          void *stream);
 
 /* ---- Linear cross entropy --------------------------------------------------
  *

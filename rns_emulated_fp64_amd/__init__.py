@@ -40,7 +40,9 @@ EXPORTS = (
     "ozaki2_xent", "ozaki2_xent_ws", "ozaki2_xent_workspace_size", "ozaki2_i8xent", "ozaki2_i8xent_ws",
     "ozaki2_i8xent_workspace_size",
     "ozaki2_xent_grad", "ozaki2_xent_grad_ws", "ozaki2_xent_grad_workspace_size",
-    "ozaki2_rmsnorm_quantize",
+    "ozaki2_rmsnorm_quantize", "ozaki2_i8gemm_act", "ozaki2_i8gemm_act_ws", "ozaki2_i8linear_act", "ozaki2_i8linear_act_ws",
+    "ozaki2_linear", "ozaki2_linear_ws", "ozaki2_linear_workspace_size", "ozaki2_linear_grad", "ozaki2_linear_grad_ws",
+    "ozaki2_linear_grad_workspace_size",
 )
 
 _lib = None
@@ -114,6 +116,15 @@ def lib() -> ctypes.CDLL:
     i8 = [i64, i64, i64, p, i64, i32, p, i64, p, p, p, i64, i32]
     L.ozaki2_i8linear.argtypes = i8 + [p]
     L.ozaki2_i8linear_ws.argtypes = i8 + [p, sz, p]
+    i8 = [i64, i64, i64, p, i64, p, p, i64, p, p, i32, p, i64, p, i64, i32]
+    L.ozaki2_i8gemm_act.argtypes = i8 + [p]
+    L.ozaki2_i8gemm_act_ws.argtypes = i8 + [p, sz, p]
+    i8 = [i64, i64, i64, p, i64, i32, p, i64, p, p, i32, p, i64, p, i64, i32]
+    L.ozaki2_i8linear_act.argtypes = i8 + [p]
+    L.ozaki2_i8linear_act_ws.argtypes = i8 + [p, sz, p]
+    for name in ("ozaki2_i8gemm_act", "ozaki2_i8linear_act"):
+        getattr(L, name).restype = i32
+        getattr(L, name + "_ws").restype = i32
     for name in ("ozaki2_i8gemm", "ozaki2_i8linear"):
         getattr(L, name).restype = i32
         getattr(L, name + "_ws").restype = i32
@@ -137,6 +148,19 @@ def lib() -> ctypes.CDLL:
     L.ozaki2_i8xent_workspace_size.restype = sz
     L.ozaki2_xent_grad_workspace_size.argtypes = [i64, i64, i64, i32, i32]
     L.ozaki2_xent_grad_workspace_size.restype = sz
+    lin = [i64, i64, i64, p, i64, p, i64, i32, p, i32, p, i64, p, i64, i32, p, i64]
+    L.ozaki2_linear.argtypes = lin + [p]
+    L.ozaki2_linear_ws.argtypes = lin + [p, sz, p]
+    lin = [i64, i64, i64, p, i64, p, i64, p, i64, i32, i32, p, i64, p, i64, p, i64, p]
+    L.ozaki2_linear_grad.argtypes = lin + [p]
+    L.ozaki2_linear_grad_ws.argtypes = lin + [p, sz, p]
+    for name in ("ozaki2_linear", "ozaki2_linear_grad"):
+        getattr(L, name).restype = i32
+        getattr(L, name + "_ws").restype = i32
+    L.ozaki2_linear_workspace_size.argtypes = [i64, i64, i64]
+    L.ozaki2_linear_workspace_size.restype = sz
+    L.ozaki2_linear_grad_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32]
+    L.ozaki2_linear_grad_workspace_size.restype = sz
     L.ozaki2_rmsnorm_quantize.argtypes = [i64, i64, p, i64, i32, p, i64, p, f64, p, i64, p, p, i64, p]
     L.ozaki2_rmsnorm_quantize.restype = i32
     L.ozaki2_finalize.argtypes = []
@@ -312,6 +336,60 @@ def ozaki2_xent_grad_ws(t, v, d, X, ldx, W, ldw, type, targets, ignore_index, ls
 
 def ozaki2_xent_grad_workspace_size(t, v, d, want_dx=True, want_dw=True) -> int:
     return lib().ozaki2_xent_grad_workspace_size(t, v, d, 1 if want_dx else 0, 1 if want_dw else 0)
+
+
+def ozaki2_i8gemm_act(t, n, k, A, lda, a_scale, B, ldb, b_scale, bias, activation, residual, ldr, C, ldc, ctype,
+                      stream=0) -> int:
+    return lib().ozaki2_i8gemm_act(t, n, k, A, lda, a_scale, B, ldb, b_scale, bias, activation, residual, ldr, C, ldc, ctype,
+                                   stream)
+
+
+def ozaki2_i8gemm_act_ws(t, n, k, A, lda, a_scale, B, ldb, b_scale, bias, activation, residual, ldr, C, ldc, ctype, workspace,
+                         workspace_bytes, stream=0) -> int:
+    return lib().ozaki2_i8gemm_act_ws(t, n, k, A, lda, a_scale, B, ldb, b_scale, bias, activation, residual, ldr, C, ldc, ctype,
+                                      workspace, workspace_bytes, stream)
+
+
+def ozaki2_i8linear_act(t, n, k, X, ldx, xtype, B, ldb, b_scale, bias, activation, residual, ldr, C, ldc, ctype,
+                        stream=0) -> int:
+    return lib().ozaki2_i8linear_act(t, n, k, X, ldx, xtype, B, ldb, b_scale, bias, activation, residual, ldr, C, ldc, ctype,
+                                     stream)
+
+
+def ozaki2_i8linear_act_ws(t, n, k, X, ldx, xtype, B, ldb, b_scale, bias, activation, residual, ldr, C, ldc, ctype, workspace,
+                           workspace_bytes, stream=0) -> int:
+    return lib().ozaki2_i8linear_act_ws(t, n, k, X, ldx, xtype, B, ldb, b_scale, bias, activation, residual, ldr, C, ldc, ctype,
+                                        workspace, workspace_bytes, stream)
+
+
+def ozaki2_linear(t, n, k, X, ldx, W, ldw, type, bias, activation, residual, ldr, Y, ldy, ytype, Z, ldz, stream=0) -> int:
+    return lib().ozaki2_linear(t, n, k, X, ldx, W, ldw, type, bias, activation, residual, ldr, Y, ldy, ytype, Z, ldz, stream)
+
+
+def ozaki2_linear_ws(t, n, k, X, ldx, W, ldw, type, bias, activation, residual, ldr, Y, ldy, ytype, Z, ldz, workspace,
+                     workspace_bytes, stream=0) -> int:
+    return lib().ozaki2_linear_ws(t, n, k, X, ldx, W, ldw, type, bias, activation, residual, ldr, Y, ldy, ytype, Z, ldz,
+                                  workspace, workspace_bytes, stream)
+
+
+def ozaki2_linear_workspace_size(t, n, k) -> int:
+    return lib().ozaki2_linear_workspace_size(t, n, k)
+
+
+def ozaki2_linear_grad(t, n, k, dY, lddy, X, ldx, W, ldw, type, activation, Z, ldz, dX, lddx, dW, lddw, dbias,
+                       stream=0) -> int:
+    return lib().ozaki2_linear_grad(t, n, k, dY, lddy, X, ldx, W, ldw, type, activation, Z, ldz, dX, lddx, dW, lddw, dbias,
+                                    stream)
+
+
+def ozaki2_linear_grad_ws(t, n, k, dY, lddy, X, ldx, W, ldw, type, activation, Z, ldz, dX, lddx, dW, lddw, dbias, workspace,
+                          workspace_bytes, stream=0) -> int:
+    return lib().ozaki2_linear_grad_ws(t, n, k, dY, lddy, X, ldx, W, ldw, type, activation, Z, ldz, dX, lddx, dW, lddw, dbias,
+                                       workspace, workspace_bytes, stream)
+
+
+def ozaki2_linear_grad_workspace_size(t, n, k, want_dx=True, want_dw=True, want_dbias=True) -> int:
+    return lib().ozaki2_linear_grad_workspace_size(t, n, k, 1 if want_dx else 0, 1 if want_dw else 0, 1 if want_dbias else 0)
 
 
 def ozaki2_rmsnorm_quantize(t, k, X, ldx, type, residual, ldr, weight, eps, Q, ldq, scale, sum, lds, stream=0) -> int:
@@ -572,13 +650,37 @@ def quantize_rows(X):
     return q, scale
 
 
-def i8gemm(A, B, a_scale, b_scale, bias=None, out_dtype=None, out=None, workspace=None):
-    """C[t, n] = (sum_k A[t, k] B[n, k]) * a_scale[t] * b_scale[n] + bias[n] for int8 A (t, k) and B (n, k), the
-    layout of a linear layer (ozaki2_i8gemm_ws). The scales and the bias are float32; ``out_dtype`` is bfloat16
-    (default), float16 or float32; ``workspace`` (optional) a tensor of ``ozaki2_i8gemm_workspace_size`` bytes."""
+#: names of the activations, as enum ozaki2_activation numbers them
+ACTIVATIONS = {None: 0, "none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4}
+
+
+def _activation(name):
+    act = ACTIVATIONS.get(name)
+    if act is None:
+        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, not {name!r}")
+    return act
+
+
+def _residual(residual, t, n, dtype, device):
+    """A residual's tensor (a copy if its rows are not contiguous), pointer and pitch."""
+    if residual is None:
+        return None, None, 0
+    if residual.dtype != dtype or residual.device != device or tuple(residual.shape) != (t, n):
+        raise ValueError(f"residual must be a ({t}, {n}) {dtype} tensor on {device}")
+    residual, ldr = _rows(residual, "residual")
+    return residual, residual.data_ptr(), ldr
+
+
+def i8gemm(A, B, a_scale, b_scale, bias=None, out_dtype=None, out=None, workspace=None, activation=None, residual=None):
+    """C[t, n] = act((sum_k A[t, k] B[n, k]) * a_scale[t] * b_scale[n] + bias[n]) + residual[t, n] for int8 A (t, k) and
+    B (n, k), the layout of a linear layer (ozaki2_i8gemm_ws; with an activation, a name from ACTIVATIONS, or a residual
+    ozaki2_i8gemm_act_ws). The scales and the bias are float32; ``out_dtype`` is bfloat16 (default), float16 or
+    float32; the residual has that dtype and shares no memory with ``out``; ``workspace`` (optional) a tensor of
+    ``ozaki2_i8gemm_workspace_size`` bytes."""
     torch = _torch or _load_torch()
     dt = out_dtype if out_dtype is not None else out.dtype if out is not None else torch.bfloat16
     ctype = _type_of(dt, "out_dtype")
+    act = _activation(activation)
     device = A.device
     if A.dtype != torch.int8 or B.dtype != torch.int8 or device.type != "cuda" or B.device != device:
         raise TypeError("A and B must be int8 tensors on the same GPU")
@@ -595,19 +697,27 @@ def i8gemm(A, B, a_scale, b_scale, bias=None, out_dtype=None, out=None, workspac
     C, ldc = _product_out(t, n, dt, out, device)
     L = lib()
     ws, wp, wb = _workspace(L.ozaki2_i8gemm_workspace_size(t, n, k), workspace, device)
+    if act or residual is not None:
+        residual, rp, ldr = _residual(residual, t, n, dt, device)
+        _call(L.ozaki2_i8gemm_act_ws, "ozaki2_i8gemm_act_ws", device, t, n, k, A.data_ptr(), lda, a_scale.data_ptr(),
+              B.data_ptr(), ldb, b_scale.data_ptr(), None if bias is None else bias.data_ptr(), act, rp, ldr, C.data_ptr(), ldc,
+              ctype, wp, wb)
+        return C
     _call(L.ozaki2_i8gemm_ws, "ozaki2_i8gemm_ws", device, t, n, k, A.data_ptr(), lda, a_scale.data_ptr(), B.data_ptr(),
           ldb, b_scale.data_ptr(), None if bias is None else bias.data_ptr(), C.data_ptr(), ldc, ctype, wp, wb)
     return C
 
 
-def i8linear(X, B, b_scale, bias=None, out_dtype=None, out=None, workspace=None):
+def i8linear(X, B, b_scale, bias=None, out_dtype=None, out=None, workspace=None, activation=None, residual=None):
     """A linear layer with int8 weights B (n, k) and a scale per channel: the rows of X (t, k; bfloat16, float16 or
-    float32) are quantised as quantize_rows does and multiplied as i8gemm does, bit for bit (ozaki2_i8linear_ws).
-    The result has X's dtype unless ``out_dtype`` or ``out`` says otherwise."""
+    float32) are quantised as quantize_rows does and multiplied as i8gemm does, bit for bit (ozaki2_i8linear_ws,
+    ozaki2_i8linear_act_ws). The result has X's dtype unless ``out_dtype`` or ``out`` says otherwise, and so has the
+    residual."""
     torch = _torch or _load_torch()
     xtype = _type_of(X.dtype, "X")
     dt = out_dtype if out_dtype is not None else out.dtype if out is not None else X.dtype
     ctype = _type_of(dt, "out_dtype")
+    act = _activation(activation)
     device = X.device
     if B.dtype != torch.int8 or device.type != "cuda" or B.device != device:
         raise TypeError("X and int8 B must be on the same GPU")
@@ -623,6 +733,11 @@ def i8linear(X, B, b_scale, bias=None, out_dtype=None, out=None, workspace=None)
     C, ldc = _product_out(t, n, dt, out, device)
     L = lib()
     ws, wp, wb = _workspace(L.ozaki2_i8linear_workspace_size(t, n, k), workspace, device)
+    if act or residual is not None:
+        residual, rp, ldr = _residual(residual, t, n, dt, device)
+        _call(L.ozaki2_i8linear_act_ws, "ozaki2_i8linear_act_ws", device, t, n, k, X.data_ptr(), ldx, xtype, B.data_ptr(), ldb,
+              b_scale.data_ptr(), None if bias is None else bias.data_ptr(), act, rp, ldr, C.data_ptr(), ldc, ctype, wp, wb)
+        return C
     _call(L.ozaki2_i8linear_ws, "ozaki2_i8linear_ws", device, t, n, k, X.data_ptr(), ldx, xtype, B.data_ptr(), ldb,
           b_scale.data_ptr(), None if bias is None else bias.data_ptr(), C.data_ptr(), ldc, ctype, wp, wb)
     return C
@@ -665,6 +780,75 @@ def rmsnorm_quantize(X, weight=None, residual=None, eps=1e-6, sum_out=None):
           None if residual is None else residual.data_ptr(), ldr, None if weight is None else weight.data_ptr(), eps,
           q.data_ptr(), max(k, 1), scale.data_ptr(), None if total is None else total.data_ptr(), lds)
     return q, scale, total
+
+
+# ---- 16-bit layers -----------------------------------------------------------
+def _layer_operands(X, W):
+    torch = _torch or _load_torch()
+    device = X.device
+    if device.type != "cuda" or W.device != device:
+        raise TypeError("X and W must be on the same GPU")
+    kind = _xent_type(X, W)
+    X, ldx = _rows(X, "X")
+    W, ldw = _rows(W, "W")
+    t, k = X.shape
+    if W.shape[1] != k:
+        raise ValueError("X and W must have the same number of columns")
+    return device, kind, t, W.shape[0], k, X, ldx, W, ldw
+
+
+def linear(X, W, bias=None, activation=None, residual=None, out_dtype=None, out=None, want_pre=False, workspace=None):
+    """A linear layer with what follows it: (Y, Z) with Z = X @ W.T + bias and Y = act(Z) + residual (ozaki2_linear_ws).
+    X (t, k) and W (n, k) are bfloat16 or float16, the bias float32 (n,), the activation a name from ACTIVATIONS. Y has
+    X's dtype unless ``out_dtype`` or ``out`` says float32, and the residual (t, n) has Y's and shares no memory with
+    ``out``. Z, in X's dtype, is what linear_grad needs of a layer with an activation; it is None unless ``want_pre``.
+    Autograd does not see the call."""
+    torch = _torch or _load_torch()
+    device, kind, t, n, k, X, ldx, W, ldw = _layer_operands(X, W)
+    act = _activation(activation)
+    dt = out_dtype if out_dtype is not None else out.dtype if out is not None else X.dtype
+    if dt != X.dtype and dt != torch.float32:
+        raise TypeError(f"the result must be {X.dtype} or float32, not {dt}")
+    if bias is not None:
+        bias = _vector(bias, n, torch.float32, device, "bias")
+    residual, rp, ldr = _residual(residual, t, n, dt, device)
+    Y, ldy = _product_out(t, n, dt, out, device)
+    Z = torch.empty((t, n), dtype=X.dtype, device=device) if want_pre else None
+    L = lib()
+    ws, wp, wb = _workspace(L.ozaki2_linear_workspace_size(t, n, k), workspace, device)
+    _call(L.ozaki2_linear_ws, "ozaki2_linear_ws", device, t, n, k, X.data_ptr(), ldx, W.data_ptr(), ldw, kind,
+          None if bias is None else bias.data_ptr(), act, rp, ldr, Y.data_ptr(), ldy, FP32 if dt == torch.float32 else kind,
+          Z.data_ptr() if want_pre else None, max(n, 1), wp, wb)
+    return Y, Z
+
+
+def linear_grad(dY, X, W, Z=None, activation=None, want_dx=True, want_dw=True, want_dbias=True, workspace=None):
+    """(dX, dW, dbias), the gradients of linear's layer from that of Y (ozaki2_linear_grad_ws); None for one that is not
+    wanted. dY (t, n) has X's dtype, and so has Z, which linear returned with ``want_pre`` and which a layer without an
+    activation does not need. dX and dW have X's dtype, dbias is float32; the residual's gradient is dY itself."""
+    torch = _torch or _load_torch()
+    device, kind, t, n, k, X, ldx, W, ldw = _layer_operands(X, W)
+    act = _activation(activation)
+    if act and Z is None:
+        raise ValueError("a layer with an activation needs Z")
+    for x, what in ((dY, "dY"), (Z if act else None, "Z")):
+        if x is not None and (x.dtype != X.dtype or x.device != device or tuple(x.shape) != (t, n)):
+            raise ValueError(f"{what} must be a ({t}, {n}) {X.dtype} tensor on {device}")
+    dY, lddy = _rows(dY, "dY")
+    zp = ldz = 0
+    if act:
+        Z, ldz = _rows(Z, "Z")
+        zp = Z.data_ptr()
+    dX = torch.empty((t, k), dtype=X.dtype, device=device) if want_dx else None
+    dW = torch.empty((n, k), dtype=X.dtype, device=device) if want_dw else None
+    dbias = torch.empty(n, dtype=torch.float32, device=device) if want_dbias else None
+    L = lib()
+    size = L.ozaki2_linear_grad_workspace_size(t, n, k, 1 if want_dx else 0, 1 if want_dw else 0, 1 if want_dbias else 0)
+    ws, wp, wb = _workspace(size, workspace, device)
+    _call(L.ozaki2_linear_grad_ws, "ozaki2_linear_grad_ws", device, t, n, k, dY.data_ptr(), lddy, X.data_ptr(), ldx,
+          W.data_ptr(), ldw, kind, act, zp, ldz, dX.data_ptr() if want_dx else None, max(k, 1),
+          dW.data_ptr() if want_dw else None, max(k, 1), dbias.data_ptr() if want_dbias else None, wp, wb)
+    return dX, dW, dbias
 
 
 # ---- linear cross entropy ----------------------------------------------------

@@ -1,0 +1,329 @@
+// epilogue.h -- what follows a layer's product before it reaches memory, for the
+// tiles of tile.h:
+//
+//   Z = R (sb[b] sa[a]) + bias[a],   Y = act(Z) + residual[b][a]
+//
+// in binary32, Z and Y rounded once each. The activation is one of five, chosen per
+// launch outside the loops over the accumulators.
+#pragma once
+
+#include "tile.h"
+
+namespace oz2 {
+
+constexpr bool is_activation(int act) { return act >= OZAKI2_ACT_NONE && act <= OZAKI2_ACT_SILU; }
+
+// 1 / (1 + exp(-x)): 0 and 1 at the infinities. The hardware's exponential and
+// reciprocal, each off by a step of binary32.
+__device__ __forceinline__ float sigmoid(float x) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * x));
+}
+// The two parts of the normal distribution's function at z: below min(z, -z), and exp(-z^2 / 2).
+// erfc(x) = t (a1 + .. + a5 t^4) exp(-x^2), t = 1 / (1 + p x), by Abramowitz and
+// Stegun, Handbook of Mathematical Functions, 7.1.26: off by 1.5e-7 at most, and less
+// where the exponential is small.
+__device__ __forceinline__ float normal_tail(float z, float &bell) {
+    const float x = fabsf(z);
+    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f * 0.70710678f, x, 1.f));
+    float p = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+    p = fmaf(t, p, 0.5f * 1.421413741f);
+    p = fmaf(t, p, 0.5f * -0.284496736f);
+    p = fmaf(t, p, 0.5f * 0.254829592f);
+    bell = __builtin_amdgcn_exp2f(z * z * (-0.5f * kLog2e));
+    return t * p * bell;
+}
+constexpr float kTanhScale = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kTanhCubic = 0.044715f;
+
+// act(z). -inf gives NaN for the last three, as z times 0 does.
+template <int ACT>
+__device__ __forceinline__ float activated(float z) {
+    if constexpr (ACT == OZAKI2_ACT_RELU) return z < 0.f ? 0.f : z;
+    if constexpr (ACT == OZAKI2_ACT_GELU) {
+        float bell;
+        const float tail = normal_tail(z, bell);
+        return z * (z > 0.f ? 1.f - tail : tail);
+    }
+    // (1 + tanh u) / 2 = sigmoid(2 u)
+    if constexpr (ACT == OZAKI2_ACT_GELU_TANH) return z * sigmoid(z * fmaf(kTanhScale * kTanhCubic, z * z, kTanhScale));
+    if constexpr (ACT == OZAKI2_ACT_SILU) return z * sigmoid(z);
+    return z;
+}
+// d act / dz; 0 for relu at 0. The factor z stays finite (beyond 64 what it meets is 0), so
+// that a Z that overflowed its type has the slope of the infinity, 0 or 1.
+template <int ACT>
+__device__ __forceinline__ float slope_of(float z) {
+    const float near = fminf(fmaxf(z, -64.f), 64.f);
+    if constexpr (ACT == OZAKI2_ACT_RELU) return z > 0.f ? 1.f : z <= 0.f ? 0.f : z;
+    if constexpr (ACT == OZAKI2_ACT_GELU) {
+        float bell;
+        const float tail = normal_tail(z, bell);
+        return fmaf(near, 0.3989422804f * bell, z > 0.f ? 1.f - tail : tail);
+    }
+    if constexpr (ACT == OZAKI2_ACT_GELU_TANH || ACT == OZAKI2_ACT_SILU) {
+        // d (z s(f)) = s + z f' s (1 - s), 1 - s taken as s(-f) so that far tails are not a difference
+        float f = z, df = near;
+        if constexpr (ACT == OZAKI2_ACT_GELU_TANH) {
+            f = z * fmaf(kTanhScale * kTanhCubic, z * z, kTanhScale);
+            df *= fmaf(3.f * kTanhScale * kTanhCubic, near * near, kTanhScale);
+        }
+        const float s = sigmoid(f), c = sigmoid(-f);
+        return fmaf(df * s, c, s);
+    }
+    return 1.f;
+}
+// body(std::integral_constant<int, ACT>) for the activation of a launch.
+template <class Body>
+__device__ __forceinline__ void with_activation(int act, Body body) {
+    switch (act) {
+    case OZAKI2_ACT_RELU: return body(std::integral_constant<int, OZAKI2_ACT_RELU>{});
+    case OZAKI2_ACT_GELU: return body(std::integral_constant<int, OZAKI2_ACT_GELU>{});
+    case OZAKI2_ACT_GELU_TANH: return body(std::integral_constant<int, OZAKI2_ACT_GELU_TANH>{});
+    case OZAKI2_ACT_SILU: return body(std::integral_constant<int, OZAKI2_ACT_SILU>{});
+    default: return body(std::integral_constant<int, OZAKI2_ACT_NONE>{});
+    }
+}
+
+// 16 bytes of a row, of which `left` elements are the row's own; zeros beyond.
+template <class T>
+__device__ __forceinline__ U16 load_some(const T *src, int64_t left) {
+    constexpr int N = 16 / (int)sizeof(T);
+    if (left >= N) return *(const U16 *)src;
+    T e[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) e[i] = i < left ? src[i] : (T)0.f;
+    return __builtin_bit_cast(U16, e);
+}
+template <class T>
+__device__ __forceinline__ void unpack2(uint32_t w, float &x, float &y) {
+    typedef T v2 __attribute__((ext_vector_type(2)));
+    const v2 p = __builtin_bit_cast(v2, w);
+    x = (float)p[0];
+    y = (float)p[1];
+}
+
+// What a layer's epilogue does. PreT: the type of Z where it may be stored, or void.
+template <class OutT, class PreT>
+struct Finish {
+    const float *bias;      // per row of A, or null
+    int act;
+    const OutT *residual;   // or null
+    int64_t ldr;
+    PreT *pre;              // or null
+    int64_t ldpre;
+};
+
+// SCALED: integer sums, times sb[b] sa[a], with the roundings of EpiScale.
+template <class OutT, class PreT, bool SCALED>
+struct EpiAct {
+    struct Args {
+        OutT *out;
+        int64_t ldo;            // elements
+        const float *sa, *sb;   // SCALED
+        Finish<OutT, PreT> f;
+        int64_t na, nb;
+    };
+    static constexpr int STORES = sizeof(OutT) == 2 ? 1 : 2;  // at least: Z's come on top
+    static constexpr bool PADDED = false;
+
+    template <class M, int RT, int CT, bool EDGE, bool AGPR = false>
+    static __device__ __forceinline__ void run(v4i (&acc)[RT][CT], const TileWhere &w, const Args &e) {
+        with_activation(e.f.act, [&](auto act) { body<decltype(act)::value, M, RT, CT, EDGE, AGPR>(acc, w, e); });
+    }
+
+    template <int ACT, class M, int RT, int CT, bool EDGE, bool AGPR>
+    static __device__ __forceinline__ void body(v4i (&acc)[RT][CT], const TileWhere &w, const Args &e) {
+        const int lane = fresh_lane();
+        const int64_t b0 = w.b0 + (lane & 15);
+        const int64_t a0 = w.a0 + 4 * (lane >> 4);
+        float sb[SCALED ? CT : 1];
+        if constexpr (SCALED) {
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                const int64_t b = b0 + 16 * j;
+                sb[j] = e.sb[EDGE && b >= e.nb ? e.nb - 1 : b];
+            }
+        }
+        // four values of a vector per row of A, zeros past its end
+        auto four = [&](const float *p, int64_t a, float(&x)[4]) {
+            if (!EDGE || a + 4 <= e.na) {
+                const U16 u = *(const U16 *)(p + a);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) x[v] = __uint_as_float(u.w[v]);
+            } else {
+#pragma unroll
+                for (int v = 0; v < 4; ++v) x[v] = a + v < e.na ? p[a + v] : 0.f;
+            }
+        };
+        auto before = [&](int bits, int j, float sa, float bias) {
+            if constexpr (SCALED) return fmaf(M::value(bits) * sb[j], sa, bias);
+            return M::value(bits) + bias;
+        };
+        if constexpr (RT == 1) {  // no neighbour to trade with: four results per store
+            static_assert(EDGE, "the short kernels check every store");
+            float sa[4] = {0.f, 0.f, 0.f, 0.f}, bi[4] = {0.f, 0.f, 0.f, 0.f};
+            if constexpr (SCALED) four(e.sa, a0, sa);
+            if (e.f.bias) four(e.f.bias, a0, bi);
+            const int64_t left = e.na - a0;
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                const int64_t b = b0 + 16 * j;
+                if (b >= e.nb) continue;
+                float x[4];
+#pragma unroll
+                for (int v = 0; v < 4; ++v) x[v] = before(acc[0][j][v], j, sa[v], bi[v]);
+                if constexpr (!std::is_void_v<PreT>)
+                    if (e.f.pre) store_four(e.f.pre + b * e.f.ldpre + a0, x, left);
+#pragma unroll
+                for (int v = 0; v < 4; ++v) x[v] = activated<ACT>(x[v]);
+                if (e.f.residual) {
+                    const OutT *r = e.f.residual + b * e.f.ldr + a0;
+#pragma unroll
+                    for (int v = 0; v < 4; ++v)
+                        if (v < left) x[v] += (float)r[v];
+                }
+                store_four(e.out + b * e.ldo + a0, x, left);
+            }
+        } else {
+            constexpr int RW = sizeof(OutT) == 2 ? 1 : 2;  // 16-byte loads of the residual per pair of tiles
+            const int64_t st0 = w.a0 + pair_start<OutT>(lane);
+#pragma unroll
+            for (int i = 0; i < RT; i += 2) {
+                float sa[2][4], bi[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if constexpr (SCALED) four(e.sa, a0 + 16 * (i + h), sa[h]);
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) bi[h][v] = 0.f;
+                    if (e.f.bias) four(e.f.bias, a0 + 16 * (i + h), bi[h]);
+                }
+                // the residual in the layout of the stores, all of it on its way at once
+                U16 r[CT][RW];
+                if (e.f.residual) {
+#pragma unroll
+                    for (int j = 0; j < CT; ++j)
+#pragma unroll
+                        for (int h = 0; h < RW; ++h) {
+                            const int64_t b = b0 + 16 * j, a = st0 + 16 * (i + h);
+                            const OutT *from = e.f.residual + b * e.f.ldr + a;
+                            r[j][h] = EDGE ? load_some(from, b < e.nb ? e.na - a : 0) : *(const U16 *)from;
+                        }
+                }
+#pragma unroll
+                for (int j = 0; j < CT; ++j) {
+                    float x[2][4];
+                    keep<AGPR>(acc[i][j]);
+                    keep<AGPR>(acc[i + 1][j]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) x[h][v] = before(acc[i + h][j][v], j, SCALED ? sa[h][v] : 1.f, bi[h][v]);
+                    const int64_t b = b0 + 16 * j;
+                    if constexpr (!std::is_void_v<PreT>)
+                        if (e.f.pre)
+                            store_pair<PreT, EDGE>(x, e.f.pre + b * e.f.ldpre, w.a0 + pair_start<PreT>(lane) + 16 * i, e.na,
+                                                   b < e.nb);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int v = 0; v < 4; ++v) x[h][v] = activated<ACT>(x[h][v]);
+                    if (e.f.residual) {
+                        if constexpr (RW == 1) {
+                            // trade_pair's exchange is its own inverse
+                            const auto p = __builtin_amdgcn_permlane16_swap(r[j][0].w[0], r[j][0].w[2], false, false);
+                            const auto q = __builtin_amdgcn_permlane16_swap(r[j][0].w[1], r[j][0].w[3], false, false);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float o[4];
+                                unpack2<OutT>(p[h], o[0], o[1]);
+                                unpack2<OutT>(q[h], o[2], o[3]);
+#pragma unroll
+                                for (int v = 0; v < 4; ++v) x[h][v] += o[v];
+                            }
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int v = 0; v < 4; ++v) x[h][v] += __uint_as_float(r[j][RW - 1 < h ? 0 : h].w[v]);
+                        }
+                    }
+                    store_pair<OutT, EDGE>(x, e.out + b * e.ldo, st0 + 16 * i, e.na, b < e.nb);
+                    // one pair of tiles at a time (see EpiScale)
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        }
+    }
+
+    template <class T>
+    static __device__ __forceinline__ void store_four(T *dst, const float (&x)[4], int64_t left) {
+        if constexpr (sizeof(T) == 4) {
+            store_some(dst, U16{{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])}},
+                       left);
+        } else if (left >= 4) {
+            *(U8 *)dst = U8{{pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3])}};
+        } else {
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+                if (v < left) dst[v] = rounded<T>(x[v]);
+        }
+    }
+};
+
+// Sums the planes of a product's slices of k (EpiRaw) in their order and finishes them as
+// EpiAct does; four outputs per thread.
+template <class OutT, class PreT, bool SCALED>
+__global__ __launch_bounds__(256) void k_join_act(const uint32_t *__restrict__ planes, int splits, int64_t plane, int64_t ldp,
+                                                  typename EpiAct<OutT, PreT, SCALED>::Args e) {
+    typedef std::conditional_t<SCALED, v4i, v4f> Sum;
+    const int64_t a = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+    if (a >= e.na) return;
+    with_activation(e.f.act, [&](auto act) {
+        for (int64_t b = blockIdx.y; b < e.nb; b += gridDim.y) {
+            const uint32_t *from = planes + b * ldp + a;
+            Sum s = *(const Sum *)from;
+            int i = 1;
+            for (; i + 8 <= splits; i += 8) {  // eight loads on their way at a time
+                Sum o[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = *(const Sum *)(from + (i + j) * plane);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s += o[j];
+            }
+            for (; i < splits; ++i) s += *(const Sum *)(from + i * plane);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                if (a + v >= e.na) continue;
+                const float bias = e.f.bias ? e.f.bias[a + v] : 0.f;
+                float x;
+                if constexpr (SCALED)
+                    x = fmaf((float)s[v] * e.sb[b], e.sa[a + v], bias);
+                else
+                    x = s[v] + bias;
+                if constexpr (!std::is_void_v<PreT>)
+                    if (e.f.pre) e.f.pre[b * e.f.ldpre + a + v] = rounded<PreT>(x);
+                x = activated<decltype(act)::value>(x);
+                if (e.f.residual) x += (float)e.f.residual[b * e.f.ldr + a + v];
+                e.out[b * e.ldo + a + v] = rounded<OutT>(x);
+            }
+        }
+    });
+}
+template <class OutT, class PreT, bool SCALED>
+hipError_t launch_join_act(const void *planes, int splits, int64_t plane, int64_t ldp,
+                           const typename EpiAct<OutT, PreT, SCALED>::Args &e, hipStream_t s) {
+    const dim3 grid((unsigned)((e.na + 1023) / 1024), (unsigned)(e.nb < 65535 ? e.nb : 65535));
+    hipLaunchKernelGGL((k_join_act<OutT, PreT, SCALED>), grid, dim3(256), 0, s, (const uint32_t *)planes, splits, plane, ldp, e);
+    return hipGetLastError();
+}
+
+// Whether two row-major matrices of t x n elements of `size` bytes share memory, from
+// the first byte of each to its last.
+inline bool share_memory(const void *p, int64_t ldp, const void *q, int64_t ldq, int64_t t, int64_t n, int64_t size) {
+    if (p == nullptr || q == nullptr || t <= 0 || n <= 0) return false;
+    const uintptr_t p0 = (uintptr_t)p, p1 = p0 + (uintptr_t)(((t - 1) * ldp + n) * size);
+    const uintptr_t q0 = (uintptr_t)q, q1 = q0 + (uintptr_t)(((t - 1) * ldq + n) * size);
+    return p0 < q1 && q0 < p1;
+}
+
+}  // namespace oz2

@@ -1,0 +1,514 @@
+// linear.hip -- layers of 16-bit weights and their gradients, through their C entry
+// points (include/ozaki2.h):
+//
+//   ozaki2_linear       Z[t][n] = X[t] . W[n] + bias[n],  Y = act(Z) + residual
+//   ozaki2_linear_grad  G = dY act'(Z),  dX = G W,  dW = G^T X,  dbias[n] = sum_t G[t][n]
+//
+// The products run on tile.h's kernels; what follows them is their epilogue
+// (epilogue.h), so Z and Y go to memory once, rounded once. Backward, one pass over dY
+// and Z leaves G in 16 bits and the sums of its columns; the two products then read
+// W, X and G across their rows where they need them so (k_tile_p's K-major
+// operands). The matrix cores bound all of it but for few tokens, where W's bytes do.
+#include <hip/hip_runtime.h>
+
+#include "common.h"
+#include "epilogue.h"
+#include "ozaki2.h"
+
+namespace oz2 {
+namespace {
+
+// ---- forward ----------------------------------------------------------------------
+struct LinearArgs {
+    int64_t t, n, k;
+    const void *X;
+    int64_t ldx;
+    const void *W;
+    int64_t ldw;
+    const float *bias;
+    int act;
+    const void *residual;  // of Y's type, or null
+    int64_t ldr;
+    void *Y;
+    int64_t ldy;
+    void *Z;  // of X's type, or null
+    int64_t ldz;
+};
+
+TileArgs rows_of(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, const void *W, int64_t ldw) {
+    TileArgs ta{};
+    ta.A = (const int8_t *)W;  // the index that is contiguous in the result
+    ta.B = (const int8_t *)X;
+    ta.lda = 2 * ldw;
+    ta.ldb = 2 * ldx;
+    ta.na = n;
+    ta.nb = t;
+    ta.kbytes = 2 * k;
+    return ta;
+}
+// Slices of k, from the sizes alone: operands that are not aligned take as many.
+int splits_of(int64_t t, int64_t n, int64_t k) {
+    TileArgs ta{};
+    ta.na = n;
+    ta.nb = t;
+    ta.kbytes = (2 * k + 15) / 16 * 16;
+    return tile_splits(choose_tile(ta, false), n, t, ta.kbytes);
+}
+int64_t plane_pitch(int64_t n) { return (n + 7) / 8 * 8; }
+size_t plane_bytes(int64_t t, int64_t n, int splits) {
+    return splits > 1 ? up256((size_t)splits * (size_t)t * (size_t)plane_pitch(n) * 4) : 0;
+}
+// Aligned copies of X and of a run of W where a row is no multiple of 16 bytes, and the
+// planes; the last, shorter run may have more slices than the others.
+size_t forward_bytes(int64_t t, int64_t n, int64_t k) {
+    if (!needs_pack(2 * k, t)) return plane_bytes(t, n, splits_of(t, n, k));
+    const int64_t run = pack_rows(n, 2 * k), rest = n % run;
+    const size_t full = plane_bytes(t, run, splits_of(t, run, k)), last = rest ? plane_bytes(t, rest, splits_of(t, rest, k)) : 0;
+    return up256((size_t)t * (size_t)pack_pitch(2 * k)) + up256((size_t)run * (size_t)pack_pitch(2 * k)) +
+           (full > last ? full : last);
+}
+
+template <class M, class OutT>
+int forward_rows(const LinearArgs &p, char *ws, hipStream_t s) {
+    typedef typename M::Elem T;
+    typedef EpiAct<OutT, T, false> Epi;
+    const TileArgs ta = rows_of(p.t, p.n, p.k, p.X, p.ldx, p.W, p.ldw);
+    const typename Epi::Args e = {(OutT *)p.Y, p.ldy, nullptr, nullptr,
+                                  {p.bias, p.act, (const OutT *)p.residual, p.ldr, (T *)p.Z, p.ldz}, p.n, p.t};
+    const Tile tile = choose_tile(ta, false);
+    const int splits = tile == Tile::skinny ? 1 : splits_of(p.t, p.n, p.k);
+    if (splits == 1) {
+        HIP_TRY((launch_tile<M, Epi, false>(ta, e, tile, 1, s)));
+        return OZAKI2_SUCCESS;
+    }
+    const int64_t ldp = plane_pitch(p.n), plane = p.t * ldp;
+    HIP_TRY((launch_tile<M, EpiRaw, false>(ta, {(uint32_t *)ws, ldp, plane, p.n, p.t}, tile, splits, s)));
+    HIP_TRY((launch_join_act<OutT, T, false>(ws, splits, plane, ldp, e, s)));
+    return OZAKI2_SUCCESS;
+}
+
+template <class M, class OutT>
+int forward(const LinearArgs &p, char *ws, hipStream_t s) {
+    if (!needs_pack(2 * p.k, p.t)) return forward_rows<M, OutT>(p, ws, s);
+    const int64_t pitch = pack_pitch(2 * p.k), run = pack_rows(p.n, 2 * p.k);
+    char *w = ws + up256((size_t)p.t * (size_t)pitch), *planes = w + up256((size_t)run * (size_t)pitch);
+    HIP_TRY(launch_pack_rows(p.X, 2 * p.ldx, p.t, 2 * p.k, ws, pitch, s));
+    for (int64_t n0 = 0; n0 < p.n; n0 += run) {
+        LinearArgs q = p;
+        q.n = p.n - n0 < run ? p.n - n0 : run;
+        q.k = (p.k + 7) / 8 * 8;
+        q.X = ws;
+        q.W = w;
+        q.ldx = q.ldw = pitch / 2;
+        if (q.bias) q.bias += n0;
+        if (q.residual) q.residual = (const OutT *)p.residual + n0;
+        q.Y = (OutT *)p.Y + n0;
+        if (q.Z) q.Z = (typename M::Elem *)p.Z + n0;
+        HIP_TRY(launch_pack_rows((const char *)p.W + 2 * n0 * p.ldw, 2 * p.ldw, q.n, 2 * p.k, w, pitch, s));
+        const int st = forward_rows<M, OutT>(q, planes, s);
+        if (st) return st;
+    }
+    return OZAKI2_SUCCESS;
+}
+
+// ---- backward ---------------------------------------------------------------------
+// out[b][a] = round(R).
+template <class OutT>
+struct EpiRound {
+    struct Args {
+        OutT *out;
+        int64_t ldo;
+        int64_t na, nb;
+    };
+    static constexpr int STORES = 1;
+    static constexpr bool PADDED = false;
+
+    template <class M, int RT, int CT, bool EDGE, bool AGPR = false>
+    static __device__ __forceinline__ void run(v4i (&acc)[RT][CT], const TileWhere &w, const Args &e) {
+        const int lane = fresh_lane();
+        const int64_t st0 = w.a0 + pair_start<OutT>(lane), b0 = w.b0 + (lane & 15);
+#pragma unroll
+        for (int i = 0; i < RT; i += 2)
+#pragma unroll
+            for (int j = 0; j < CT; ++j) {
+                keep<AGPR>(acc[i][j]);
+                keep<AGPR>(acc[i + 1][j]);
+                float x[2][4];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) x[h][v] = M::value(acc[i + h][j][v]);
+                const int64_t b = b0 + 16 * j;
+                store_pair<OutT, EDGE>(x, e.out + b * e.ldo, st0 + 16 * i, e.na, b < e.nb);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+    }
+};
+
+// G = dY act'(Z) in 16 bits, rounded once, half a step relative (dY's own precision),
+// and the sums of its columns in binary32 over a slab of rows, before that
+// rounding. A block takes 512 columns, a wavefront every fourth row of the slab, a
+// lane 8 columns. Columns of G up to the next multiple of 8 are zeros. Memory bound.
+template <class T>
+struct GradArgs {
+    const T *dY;
+    int64_t lddy;
+    const T *Z;  // null: act' is 1
+    int64_t ldz;
+    int act;
+    T *G;  // or null
+    int64_t ldg;
+    float *sums;  // or null; a row per slab, ldsum apart
+    int64_t ldsum;
+    int64_t t, n, slab;  // rows of a slab
+};
+constexpr int kGradCols = 512;
+template <class T>
+__global__ __launch_bounds__(256) void k_act_grad(GradArgs<T> p) {
+    __shared__ float part[3][kGradCols];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t c = (int64_t)blockIdx.x * kGradCols + 8 * lane;
+    const int64_t r0 = (int64_t)blockIdx.y * p.slab, r1 = min(r0 + p.slab, p.t);
+    float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    with_activation(p.act, [&](auto act) {
+        constexpr int U = 4;  // rows on their way at a time
+        for (int64_t r = r0 + wave; r < r1; r += 4 * U) {
+            float g[U][8], z[U][8];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t at = r + 4 * u < r1 ? c : p.n;  // past the end: zeros
+                load8(p.dY + (r + 4 * u) * p.lddy, at, p.n, g[u]);
+                if constexpr (decltype(act)::value != OZAKI2_ACT_NONE) load8(p.Z + (r + 4 * u) * p.ldz, at, p.n, z[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if constexpr (decltype(act)::value != OZAKI2_ACT_NONE) g[u][i] *= slope_of<decltype(act)::value>(z[u][i]);
+                    sum[i] += g[u][i];
+                }
+                if (p.G && r + 4 * u < r1 && c < p.n) {
+                    const U16 o = {{pack2<T>(g[u][0], g[u][1]), pack2<T>(g[u][2], g[u][3]), pack2<T>(g[u][4], g[u][5]),
+                                    pack2<T>(g[u][6], g[u][7])}};
+                    *(U16 *)(p.G + (r + 4 * u) * p.ldg + c) = o;
+                }
+            }
+        }
+    });
+    if (p.sums == nullptr) return;
+    if (wave > 0)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) part[wave - 1][8 * lane + i] = sum[i];
+    __syncthreads();
+    if (wave == 0)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < p.n)
+                p.sums[blockIdx.y * p.ldsum + c + i] =
+                    (sum[i] + part[0][8 * lane + i]) + (part[1][8 * lane + i] + part[2][8 * lane + i]);
+}
+// The slabs' sums, joined in a fixed order: a block takes 64 columns, each wavefront every fourth slab.
+__global__ __launch_bounds__(256) void k_join_columns(const float *__restrict__ sums, int slabs, int64_t ld, int64_t n,
+                                                      float *__restrict__ out) {
+    __shared__ float part[4][64];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    float s = 0.f;
+    if (c < n)
+        for (int i = wave; i < slabs; i += 4) s += sums[i * ld + c];
+    part[wave][lane] = s;
+    __syncthreads();
+    if (wave == 0 && c < n) out[c] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+}
+
+__global__ __launch_bounds__(256) void k_zero_matrix16(uint16_t *out, int64_t ldo, int64_t rows, int64_t cols) {
+    for (int64_t r = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6); r < rows; r += (int64_t)gridDim.x * 4)
+        for (int64_t c = threadIdx.x & 63; c < cols; c += 64) out[r * ldo + c] = 0;
+}
+hipError_t zero_matrix16(void *out, int64_t ldo, int64_t rows, int64_t cols, hipStream_t s) {
+    if (rows == 0 || cols == 0) return hipSuccess;
+    hipLaunchKernelGGL(k_zero_matrix16, dim3((unsigned)((rows + 3) / 4 < 65535 ? (rows + 3) / 4 : 65535)), dim3(256), 0, s,
+                       (uint16_t *)out, ldo, rows, cols);
+    return hipGetLastError();
+}
+
+// Pitch in 16-bit elements of a workspace matrix (see pack_pitch).
+int64_t pitch16(int64_t n) { return pack_pitch(2 * n) / 2; }
+// Slices of k of a K-major product of t x n results over k rows.
+int kmajor_splits(int64_t t, int64_t n, int64_t k) {
+    return use_large_tile(n, t) ? 1 : tile_splits(Tile::p4, n, t, 2 * k);
+}
+
+struct GradPlan {
+    int slabs;
+    int64_t slab;
+    int dx_splits, dw_splits;
+    size_t sums, g, x, w, planes, total;
+};
+GradPlan plan_grad(int64_t t, int64_t n, int64_t k, bool dx, bool dw, bool db) {
+    GradPlan p{};
+    // about eight blocks per compute unit, of 16 rows or more
+    const int64_t cols = (n + kGradCols - 1) / kGradCols, most = (t + 15) / 16;
+    int64_t slabs = 8 * kPlanUnits / cols;
+    slabs = slabs < 1 ? 1 : slabs > most ? most : slabs;
+    if (slabs < 1) slabs = 1;
+    if (t / slabs > ((int64_t)1 << 20)) slabs = (t >> 20) + 1;
+    if (slabs > 65535) slabs = 65535;
+    p.slab = (t + slabs - 1) / slabs;
+    if (p.slab < 1) p.slab = 1;
+    p.slabs = (int)((t + p.slab - 1) / p.slab);
+    p.dx_splits = dx ? kmajor_splits(t, k, (n + 7) / 8 * 8) : 1;
+    // (up to kShortRows tokens run on k_tile_short, which takes no slices)
+    p.dw_splits = dw && t > kShortRows ? kmajor_splits(n, k, t) : 1;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += up256(bytes);
+        return at;
+    };
+    p.sums = take(db ? 4 * (size_t)p.slabs * (size_t)n : 0);
+    // (sizes alone do not say what is aligned)
+    p.g = take(dx || dw ? 2 * (size_t)t * (size_t)pitch16(n) : 0);
+    p.x = take(dw ? 2 * (size_t)t * (size_t)pitch16(k) : 0);
+    p.w = take(dx ? 2 * (size_t)n * (size_t)pitch16(k) : 0);
+    // one product's planes after the other's
+    const size_t a = plane_bytes(t, k, p.dx_splits), b = plane_bytes(n, k, p.dw_splits);
+    p.planes = take(a > b ? a : b);
+    p.total = off;
+    return p;
+}
+
+struct GradCallArgs {
+    int64_t t, n, k;
+    const void *dY;
+    int64_t lddy;
+    const void *X;
+    int64_t ldx;
+    const void *W;
+    int64_t ldw;
+    int act;
+    const void *Z;
+    int64_t ldz;
+    void *dX;
+    int64_t lddx;
+    void *dW;
+    int64_t lddw;
+    float *dbias;
+};
+// Whether a matrix can be a K-major operand as it is.
+bool kmajor_ready(const void *p, int64_t ld, int64_t cols) {
+    return (((uintptr_t)p | (uintptr_t)(2 * ld) | (uintptr_t)(2 * cols)) & 15) == 0 && 2 * ld < (1 << 24);
+}
+
+// R[b][a] over krows rows of k, rounded to T.
+template <class M, bool KB>
+int kmajor_product(TileArgs ta, int64_t krows, int splits, void *out, int64_t ldo, char *planes, hipStream_t s) {
+    typedef typename M::Elem T;
+    ta.krows = (int)krows;
+    if (splits == 1) {
+        HIP_TRY((launch_kmajor<M, EpiRound<T>, true, KB>(ta, {(T *)out, ldo, ta.na, ta.nb}, 1, s)));
+        return OZAKI2_SUCCESS;
+    }
+    const int64_t ldp = plane_pitch(ta.na), plane = ta.nb * ldp;
+    HIP_TRY((launch_kmajor<M, EpiRaw, true, KB>(ta, {(uint32_t *)planes, ldp, plane, ta.na, ta.nb}, splits, s)));
+    HIP_TRY((launch_join_act<T, void, false>(planes, splits, plane, ldp,
+                                             {(T *)out, ldo, nullptr, nullptr,
+                                              {nullptr, OZAKI2_ACT_NONE, nullptr, 0, nullptr, 0}, ta.na, ta.nb}, s)));
+    return OZAKI2_SUCCESS;
+}
+
+template <class M>
+int backward(const GradCallArgs &c, char *ws, hipStream_t s) {
+    typedef typename M::Elem T;
+    const bool dx = c.dX != nullptr && c.k > 0, dw = c.dW != nullptr && c.k > 0, db = c.dbias != nullptr;
+    if (c.t == 0 || c.n == 0) {
+        if (dx) HIP_TRY(zero_matrix16(c.dX, c.lddx, c.t, c.k, s));
+        if (dw) HIP_TRY(zero_matrix16(c.dW, c.lddw, c.n, c.k, s));
+        if (db) HIP_TRY(zero_matrix16(c.dbias, 2 * c.n, c.n > 0 ? 1 : 0, 2 * c.n, s));
+        return OZAKI2_SUCCESS;
+    }
+    const GradPlan p = plan_grad(c.t, c.n, c.k, dx, dw, db);
+    const void *g = c.dY;
+    int64_t ldg = c.lddy;
+    const bool makes_g = (dx || dw) && (c.act != OZAKI2_ACT_NONE || !kmajor_ready(c.dY, c.lddy, c.n));
+    if (makes_g) {
+        g = ws + p.g;
+        ldg = pitch16(c.n);
+    }
+    if (makes_g || db) {
+        const dim3 grid((unsigned)((c.n + kGradCols - 1) / kGradCols), (unsigned)p.slabs);
+        hipLaunchKernelGGL((k_act_grad<T>), grid, dim3(256), 0, s,
+                           GradArgs<T>{(const T *)c.dY, c.lddy, (const T *)c.Z, c.ldz, c.act, makes_g ? (T *)g : nullptr, ldg,
+                                       db ? (float *)(ws + p.sums) : nullptr, c.n, c.t, c.n, p.slab});
+        HIP_TRY(hipGetLastError());
+    }
+    if (db) {
+        hipLaunchKernelGGL(k_join_columns, dim3((unsigned)((c.n + 63) / 64)), dim3(256), 0, s, (const float *)(ws + p.sums),
+                           p.slabs, c.n, c.n, c.dbias);
+        HIP_TRY(hipGetLastError());
+    }
+    if (dx) {
+        // rows of W as the rows of k; G's columns past n are zeros
+        const void *w = c.W;
+        int64_t ldw = c.ldw;
+        if (!kmajor_ready(w, ldw, c.k)) {
+            HIP_TRY(launch_pack_rows(w, 2 * ldw, c.n, 2 * c.k, ws + p.w, 2 * pitch16(c.k), s));
+            w = ws + p.w;
+            ldw = pitch16(c.k);
+        }
+        const int st = kmajor_product<M, false>(rows_of(c.t, c.k, (c.n + 7) / 8 * 8, g, ldg, w, ldw), c.n, p.dx_splits, c.dX,
+                                                c.lddx, ws + p.planes, s);
+        if (st) return st;
+    }
+    if (dw) {
+        // rows of X and of G as the rows of k
+        const void *x = c.X;
+        int64_t ldx = c.ldx;
+        if (!kmajor_ready(x, ldx, c.k)) {
+            HIP_TRY(launch_pack_rows(x, 2 * ldx, c.t, 2 * c.k, ws + p.x, 2 * pitch16(c.k), s));
+            x = ws + p.x;
+            ldx = pitch16(c.k);
+        }
+        const int st = kmajor_product<M, true>(rows_of(c.n, c.k, c.t, g, ldg, x, ldx), c.t, p.dw_splits, c.dW, c.lddw,
+                                               ws + p.planes, s);
+        if (st) return st;
+    }
+    return OZAKI2_SUCCESS;
+}
+
+// ---- checks -------------------------------------------------------------------------
+bool is_type16(int type) { return type == OZAKI2_BF16 || type == OZAKI2_FP16; }
+bool linear_fits(int64_t t, int64_t n, int64_t k) {
+    return t < kMostTokens && n < kMostChannels && k < (int64_t)1 << 29;
+}
+// Rows of G, X and W in the workspace of less than 2^24 bytes.
+bool grad_fits(int64_t t, int64_t n, int64_t k) {
+    return t < kMostTokens && n < (int64_t)1 << 22 && k < (int64_t)1 << 22;
+}
+
+struct LinearCall {
+    LinearArgs a;
+    int type, ytype;
+    hipStream_t s;
+};
+int run_linear(void *ctx, char *ws) {
+    const LinearCall &c = *(const LinearCall *)ctx;
+    if (c.type == OZAKI2_BF16)
+        return c.ytype == OZAKI2_FP32 ? forward<MmaBf16, float>(c.a, ws, c.s) : forward<MmaBf16, __bf16>(c.a, ws, c.s);
+    return c.ytype == OZAKI2_FP32 ? forward<MmaF16, float>(c.a, ws, c.s) : forward<MmaF16, _Float16>(c.a, ws, c.s);
+}
+int front_linear(LinearCall c, bool cached, void *workspace, size_t bytes) {
+    const LinearArgs &a = c.a;
+    const bool any = a.t > 0 && a.n > 0;
+    const int64_t row = a.k > 1 ? a.k : 1, col = a.n > 1 ? a.n : 1;
+    if (a.t < 0) return -1;
+    if (a.n < 0) return -2;
+    if (a.k < 0) return -3;
+    if (a.X == nullptr && any && a.k > 0) return -4;
+    if (a.ldx < row) return -5;
+    if (a.W == nullptr && any && a.k > 0) return -6;
+    if (a.ldw < row) return -7;
+    if (!is_type16(c.type)) return -8;
+    if (!is_activation(a.act)) return -10;
+    if (a.residual != nullptr && any && a.ldr < col) return -12;
+    if (a.Y == nullptr && any) return -13;
+    if (a.ldy < col) return -14;
+    if (c.ytype != c.type && c.ytype != OZAKI2_FP32) return -15;
+    if (a.Z != nullptr && any && a.ldz < col) return -17;
+    // tiles at the edge may compute an entry twice, so Y must not be where the residual is read
+    if (share_memory(a.residual, a.ldr, a.Y, a.ldy, a.t, a.n, c.ytype == OZAKI2_FP32 ? 4 : 2)) return -11;
+    if (!linear_fits(a.t, a.n, a.k)) return OZAKI2_ERR_UNSUPPORTED;
+    if (!any) return OZAKI2_SUCCESS;
+    const size_t need = forward_bytes(a.t, a.n, a.k);
+    if (need == 0) return run_linear(&c, nullptr);
+    if (cached) return with_workspace(need, c.s, run_linear, &c);
+    if (workspace == nullptr || ((uintptr_t)workspace & (kWsAlign - 1)) != 0) return -18;
+    if (bytes < need) return OZAKI2_ERR_WORKSPACE;
+    return run_linear(&c, (char *)workspace);
+}
+
+struct GradCall {
+    GradCallArgs a;
+    int type;
+    hipStream_t s;
+};
+int run_grad(void *ctx, char *ws) {
+    const GradCall &c = *(const GradCall *)ctx;
+    return c.type == OZAKI2_BF16 ? backward<MmaBf16>(c.a, ws, c.s) : backward<MmaF16>(c.a, ws, c.s);
+}
+int front_grad(GradCall c, bool cached, void *workspace, size_t bytes) {
+    const GradCallArgs &a = c.a;
+    const bool any = a.t > 0 && a.n > 0, dx = a.dX != nullptr, dw = a.dW != nullptr;
+    const int64_t row = a.k > 1 ? a.k : 1, col = a.n > 1 ? a.n : 1;
+    if (a.t < 0) return -1;
+    if (a.n < 0) return -2;
+    if (a.k < 0) return -3;
+    if (a.dY == nullptr && any && (dx || dw || a.dbias)) return -4;
+    if (a.lddy < col) return -5;
+    if (a.X == nullptr && any && a.k > 0 && dw) return -6;
+    if (a.ldx < row) return -7;
+    if (a.W == nullptr && any && a.k > 0 && dx) return -8;
+    if (a.ldw < row) return -9;
+    if (!is_type16(c.type)) return -10;
+    if (!is_activation(a.act)) return -11;
+    if (a.Z == nullptr && any && a.act != OZAKI2_ACT_NONE && (dx || dw || a.dbias)) return -12;
+    if (a.act != OZAKI2_ACT_NONE && a.ldz < col) return -13;
+    if (dx && a.lddx < row) return -15;
+    if (dw && a.lddw < row) return -17;
+    if (!grad_fits(a.t, a.n, a.k)) return OZAKI2_ERR_UNSUPPORTED;
+    if (!dx && !dw && a.dbias == nullptr) return OZAKI2_SUCCESS;
+    const size_t need = any ? plan_grad(a.t, a.n, a.k, dx && a.k > 0, dw && a.k > 0, a.dbias != nullptr).total : 0;
+    if (need == 0) return run_grad(&c, nullptr);
+    if (cached) return with_workspace(need, c.s, run_grad, &c);
+    if (workspace == nullptr || ((uintptr_t)workspace & (kWsAlign - 1)) != 0) return -19;
+    if (bytes < need) return OZAKI2_ERR_WORKSPACE;
+    return run_grad(&c, (char *)workspace);
+}
+
+}  // namespace
+}  // namespace oz2
+
+using namespace oz2;
+
+extern "C" {
+
+int ozaki2_linear(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, const void *W, int64_t ldw, int type,
+                  const float *bias, int activation, const void *residual, int64_t ldr, void *Y, int64_t ldy, int ytype, void *Z,
+                  int64_t ldz, void *stream) {
+    return front_linear({{t, n, k, X, ldx, W, ldw, bias, activation, residual, ldr, Y, ldy, Z, ldz}, type, ytype,
+                         (hipStream_t)stream}, true, nullptr, 0);
+}
+
+size_t ozaki2_linear_workspace_size(int64_t t, int64_t n, int64_t k) {
+    if (t <= 0 || n <= 0 || k < 0 || !linear_fits(t, n, k)) return 0;
+    return forward_bytes(t, n, k);
+}
+
+int ozaki2_linear_ws(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, const void *W, int64_t ldw, int type,
+                     const float *bias, int activation, const void *residual, int64_t ldr, void *Y, int64_t ldy, int ytype,
+                     void *Z, int64_t ldz, void *workspace, size_t workspace_bytes, void *stream) {
+    return front_linear({{t, n, k, X, ldx, W, ldw, bias, activation, residual, ldr, Y, ldy, Z, ldz}, type, ytype,
+                         (hipStream_t)stream}, false, workspace, workspace_bytes);
+}
+
+int ozaki2_linear_grad(int64_t t, int64_t n, int64_t k, const void *dY, int64_t lddy, const void *X, int64_t ldx, const void *W,
+                       int64_t ldw, int type, int activation, const void *Z, int64_t ldz, void *dX, int64_t lddx, void *dW,
+                       int64_t lddw, float *dbias, void *stream) {
+    return front_grad({{t, n, k, dY, lddy, X, ldx, W, ldw, activation, Z, ldz, dX, lddx, dW, lddw, dbias}, type,
+                       (hipStream_t)stream}, true, nullptr, 0);
+}
+
+size_t ozaki2_linear_grad_workspace_size(int64_t t, int64_t n, int64_t k, int want_dx, int want_dw, int want_dbias) {
+    if (t <= 0 || n <= 0 || k < 0 || !grad_fits(t, n, k)) return 0;
+    return plan_grad(t, n, k, want_dx && k > 0, want_dw && k > 0, want_dbias).total;
+}
+
+int ozaki2_linear_grad_ws(int64_t t, int64_t n, int64_t k, const void *dY, int64_t lddy, const void *X, int64_t ldx,
+                          const void *W, int64_t ldw, int type, int activation, const void *Z, int64_t ldz, void *dX,
+                          int64_t lddx, void *dW, int64_t lddw, float *dbias, void *workspace, size_t workspace_bytes,
+                          void *stream) {
+    return front_grad({{t, n, k, dY, lddy, X, ldx, W, ldw, activation, Z, ldz, dX, lddx, dW, lddw, dbias}, type,
+                       (hipStream_t)stream}, false, workspace, workspace_bytes);
+}
+
+}  // extern "C"

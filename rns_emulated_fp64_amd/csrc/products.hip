@@ -5,14 +5,15 @@
 //                         the binary32 operations of row_scale
 //   ozaki2_i8gemm         C[t][n] = (sum_k A[t][k] B[n][k]) sa[t] sb[n] + bias[n]
 //   ozaki2_i8linear       both: activations quantised row by row, then the product
+//   ozaki2_i8gemm_act, ozaki2_i8linear_act   C = act(the same) + residual[t][n]
 //
 // The int32 sums are exact (k < 2^17), so every kernel and every split of k
 // gives the same sums, and the results differ by nothing.
 #include <hip/hip_runtime.h>
 
 #include "common.h"
+#include "epilogue.h"
 #include "ozaki2.h"
-#include "tile.h"
 
 namespace oz2 {
 namespace {
@@ -171,6 +172,10 @@ struct Product {
     const float *b_scale, *bias;
     void *C;
     int64_t ldc;
+    int act;
+    const void *residual;  // of C's type, or null
+    int64_t ldr;
+    bool finishes() const { return act != OZAKI2_ACT_NONE || residual != nullptr; }
 };
 
 template <class OutT>
@@ -184,14 +189,24 @@ int product_rows(const Product &p, char *ws, hipStream_t s) {
     ta.nb = p.t;
     ta.kbytes = p.k;
     const typename EpiScale<OutT>::Args e = {(OutT *)p.C, p.ldc, p.b_scale, p.a_scale, p.bias, p.n, p.t};
+    typedef EpiAct<OutT, void, true> Act;
+    const typename Act::Args f = {(OutT *)p.C, p.ldc, p.b_scale, p.a_scale,
+                                  {p.bias, p.act, (const OutT *)p.residual, p.ldr, nullptr, 0}, p.n, p.t};
     const Tile tile = choose_tile(ta, false);
     const int splits = tile == Tile::skinny ? 1 : splits_of(p.t, p.n, p.k);
     if (splits == 1) {
-        HIP_TRY((launch_tile<MmaI8, EpiScale<OutT>, false>(ta, e, tile, 1, s)));
+        if (p.finishes())
+            HIP_TRY((launch_tile<MmaI8, Act, false>(ta, f, tile, 1, s)));
+        else
+            HIP_TRY((launch_tile<MmaI8, EpiScale<OutT>, false>(ta, e, tile, 1, s)));
         return OZAKI2_SUCCESS;
     }
     const int64_t ldp = plane_pitch(p.n), plane = p.t * ldp;
     HIP_TRY((launch_tile<MmaI8, EpiRaw, false>(ta, {(uint32_t *)ws, ldp, plane, p.n, p.t}, tile, splits, s)));
+    if (p.finishes()) {
+        HIP_TRY((launch_join_act<OutT, void, true>(ws, splits, plane, ldp, f, s)));
+        return OZAKI2_SUCCESS;
+    }
     const dim3 grid((unsigned)((p.n + 1023) / 1024), (unsigned)(p.t < 65535 ? p.t : 65535));
     hipLaunchKernelGGL((k_join_scale<OutT>), grid, dim3(256), 0, s, (const int32_t *)ws, splits, plane, ldp, e);
     HIP_TRY(hipGetLastError());
@@ -220,6 +235,7 @@ int product_t(Product p, bool own_a, char *ws, hipStream_t s) {
         q.b_scale += n0;
         if (q.bias) q.bias += n0;
         q.C = (OutT *)p.C + n0;
+        if (q.residual) q.residual = (const OutT *)p.residual + n0;
         HIP_TRY(launch_pack_rows(p.B + n0 * p.ldb, p.ldb, q.n, p.k, ws, pitch, s));
         const int st = product_rows<OutT>(q, planes, s);
         if (st) return st;
@@ -233,30 +249,33 @@ int product(const Product &p, bool own_a, int ctype, char *ws, hipStream_t s) {
     return product_t<float>(p, own_a, ws, s);
 }
 
+// The layer of a few rows, quantised by the product's own blocks.
 template <class XT, class OutT>
-hipError_t few_rows_t(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, const int8_t *B, int64_t ldb,
-                      const float *b_scale, const float *bias, void *C, int64_t ldc, hipStream_t s) {
+hipError_t few_rows_t(const Product &p, const XT *X, int64_t ldx, hipStream_t s) {
     TileArgs ta{};
-    ta.A = B;
-    ta.lda = ldb;
-    ta.na = n;
-    ta.nb = t;
-    ta.kbytes = k;
-    return launch_skinny<MmaI8, EpiScale<OutT>, BQuant<XT>>(
-        ta, {(OutT *)C, ldc, b_scale, nullptr, bias, n, t}, {(const XT *)X, ldx, (int)quant_pitch(k)}, s);
+    ta.A = p.B;
+    ta.lda = p.ldb;
+    ta.na = p.n;
+    ta.nb = p.t;
+    ta.kbytes = p.k;
+    const typename BQuant<XT>::Args src = {X, ldx, (int)quant_pitch(p.k)};
+    if (p.finishes())
+        return launch_skinny<MmaI8, EpiAct<OutT, void, true>, BQuant<XT>>(
+            ta, {(OutT *)p.C, p.ldc, p.b_scale, nullptr, {p.bias, p.act, (const OutT *)p.residual, p.ldr, nullptr, 0}, p.n, p.t},
+            src, s);
+    return launch_skinny<MmaI8, EpiScale<OutT>, BQuant<XT>>(ta, {(OutT *)p.C, p.ldc, p.b_scale, nullptr, p.bias, p.n, p.t}, src,
+                                                            s);
 }
 template <class XT>
-hipError_t few_rows_x(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, const int8_t *B, int64_t ldb,
-                      const float *b_scale, const float *bias, void *C, int64_t ldc, int ctype, hipStream_t s) {
-    if (ctype == OZAKI2_BF16) return few_rows_t<XT, __bf16>(t, n, k, X, ldx, B, ldb, b_scale, bias, C, ldc, s);
-    if (ctype == OZAKI2_FP16) return few_rows_t<XT, _Float16>(t, n, k, X, ldx, B, ldb, b_scale, bias, C, ldc, s);
-    return few_rows_t<XT, float>(t, n, k, X, ldx, B, ldb, b_scale, bias, C, ldc, s);
+hipError_t few_rows_x(const Product &p, const void *X, int64_t ldx, int ctype, hipStream_t s) {
+    if (ctype == OZAKI2_BF16) return few_rows_t<XT, __bf16>(p, (const XT *)X, ldx, s);
+    if (ctype == OZAKI2_FP16) return few_rows_t<XT, _Float16>(p, (const XT *)X, ldx, s);
+    return few_rows_t<XT, float>(p, (const XT *)X, ldx, s);
 }
-hipError_t few_rows(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, int xtype, const int8_t *B, int64_t ldb,
-                    const float *b_scale, const float *bias, void *C, int64_t ldc, int ctype, hipStream_t s) {
-    if (xtype == OZAKI2_BF16) return few_rows_x<__bf16>(t, n, k, X, ldx, B, ldb, b_scale, bias, C, ldc, ctype, s);
-    if (xtype == OZAKI2_FP16) return few_rows_x<_Float16>(t, n, k, X, ldx, B, ldb, b_scale, bias, C, ldc, ctype, s);
-    return few_rows_x<float>(t, n, k, X, ldx, B, ldb, b_scale, bias, C, ldc, ctype, s);
+hipError_t few_rows(const Product &p, const void *X, int64_t ldx, int xtype, int ctype, hipStream_t s) {
+    if (xtype == OZAKI2_BF16) return few_rows_x<__bf16>(p, X, ldx, ctype, s);
+    if (xtype == OZAKI2_FP16) return few_rows_x<_Float16>(p, X, ldx, ctype, s);
+    return few_rows_x<float>(p, X, ldx, ctype, s);
 }
 
 // ---- checks ---------------------------------------------------------------------------
@@ -284,6 +303,15 @@ int check_i8gemm(int64_t t, int64_t n, int64_t k, const void *A, int64_t lda, co
     return 0;
 }
 
+// Of the activation and the residual, arguments -11 to -13 of the _act forms; C and what follows it
+// come three places later there.
+int check_finish(int64_t t, int64_t n, int act, const void *residual, int64_t ldr) {
+    if (!is_activation(act)) return -11;
+    if (residual != nullptr && t > 0 && n > 0 && ldr < (n > 1 ? n : 1)) return -13;
+    return 0;
+}
+int type_size(int type) { return type == OZAKI2_FP32 ? 4 : 2; }
+
 struct GemmCall {
     int64_t t, n, k, lda, ldb, ldc;
     const int8_t *A, *B;
@@ -291,21 +319,38 @@ struct GemmCall {
     void *C;
     int ctype;
     hipStream_t s;
+    // the _act forms'
+    bool acts = false;
+    int act = OZAKI2_ACT_NONE;
+    const void *residual = nullptr;
+    int64_t ldr = 0;
 };
+// The status of a call's arguments, from that of those that its plain form has too.
+template <class Call>
+int checked(const Call &c, int st) {
+    if (!c.acts) return st;
+    if (st < 0 && st > -11) return st;
+    const int more = check_finish(c.t, c.n, c.act, c.residual, c.ldr);
+    if (more) return more;
+    if (st) return st - 3;
+    // tiles at the edge may compute an entry twice, so C must not be where the residual is read
+    if (share_memory(c.residual, c.ldr, c.C, c.ldc, c.t, c.n, type_size(c.ctype))) return -12;
+    return 0;
+}
 int run_i8gemm(void *ctx, char *ws) {
     const GemmCall &c = *(const GemmCall *)ctx;
-    return product({c.t, c.n, c.k, c.A, c.lda, c.a_scale, c.B, c.ldb, c.b_scale, c.bias, c.C, c.ldc}, false, c.ctype, ws,
-                   c.s);
+    return product({c.t, c.n, c.k, c.A, c.lda, c.a_scale, c.B, c.ldb, c.b_scale, c.bias, c.C, c.ldc, c.act, c.residual, c.ldr},
+                   false, c.ctype, ws, c.s);
 }
 int front_i8gemm(GemmCall c, bool cached, void *workspace, size_t bytes) {
-    const int st = check_i8gemm(c.t, c.n, c.k, c.A, c.lda, c.a_scale, c.B, c.ldb, c.b_scale, c.C, c.ldc, c.ctype);
+    const int st = checked(c, check_i8gemm(c.t, c.n, c.k, c.A, c.lda, c.a_scale, c.B, c.ldb, c.b_scale, c.C, c.ldc, c.ctype));
     if (st) return st;
     if (!fits(c.t, c.n, c.k)) return OZAKI2_ERR_UNSUPPORTED;
     if (c.t == 0 || c.n == 0) return OZAKI2_SUCCESS;
     const size_t need = product_bytes(c.t, c.n, c.k, false);
     if (need == 0) return run_i8gemm(&c, nullptr);
     if (cached) return with_workspace(need, c.s, run_i8gemm, &c);
-    if (workspace == nullptr || ((uintptr_t)workspace & (kWsAlign - 1)) != 0) return -14;
+    if (workspace == nullptr || ((uintptr_t)workspace & (kWsAlign - 1)) != 0) return c.acts ? -17 : -14;
     if (bytes < need) return OZAKI2_ERR_WORKSPACE;
     return run_i8gemm(&c, (char *)workspace);
 }
@@ -336,6 +381,11 @@ struct LinearCall {
     void *C;
     int xtype, ctype;
     hipStream_t s;
+    // the _act forms'
+    bool acts = false;
+    int act = OZAKI2_ACT_NONE;
+    const void *residual = nullptr;
+    int64_t ldr = 0;
 };
 // Workspace of ozaki2_i8linear: the quantised rows, their scales, the product's own.
 int64_t q_pitch(int64_t k) { return pack_pitch(k); }
@@ -346,26 +396,29 @@ size_t i8linear_bytes(int64_t t, int64_t n, int64_t k) {
 }
 int run_i8linear(void *ctx, char *ws) {
     const LinearCall &c = *(const LinearCall *)ctx;
+    Product p = {c.t, c.n, c.k, nullptr, 0, nullptr, c.B, c.ldb, c.b_scale, c.bias, c.C, c.ldc, c.act, c.residual, c.ldr};
     if (quantises_in_product(c.t, c.k)) {
-        HIP_TRY(few_rows(c.t, c.n, c.k, c.X, c.ldx, c.xtype, c.B, c.ldb, c.b_scale, c.bias, c.C, c.ldc, c.ctype, c.s));
+        HIP_TRY(few_rows(p, c.X, c.ldx, c.xtype, c.ctype, c.s));
         return OZAKI2_SUCCESS;
     }
     int8_t *q = (int8_t *)ws;
     float *scale = (float *)(ws + q_bytes(c.t, c.k));
     char *rest = ws + q_bytes(c.t, c.k) + up256(4 * (size_t)c.t);
     HIP_TRY(launch_quantize_rows(c.xtype, c.X, c.ldx, c.t, c.k, q, q_pitch(c.k), scale, c.s));
-    return product({c.t, c.n, c.k, q, q_pitch(c.k), scale, c.B, c.ldb, c.b_scale, c.bias, c.C, c.ldc}, true, c.ctype, rest,
-                   c.s);
+    p.A = q;
+    p.lda = q_pitch(c.k);
+    p.a_scale = scale;
+    return product(p, true, c.ctype, rest, c.s);
 }
 int front_i8linear(LinearCall c, bool cached, void *workspace, size_t bytes) {
-    const int st = check_i8linear(c.t, c.n, c.k, c.X, c.ldx, c.xtype, c.B, c.ldb, c.b_scale, c.C, c.ldc, c.ctype);
+    const int st = checked(c, check_i8linear(c.t, c.n, c.k, c.X, c.ldx, c.xtype, c.B, c.ldb, c.b_scale, c.C, c.ldc, c.ctype));
     if (st) return st;
     if (!fits(c.t, c.n, c.k)) return OZAKI2_ERR_UNSUPPORTED;
     if (c.t == 0 || c.n == 0) return OZAKI2_SUCCESS;
     const size_t need = i8linear_bytes(c.t, c.n, c.k);
     if (need == 0) return run_i8linear(&c, nullptr);
     if (cached) return with_workspace(need, c.s, run_i8linear, &c);
-    if (workspace == nullptr || ((uintptr_t)workspace & (kWsAlign - 1)) != 0) return -14;
+    if (workspace == nullptr || ((uintptr_t)workspace & (kWsAlign - 1)) != 0) return c.acts ? -17 : -14;
     if (bytes < need) return OZAKI2_ERR_WORKSPACE;
     return run_i8linear(&c, (char *)workspace);
 }
@@ -427,6 +480,38 @@ int ozaki2_i8linear_ws(int64_t t, int64_t n, int64_t k, const void *X, int64_t l
                        void *workspace, size_t workspace_bytes, void *stream) {
     return front_i8linear({t, n, k, ldx, ldb, ldc, X, B, b_scale, bias, C, xtype, ctype, (hipStream_t)stream}, false,
                           workspace, workspace_bytes);
+}
+
+int ozaki2_i8gemm_act(int64_t t, int64_t n, int64_t k, const int8_t *A, int64_t lda, const float *a_scale, const int8_t *B,
+                      int64_t ldb, const float *b_scale, const float *bias, int activation, const void *residual, int64_t ldr,
+                      void *C, int64_t ldc, int ctype, void *stream) {
+    return front_i8gemm({t, n, k, lda, ldb, ldc, A, B, a_scale, b_scale, bias, C, ctype, (hipStream_t)stream, true, activation,
+                         residual, ldr},
+                        true, nullptr, 0);
+}
+
+int ozaki2_i8gemm_act_ws(int64_t t, int64_t n, int64_t k, const int8_t *A, int64_t lda, const float *a_scale, const int8_t *B,
+                         int64_t ldb, const float *b_scale, const float *bias, int activation, const void *residual,
+                         int64_t ldr, void *C, int64_t ldc, int ctype, void *workspace, size_t workspace_bytes, void *stream) {
+    return front_i8gemm({t, n, k, lda, ldb, ldc, A, B, a_scale, b_scale, bias, C, ctype, (hipStream_t)stream, true, activation,
+                         residual, ldr},
+                        false, workspace, workspace_bytes);
+}
+
+int ozaki2_i8linear_act(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, int xtype, const int8_t *B, int64_t ldb,
+                        const float *b_scale, const float *bias, int activation, const void *residual, int64_t ldr, void *C,
+                        int64_t ldc, int ctype, void *stream) {
+    return front_i8linear({t, n, k, ldx, ldb, ldc, X, B, b_scale, bias, C, xtype, ctype, (hipStream_t)stream, true, activation,
+                           residual, ldr},
+                          true, nullptr, 0);
+}
+
+int ozaki2_i8linear_act_ws(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, int xtype, const int8_t *B, int64_t ldb,
+                           const float *b_scale, const float *bias, int activation, const void *residual, int64_t ldr, void *C,
+                           int64_t ldc, int ctype, void *workspace, size_t workspace_bytes, void *stream) {
+    return front_i8linear({t, n, k, ldx, ldb, ldc, X, B, b_scale, bias, C, xtype, ctype, (hipStream_t)stream, true, activation,
+                           residual, ldr},
+                          false, workspace, workspace_bytes);
 }
 
 }  // extern "C"

@@ -749,6 +749,9 @@ __global__ __launch_bounds__(256) void k_tile_s(TileArgs ta, typename Epi::Args 
     const uint32_t lda = (uint32_t)ta.lda, ldb = (uint32_t)ta.ldb;
     int tile_a, tile_b;
     tile_of(blockIdx.x, ta.tiles_a * ta.tiles_b, ta.tiles_a, ta.tiles_b, ta.group, tile_a, tile_b);
+    // (the copies' buffers are scalar operands: nothing in them may come to lie in vector registers)
+    tile_a = __builtin_amdgcn_readfirstlane(tile_a);
+    tile_b = __builtin_amdgcn_readfirstlane(tile_b);
     const int64_t a0 = (int64_t)tile_a * (32 * RT), b0 = (int64_t)tile_b * (32 * CT);
     const int k0 = (int)(blockIdx.y * ta.split_bytes);
     const int k1 = (int)min((int64_t)k0 + ta.split_bytes, ta.kbytes);
