@@ -30,7 +30,7 @@ def test_i8gemm_act_refusals():
     # the first argument that is wrong is named
     assert oz.ozaki2_i8gemm_act(*with_arg(with_arg(good, 10, 9), 2, -1)) == -3
     assert oz.ozaki2_i8gemm_act(*with_arg(with_arg(good, 14, 1), 10, 9)) == -11
-    assert oz.ozaki2_i8gemm_act(1 << 31, *good[1:]) == 3
+    assert oz.ozaki2_i8gemm_act(1 << 31, *with_arg(good, 11, 0)[1:]) == 3
     assert oz.ozaki2_i8gemm_act(0, 6, 16, 0, 16, 0, 0, 16, 0, 0, 4, 0, 0, 0, 6, oz.FP32) == 0
     t, n, k = 128, 512, 65536
     need = oz.ozaki2_i8gemm_workspace_size(t, n, k)
