@@ -675,6 +675,41 @@ int ozaki2_xent_grad_ws(int64_t t, int64_t v, int64_t d, const void *X, int64_t 
                         const float *grad_loss, void *dX, int64_t lddx, void *dW, int64_t lddw, void *workspace,
                         size_t workspace_bytes, void *stream);
 
+/* ---- The next token ---------------------------------------------------------
+ *
+ * A token per row of logits (of an output layer, for tokens that are to be continued), from a random number u per row:
+ * with w[j] = exp((l[j] - max_j l[j]) / temperature), and entries ordered from the largest logit to the smallest, equal ones
+ * from the lowest index on,
+ *   1. top_k: the first top_k entries are kept (all if it is 0, negative or at least v);
+ *   2. top_p: of those the shortest run from the first whose sum of w is at least top_p times the sum over them (all if
+ *      it is 1 or more; the first alone if it is 0 or less);
+ *   3. min_p: of those the entries with w[j] >= min_p;
+ *   4. token[i] is the lowest kept index j such that the sum of w over the kept indexes up to and with j exceeds u times
+ *      the sum over all kept ones, and logprob[i] the logarithm of w[j] over that sum.
+ * temperature 0: the largest logit's index, the lowest if there are several, with logprob 0.
+ *   t, v      rows, entries; t < 2^31, v < 2^23; v >= 1 unless t == 0.
+ *   logits, ldl   DEVICE, of `type` (bf16, fp16 or fp32), element (i, j) at logits[i*ldl + j], ldl >= max(1, v).
+ *   u         DEVICE binary64 [t], in [0, 1): below it counts as 0, above as just below 1.
+ *   temperature, top_k, top_p, min_p   for all rows (temperature >= 0, top_p and min_p in [0, 1]); each has a DEVICE vector
+ *             [t] after it whose values are taken instead, or NULL. min_p above 1 in a vector counts as 1, and below 0 as 0.
+ *   tokens    DEVICE output [t].
+ *   logprobs  DEVICE output [t], or NULL.
+ * Logits of -inf are never drawn. Beside one of +inf only those of +inf are. A row that holds NaN or nothing but -inf, or whose
+ * settings or u are NaN or whose temperature is below 0, gives token -1 and logprob NaN.
+ * w is computed in binary64 and held as w 2^40 rounded to an integer, so sums are exact and the token does not depend on how
+ * a row is spread over threads; entries with w < 2^-41 count as 0. The workspace (ozaki2_sample_workspace_size bytes, about 68 KB a
+ * row for at most 1024 rows at a time) is cached, or the caller's in the _ws form (256-byte aligned, capturable, ordered on one
+ * stream if shared). Returns 0, -1..-15 for an invalid argument, -17 for the workspace, or an OZAKI2_ERR_* code.
+ */
+int ozaki2_sample(int64_t t, int64_t v, const void *logits, int64_t ldl, int type, const double *u, double temperature,
+                  const float *temperatures, int64_t top_k, const int32_t *top_ks, double top_p, const float *top_ps,
+                  double min_p, const float *min_ps, int64_t *tokens, float *logprobs, void *stream);
+size_t ozaki2_sample_workspace_size(int64_t t, int64_t v);
+int ozaki2_sample_ws(int64_t t, int64_t v, const void *logits, int64_t ldl, int type, const double *u, double temperature,
+                     const float *temperatures, int64_t top_k, const int32_t *top_ks, double top_p, const float *top_ps,
+                     double min_p, const float *min_ps, int64_t *tokens, float *logprobs, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
 /* Largest supported number of moduli (20). */
 int ozaki2_max_moduli(void);
 

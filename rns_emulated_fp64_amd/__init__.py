@@ -42,7 +42,7 @@ EXPORTS = (
     "ozaki2_xent_grad", "ozaki2_xent_grad_ws", "ozaki2_xent_grad_workspace_size",
     "ozaki2_rmsnorm_quantize", "ozaki2_i8gemm_act", "ozaki2_i8gemm_act_ws", "ozaki2_i8linear_act", "ozaki2_i8linear_act_ws",
     "ozaki2_linear", "ozaki2_linear_ws", "ozaki2_linear_workspace_size", "ozaki2_linear_grad", "ozaki2_linear_grad_ws",
-    "ozaki2_linear_grad_workspace_size",
+    "ozaki2_linear_grad_workspace_size", "ozaki2_sample", "ozaki2_sample_ws", "ozaki2_sample_workspace_size",
 )
 
 _lib = None
@@ -161,6 +161,13 @@ def lib() -> ctypes.CDLL:
     L.ozaki2_linear_workspace_size.restype = sz
     L.ozaki2_linear_grad_workspace_size.argtypes = [i64, i64, i64, i32, i32, i32]
     L.ozaki2_linear_grad_workspace_size.restype = sz
+    smp = [i64, i64, p, i64, i32, p, f64, p, i64, p, f64, p, f64, p, p, p]
+    L.ozaki2_sample.argtypes = smp + [p]
+    L.ozaki2_sample.restype = i32
+    L.ozaki2_sample_ws.argtypes = smp + [p, sz, p]
+    L.ozaki2_sample_ws.restype = i32
+    L.ozaki2_sample_workspace_size.argtypes = [i64, i64]
+    L.ozaki2_sample_workspace_size.restype = sz
     L.ozaki2_rmsnorm_quantize.argtypes = [i64, i64, p, i64, i32, p, i64, p, f64, p, i64, p, p, i64, p]
     L.ozaki2_rmsnorm_quantize.restype = i32
     L.ozaki2_finalize.argtypes = []
@@ -390,6 +397,22 @@ def ozaki2_linear_grad_ws(t, n, k, dY, lddy, X, ldx, W, ldw, type, activation, Z
 
 def ozaki2_linear_grad_workspace_size(t, n, k, want_dx=True, want_dw=True, want_dbias=True) -> int:
     return lib().ozaki2_linear_grad_workspace_size(t, n, k, 1 if want_dx else 0, 1 if want_dw else 0, 1 if want_dbias else 0)
+
+
+def ozaki2_sample(t, v, logits, ldl, type, u, temperature, temperatures, top_k, top_ks, top_p, top_ps, min_p, min_ps, tokens,
+                  logprobs, stream=0) -> int:
+    return lib().ozaki2_sample(t, v, logits, ldl, type, u, temperature, temperatures, top_k, top_ks, top_p, top_ps, min_p,
+                               min_ps, tokens, logprobs, stream)
+
+
+def ozaki2_sample_ws(t, v, logits, ldl, type, u, temperature, temperatures, top_k, top_ks, top_p, top_ps, min_p, min_ps, tokens,
+                     logprobs, workspace, workspace_bytes, stream=0) -> int:
+    return lib().ozaki2_sample_ws(t, v, logits, ldl, type, u, temperature, temperatures, top_k, top_ks, top_p, top_ps, min_p,
+                                  min_ps, tokens, logprobs, workspace, workspace_bytes, stream)
+
+
+def ozaki2_sample_workspace_size(t, v) -> int:
+    return lib().ozaki2_sample_workspace_size(t, v)
 
 
 def ozaki2_rmsnorm_quantize(t, k, X, ldx, type, residual, ldr, weight, eps, Q, ldq, scale, sum, lds, stream=0) -> int:
@@ -932,3 +955,42 @@ def xent_grad(X, W, targets, lse, grad_loss, ignore_index=-100, want_dx=True, wa
           targets.data_ptr(), ignore_index, lse.data_ptr(), grad_loss.data_ptr(),
           dX.data_ptr() if want_dx else None, max(d, 1), dW.data_ptr() if want_dw else None, max(d, 1), wp, wb)
     return dX, dW
+
+
+# ---- the next token ------------------------------------------------------------
+def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, workspace=None):
+    """A token per row of logits (t, v; bfloat16, float16 or float32), and the logarithm of its probability among what the
+    filters keep: (tokens int64, logprobs float32) (ozaki2_sample_ws). u (t,) holds float64 random numbers in [0, 1): the
+    token is the first kept index whose running sum of probabilities exceeds u, so the same u gives the same token.
+    ``temperature`` (0: the largest logit), ``top_k`` (0: off), ``top_p`` (1: off) and ``min_p`` (0: off) are numbers, or
+    vectors (t,) with a value per row, float32 (top_k int32); include/ozaki2.h says what each keeps, in that order. A row
+    without an entry to draw (all -inf, or NaN among them) gives -1 and NaN."""
+    torch = _torch or _load_torch()
+    kind = _type_of(logits.dtype, "logits")
+    device = logits.device
+    if device.type != "cuda":
+        raise TypeError("logits must be on a GPU")
+    logits, ldl = _rows(logits, "logits")
+    t, v = logits.shape
+    if t and not v:
+        raise ValueError("logits have no columns")
+    u = _vector(u, t, torch.float64, device, "u")
+
+    def setting(x, dtype, what):
+        """Its number and its vector, of which the call takes one."""
+        if isinstance(x, torch.Tensor):
+            x = _vector(x, t, dtype, device, what)
+            return 0, x, x.data_ptr()
+        return x, None, None
+
+    temperature, temperatures, tp = setting(temperature, torch.float32, "temperature")
+    top_k, top_ks, kp = setting(top_k, torch.int32, "top_k")
+    top_p, top_ps, pp = setting(top_p, torch.float32, "top_p")
+    min_p, min_ps, mp = setting(min_p, torch.float32, "min_p")
+    tokens = torch.empty(t, dtype=torch.int64, device=device)
+    logprobs = torch.empty(t, dtype=torch.float32, device=device)
+    L = lib()
+    ws, wp, wb = _workspace(L.ozaki2_sample_workspace_size(t, v), workspace, device)
+    _call(L.ozaki2_sample_ws, "ozaki2_sample_ws", device, t, v, logits.data_ptr(), ldl, kind, u.data_ptr(), temperature, tp, top_k,
+          kp, top_p, pp, min_p, mp, tokens.data_ptr(), logprobs.data_ptr(), wp, wb)
+    return tokens, logprobs
