@@ -11,19 +11,18 @@
 // number of threads, and the token is always the same. The exponential behind them is
 // computed in binary64.
 //
-// Nothing is sorted but what a filter leaves. Five launches, a row's work spread over as many blocks
-// as fill the chip:
-//   k_sample_top      the largest logit
-//   k_sample_count    a histogram of the logits over 2048 steps below it, or, without top_k and top_p,
-//                     the sums of weights of ranges of indexes
-//   k_sample_collect  the entries down to the step in which the filter cuts, if few; else those of that step
-//                     alone and the sums of the ranges for what lies above it
-//   k_sample_draw     one block per row: few entries are sorted and filtered in LDS and the token drawn
-//                     among them; else the cut is found among its step's entries, then the range
-//                     that u falls in, then the token in it
-//   k_sample_slow     rows that fit neither (a step with thousands of equal logits, a top_k of thousands
-//                     with a top_p), from the whole row, by histograms over ever smaller ranges
-// The row is read from memory once, and twice more mostly from the last-level cache.
+// Nothing is sorted but what a filter leaves undecided. A row goes through four phases:
+//   top      its largest logit
+//   count    a histogram of the logits over 4096 steps below it, in entries or in weights; the step in which
+//            the filter cuts follows from it
+//   collect  the undecided entries, a few hundred at most as a rule, into a list: those of that step, or all down to it
+//            where they are few; and the sums of the weights of what lies above it, by ranges of indexes
+//   draw     which of the list are kept; then the token among them, or the range that u falls in and the
+//            token in it
+// One block does all four where there are many rows or they are short (k_sample); few long rows are spread over
+// blocks, with a launch per phase (k_sample_top, ...). Rows whose list would be too long (thousands of equal
+// logits in a step, a top_k of thousands beside a top_p) are left to k_sample_slow, which finds the cut by
+// histograms over ever smaller ranges. The row is read from memory once, and twice more mostly from caches.
 #include <hip/hip_runtime.h>
 #include <math.h>
 
@@ -35,10 +34,14 @@ namespace oz2 {
 namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
-constexpr int kBins = 2048;
-constexpr int kList = 4 * kThreads;
-// Weights below 2^-41 round to 0: entries that low are in no histogram.
-constexpr double kLowest = -41.0, kBinsPerOctave = 49.0;  // 41 * 49 < kBins
+constexpr int kBins = 4096;
+constexpr int kList = 2048;   // undecided entries that a row has room for
+constexpr int kPairs = 256;   // those that are compared each with each
+constexpr int kRanges = 1024; // ranges of indexes, at most
+// Weights below 2^-41 round to 0: entries that low are in no histogram. (The steps are found in
+// binary32, so a little is left below.)
+constexpr double kLowest = -41.0;
+constexpr float kLowestStep = -41.01f, kStepsPerOctave = 99.5f;  // 41.01 * 99.5 < kBins
 constexpr double kUnit = 0x1p40;
 
 // ---- weights ------------------------------------------------------------------------
@@ -51,23 +54,26 @@ __device__ __forceinline__ float of_key(uint32_t k) {
     return __uint_as_float(k ^ ((int32_t)k < 0 ? 0x80000000u : 0xffffffffu));
 }
 // Larger logits first, then lower indexes: a descending order of these is the filters' order.
-__device__ __forceinline__ uint64_t code_of(float x, int64_t j) { return (uint64_t)key_of(x) << 32 | (uint32_t)~(uint32_t)j; }
+__device__ __forceinline__ uint64_t code_of(float x, uint32_t j) { return (uint64_t)key_of(x) << 32 | ~j; }
+__device__ __forceinline__ uint32_t index_of(uint64_t code) { return ~(uint32_t)code; }
+__device__ __forceinline__ float logit_of(uint64_t code) { return of_key((uint32_t)(code >> 32)); }
 
 struct Row {
-    double top, c;   // largest logit; log2(e) / temperature
-    bool infinite;   // the largest is +inf: entries that are have weight 1, others 0
+    double c;        // log2(e) / temperature
+    float top, c32;  // largest logit
+    bool infinite;   // it is +inf: entries that are have weight 1, others 0
     double min40;    // min_p 2^40
+    __device__ __forceinline__ float mapped(float x) const { return infinite ? (x == INFINITY ? 0.f : -INFINITY) : x; }
     // log2 of the weight
-    __device__ __forceinline__ double level(float x) const {
-        if (infinite) x = x == INFINITY ? 0.f : -INFINITY;
-        return ((double)x - top) * c;
-    }
+    __device__ __forceinline__ double level(float x) const { return ((double)mapped(x) - (double)top) * c; }
+    // The same in binary32, for the steps: both roundings keep the order of the logits.
+    __device__ __forceinline__ float near(float x) const { return (mapped(x) - top) * c32; }
 };
+__device__ __forceinline__ int bin_of(float t) { return (int)(t * -kStepsPerOctave); }
 // 2^40 2^t for t in [-41, 0]: 2^f for |f| <= 1/2 by its Taylor series (remainder below 2^-47), the rest in
 // the exponent. 0 below.
 __device__ __forceinline__ double weight_of(double t) {
-    if (!(t >= kLowest)) return 0.0;
-    const double n = rint(t), f = t - n;
+    const double n = rint(fmax(t, -64.0)), f = t - n;
     double p = 4.44553827187081e-10;  // ln2^11 / 11!
     p = fma(p, f, 7.054911620801121e-09);
     p = fma(p, f, 1.0178086009239696e-07);
@@ -80,29 +86,33 @@ __device__ __forceinline__ double weight_of(double t) {
     p = fma(p, f, 0.2402265069591007);
     p = fma(p, f, 0.6931471805599453);
     p = fma(p, f, 1.0);
-    return p * __longlong_as_double((int64_t)(1023 + 40 + (int)n) << 52);
+    const double w = p * __longlong_as_double((int64_t)(1023 + 40 + (int)n) << 52);
+    return t >= kLowest ? w : 0.0;
 }
 // Rounded to an integer: the significand of the sum with 2^52.
 __device__ __forceinline__ uint64_t units(double w) {
     return (uint64_t)__double_as_longlong(w + 0x1p52) - (uint64_t)__double_as_longlong(0x1p52);
 }
-__device__ __forceinline__ int bin_of(double t) { return (int)(-t * kBinsPerOctave); }
 
 // ---- a block's shared memory and its collective steps ----------------------------------
 struct Shared {
     uint64_t weight[kBins];
-    uint64_t list[kList];
     uint32_t count[kBins];
+    uint64_t list[kList];
+    uint64_t few[kPairs];
+    uint64_t range[kRanges];
     uint64_t part[kWaves];
     uint64_t found[4];
-    int n;
+    int n;  // of the list
 };
 
 __device__ __forceinline__ uint64_t shfl_up64(uint64_t x, int o) { return (uint64_t)__shfl_up((unsigned long long)x, o, 64); }
 __device__ __forceinline__ uint64_t shfl_xor64(uint64_t x, int o) { return (uint64_t)__shfl_xor((unsigned long long)x, o, 64); }
+__device__ __forceinline__ uint64_t shfl64(uint64_t x, int lane) { return (uint64_t)__shfl((unsigned long long)x, lane, 64); }
+__device__ __forceinline__ void add64(uint64_t *to, uint64_t x) { atomicAdd((unsigned long long *)to, (unsigned long long)x); }
 
 // The sum of x over the threads before this one; total: over all. Ends behind a barrier, so s.part is free again.
-__device__ uint64_t scan(uint64_t x, Shared &s, uint64_t &total) {
+__device__ __forceinline__ uint64_t scan(uint64_t x, Shared &s, uint64_t &total) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     uint64_t in = x;
 #pragma unroll
@@ -112,25 +122,29 @@ __device__ uint64_t scan(uint64_t x, Shared &s, uint64_t &total) {
     }
     if (lane == 63) s.part[wave] = in;
     __syncthreads();
-    uint64_t before = 0;
-    total = 0;
+    uint64_t parts = s.part[lane & (kWaves - 1)];
+    const uint64_t own = parts;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) {
-        if (i == wave) before = total;
-        total += s.part[i];
+    for (int o = 1; o < kWaves; o <<= 1) {
+        const uint64_t y = shfl_up64(parts, o);
+        if ((lane & (kWaves - 1)) >= o) parts += y;
     }
+    total = shfl64(parts, kWaves - 1);
+    const uint64_t before = shfl64(parts - own, wave);
     __syncthreads();
     return before + in - x;
 }
+// The largest (or smallest) x of all threads.
 template <bool MAX>
-__device__ uint64_t extreme(uint64_t x, Shared &s) {
+__device__ __forceinline__ uint64_t extreme(uint64_t x, Shared &s) {
     auto of = [](uint64_t a, uint64_t b) { return MAX ? (a > b ? a : b) : (a < b ? a : b); };
 #pragma unroll
     for (int o = 32; o >= 1; o >>= 1) x = of(x, shfl_xor64(x, o));
     if ((threadIdx.x & 63) == 0) s.part[threadIdx.x >> 6] = x;
     __syncthreads();
+    x = s.part[threadIdx.x & (kWaves - 1)];
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) x = of(x, s.part[i]);
+    for (int o = kWaves / 2; o >= 1; o >>= 1) x = of(x, shfl_xor64(x, o));
     __syncthreads();
     return x;
 }
@@ -141,7 +155,7 @@ __device__ void sort_list(int n, Shared &s) {
         for (int step = size >> 1; step >= 1; step >>= 1) {
             __syncthreads();
             for (int i = threadIdx.x; i < n / 2; i += kThreads) {
-                const int a = (i / step) * 2 * step + i % step, b = a + step;
+                const int a = 2 * i - (i & (step - 1)), b = a + step;
                 const uint64_t x = s.list[a], y = s.list[b];
                 if ((x < y) == (((a & size) == 0) == DOWN)) {
                     s.list[a] = y;
@@ -154,89 +168,104 @@ __device__ void sort_list(int n, Shared &s) {
 __device__ __forceinline__ int power_of_two(int n) { return n <= 1 ? 1 : 1 << (32 - __clz(n - 1)); }
 
 // f(x, j) for the entries j in [a, b) of a row, by `threads` threads of which this is the one
-// numbered `at`: U vectors of 8 each at a time, and those of the next turn on their way meanwhile.
-template <int U, class T, class F>
-__device__ __forceinline__ void sweep(const T *row, int64_t a, int64_t b, int at, int threads, F f) {
-    float x[U][8];
-    auto load = [&](int64_t j, float(&to)[U][8]) {
+// numbered `at`, 8 consecutive ones at a time, U such vectors on their way at once and those of the next turn
+// while f works. Beyond b x is -inf, which no f counts.
+template <class T>
+struct Eight {
+    U16 u[sizeof(T) / 2];
+};
+template <class T>
+__device__ __forceinline__ Eight<T> load_eight(const T *row, uint32_t j, uint32_t b) {
+    Eight<T> r;
+    if (j + 8 <= b) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) load8(row, j + 8 * u * threads, b, to[u]);
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = *(const U16 *)((const char *)(row + j) + 16 * i);
+    } else {
+        T e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = j + i < b ? row[j + i] : (T)-INFINITY;
+        r = __builtin_bit_cast(Eight<T>, e);
+    }
+    return r;
+}
+template <int U, class T, class F>
+__device__ __forceinline__ void sweep(const T *row, uint32_t a, uint32_t b, uint32_t at, uint32_t threads, F f) {
+    Eight<T> v[U];
+    auto load = [&](uint32_t j) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) v[u] = load_eight(row, j + 8 * u * threads, b);
     };
-    int64_t j = a + 8 * at;
-    load(j, x);
-    while (j < b) {
-        float next[U][8];
-        load(j + 8 * U * threads, next);
+    uint32_t j = a + 8 * at;
+    load(j);
+    for (; j < b; j += 8 * U * threads) {
+        float x[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            struct { T e[8]; } e = __builtin_bit_cast(decltype(e), v[u]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[u][i] = (float)e.e[i];
+        }
+        load(j + 8 * U * threads);
 #pragma unroll
         for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int64_t k = j + 8 * u * threads + i;
-                if (k < b) f(x[u][i], k);
-                __builtin_amdgcn_sched_barrier(0);
+                f(x[u][i], j + 8 * u * threads + i);
+                // one exponential at a time: eight side by side run out of registers
+                if constexpr (U == 1) __builtin_amdgcn_sched_barrier(0);
             }
-#pragma unroll
-        for (int u = 0; u < U; ++u)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[u][i] = next[u][i];
-        j += 8 * U * threads;
     }
 }
+// The list as a source of the same kind.
+template <class F>
+__device__ __forceinline__ void sweep_list(int n, Shared &s, F f) {
+    for (int i = threadIdx.x; i < n; i += kThreads) f(logit_of(s.list[i]), index_of(s.list[i]));
+}
 
-// The histogram over the steps below the largest, of the entries whose code is not below `cut`.
-template <bool WEIGHTS, class T>
-__device__ void histogram(const T *row, int64_t v, const Row &r, uint64_t cut, Shared &s) {
+__device__ __forceinline__ void clear_histogram(Shared &s) {
     for (int i = threadIdx.x; i < kBins; i += kThreads) {
         s.count[i] = 0;
-        if (WEIGHTS) s.weight[i] = 0;
+        s.weight[i] = 0;
     }
-    __syncthreads();
-    sweep<1>(row, 0, v, threadIdx.x, kThreads, [&](float x, int64_t j) {
-        const double t = r.level(x);
-        if (t >= kLowest && (cut == 0 || code_of(x, j) >= cut)) {
-            const int b = bin_of(t);
-            atomicAdd(&s.count[b], 1u);
-            if (WEIGHTS) atomicAdd((unsigned long long *)&s.weight[b], (unsigned long long)units(weight_of(t)));
-        }
-    });
     __syncthreads();
 }
 
-// What the histogram says: of its bins in order (from the last one down if DOWN) the first at which `reaches`
+// What a histogram says: of its bins in order (from the last one down if DOWN) the first at which `reaches`
 // holds of the count and the weight up to and with it.
 struct Crossing {
     int bin;                   // -1: none
     uint64_t count_before, weight_before;
     uint64_t count, weight;    // of all bins
 };
-template <bool WEIGHTS, bool DOWN, class Reaches>
-__device__ Crossing crossing(Shared &s, Reaches reaches) {
+template <bool DOWN, class Reaches>
+__device__ __forceinline__ Crossing crossing(Shared &s, bool weights, Reaches reaches) {
     constexpr int PER = kBins / kThreads;
-    uint64_t c[PER], w[PER], cs = 0, ws = 0;
+    // (read twice, so that they need no registers in between)
+    auto count_of = [&](int i) -> uint64_t { return s.count[DOWN ? kBins - 1 - i : i]; };
+    auto weight_at = [&](int i) -> uint64_t { return weights ? s.weight[DOWN ? kBins - 1 - i : i] : 0; };
+    uint64_t cs = 0, ws = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        const int b = PER * (int)threadIdx.x + i;
-        c[i] = s.count[DOWN ? kBins - 1 - b : b];
-        w[i] = WEIGHTS ? s.weight[DOWN ? kBins - 1 - b : b] : 0;
-        cs += c[i];
-        ws += w[i];
+        cs += count_of(PER * (int)threadIdx.x + i);
+        ws += weight_at(PER * (int)threadIdx.x + i);
     }
     Crossing r;
     if (threadIdx.x == 0) s.found[0] = ~(uint64_t)0;
     uint64_t cb = scan(cs, s, r.count), wb = 0;
     r.weight = 0;
-    if (WEIGHTS) wb = scan(ws, s, r.weight);
+    if (weights) wb = scan(ws, s, r.weight);
     auto done = [&](uint64_t count, uint64_t weight) { return reaches(count, weight, r); };
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-        if (c[i] != 0 && !done(cb, wb) && done(cb + c[i], wb + w[i])) {
-            const int b = PER * (int)threadIdx.x + i;
+        const int b = PER * (int)threadIdx.x + i;
+        const uint64_t c = count_of(b), w = weight_at(b);
+        if (c != 0 && !done(cb, wb) && done(cb + c, wb + w)) {
             s.found[0] = (uint64_t)(DOWN ? kBins - 1 - b : b);
             s.found[1] = cb;
             s.found[2] = wb;
         }
-        cb += c[i];
-        wb += w[i];
+        cb += c;
+        wb += w;
     }
     __syncthreads();
     r.bin = (int)(int64_t)s.found[0];
@@ -246,88 +275,73 @@ __device__ Crossing crossing(Shared &s, Reaches reaches) {
     return r;
 }
 
-// Entries for which `in` holds, as codes, into s.list (which has room); their number.
-template <class T, class In>
-__device__ int collect(const T *row, int64_t v, Shared &s, In in) {
-    if (threadIdx.x == 0) s.n = 0;
+// ---- cuts ---------------------------------------------------------------------------------
+// For up to kPairs codes: of each the number and the weight of those above it, by four threads that
+// compare it with a quarter of the others each. This thread's is code threadIdx.x / 4. Leaves the
+// weights of the codes in s.weight.
+struct Place {
+    uint64_t code, weight, count_before, weight_before;
+    double w;   // the weight before its rounding
+    bool real;  // there is such a code
+};
+__device__ __forceinline__ Place place_in(const uint64_t *list, int n, const Row &r, Shared &s) {
+    Place p;
+    const int e = threadIdx.x >> 2;
+    p.real = e < n;
+    p.code = p.real ? list[e] : 0;
+    p.w = p.real ? weight_of(r.level(logit_of(p.code))) : 0.0;
+    p.weight = units(p.w);
+    if (p.real && (threadIdx.x & 3) == 0) s.weight[e] = p.weight;
     __syncthreads();
-    sweep<1>(row, 0, v, threadIdx.x, kThreads, [&](float x, int64_t j) {
-        const uint64_t code = code_of(x, j);
-        if (in(x, code)) s.list[min(atomicAdd(&s.n, 1), kList - 1)] = code;
-    });
-    __syncthreads();
-    return min(s.n, kList);
-}
-__device__ void sort_codes(int n, Shared &s) {
-    const int p = power_of_two(n);
-    for (int i = n + threadIdx.x; i < p; i += kThreads) s.list[i] = 0;
-    sort_list<true>(p, s);
+    uint32_t count = 0;
+    uint64_t weight = 0;
+    if (p.real)
+        for (int j = threadIdx.x & 3; j < n; j += 4) {
+            const bool above = list[j] > p.code;
+            count += above;
+            weight += above ? s.weight[j] : 0;
+        }
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        count += __shfl_xor(count, o, 64);
+        weight += shfl_xor64(weight, o);
+    }
+    p.count_before = count;
+    p.weight_before = weight;
+    return p;
 }
 
-// The code in the sorted list s.list[0 .. n) at which `reaches` first holds of the number and the weight of
-// the entries down to and with it; the last one if at none. count, weight: of those before the list.
-template <class Reaches>
-__device__ uint64_t crossing_of_list(int n, const Row &r, uint64_t count, uint64_t weight, Shared &s, Reaches reaches) {
-    uint64_t w[4], sum = 0, total;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int at = 4 * (int)threadIdx.x + i;
-        w[i] = at < n ? units(weight_of(r.level(of_key((uint32_t)(s.list[at] >> 32))))) : 0;
-        sum += w[i];
-    }
-    weight += scan(sum, s, total);
-    if (threadIdx.x == 0) s.found[0] = s.list[n - 1];
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int at = 4 * (int)threadIdx.x + i;
-        if (at < n && !reaches(count + at, weight) && reaches(count + at + 1, weight + w[i])) s.found[0] = s.list[at];
-        weight += w[i];
-    }
-    __syncthreads();
-    const uint64_t found = s.found[0];
-    __syncthreads();
-    return found;
-}
-
-// The code of the entry at which `reaches` first holds of the number and the weight of the entries down to
-// and with it, in the filters' order, given that this is in step `bin` of the histogram and what is before it.
-// Histograms over ever smaller ranges of codes until what is left fits the list.
-template <bool WEIGHTS, class T, class Reaches>
-__device__ uint64_t refine(const T *row, int64_t v, const Row &r, uint64_t cut, int bin, uint64_t count, uint64_t weight,
-                           uint64_t members, Shared &s, Reaches reaches) {
-    auto in_step = [&](float x, uint64_t code) {
-        const double t = r.level(x);
-        return t >= kLowest && bin_of(t) == bin && code >= cut;
-    };
+// The lowest code that is kept among those entries of a source for which `in` holds and whose code is not below
+// `cut`: an entry is kept if `reaches` does not hold of the number and the weight of the entries above it. count,
+// weight: of those above all of these; members: how many these are. Histograms over ever smaller ranges of codes until few are
+// left, which are compared with each other. each(f) calls f(x, j) for the source's entries.
+template <class Each, class In, class Reaches>
+__device__ __forceinline__ uint64_t refine(Each each, In in, bool weights, uint64_t cut, uint64_t count, uint64_t weight,
+                                           uint64_t members, const Row &r, Shared &s, Reaches reaches) {
     uint64_t lo = ~(uint64_t)0, hi = 0;
-    sweep<1>(row, 0, v, threadIdx.x, kThreads, [&](float x, int64_t j) {
+    each([&](float x, uint32_t j) {
         const uint64_t code = code_of(x, j);
-        if (in_step(x, code)) {
+        if (code >= cut && in(x)) {
             lo = code < lo ? code : lo;
             hi = code > hi ? code : hi;
         }
     });
     lo = extreme<false>(lo, s);
     hi = extreme<true>(hi, s);
-    while (members > kList) {
+    while (members > kPairs) {
         // (here lo < hi, since codes differ)
-        const int shift = max(0, 64 - __clzll((long long)(hi - lo)) - 11);
-        for (int i = threadIdx.x; i < kBins; i += kThreads) {
-            s.count[i] = 0;
-            if (WEIGHTS) s.weight[i] = 0;
-        }
-        __syncthreads();
-        sweep<1>(row, 0, v, threadIdx.x, kThreads, [&](float x, int64_t j) {
+        const int shift = max(0, 64 - __clzll((long long)(hi - lo)) - 12);
+        clear_histogram(s);
+        each([&](float x, uint32_t j) {
             const uint64_t code = code_of(x, j);
-            if (code >= lo && code <= hi && in_step(x, code)) {
+            if (code >= lo && code <= hi && in(x)) {
                 const int b = (int)((code - lo) >> shift);
                 atomicAdd(&s.count[b], 1u);
-                if (WEIGHTS) atomicAdd((unsigned long long *)&s.weight[b], (unsigned long long)units(weight_of(r.level(x))));
+                if (weights) add64(&s.weight[b], units(weight_of(r.level(x))));
             }
         });
         __syncthreads();
-        const Crossing x = crossing<WEIGHTS, true>(s, [&](uint64_t c, uint64_t w, const Crossing &) {
+        const Crossing x = crossing<true>(s, weights, [&](uint64_t c, uint64_t w, const Crossing &) {
             return reaches(count + c, weight + w);
         });
         count += x.count_before;
@@ -338,96 +352,143 @@ __device__ uint64_t refine(const T *row, int64_t v, const Row &r, uint64_t cut, 
         hi = end < hi ? end : hi;
         __syncthreads();
     }
-    const int n = collect(row, v, s, [&](float x, uint64_t code) { return code >= lo && code <= hi && in_step(x, code); });
-    sort_codes(n, s);
-    return crossing_of_list(n, r, count, weight, s, reaches);
+    if (threadIdx.x == 0) s.n = 0;
+    __syncthreads();
+    each([&](float x, uint32_t j) {
+        const uint64_t code = code_of(x, j);
+        if (code >= lo && code <= hi && in(x)) s.few[min(atomicAdd(&s.n, 1), kPairs - 1)] = code;
+    });
+    __syncthreads();
+    const Place p = place_in(s.few, min(s.n, kPairs), r, s);
+    const bool kept = p.real && !reaches(count + p.count_before, weight + p.weight_before);
+    return extreme<false>(kept ? p.code : ~(uint64_t)0, s);
 }
 
+// ---- the token ----------------------------------------------------------------------------
+struct Drawn {
+    uint64_t code;   // of the entry
+    uint64_t total;  // the sum of the kept weights
+};
 // Where u falls in a sum of units: below it at any rate.
 __device__ __forceinline__ uint64_t place_of(double u, uint64_t total) {
     const double x = u > 0.0 ? u * (double)total : 0.0;
     return x < (double)(total - 1) ? (uint64_t)x : total - 1;
 }
 
-struct Drawn {
-    int64_t token;
-    uint64_t total;
-    float logit;
+// The settings of a row and its largest entry.
+enum class Answer { invalid, greedy, draw };
+struct Request {
+    double top_p, u;
+    int64_t top_k;   // 0: off
+    Row r;
+    uint64_t code;   // of the largest entry
+    Answer answer;
+    __device__ __forceinline__ bool filters() const { return top_k > 0 || top_p < 1.0; }
+    __device__ __forceinline__ double share(uint64_t whole) const { return fmax(top_p * (double)whole, 0.5); }
 };
 
-// The token from a list that holds every entry that the filters may keep (and is in no order): n entries,
-// of which the top_k largest are kept (0: all); `whole`: the sum that top_p is a part of, 0 for that of the
-// entries kept so far.
-__device__ Drawn draw_from_list(int n, const Row &r, int64_t top_k, double top_p, uint64_t whole, double u, Shared &s) {
-    sort_codes(n, s);
-    if (top_k > 0 && top_k < n) n = (int)top_k;
-    double w[4];
+// From a list of up to kPairs entries that holds all that may be kept; `whole`: the sum that top_p is a part of
+// where top_k is off.
+__device__ __forceinline__ Drawn draw_from_few(int n, const Request &q, uint64_t whole, Shared &s) {
+    const Place p = place_in(s.list, n, q.r, s);
+    const bool first = (threadIdx.x & 3) == 0;
+    bool kept = p.real;
+    if (q.top_k > 0) {
+        kept = kept && p.count_before < (uint64_t)q.top_k;
+        if (q.top_p < 1.0) scan(kept && first ? p.weight : 0, s, whole);
+    }
+    if (q.top_p < 1.0) kept = kept && (double)p.weight_before < q.share(whole);
+    kept = kept && p.w >= q.r.min40;
+    uint64_t total;
+    scan(kept && first ? p.weight : 0, s, total);
+    if (p.real && first) s.weight[threadIdx.x >> 2] = kept ? p.weight : 0;
+    __syncthreads();
+    uint64_t before = 0;
+    if (p.real)
+        for (int j = threadIdx.x & 3; j < n; j += 4)
+            // (the lower half of a code falls with the index)
+            before += (uint32_t)s.list[j] > (uint32_t)p.code ? s.weight[j] : 0;
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) before += shfl_xor64(before, o);
+    const uint64_t place = place_of(q.u, total);
+    if (kept && before <= place && place < before + p.weight) s.found[0] = p.code;
+    __syncthreads();
+    return {s.found[0], total};
+}
+
+// The same for a longer list: sorted, cut, and sorted by index.
+__device__ Drawn draw_from_list(int n, const Request &q, uint64_t whole, Shared &s) {
+    constexpr int PER = kList / kThreads;
+    for (int i = n + threadIdx.x; i < power_of_two(n); i += kThreads) s.list[i] = 0;
+    sort_list<true>(power_of_two(n), s);
+    if (q.top_k > 0 && q.top_k < n) n = (int)q.top_k;
+    double w[PER];
     uint64_t sum = 0, total;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int at = 4 * (int)threadIdx.x + i;
-        w[i] = at < n ? weight_of(r.level(of_key((uint32_t)(s.list[at] >> 32)))) : 0.0;
+    for (int i = 0; i < PER; ++i) {
+        const int at = PER * (int)threadIdx.x + i;
+        w[i] = at < n ? weight_of(q.r.level(logit_of(s.list[at]))) : 0.0;
         sum += units(w[i]);
     }
     uint64_t before = scan(sum, s, total);
     if (threadIdx.x == 0) s.n = n;
     __syncthreads();
-    const double part = top_p < 1.0 ? top_p * (double)(whole ? whole : total) : INFINITY;
+    const double part = q.top_p < 1.0 ? q.share(q.top_k > 0 ? total : whole) : INFINITY;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int at = 4 * (int)threadIdx.x + i;
-        // the first entry that is not kept: below min_p, or behind the one that reaches top_p
-        if (at > 0 && at < n && (w[i] < r.min40 || (double)before >= part)) atomicMin(&s.n, at);
+    for (int i = 0; i < PER; ++i) {
+        const int at = PER * (int)threadIdx.x + i;
+        // the first entry that is not kept
+        if (at < n && (w[i] < q.r.min40 || (double)before >= part)) atomicMin(&s.n, at);
         before += units(w[i]);
     }
     __syncthreads();
     n = s.n;
-    // in the order of the indexes
     const int p = power_of_two(n);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int at = 4 * (int)threadIdx.x + i;
+    for (int i = 0; i < PER; ++i) {
+        const int at = PER * (int)threadIdx.x + i;
         if (at < p) {
             const uint64_t code = s.list[at];
-            s.list[at] = at < n ? (uint64_t)(uint32_t)~(uint32_t)code << 32 | code >> 32 : ~(uint64_t)0;
+            s.list[at] = at < n ? (uint64_t)index_of(code) << 32 | code >> 32 : ~(uint64_t)0;
         }
     }
     sort_list<false>(p, s);
-    uint64_t k[4];
+    uint64_t k[PER];
     sum = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int at = 4 * (int)threadIdx.x + i;
-        k[i] = at < n ? units(weight_of(r.level(of_key((uint32_t)s.list[at])))) : 0;
+    for (int i = 0; i < PER; ++i) {
+        const int at = PER * (int)threadIdx.x + i;
+        k[i] = at < n ? units(weight_of(q.r.level(of_key((uint32_t)s.list[at])))) : 0;
         sum += k[i];
     }
     before = scan(sum, s, total);
-    const uint64_t place = place_of(u, total);
+    const uint64_t place = place_of(q.u, total);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (before <= place && place < before + k[i]) s.found[0] = s.list[4 * threadIdx.x + i];
+    for (int i = 0; i < PER; ++i) {
+        if (before <= place && place < before + k[i]) s.found[0] = s.list[PER * threadIdx.x + i];
         before += k[i];
     }
     __syncthreads();
     const uint64_t found = s.found[0];
-    return {(int64_t)(found >> 32), total, of_key((uint32_t)found)};
+    return {found << 32 | (uint32_t)~(uint32_t)(found >> 32), total};
 }
 
-// The token in the range [a, b) of indexes, where `place` falls in the sum of its kept weights: sums over
+// The code of the entry in the range [a, b) of indexes where `place` falls in the sum of its kept weights: sums over
 // sixteenths of the range, one per wavefront, then the sixteenth that holds it, down to one that the block
 // takes in one step.
 template <class T>
-__device__ Drawn draw_from_range(const T *row, int64_t a, int64_t b, const Row &r, uint64_t cut, uint64_t place, Shared &s) {
+__device__ __forceinline__ uint64_t draw_from_range(const T *row, uint32_t a, uint32_t b, const Row &r, uint64_t cut,
+                                                    uint64_t place, Shared &s) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    auto kept = [&](float x, int64_t j) -> uint64_t {
+    auto kept = [&](float x, uint32_t j) -> uint64_t {
         const double w = weight_of(r.level(x));
-        return w >= r.min40 && (cut == 0 || code_of(x, j) >= cut) ? units(w) : 0;
+        return w >= r.min40 && code_of(x, j) >= cut ? units(w) : 0;
     };
     while (b - a > 8 * kThreads) {
-        const int64_t part = ((b - a + kWaves - 1) / kWaves + 511) / 512 * 512;
-        const int64_t from = a + wave * part;
+        const uint32_t part = ((b - a + kWaves - 1) / kWaves + 511) / 512 * 512;
+        const uint32_t from = min(a + wave * part, b);
         uint64_t sum = 0;
-        sweep<1>(row, min(from, b), min(from + part, b), lane, 64, [&](float x, int64_t j) { sum += kept(x, j); });
+        sweep<1>(row, from, min(from + part, b), lane, 64, [&](float x, uint32_t j) { sum += kept(x, j); });
 #pragma unroll
         for (int o = 32; o >= 1; o >>= 1) sum += shfl_xor64(sum, o);
         if (lane == 0) s.part[wave] = sum;
@@ -442,66 +503,26 @@ __device__ Drawn draw_from_range(const T *row, int64_t a, int64_t b, const Row &
     }
     uint64_t k[8], sum = 0, total;
     float x[8];
-    load8(row, a + 8 * threadIdx.x, b, x);
+    const uint32_t j0 = a + 8 * threadIdx.x;
+    struct { T e[8]; } e = __builtin_bit_cast(decltype(e), load_eight(row, j0, b));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const int64_t j = a + 8 * threadIdx.x + i;
-        k[i] = j < b ? kept(x[i], j) : 0;
+        x[i] = (float)e.e[i];
+        k[i] = kept(x[i], j0 + i);
         sum += k[i];
+        __builtin_amdgcn_sched_barrier(0);
     }
     uint64_t before = scan(sum, s, total);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if (before <= place && place < before + k[i]) {
-            s.found[0] = (uint64_t)(a + 8 * threadIdx.x + i);
-            s.found[1] = __float_as_uint(x[i]);
-        }
+        if (before <= place && place < before + k[i]) s.found[0] = code_of(x[i], j0 + i);
         before += k[i];
     }
     __syncthreads();
-    return {(int64_t)s.found[0], 0, __uint_as_float((uint32_t)s.found[1])};
+    return s.found[0];
 }
 
-// A row's token by one block: top_k's cut, then top_p's among what that leaves, each from a histogram and what
-// refine finds inside its step, then the sums of ranges.
-template <class T, class Q>
-__device__ Drawn draw_slowly(const T *row, int64_t v, const Q &q, Shared &s) {
-    uint64_t cut = 0;
-    if (q.by_count) {
-        histogram<false>(row, v, q.r, 0, s);
-        const uint64_t k = (uint64_t)q.top_k;
-        const Crossing x = crossing<false, false>(s, [&](uint64_t c, uint64_t, const Crossing &) { return c >= k; });
-        if (x.bin >= 0) {
-            const uint64_t members = s.count[x.bin];
-            __syncthreads();
-            cut = refine<false>(row, v, q.r, 0, x.bin, x.count_before, 0, members, s, [&](uint64_t c, uint64_t) { return c >= k; });
-        }
-    }
-    if (q.top_p < 1.0) {
-        histogram<true>(row, v, q.r, cut, s);
-        const Crossing x = crossing<true, false>(s, [&](uint64_t, uint64_t w, const Crossing &all) {
-            return (double)w >= fmax(q.top_p * (double)all.weight, 0.5);
-        });
-        const double part = fmax(q.top_p * (double)x.weight, 0.5);
-        if (x.bin >= 0) {
-            const uint64_t members = s.count[x.bin];
-            __syncthreads();
-            cut = refine<true>(row, v, q.r, cut, x.bin, x.count_before, x.weight_before, members, s,
-                               [&](uint64_t, uint64_t w) { return (double)w >= part; });
-        }
-    }
-    uint64_t sum = 0, whole;
-    sweep<1>(row, 0, v, threadIdx.x, kThreads, [&](float x, int64_t j) {
-        const double w = weight_of(q.r.level(x));
-        if (w >= q.r.min40 && (cut == 0 || code_of(x, j) >= cut)) sum += units(w);
-    });
-    scan(sum, s, whole);
-    Drawn d = draw_from_range(row, 0, v, q.r, cut, place_of(q.u, whole), s);
-    d.total = whole;
-    return d;
-}
-
-// ---- the kernels -------------------------------------------------------------------------
+// ---- the phases --------------------------------------------------------------------------
 struct SampleArgs {
     const void *logits;
     int64_t ld, t, v;
@@ -512,59 +533,278 @@ struct SampleArgs {
     const int32_t *top_ks;
     int64_t *tokens;
     float *logprobs;  // or null
-    int64_t chunk;    // entries of a block, a multiple of 8192
+    // rows spread over blocks: entries of a block, a multiple of 8192, and blocks
+    uint32_t chunk;
     int chunks;
 };
-// A row's part of the workspace.
-constexpr int kMostChunks = 64, kRanges = kMostChunks * kWaves;  // a range is a sixteenth of a chunk
-struct RowState {
-    uint64_t weight[kBins];
-    uint32_t count[kBins];
-    uint64_t list[kList];
-    uint64_t range[kRanges];
-    uint64_t top[kMostChunks];  // the largest code of each chunk, all ones beside a NaN
-    int n;                      // of the list; kSlow: the row is left to k_sample_slow
-};
-constexpr int kSlow = -1;
+constexpr int64_t kLeft = -2;  // in `tokens` meanwhile: the row is left to k_sample_slow
 
-enum class Answer { invalid, greedy, draw };
-struct Request {
-    double temperature, top_p, u;
-    int64_t top_k;   // 0: off
-    bool by_count;   // whether top_k cuts first
-    bool filters;    // top_k or top_p
-    Row r;
-    uint64_t code;   // of the largest entry
-    Answer answer;
-};
-// The settings of row i of this launch, and its largest entry.
-__device__ __forceinline__ Request request_of(const SampleArgs &p, int64_t i, const RowState &state) {
+template <class T>
+__device__ __forceinline__ uint64_t top_of(const T *row, uint32_t a, uint32_t b, Shared &s) {
+    float best = -INFINITY;
+    uint32_t at = a;
+    bool nan = false;
+    sweep<2>(row, a, b, threadIdx.x, kThreads, [&](float x, uint32_t j) {
+        nan |= x != x;
+        if (x > best) {
+            best = x;
+            at = j;
+        }
+    });
+    return extreme<true>(nan ? ~(uint64_t)0 : code_of(best, at), s);
+}
+
+__device__ __forceinline__ Request request_of(const SampleArgs &p, int64_t i, uint64_t code) {
     Request q;
-    q.temperature = p.temperatures ? (double)p.temperatures[i] : p.temperature;
-    q.top_p = p.top_ps ? (double)p.top_ps[i] : p.top_p;
+    const double temperature = p.temperatures ? (double)p.temperatures[i] : p.temperature;
     const double min_p = p.min_ps ? (double)p.min_ps[i] : p.min_p;
+    q.top_p = p.top_ps ? (double)p.top_ps[i] : p.top_p;
     q.top_k = p.top_ks ? (int64_t)p.top_ks[i] : p.top_k;
     q.u = p.u[i];
-    q.code = 0;
-    for (int c = 0; c < p.chunks; ++c) q.code = max(q.code, state.top[c]);
-    const float top = of_key((uint32_t)(q.code >> 32));
+    q.code = code;
+    const float top = logit_of(code);
     // NaN fails the comparisons
-    const bool fine = q.code != ~(uint64_t)0 && top != -INFINITY && q.temperature >= 0.0 && q.top_p == q.top_p &&
-                      min_p == min_p && q.u == q.u;
-    q.answer = !fine ? Answer::invalid : q.temperature == 0.0 ? Answer::greedy : Answer::draw;
+    const bool fine = code != ~(uint64_t)0 && top != -INFINITY && temperature >= 0.0 && q.top_p == q.top_p && min_p == min_p &&
+                      q.u == q.u;
+    q.answer = !fine ? Answer::invalid : temperature == 0.0 ? Answer::greedy : Answer::draw;
     if (q.top_p <= 0.0) {  // the largest alone
         q.top_k = 1;
         q.top_p = 1.0;
     }
     if (q.top_k <= 0 || q.top_k >= p.v) q.top_k = 0;
-    q.by_count = q.top_k > 0;
-    q.filters = q.by_count || q.top_p < 1.0;
     q.r.infinite = top == INFINITY;
-    q.r.top = q.r.infinite ? 0.0 : (double)top;
-    // (finite, so that it can be a factor of 0 and of infinities)
-    q.r.c = fmin(fmax(1.4426950408889634 / q.temperature, 1e-300), 1e300);
+    q.r.top = q.r.infinite ? 0.f : top;
+    // (so that it is a finite binary32 number, and can be a factor of 0 and of infinities)
+    q.r.c = fmin(fmax(1.4426950408889634 / temperature, 1e-30), 1e30);
+    q.r.c32 = (float)q.r.c;
     q.r.min40 = fmin(min_p, 1.0) * kUnit;
     return q;
+}
+
+// Counts the entries in [a, b) into the block's histogram; with their weights where top_p cuts first.
+template <class T>
+__device__ __forceinline__ void count_steps(const T *row, uint32_t a, uint32_t b, const Request &q, Shared &s) {
+    if (q.top_k > 0)
+        sweep<2>(row, a, b, threadIdx.x, kThreads, [&](float x, uint32_t) {
+            const float t = q.r.near(x);
+            if (t >= kLowestStep) atomicAdd(&s.count[bin_of(t)], 1u);
+        });
+    else
+        sweep<1>(row, a, b, threadIdx.x, kThreads, [&](float x, uint32_t) {
+            const float t = q.r.near(x);
+            if (t >= kLowestStep) {
+                atomicAdd(&s.count[bin_of(t)], 1u);
+                add64(&s.weight[bin_of(t)], units(weight_of(q.r.level(x))));
+            }
+        });
+    __syncthreads();
+}
+
+// What the histogram decides: entries in steps before `first` are kept by the filters, those after `last` are
+// not, and those between are to be collected.
+struct Border {
+    int first, last;
+    bool left;               // too many of them
+    bool near;               // first is 0: the list holds all that may be kept
+    uint64_t count_before, weight_before, whole;
+};
+__device__ __forceinline__ Border border_of(const Request &q, Shared &s) {
+    Border d = {kBins, -1, false, false, 0, 0, 0};
+    if (!q.filters()) return d;
+    const bool by_count = q.top_k > 0;
+    const Crossing x = crossing<false>(s, !by_count, [&](uint64_t count, uint64_t w, const Crossing &all) {
+        return by_count ? count >= (uint64_t)q.top_k : (double)w >= q.share(all.weight);
+    });
+    d.whole = x.weight;
+    const uint64_t members = x.bin < 0 ? 0 : s.count[x.bin];
+    const uint64_t down_to = x.bin < 0 ? x.count : x.count_before + members;
+    const bool both = by_count && q.top_p < 1.0;
+    if (down_to <= (uint64_t)(both ? kList : kPairs)) {
+        d.first = 0;
+        d.last = x.bin < 0 ? kBins - 1 : x.bin;
+        d.near = true;
+    } else if (both || members > (uint64_t)kList) {
+        d.left = true;
+    } else if (x.bin >= 0) {  // (else top_k is more than there are entries of any weight)
+        d.first = d.last = x.bin;
+        d.count_before = x.count_before;
+        d.weight_before = x.weight_before;
+    }
+    __syncthreads();
+    return d;
+}
+
+// This wavefront's range [a, b): its undecided entries to take(code), and the sum over those that are decided.
+template <class T, class Take>
+__device__ __forceinline__ uint64_t collect(const T *row, uint32_t a, uint32_t b, const Request &q, const Border &d, Take take) {
+    const int lane = threadIdx.x & 63;
+    uint64_t sum = 0;
+    if (d.near)
+        sweep<2>(row, a, b, lane, 64, [&](float x, uint32_t j) {
+            const float t = q.r.near(x);
+            if (t >= kLowestStep && bin_of(t) <= d.last) take(code_of(x, j));
+        });
+    else
+        sweep<1>(row, a, b, lane, 64, [&](float x, uint32_t j) {
+            const float t = q.r.near(x);
+            const int bin = t >= kLowestStep ? bin_of(t) : kBins;
+            if (bin < d.first) {
+                const double w = weight_of(q.r.level(x));
+                sum += w >= q.r.min40 ? units(w) : 0;
+            }
+            if (bin <= d.last && bin >= d.first) take(code_of(x, j));
+        });
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) sum += shfl_xor64(sum, o);
+    return sum;
+}
+
+// From the list (n entries in s.list) and the sums of `ranges` ranges of `part` indexes (s.range).
+template <class T>
+__device__ __forceinline__ Drawn draw(const T *row, uint32_t v, const Request &q, const Border &d, int n, int ranges,
+                                      uint32_t part, Shared &s) {
+    if (d.near) return n <= kPairs ? draw_from_few(n, q, d.whole, s) : draw_from_list(n, q, d.whole, s);
+    uint64_t cut = 0;
+    if (n > 0) {
+        const double share = q.share(d.whole);
+        cut = refine([&](auto f) { sweep_list(n, s, f); }, [](float) { return true; }, q.top_k == 0, 0, d.count_before,
+                     d.weight_before, (uint64_t)n, q.r, s, [&](uint64_t count, uint64_t w) {
+                         return q.top_k > 0 ? count >= (uint64_t)q.top_k : (double)w >= share;
+                     });
+        for (int k = threadIdx.x; k < n; k += kThreads) {
+            const uint64_t code = s.list[k];
+            const double w = weight_of(q.r.level(logit_of(code)));
+            if (code >= cut && w >= q.r.min40) add64(&s.range[index_of(code) / part], units(w));
+        }
+        __syncthreads();
+    }
+    Drawn out;
+    const uint64_t mine = (int)threadIdx.x < ranges ? s.range[threadIdx.x] : 0, before = scan(mine, s, out.total);
+    const uint64_t place = place_of(q.u, out.total);
+    if (before <= place && place < before + mine) {
+        s.found[0] = threadIdx.x;
+        s.found[1] = place - before;
+    }
+    __syncthreads();
+    const uint32_t a = (uint32_t)s.found[0] * part;
+    const uint64_t left = s.found[1];
+    __syncthreads();
+    // (an entry below the cut's step, which the ranges do not count, is below the cut)
+    out.code = draw_from_range(row, a, min(a + part, v), q.r, cut, left, s);
+    return out;
+}
+
+__device__ __forceinline__ void answer(const SampleArgs &p, int64_t i, int64_t token, double logprob) {
+    if (threadIdx.x == 0) {
+        p.tokens[i] = token;
+        if (p.logprobs) p.logprobs[i] = (float)logprob;
+    }
+}
+__device__ __forceinline__ void answer(const SampleArgs &p, int64_t i, const Row &r, const Drawn &d) {
+    answer(p, i, index_of(d.code), r.level(logit_of(d.code)) * 0.6931471805599453 - log((double)d.total / kUnit));
+}
+// Whether the row has its answer already.
+__device__ __forceinline__ bool answered(const SampleArgs &p, int64_t i, const Request &q) {
+    if (q.answer == Answer::invalid) answer(p, i, -1, NAN);
+    if (q.answer == Answer::greedy) answer(p, i, index_of(q.code), 0.0);
+    return q.answer != Answer::draw;
+}
+
+// ---- a block per row ---------------------------------------------------------------------
+template <class T>
+__global__ __launch_bounds__(kThreads) void k_sample(SampleArgs p) {
+    __shared__ Shared s;
+    const int64_t i = blockIdx.x;
+    const T *row = (const T *)p.logits + i * p.ld;
+    const uint32_t v = (uint32_t)p.v;
+    const Request q = request_of(p, i, top_of(row, 0, v, s));
+    if (answered(p, i, q)) return;
+    if (q.filters()) {
+        clear_histogram(s);
+        count_steps(row, 0, v, q, s);
+    }
+    const Border d = border_of(q, s);
+    if (d.left) return answer(p, i, kLeft, 0.0);
+    if (threadIdx.x == 0) s.n = 0;
+    __syncthreads();
+    const int wave = threadIdx.x >> 6;
+    const uint32_t part = ((v + kWaves - 1) / kWaves + 511) / 512 * 512, a = min(wave * part, v);
+    const uint64_t sum = collect(row, a, min(a + part, v), q, d, [&](uint64_t code) {
+        s.list[min(atomicAdd(&s.n, 1), kList - 1)] = code;
+    });
+    if ((threadIdx.x & 63) == 0) s.range[wave] = sum;
+    __syncthreads();
+    const int n = min(s.n, kList);
+    __syncthreads();
+    answer(p, i, q.r, draw(row, v, q, d, n, kWaves, part, s));
+}
+
+// The rows that are left over: top_k's cut, then top_p's among what that leaves, each from a histogram and what
+// refine finds inside its step, then the sums of ranges. (A kernel of its own, whose registers are not the others'.)
+template <class T>
+__global__ __launch_bounds__(kThreads) void k_sample_slow(SampleArgs p) {
+    __shared__ Shared s;
+    const int64_t i = blockIdx.x;
+    if (p.tokens[i] != kLeft) return;
+    const T *row = (const T *)p.logits + i * p.ld;
+    const uint32_t v = (uint32_t)p.v;
+    const Request q = request_of(p, i, top_of(row, 0, v, s));
+    const Row &r = q.r;
+    uint64_t cut = 0;
+    auto each = [&](auto f) { sweep<1>(row, 0, v, threadIdx.x, kThreads, f); };
+    for (int filter = 0; filter < 2; ++filter) {
+        const bool weights = filter == 1;
+        if (weights ? q.top_p >= 1.0 : q.top_k == 0) continue;
+        clear_histogram(s);
+        each([&](float x, uint32_t j) {
+            const float t = r.near(x);
+            if (t >= kLowestStep && code_of(x, j) >= cut) {
+                atomicAdd(&s.count[bin_of(t)], 1u);
+                if (weights) add64(&s.weight[bin_of(t)], units(weight_of(r.level(x))));
+            }
+        });
+        __syncthreads();
+        double share = 0.0;
+        const Crossing x = crossing<false>(s, weights, [&](uint64_t c, uint64_t w, const Crossing &all) {
+            return weights ? (double)w >= q.share(all.weight) : c >= (uint64_t)q.top_k;
+        });
+        share = q.share(x.weight);
+        if (x.bin < 0) continue;
+        const uint64_t members = s.count[x.bin];
+        __syncthreads();
+        cut = refine(each, [&](float y) {
+            const float t = r.near(y);
+            return t >= kLowestStep && bin_of(t) == x.bin;
+        }, weights, cut, x.count_before, x.weight_before, members, r, s, [&](uint64_t c, uint64_t w) {
+            return weights ? (double)w >= share : c >= (uint64_t)q.top_k;
+        });
+    }
+    uint64_t sum = 0;
+    Drawn d;
+    each([&](float x, uint32_t j) {
+        const double w = weight_of(r.level(x));
+        if (w >= r.min40 && code_of(x, j) >= cut) sum += units(w);
+    });
+    scan(sum, s, d.total);
+    d.code = draw_from_range(row, 0, v, r, cut, place_of(q.u, d.total), s);
+    answer(p, i, r, d);
+}
+
+// ---- a row spread over blocks -------------------------------------------------------------
+// A row's part of the workspace. A range is a sixteenth of a chunk.
+constexpr int kMostChunks = kRanges / kWaves;
+struct RowState {
+    uint64_t weight[kBins];
+    uint32_t count[kBins];
+    uint64_t list[kList];
+    uint64_t range[kRanges];
+    uint64_t top[kMostChunks];
+    int n;
+};
+__device__ __forceinline__ Request request_of(const SampleArgs &p, int64_t i, const RowState &state) {
+    uint64_t code = 0;
+    for (int c = 0; c < p.chunks; ++c) code = max(code, state.top[c]);
+    return request_of(p, i, code);
 }
 
 template <class T>
@@ -572,18 +812,8 @@ __global__ __launch_bounds__(kThreads) void k_sample_top(SampleArgs p, RowState 
     __shared__ Shared s;
     const int64_t i = blockIdx.y;
     RowState &state = states[i];
-    const int64_t a = blockIdx.x * p.chunk, b = min(a + p.chunk, p.v);
-    float best = -INFINITY;
-    int64_t at = a;
-    bool nan = false;
-    sweep<4>((const T *)p.logits + i * p.ld, a, b, threadIdx.x, kThreads, [&](float x, int64_t j) {
-        nan |= x != x;
-        if (x > best) {
-            best = x;
-            at = j;
-        }
-    });
-    const uint64_t code = extreme<true>(nan ? ~(uint64_t)0 : code_of(best, at), s);
+    const uint32_t a = blockIdx.x * p.chunk;
+    const uint64_t code = top_of((const T *)p.logits + i * p.ld, a, min(a + p.chunk, (uint32_t)p.v), s);
     if (threadIdx.x == 0) state.top[blockIdx.x] = code;
     // what the next launches add to
     for (int k = (int)blockIdx.x * kThreads + threadIdx.x; k < kBins; k += p.chunks * kThreads) {
@@ -593,103 +823,32 @@ __global__ __launch_bounds__(kThreads) void k_sample_top(SampleArgs p, RowState 
     if (blockIdx.x == 0 && threadIdx.x == 0) state.n = 0;
 }
 
-// The sums of `kept` weights over this block's ranges.
-template <class T, class Kept>
-__device__ __forceinline__ void sum_ranges(const SampleArgs &p, const T *row, RowState &state, Kept kept) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t part = p.chunk / kWaves, a = min(blockIdx.x * p.chunk + wave * part, p.v);
-    uint64_t sum = 0;
-    sweep<1>(row, a, min(a + part, p.v), lane, 64, [&](float x, int64_t j) { sum += kept(x, j); });
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) sum += shfl_xor64(sum, o);
-    if (lane == 0) state.range[(int)blockIdx.x * kWaves + wave] = sum;
-}
-
 template <class T>
 __global__ __launch_bounds__(kThreads) void k_sample_count(SampleArgs p, RowState *states) {
-    __shared__ uint64_t weight[kBins];
-    __shared__ uint32_t count[kBins];
+    __shared__ Shared s;
     const int64_t i = blockIdx.y;
     RowState &state = states[i];
     const Request q = request_of(p, i, state);
-    if (q.answer != Answer::draw) return;
-    const T *row = (const T *)p.logits + i * p.ld;
-    if (!q.filters) {
-        sum_ranges(p, row, state, [&](float x, int64_t) -> uint64_t {
-            const double w = weight_of(q.r.level(x));
-            return w >= q.r.min40 ? units(w) : 0;
-        });
-        return;
-    }
-    for (int k = threadIdx.x; k < kBins; k += kThreads) {
-        count[k] = 0;
-        weight[k] = 0;
-    }
-    __syncthreads();
-    const int64_t a = blockIdx.x * p.chunk, b = min(a + p.chunk, p.v);
-    if (q.by_count)
-        sweep<1>(row, a, b, threadIdx.x, kThreads, [&](float x, int64_t) {
-            const double t = q.r.level(x);
-            if (t >= kLowest) atomicAdd(&count[bin_of(t)], 1u);
-        });
-    else
-        sweep<1>(row, a, b, threadIdx.x, kThreads, [&](float x, int64_t) {
-            const double t = q.r.level(x);
-            if (t >= kLowest) {
-                atomicAdd(&count[bin_of(t)], 1u);
-                atomicAdd((unsigned long long *)&weight[bin_of(t)], (unsigned long long)units(weight_of(t)));
-            }
-        });
-    __syncthreads();
+    if (q.answer != Answer::draw || !q.filters()) return;
+    clear_histogram(s);
+    const uint32_t a = blockIdx.x * p.chunk;
+    count_steps((const T *)p.logits + i * p.ld, a, min(a + p.chunk, (uint32_t)p.v), q, s);
     for (int k = threadIdx.x; k < kBins; k += kThreads)
-        if (count[k] != 0) {
-            if (p.chunks == 1) {
-                state.count[k] = count[k];
-                state.weight[k] = weight[k];
-            } else {
-                atomicAdd(&state.count[k], count[k]);
-                if (!q.by_count) atomicAdd((unsigned long long *)&state.weight[k], (unsigned long long)weight[k]);
-            }
+        if (s.count[k] != 0) {
+            atomicAdd(&state.count[k], s.count[k]);
+            if (q.top_k == 0) add64(&state.weight[k], s.weight[k]);
         }
 }
 
-// What the first filter's histogram says about the entries to collect.
-enum class Plan {
-    all,   // the filter keeps every entry: the token comes from the whole row
-    near,  // the list holds all entries down to step `bin`
-    far,   // the list holds those of step `bin`, the ranges the sums for the steps before it
-    slow   // neither
-};
-struct Cut {
-    Plan plan;
-    Crossing x;
-    uint64_t members;  // of the step
-    double part;       // the sum that top_p asks for
-};
-// (reads the row's histogram, into s)
-__device__ __forceinline__ Cut cut_of(const Request &q, const RowState &state, Shared &s) {
-    for (int k = threadIdx.x; k < kBins; k += kThreads) {
-        s.count[k] = state.count[k];
-        s.weight[k] = state.weight[k];
+__device__ __forceinline__ Border border_of(const Request &q, const RowState &state, Shared &s) {
+    if (q.filters()) {
+        for (int k = threadIdx.x; k < kBins; k += kThreads) {
+            s.count[k] = state.count[k];
+            s.weight[k] = state.weight[k];
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    Cut c;
-    c.x = crossing<true, false>(s, [&](uint64_t count, uint64_t w, const Crossing &all) {
-        return q.by_count ? count >= (uint64_t)q.top_k : (double)w >= fmax(q.top_p * (double)all.weight, 0.5);
-    });
-    c.part = fmax(q.top_p * (double)c.x.weight, 0.5);
-    c.members = c.x.bin < 0 ? 0 : s.count[c.x.bin];
-    if (c.x.bin < 0) {  // fewer entries of any weight than top_k
-        c.x.bin = kBins - 1;
-        c.x.count_before = c.x.count;
-        c.members = 0;
-        c.plan = c.x.count <= (uint64_t)kList ? Plan::near : q.top_p < 1.0 ? Plan::slow : Plan::all;
-    } else
-        c.plan = c.x.count_before + c.members <= (uint64_t)kList         ? Plan::near
-                     : c.members > (uint64_t)kList || (q.by_count && q.top_p < 1.0) ? Plan::slow
-                                                                                    : Plan::far;
-    __syncthreads();
-    return c;
+    return border_of(q, s);
 }
 
 template <class T>
@@ -698,35 +857,15 @@ __global__ __launch_bounds__(kThreads) void k_sample_collect(SampleArgs p, RowSt
     const int64_t i = blockIdx.y;
     RowState &state = states[i];
     const Request q = request_of(p, i, state);
-    if (q.answer != Answer::draw || !q.filters) return;
-    const Cut c = cut_of(q, state, s);
-    const T *row = (const T *)p.logits + i * p.ld;
-    auto take = [&](float x, int64_t j) { state.list[min(atomicAdd(&state.n, 1), kList - 1)] = code_of(x, j); };
-    if (c.plan == Plan::near) {
-        const int64_t a = blockIdx.x * p.chunk, b = min(a + p.chunk, p.v);
-        sweep<1>(row, a, b, threadIdx.x, kThreads, [&](float x, int64_t j) {
-            const double t = q.r.level(x);
-            if (t >= kLowest && bin_of(t) <= c.x.bin) take(x, j);
-        });
-    } else if (c.plan == Plan::far) {
-        sum_ranges(p, row, state, [&](float x, int64_t j) -> uint64_t {
-            const double t = q.r.level(x);
-            if (!(t >= kLowest)) return 0;
-            const int bin = bin_of(t);
-            if (bin > c.x.bin) return 0;
-            if (bin == c.x.bin) {
-                take(x, j);
-                return 0;
-            }
-            const double w = weight_of(t);
-            return w >= q.r.min40 ? units(w) : 0;
-        });
-    } else if (c.plan == Plan::all) {
-        sum_ranges(p, row, state, [&](float x, int64_t) -> uint64_t {
-            const double w = weight_of(q.r.level(x));
-            return w >= q.r.min40 ? units(w) : 0;
-        });
-    }
+    if (q.answer != Answer::draw) return;
+    const Border d = border_of(q, state, s);
+    if (d.left) return;
+    const int wave = threadIdx.x >> 6;
+    const uint32_t v = (uint32_t)p.v, part = p.chunk / kWaves, a = min(blockIdx.x * p.chunk + wave * part, v);
+    const uint64_t sum = collect((const T *)p.logits + i * p.ld, a, min(a + part, v), q, d, [&](uint64_t code) {
+        state.list[min(atomicAdd(&state.n, 1), kList - 1)] = code;
+    });
+    if ((threadIdx.x & 63) == 0) state.range[(int)blockIdx.x * kWaves + wave] = sum;
 }
 
 template <class T>
@@ -735,98 +874,35 @@ __global__ __launch_bounds__(kThreads) void k_sample_draw(SampleArgs p, RowState
     const int64_t i = blockIdx.x;
     RowState &state = states[i];
     const Request q = request_of(p, i, state);
-    auto answer = [&](int64_t token, double logprob) {
-        if (threadIdx.x == 0) {
-            p.tokens[i] = token;
-            if (p.logprobs) p.logprobs[i] = (float)logprob;
-        }
-    };
-    if (q.answer == Answer::invalid) return answer(-1, NAN);
-    if (q.answer == Answer::greedy) return answer((int64_t)(uint32_t)~(uint32_t)q.code, 0.0);
-    const T *row = (const T *)p.logits + i * p.ld;
-    Cut c;
-    c.plan = Plan::all;
-    if (q.filters) c = cut_of(q, state, s);
-    Drawn d;
-    if (c.plan == Plan::near || c.plan == Plan::far) {
-        const int n = min(state.n, kList);
-        for (int k = threadIdx.x; k < n; k += kThreads) s.list[k] = state.list[k];
-        __syncthreads();
-    }
-    if (c.plan == Plan::near) {
-        d = draw_from_list(min(state.n, kList), q.r, q.top_k, q.top_p, q.by_count ? 0 : c.x.weight, q.u, s);
-    } else if (c.plan == Plan::slow) {
-        if (threadIdx.x == 0) state.n = kSlow;
-        return;
-    } else {
-        uint64_t cut = 0;
-        const int ranges = p.chunks * kWaves;
-        const int64_t part = p.chunk / kWaves;
-        uint64_t *sum = s.weight;  // (the histogram has been read)
-        for (int k = threadIdx.x; k < ranges; k += kThreads) sum[k] = state.range[k];
-        if (c.plan == Plan::far) {
-            const int n = min(state.n, kList);
-            sort_codes(n, s);
-            cut = crossing_of_list(n, q.r, c.x.count_before, c.x.weight_before, s, [&](uint64_t count, uint64_t w) {
-                return q.by_count ? count >= (uint64_t)q.top_k : (double)w >= c.part;
-            });
-            for (int k = threadIdx.x; k < n; k += kThreads) {
-                const uint64_t code = s.list[k];
-                const double w = weight_of(q.r.level(of_key((uint32_t)(code >> 32))));
-                if (code >= cut && w >= q.r.min40)
-                    atomicAdd((unsigned long long *)&sum[(int64_t)(uint32_t)~(uint32_t)code / part], (unsigned long long)units(w));
-            }
-        }
-        __syncthreads();
-        uint64_t whole;
-        const uint64_t mine = (int)threadIdx.x < ranges ? sum[threadIdx.x] : 0, before = scan(mine, s, whole);
-        const uint64_t place = place_of(q.u, whole);
-        if (before <= place && place < before + mine) {
-            s.found[0] = threadIdx.x;
-            s.found[1] = place - before;
-        }
-        __syncthreads();
-        const int64_t a = (int64_t)s.found[0] * part;
-        const uint64_t left = s.found[1];
-        __syncthreads();
-        d = draw_from_range(row, a, min(a + part, p.v), q.r, cut, left, s);
-        d.total = whole;
-    }
-    answer(d.token, q.r.level(d.logit) * 0.6931471805599453 - log((double)d.total / kUnit));
+    if (answered(p, i, q)) return;
+    const Border d = border_of(q, state, s);
+    if (d.left) return answer(p, i, kLeft, 0.0);
+    const int n = min(state.n, kList), ranges = p.chunks * kWaves;
+    for (int k = threadIdx.x; k < n; k += kThreads) s.list[k] = state.list[k];
+    for (int k = threadIdx.x; k < ranges; k += kThreads) s.range[k] = state.range[k];
+    __syncthreads();
+    answer(p, i, q.r, draw((const T *)p.logits + i * p.ld, (uint32_t)p.v, q, d, n, ranges, p.chunk / kWaves, s));
 }
 
-// The rows that k_sample_draw leaves over (a kernel of its own, so that this one's registers are not its).
-template <class T>
-__global__ __launch_bounds__(kThreads) void k_sample_slow(SampleArgs p, RowState *states) {
-    __shared__ Shared s;
-    const int64_t i = blockIdx.x;
-    RowState &state = states[i];
-    if (state.n != kSlow) return;
-    const Request q = request_of(p, i, state);
-    const Drawn d = draw_slowly((const T *)p.logits + i * p.ld, p.v, q, s);
-    if (threadIdx.x == 0) {
-        p.tokens[i] = d.token;
-        if (p.logprobs) p.logprobs[i] = (float)(q.r.level(d.logit) * 0.6931471805599453 - log((double)d.total / kUnit));
-    }
-}
-
-// Rows of a run, whose states the workspace holds, and the blocks of a row: enough for two per compute unit.
-constexpr int64_t kRun = 1024;
-int64_t run_of(int64_t t) { return t < kRun ? t : kRun; }
-int chunks_of(int64_t rows, int64_t v) {
-    int64_t c = (2 * kPlanUnits + rows - 1) / rows;
+// ---- launches ------------------------------------------------------------------------------
+// Whether a row is spread over blocks.
+bool spreads(int64_t t, int64_t v) { return t < 96 && v > 65536; }
+int chunks_of(int64_t t, int64_t v) {
+    int64_t c = (kPlanUnits + t - 1) / t;
     const int64_t most = (v + 8191) / 8192;
     if (c > most) c = most;
     return (int)(c < 1 ? 1 : c > kMostChunks ? kMostChunks : c);
 }
-size_t sample_bytes(int64_t t) { return up256((size_t)run_of(t) * sizeof(RowState)); }
+size_t sample_bytes(int64_t t, int64_t v) { return spreads(t, v) ? up256((size_t)t * sizeof(RowState)) : 0; }
 
 template <class T>
 int sample(SampleArgs p, RowState *states, hipStream_t s) {
+    const dim3 block(kThreads);
+    constexpr int64_t RUN = 1 << 20;  // (a launch has fewer than 2^32 threads)
     const int64_t t = p.t;
-    for (int64_t t0 = 0; t0 < t; t0 += kRun) {
+    for (int64_t t0 = 0; t0 < t; t0 += RUN) {
         SampleArgs q = p;
-        q.t = t - t0 < kRun ? t - t0 : kRun;
+        q.t = t - t0 < RUN ? t - t0 : RUN;
         q.logits = (const T *)p.logits + t0 * p.ld;
         q.u += t0;
         if (q.temperatures) q.temperatures += t0;
@@ -835,20 +911,25 @@ int sample(SampleArgs p, RowState *states, hipStream_t s) {
         if (q.top_ks) q.top_ks += t0;
         q.tokens += t0;
         if (q.logprobs) q.logprobs += t0;
-        q.chunks = chunks_of(q.t, q.v);
-        q.chunk = ((q.v + q.chunks - 1) / q.chunks + 8191) / 8192 * 8192;
-        q.chunks = (int)((q.v + q.chunk - 1) / q.chunk);
-        const dim3 grid((unsigned)q.chunks, (unsigned)q.t), block(kThreads);
-        hipLaunchKernelGGL((k_sample_top<T>), grid, block, 0, s, q, states);
-        HIP_TRY(hipGetLastError());
-        hipLaunchKernelGGL((k_sample_count<T>), grid, block, 0, s, q, states);
-        HIP_TRY(hipGetLastError());
-        hipLaunchKernelGGL((k_sample_collect<T>), grid, block, 0, s, q, states);
-        HIP_TRY(hipGetLastError());
-        hipLaunchKernelGGL((k_sample_draw<T>), dim3((unsigned)q.t), block, 0, s, q, states);
-        HIP_TRY(hipGetLastError());
+        if (spreads(t, q.v)) {
+            q.chunks = chunks_of(q.t, q.v);
+            q.chunk = (uint32_t)(((q.v + q.chunks - 1) / q.chunks + 8191) / 8192 * 8192);
+            q.chunks = (int)((q.v + q.chunk - 1) / q.chunk);
+            const dim3 grid((unsigned)q.chunks, (unsigned)q.t);
+            hipLaunchKernelGGL((k_sample_top<T>), grid, block, 0, s, q, states);
+            HIP_TRY(hipGetLastError());
+            hipLaunchKernelGGL((k_sample_count<T>), grid, block, 0, s, q, states);
+            HIP_TRY(hipGetLastError());
+            hipLaunchKernelGGL((k_sample_collect<T>), grid, block, 0, s, q, states);
+            HIP_TRY(hipGetLastError());
+            hipLaunchKernelGGL((k_sample_draw<T>), dim3((unsigned)q.t), block, 0, s, q, states);
+            HIP_TRY(hipGetLastError());
+        } else {
+            hipLaunchKernelGGL((k_sample<T>), dim3((unsigned)q.t), block, 0, s, q);
+            HIP_TRY(hipGetLastError());
+        }
         if (q.v > kList) {  // (shorter rows fit the list whatever they hold)
-            hipLaunchKernelGGL((k_sample_slow<T>), dim3((unsigned)q.t), block, 0, s, q, states);
+            hipLaunchKernelGGL((k_sample_slow<T>), dim3((unsigned)q.t), block, 0, s, q);
             HIP_TRY(hipGetLastError());
         }
     }
@@ -881,7 +962,8 @@ int front_sample(SampleCall c, bool cached, void *workspace, size_t bytes) {
     if (a.tokens == nullptr && any) return -15;
     if (a.t >= ((int64_t)1 << 31) || a.v >= kMostChannels) return OZAKI2_ERR_UNSUPPORTED;
     if (!any) return OZAKI2_SUCCESS;
-    const size_t need = sample_bytes(a.t);
+    const size_t need = sample_bytes(a.t, a.v);
+    if (need == 0) return run_sample(&c, nullptr);
     if (cached) return with_workspace(need, c.s, run_sample, &c);
     if (workspace == nullptr || ((uintptr_t)workspace & (kWsAlign - 1)) != 0) return -17;
     if (bytes < need) return OZAKI2_ERR_WORKSPACE;
@@ -904,7 +986,7 @@ int ozaki2_sample(int64_t t, int64_t v, const void *logits, int64_t ldl, int typ
 
 size_t ozaki2_sample_workspace_size(int64_t t, int64_t v) {
     if (t <= 0 || v <= 0 || t >= ((int64_t)1 << 31) || v >= kMostChannels) return 0;
-    return sample_bytes(t);
+    return sample_bytes(t, v);
 }
 
 int ozaki2_sample_ws(int64_t t, int64_t v, const void *logits, int64_t ldl, int type, const double *u, double temperature,
