@@ -697,8 +697,9 @@ int ozaki2_xent_grad_ws(int64_t t, int64_t v, int64_t d, const void *X, int64_t 
  * Logits of -inf are never drawn. Beside one of +inf only those of +inf are. A row that holds NaN or nothing but -inf, or whose
  * settings or u are NaN or whose temperature is below 0, gives token -1 and logprob NaN.
  * w is computed in binary64 and held as w 2^40 rounded to an integer, so sums are exact and the token does not depend on how
- * a row is spread over threads; entries with w < 2^-41 count as 0. The workspace (ozaki2_sample_workspace_size bytes, about 68 KB a
- * row for at most 1024 rows at a time) is cached, or the caller's in the _ws form (256-byte aligned, capturable, ordered on one
+ * a row is spread over threads; entries with w < 2^-41 count as 0. Temperatures other than 0 count as within 1.5e-30 .. 1.4e30.
+ * A few long rows are spread over blocks, whose common state (ozaki2_sample_workspace_size bytes, about 42 KB a row, 0 where none
+ * is needed) is in the cached workspace, or the caller's in the _ws form (256-byte aligned, may be NULL if the size is 0, capturable, ordered on one
  * stream if shared). Returns 0, -1..-15 for an invalid argument, -17 for the workspace, or an OZAKI2_ERR_* code.
  */
 int ozaki2_sample(int64_t t, int64_t v, const void *logits, int64_t ldl, int type, const double *u, double temperature,

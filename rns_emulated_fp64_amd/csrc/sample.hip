@@ -38,10 +38,9 @@ constexpr int kBins = 4096;
 constexpr int kList = 2048;   // undecided entries that a row has room for
 constexpr int kPairs = 256;   // those that are compared each with each
 constexpr int kRanges = 1024; // ranges of indexes, at most
-// Weights below 2^-41 round to 0: entries that low are in no histogram. (The steps are found in
-// binary32, so a little is left below.)
-constexpr double kLowest = -41.0;
-constexpr float kLowestStep = -41.01f, kStepsPerOctave = 99.5f;  // 41.01 * 99.5 < kBins
+// A step is 1/99.5 of an octave of weights; those below 2^-41 round to 0, so entries beyond are in no histogram and not summed.
+// (The steps are found in binary32, so a little is left.)
+constexpr float kStepsPerOctave = 99.5f, kSteps = 4080.5f;  // 41.01 octaves
 constexpr double kUnit = 0x1p40;
 
 // ---- weights ------------------------------------------------------------------------
@@ -59,39 +58,43 @@ __device__ __forceinline__ uint32_t index_of(uint64_t code) { return ~(uint32_t)
 __device__ __forceinline__ float logit_of(uint64_t code) { return of_key((uint32_t)(code >> 32)); }
 
 struct Row {
-    double c;        // log2(e) / temperature
-    float top, c32;  // largest logit
-    bool infinite;   // it is +inf: entries that are have weight 1, others 0
-    double min40;    // min_p 2^40
-    __device__ __forceinline__ float mapped(float x) const { return infinite ? (x == INFINITY ? 0.f : -INFINITY) : x; }
+    double c;         // log2(e) / temperature
+    float top, unit;  // largest logit; steps per unit of logits, negative
+    double min40;     // min_p 2^40
     // log2 of the weight
-    __device__ __forceinline__ double level(float x) const { return ((double)mapped(x) - (double)top) * c; }
-    // The same in binary32, for the steps: both roundings keep the order of the logits.
-    __device__ __forceinline__ float near(float x) const { return (mapped(x) - top) * c32; }
+    __device__ __forceinline__ double level(float x) const { return ((double)x - (double)top) * c; }
+    // The same in steps below the largest, in binary32: both roundings keep the order of the logits. A step's entries
+    // are those whose step rounded down is its number.
+    __device__ __forceinline__ float step(float x) const { return (x - top) * unit; }
+    // The weight of an entry, 0 if it is not counted.
+    __device__ __forceinline__ double weight(float x) const;
 };
-__device__ __forceinline__ int bin_of(float t) { return (int)(t * -kStepsPerOctave); }
-// 2^40 2^t for t in [-41, 0]: 2^f for |f| <= 1/2 by its Taylor series (remainder below 2^-47), the rest in
-// the exponent. 0 below.
-__device__ __forceinline__ double weight_of(double t) {
-    const double n = rint(fmax(t, -64.0)), f = t - n;
-    double p = 4.44553827187081e-10;  // ln2^11 / 11!
-    p = fma(p, f, 7.054911620801121e-09);
-    p = fma(p, f, 1.0178086009239696e-07);
-    p = fma(p, f, 1.3215486790144305e-06);
-    p = fma(p, f, 1.5252733804059838e-05);
-    p = fma(p, f, 0.00015403530393381606);
-    p = fma(p, f, 0.0013333558146428441);
-    p = fma(p, f, 0.009618129107628477);
-    p = fma(p, f, 0.055504108664821576);
-    p = fma(p, f, 0.2402265069591007);
-    p = fma(p, f, 0.6931471805599453);
-    p = fma(p, f, 1.0);
-    const double w = p * __longlong_as_double((int64_t)(1023 + 40 + (int)n) << 52);
-    return t >= kLowest ? w : 0.0;
+// A constant in a scalar register, from which a multiply-add takes it as it is (in vector registers each would be copied first).
+__device__ __forceinline__ double scalar(double x) {
+    asm("" : "+s"(x));
+    return x;
 }
+// 2^40 2^t for t in [-100, 0]: 2^f for |f| <= 1/2 by the polynomial of degree 9 that is 1 at 0 and goes through it at nine
+// Chebyshev nodes (off by 2^-44.6), the rest in the exponent.
+__device__ __forceinline__ double weight_of(double t) {
+    const double magic = scalar(0x1.8p52), shifted = t + magic, f = t - (shifted - magic);
+    double p = fma(scalar(1.0203146133663105e-07), f, scalar(1.3255264681015647e-06));
+    p = fma(p, f, scalar(1.5252686752210201e-05));
+    p = fma(p, f, scalar(0.00015403455703126052));
+    p = fma(p, f, scalar(0.0013333558179141132));
+    p = fma(p, f, scalar(0.009618129159558177));
+    p = fma(p, f, scalar(0.05550410866476018));
+    p = fma(p, f, scalar(0.240226506958126));
+    p = fma(p, f, scalar(0.6931471805599453));
+    p = fma(p, f, 1.0);
+    // (the integer is in the low bits of the shifted value)
+    return __hiloint2double(__double2hiint(p) + ((__double2loint(shifted) + 40) << 20), __double2loint(p));
+}
+__device__ __forceinline__ double Row::weight(float x) const { return step(x) < kSteps ? weight_of(level(x)) : 0.0; }
 // Rounded to an integer: the significand of the sum with 2^52.
 __device__ __forceinline__ uint64_t units(double w) {
-    return (uint64_t)__double_as_longlong(w + 0x1p52) - (uint64_t)__double_as_longlong(0x1p52);
+    const uint64_t b = (uint64_t)__double_as_longlong(w + 0x1p52);
+    return (uint64_t)((uint32_t)(b >> 32) - 0x43300000u) << 32 | (uint32_t)b;
 }
 
 // ---- a block's shared memory and its collective steps ----------------------------------
@@ -102,35 +105,54 @@ struct Shared {
     uint64_t few[kPairs];
     uint64_t range[kRanges];
     uint64_t part[kWaves];
-    uint64_t found[4];
-    int n;  // of the list
+    uint64_t found[12];
+    uint64_t rest;  // the weight of what is not decided
+    int n;          // of the list
 };
 
-__device__ __forceinline__ uint64_t shfl_up64(uint64_t x, int o) { return (uint64_t)__shfl_up((unsigned long long)x, o, 64); }
 __device__ __forceinline__ uint64_t shfl_xor64(uint64_t x, int o) { return (uint64_t)__shfl_xor((unsigned long long)x, o, 64); }
-__device__ __forceinline__ uint64_t shfl64(uint64_t x, int lane) { return (uint64_t)__shfl((unsigned long long)x, lane, 64); }
 __device__ __forceinline__ void add64(uint64_t *to, uint64_t x) { atomicAdd((unsigned long long *)to, (unsigned long long)x); }
+
+// x of the lane that a DPP control names, `none` where there is none. 0x110 + i: i lanes down in a row of 16;
+// 0x142, 0x143: the last lane of the row before, of the half before.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t from_lane(uint64_t x, uint64_t none) {
+    const int lo = __builtin_amdgcn_update_dpp((int)(uint32_t)none, (int)(uint32_t)x, CTRL, ROWS, 0xf, false);
+    const int hi = __builtin_amdgcn_update_dpp((int)(uint32_t)(none >> 32), (int)(uint32_t)(x >> 32), CTRL, ROWS, 0xf, false);
+    return (uint64_t)(uint32_t)hi << 32 | (uint32_t)lo;
+}
+__device__ __forceinline__ uint64_t read_lane(uint64_t x, int lane) {
+    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(x >> 32), lane) << 32 |
+           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, lane);
+}
+// of(x) over the lanes up to and with this one: of its row of 16, then of the wavefront. `none` changes nothing.
+template <class Of>
+__device__ __forceinline__ uint64_t scan_row(uint64_t x, uint64_t none, Of of) {
+    x = of(x, from_lane<0x111, 0xf>(x, none));
+    x = of(x, from_lane<0x112, 0xf>(x, none));
+    x = of(x, from_lane<0x114, 0xf>(x, none));
+    return of(x, from_lane<0x118, 0xf>(x, none));
+}
+template <class Of>
+__device__ __forceinline__ uint64_t scan_wave(uint64_t x, uint64_t none, Of of) {
+    x = scan_row(x, none, of);
+    x = of(x, from_lane<0x142, 0xa>(x, none));
+    return of(x, from_lane<0x143, 0xc>(x, none));
+}
+__device__ __forceinline__ uint64_t plus(uint64_t a, uint64_t b) { return a + b; }
+// The sum over a wavefront.
+__device__ __forceinline__ uint64_t wave_sum(uint64_t x) { return read_lane(scan_wave(x, 0, plus), 63); }
 
 // The sum of x over the threads before this one; total: over all. Ends behind a barrier, so s.part is free again.
 __device__ __forceinline__ uint64_t scan(uint64_t x, Shared &s, uint64_t &total) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    uint64_t in = x;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const uint64_t y = shfl_up64(in, o);
-        if (lane >= o) in += y;
-    }
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint64_t in = scan_wave(x, 0, plus);
     if (lane == 63) s.part[wave] = in;
     __syncthreads();
-    uint64_t parts = s.part[lane & (kWaves - 1)];
-    const uint64_t own = parts;
-#pragma unroll
-    for (int o = 1; o < kWaves; o <<= 1) {
-        const uint64_t y = shfl_up64(parts, o);
-        if ((lane & (kWaves - 1)) >= o) parts += y;
-    }
-    total = shfl64(parts, kWaves - 1);
-    const uint64_t before = shfl64(parts - own, wave);
+    static_assert(kWaves == 16, "a row of lanes");
+    const uint64_t parts = scan_row(s.part[lane & 15], 0, plus);
+    total = read_lane(parts, 15);
+    const uint64_t before = wave > 0 ? read_lane(parts, wave - 1) : 0;
     __syncthreads();
     return before + in - x;
 }
@@ -138,13 +160,11 @@ __device__ __forceinline__ uint64_t scan(uint64_t x, Shared &s, uint64_t &total)
 template <bool MAX>
 __device__ __forceinline__ uint64_t extreme(uint64_t x, Shared &s) {
     auto of = [](uint64_t a, uint64_t b) { return MAX ? (a > b ? a : b) : (a < b ? a : b); };
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) x = of(x, shfl_xor64(x, o));
-    if ((threadIdx.x & 63) == 0) s.part[threadIdx.x >> 6] = x;
+    const uint64_t none = MAX ? 0 : ~(uint64_t)0;
+    x = scan_wave(x, none, of);
+    if ((threadIdx.x & 63) == 63) s.part[threadIdx.x >> 6] = x;
     __syncthreads();
-    x = s.part[threadIdx.x & (kWaves - 1)];
-#pragma unroll
-    for (int o = kWaves / 2; o >= 1; o >>= 1) x = of(x, shfl_xor64(x, o));
+    x = read_lane(scan_row(s.part[threadIdx.x & 15], none, of), 15);
     __syncthreads();
     return x;
 }
@@ -259,7 +279,7 @@ __device__ __forceinline__ Crossing crossing(Shared &s, bool weights, Reaches re
     for (int i = 0; i < PER; ++i) {
         const int b = PER * (int)threadIdx.x + i;
         const uint64_t c = count_of(b), w = weight_at(b);
-        if (c != 0 && !done(cb, wb) && done(cb + c, wb + w)) {
+        if (!done(cb, wb) && done(cb + c, wb + w)) {
             s.found[0] = (uint64_t)(DOWN ? kBins - 1 - b : b);
             s.found[1] = cb;
             s.found[2] = wb;
@@ -289,7 +309,7 @@ __device__ __forceinline__ Place place_in(const uint64_t *list, int n, const Row
     const int e = threadIdx.x >> 2;
     p.real = e < n;
     p.code = p.real ? list[e] : 0;
-    p.w = p.real ? weight_of(r.level(logit_of(p.code))) : 0.0;
+    p.w = p.real ? r.weight(logit_of(p.code)) : 0.0;
     p.weight = units(p.w);
     if (p.real && (threadIdx.x & 3) == 0) s.weight[e] = p.weight;
     __syncthreads();
@@ -383,21 +403,21 @@ struct Request {
     Row r;
     uint64_t code;   // of the largest entry
     Answer answer;
+    bool infinite;   // the largest is +inf: entries that are have weight 1, others 0 (k_sample_slow sees to it)
     __device__ __forceinline__ bool filters() const { return top_k > 0 || top_p < 1.0; }
     __device__ __forceinline__ double share(uint64_t whole) const { return fmax(top_p * (double)whole, 0.5); }
 };
 
-// From a list of up to kPairs entries that holds all that may be kept; `whole`: the sum that top_p is a part of
-// where top_k is off.
-__device__ __forceinline__ Drawn draw_from_few(int n, const Request &q, uint64_t whole, Shared &s) {
+// From a list of up to kPairs entries that holds all that top_k may keep.
+__device__ __forceinline__ Drawn draw_from_few(int n, const Request &q, Shared &s) {
     const Place p = place_in(s.list, n, q.r, s);
     const bool first = (threadIdx.x & 3) == 0;
-    bool kept = p.real;
-    if (q.top_k > 0) {
-        kept = kept && p.count_before < (uint64_t)q.top_k;
-        if (q.top_p < 1.0) scan(kept && first ? p.weight : 0, s, whole);
+    bool kept = p.real && p.count_before < (uint64_t)q.top_k;
+    if (q.top_p < 1.0) {
+        uint64_t whole;
+        scan(kept && first ? p.weight : 0, s, whole);
+        kept = kept && (double)p.weight_before < q.share(whole);
     }
-    if (q.top_p < 1.0) kept = kept && (double)p.weight_before < q.share(whole);
     kept = kept && p.w >= q.r.min40;
     uint64_t total;
     scan(kept && first ? p.weight : 0, s, total);
@@ -417,23 +437,23 @@ __device__ __forceinline__ Drawn draw_from_few(int n, const Request &q, uint64_t
 }
 
 // The same for a longer list: sorted, cut, and sorted by index.
-__device__ Drawn draw_from_list(int n, const Request &q, uint64_t whole, Shared &s) {
+__device__ __forceinline__ Drawn draw_from_list(int n, const Request &q, Shared &s) {
     constexpr int PER = kList / kThreads;
     for (int i = n + threadIdx.x; i < power_of_two(n); i += kThreads) s.list[i] = 0;
     sort_list<true>(power_of_two(n), s);
-    if (q.top_k > 0 && q.top_k < n) n = (int)q.top_k;
+    if (q.top_k < n) n = (int)q.top_k;
     double w[PER];
     uint64_t sum = 0, total;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int at = PER * (int)threadIdx.x + i;
-        w[i] = at < n ? weight_of(q.r.level(logit_of(s.list[at]))) : 0.0;
+        w[i] = at < n ? q.r.weight(logit_of(s.list[at])) : 0.0;
         sum += units(w[i]);
     }
     uint64_t before = scan(sum, s, total);
     if (threadIdx.x == 0) s.n = n;
     __syncthreads();
-    const double part = q.top_p < 1.0 ? q.share(q.top_k > 0 ? total : whole) : INFINITY;
+    const double part = q.top_p < 1.0 ? q.share(total) : INFINITY;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int at = PER * (int)threadIdx.x + i;
@@ -458,7 +478,7 @@ __device__ Drawn draw_from_list(int n, const Request &q, uint64_t whole, Shared 
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int at = PER * (int)threadIdx.x + i;
-        k[i] = at < n ? units(weight_of(q.r.level(of_key((uint32_t)s.list[at])))) : 0;
+        k[i] = at < n ? units(q.r.weight(of_key((uint32_t)s.list[at]))) : 0;
         sum += k[i];
     }
     before = scan(sum, s, total);
@@ -476,21 +496,20 @@ __device__ Drawn draw_from_list(int n, const Request &q, uint64_t whole, Shared 
 // The code of the entry in the range [a, b) of indexes where `place` falls in the sum of its kept weights: sums over
 // sixteenths of the range, one per wavefront, then the sixteenth that holds it, down to one that the block
 // takes in one step.
-template <class T>
+template <class T, class Map>
 __device__ __forceinline__ uint64_t draw_from_range(const T *row, uint32_t a, uint32_t b, const Row &r, uint64_t cut,
-                                                    uint64_t place, Shared &s) {
+                                                    uint64_t place, Shared &s, Map map) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     auto kept = [&](float x, uint32_t j) -> uint64_t {
-        const double w = weight_of(r.level(x));
+        const double w = r.weight(x);
         return w >= r.min40 && code_of(x, j) >= cut ? units(w) : 0;
     };
     while (b - a > 8 * kThreads) {
         const uint32_t part = ((b - a + kWaves - 1) / kWaves + 511) / 512 * 512;
         const uint32_t from = min(a + wave * part, b);
         uint64_t sum = 0;
-        sweep<1>(row, from, min(from + part, b), lane, 64, [&](float x, uint32_t j) { sum += kept(x, j); });
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) sum += shfl_xor64(sum, o);
+        sweep<1>(row, from, min(from + part, b), lane, 64, [&](float x, uint32_t j) { sum += kept(map(x), j); });
+        sum = wave_sum(sum);
         if (lane == 0) s.part[wave] = sum;
         __syncthreads();
         uint64_t before = 0;
@@ -507,7 +526,7 @@ __device__ __forceinline__ uint64_t draw_from_range(const T *row, uint32_t a, ui
     struct { T e[8]; } e = __builtin_bit_cast(decltype(e), load_eight(row, j0, b));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        x[i] = (float)e.e[i];
+        x[i] = map((float)e.e[i]);
         k[i] = kept(x[i], j0 + i);
         sum += k[i];
         __builtin_amdgcn_sched_barrier(0);
@@ -554,13 +573,21 @@ __device__ __forceinline__ uint64_t top_of(const T *row, uint32_t a, uint32_t b,
     return extreme<true>(nan ? ~(uint64_t)0 : code_of(best, at), s);
 }
 
-__device__ __forceinline__ Request request_of(const SampleArgs &p, int64_t i, uint64_t code) {
+// A row's settings (read before its logits, so that they are there in time).
+struct Settings {
+    double temperature, top_p, min_p, u;
+    int64_t top_k;
+};
+__device__ __forceinline__ Settings settings_of(const SampleArgs &p, int64_t i) {
+    return {p.temperatures ? (double)p.temperatures[i] : p.temperature, p.top_ps ? (double)p.top_ps[i] : p.top_p,
+            p.min_ps ? (double)p.min_ps[i] : p.min_p, p.u[i], p.top_ks ? (int64_t)p.top_ks[i] : p.top_k};
+}
+__device__ __forceinline__ Request request_of(const SampleArgs &p, const Settings &z, uint64_t code) {
     Request q;
-    const double temperature = p.temperatures ? (double)p.temperatures[i] : p.temperature;
-    const double min_p = p.min_ps ? (double)p.min_ps[i] : p.min_p;
-    q.top_p = p.top_ps ? (double)p.top_ps[i] : p.top_p;
-    q.top_k = p.top_ks ? (int64_t)p.top_ks[i] : p.top_k;
-    q.u = p.u[i];
+    const double temperature = z.temperature, min_p = z.min_p;
+    q.top_p = z.top_p;
+    q.top_k = z.top_k;
+    q.u = z.u;
     q.code = code;
     const float top = logit_of(code);
     // NaN fails the comparisons
@@ -572,113 +599,197 @@ __device__ __forceinline__ Request request_of(const SampleArgs &p, int64_t i, ui
         q.top_p = 1.0;
     }
     if (q.top_k <= 0 || q.top_k >= p.v) q.top_k = 0;
-    q.r.infinite = top == INFINITY;
-    q.r.top = q.r.infinite ? 0.f : top;
+    q.infinite = top == INFINITY;
+    q.r.top = q.infinite ? 0.f : top;
     // (so that it is a finite binary32 number, and can be a factor of 0 and of infinities)
     q.r.c = fmin(fmax(1.4426950408889634 / temperature, 1e-30), 1e30);
-    q.r.c32 = (float)q.r.c;
-    q.r.min40 = fmin(min_p, 1.0) * kUnit;
+    q.r.unit = (float)q.r.c * -kStepsPerOctave;
+    q.r.min40 = fmin(fmax(min_p, 0.0), 1.0) * kUnit;
     return q;
 }
 
-// Counts the entries in [a, b) into the block's histogram; with their weights where top_p cuts first.
+// Adds the entries in [a, b) to the block's histogram.
 template <class T>
 __device__ __forceinline__ void count_steps(const T *row, uint32_t a, uint32_t b, const Request &q, Shared &s) {
-    if (q.top_k > 0)
-        sweep<2>(row, a, b, threadIdx.x, kThreads, [&](float x, uint32_t) {
-            const float t = q.r.near(x);
-            if (t >= kLowestStep) atomicAdd(&s.count[bin_of(t)], 1u);
-        });
-    else
-        sweep<1>(row, a, b, threadIdx.x, kThreads, [&](float x, uint32_t) {
-            const float t = q.r.near(x);
-            if (t >= kLowestStep) {
-                atomicAdd(&s.count[bin_of(t)], 1u);
-                add64(&s.weight[bin_of(t)], units(weight_of(q.r.level(x))));
-            }
-        });
+    sweep<2>(row, a, b, threadIdx.x, kThreads, [&](float x, uint32_t) {
+        const float t = q.r.step(x);
+        if (t < kSteps) atomicAdd(&s.count[(int)t], 1u);
+    });
     __syncthreads();
 }
 
-// What the histogram decides: entries in steps before `first` are kept by the filters, those after `last` are
-// not, and those between are to be collected.
+// What the histogram decides: entries in steps before `first` are kept, those after `last` are not, and
+// those between are to be collected.
 struct Border {
     int first, last;
-    bool left;               // too many of them
-    bool near;               // first is 0: the list holds all that may be kept
-    uint64_t count_before, weight_before, whole;
+    bool left;              // too many of them
+    bool near;              // first is 0: the list holds all that may be kept
+    bool cuts;              // top_k or top_p cuts among them
+    bool open;              // ... or keeps them all
+    uint64_t count_before;  // entries before `first`
 };
+// For top_p alone: the histogram's counts, each times its step's middle weight, give a share of the whole up to a step that is off
+// by a step's width at most, 0.7%, since every weight is; and where there are many entries by far less. So the steps are
+// collected over which this estimate goes from top_p less 0.75% of it to as much above, or, if these hold too many
+// entries, a fifth of that, or a 25th; the exact sums that follow show whether the cut is among them (where it is not,
+// k_sample_slow has the row). That takes one exponential per entry, in `collect`, and none here.
+__device__ __forceinline__ void window_of(const Request &q, Border &d, Shared &s) {
+    constexpr int PER = kBins / kThreads;
+    const int b0 = PER * (int)threadIdx.x;
+    uint64_t c[PER], w[PER], cs = 0, ws = 0, entries, whole;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+        c[i] = s.count[b0 + i];
+        w[i] = (uint64_t)((float)c[i] * __builtin_amdgcn_exp2f(40.f - ((float)(b0 + i) + 0.5f) / kStepsPerOctave));
+        cs += c[i];
+        ws += w[i];
+    }
+    if (threadIdx.x < 6) {
+        s.found[2 * threadIdx.x] = threadIdx.x & 1 ? kBins - 1 : 0;
+        s.found[2 * threadIdx.x + 1] = ~(uint64_t)0;
+    }
+    uint64_t cb = scan(cs, s, entries), wb = scan(ws, s, whole);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+#pragma unroll
+        for (int k = 0; k < 6; ++k) {
+            // first and last step of the widest window, of the next one, of the narrowest
+            const double at = q.top_p * (double)whole * (1.0 + (k & 1 ? 1.0 : -1.0) * (k < 2 ? 0.0075 : k < 4 ? 0.0015 : 0.0003));
+            if ((double)wb < at && (double)(wb + w[i]) >= at) {
+                s.found[2 * k] = (uint64_t)(b0 + i);
+                s.found[2 * k + 1] = k & 1 ? cb + c[i] : cb;
+            }
+        }
+        cb += c[i];
+        wb += w[i];
+    }
+    __syncthreads();
+    d.left = true;
+#pragma unroll
+    for (int k = 0; k < 6; k += 2) {
+        const uint64_t before = s.found[2 * k + 1] == ~(uint64_t)0 ? 0 : s.found[2 * k + 1];
+        const bool open = s.found[2 * k + 3] == ~(uint64_t)0;
+        const uint64_t in = (open ? entries : s.found[2 * k + 3]) - before;
+        if (d.left && in <= (uint64_t)kList) {
+            d.left = false;
+            d.first = (int)s.found[2 * k];
+            d.last = (int)s.found[2 * k + 2];
+            d.open = open;
+        }
+    }
+    d.cuts = true;
+    __syncthreads();
+}
 __device__ __forceinline__ Border border_of(const Request &q, Shared &s) {
-    Border d = {kBins, -1, false, false, 0, 0, 0};
-    if (!q.filters()) return d;
-    const bool by_count = q.top_k > 0;
-    const Crossing x = crossing<false>(s, !by_count, [&](uint64_t count, uint64_t w, const Crossing &all) {
-        return by_count ? count >= (uint64_t)q.top_k : (double)w >= q.share(all.weight);
-    });
-    d.whole = x.weight;
-    const uint64_t members = x.bin < 0 ? 0 : s.count[x.bin];
-    const uint64_t down_to = x.bin < 0 ? x.count : x.count_before + members;
-    const bool both = by_count && q.top_p < 1.0;
-    if (down_to <= (uint64_t)(both ? kList : kPairs)) {
-        d.first = 0;
-        d.last = x.bin < 0 ? kBins - 1 : x.bin;
-        d.near = true;
-    } else if (both || members > (uint64_t)kList) {
-        d.left = true;
-    } else if (x.bin >= 0) {  // (else top_k is more than there are entries of any weight)
-        d.first = d.last = x.bin;
-        d.count_before = x.count_before;
-        d.weight_before = x.weight_before;
+    Border d = {kBins, kBins - 1, false, false, false, false, 0};
+    if (q.top_k > 0) {
+        const Crossing x = crossing<false>(s, false, [&](uint64_t count, uint64_t, const Crossing &) {
+            return count >= (uint64_t)q.top_k;
+        });
+        const uint64_t down_to = x.bin < 0 ? x.count : x.count_before + s.count[x.bin];
+        if (down_to <= (uint64_t)(q.top_p < 1.0 ? kList : kPairs)) {
+            d.first = 0;
+            d.last = x.bin < 0 ? kBins - 1 : x.bin;
+            d.near = true;
+        } else if (q.top_p < 1.0) {
+            d.left = true;
+        } else if (x.bin >= 0) {  // (else top_k is more than there are entries of any weight)
+            d.first = d.last = x.bin;
+            d.count_before = x.count_before;
+            d.cuts = true;
+        }
+    } else if (q.top_p < 1.0) {
+        window_of(q, d, s);
+    }
+    if (q.r.min40 > 0.0 && !d.near) {
+        // min_p's own step, and one on either side for binary32's roundings
+        const float t = fminf(__builtin_amdgcn_logf((float)(q.r.min40 / kUnit)) * -kStepsPerOctave, kSteps);
+        const int lower = max((int)t - 1, 0), upper = min((int)t + 1, kBins - 1);
+        if (upper < d.first) {  // above the other filters' cut
+            d.first = lower;
+            d.last = upper;
+            d.cuts = false;
+        } else {
+            if (lower < d.first) {
+                for (int b = lower; b < d.first; ++b) d.count_before -= d.cuts && q.top_k > 0 ? s.count[b] : 0;
+                d.first = lower;
+            }
+            if (upper < d.last) {
+                d.last = upper;
+                d.open = true;  // what lies behind is not kept anyhow
+            }
+        }
     }
     __syncthreads();
     return d;
 }
 
-// This wavefront's range [a, b): its undecided entries to take(code), and the sum over those that are decided.
+// This wavefront's range [a, b): its undecided entries to take(code), the sum over those that are kept, and, where top_p needs
+// it, the sum over the others.
 template <class T, class Take>
-__device__ __forceinline__ uint64_t collect(const T *row, uint32_t a, uint32_t b, const Request &q, const Border &d, Take take) {
+__device__ __forceinline__ uint64_t collect(const T *row, uint32_t a, uint32_t b, const Request &q, const Border &d,
+                                            uint64_t &rest, Take take) {
     const int lane = threadIdx.x & 63;
     uint64_t sum = 0;
-    if (d.near)
+    rest = 0;
+    const float first = (float)d.first, last = fminf((float)(d.last + 1), kSteps);
+    if (d.near) {
         sweep<2>(row, a, b, lane, 64, [&](float x, uint32_t j) {
-            const float t = q.r.near(x);
-            if (t >= kLowestStep && bin_of(t) <= d.last) take(code_of(x, j));
+            if (q.r.step(x) < last) take(code_of(x, j));
         });
-    else
-        sweep<1>(row, a, b, lane, 64, [&](float x, uint32_t j) {
-            const float t = q.r.near(x);
-            const int bin = t >= kLowestStep ? bin_of(t) : kBins;
-            if (bin < d.first) {
-                const double w = weight_of(q.r.level(x));
-                sum += w >= q.r.min40 ? units(w) : 0;
-            }
-            if (bin <= d.last && bin >= d.first) take(code_of(x, j));
-        });
-#pragma unroll
-    for (int o = 32; o >= 1; o >>= 1) sum += shfl_xor64(sum, o);
+        return 0;
+    }
+    const bool whole = q.top_k == 0 && q.top_p < 1.0 && d.cuts;
+    uint64_t all = 0;
+    const float most = whole ? kSteps : fminf(first, kSteps);
+    sweep<1>(row, a, b, lane, 64, [&](float x, uint32_t j) {
+        const float step = q.r.step(x);
+        if (step < most) {
+            const uint64_t w = units(weight_of(q.r.level(x)));
+            all += w;
+            sum += step < first ? w : 0;
+        }
+        if (step >= first && step < last) take(code_of(x, j));
+    });
+    sum = wave_sum(sum);
+    rest = wave_sum(all) - sum;
     return sum;
 }
 
-// From the list (n entries in s.list) and the sums of `ranges` ranges of `part` indexes (s.range).
+// From the list (n entries in s.list), the sums of `ranges` ranges of `part` indexes (s.range) and that of the rest (s.rest).
+// False if the cut is not where the window was.
 template <class T>
-__device__ __forceinline__ Drawn draw(const T *row, uint32_t v, const Request &q, const Border &d, int n, int ranges,
-                                      uint32_t part, Shared &s) {
-    if (d.near) return n <= kPairs ? draw_from_few(n, q, d.whole, s) : draw_from_list(n, q, d.whole, s);
+__device__ __forceinline__ bool draw(const T *row, uint32_t v, const Request &q, const Border &d, int n, int ranges,
+                                     uint32_t part, Shared &s, Drawn &out) {
+    if (d.near) {
+        out = n <= kPairs ? draw_from_few(n, q, s) : draw_from_list(n, q, s);
+        return true;
+    }
     uint64_t cut = 0;
-    if (n > 0) {
-        const double share = q.share(d.whole);
-        cut = refine([&](auto f) { sweep_list(n, s, f); }, [](float) { return true; }, q.top_k == 0, 0, d.count_before,
-                     d.weight_before, (uint64_t)n, q.r, s, [&](uint64_t count, uint64_t w) {
-                         return q.top_k > 0 ? count >= (uint64_t)q.top_k : (double)w >= share;
-                     });
+    if (d.cuts || n > 0) {
+        uint64_t in_list = 0, decided;
+        for (int k = threadIdx.x; k < n; k += kThreads) in_list += units(q.r.weight(logit_of(s.list[k])));
+        scan((int)threadIdx.x < ranges ? s.range[threadIdx.x] : 0, s, decided);
+        scan(in_list, s, in_list);
+        const double share = q.share(decided + s.rest);
+        auto reaches = [&](uint64_t count, uint64_t w) {
+            return q.top_k > 0 ? count >= (uint64_t)q.top_k : (double)w >= share;
+        };
+        if (d.cuts) {
+            if (reaches(d.count_before, decided)) return false;
+            if (reaches(d.count_before + (uint64_t)n, decided + in_list))
+                cut = refine([&](auto f) { sweep_list(n, s, f); }, [](float) { return true; }, q.top_k == 0, 0, d.count_before,
+                             decided, (uint64_t)n, q.r, s, reaches);
+            else if (!d.open)
+                return false;
+        }
         for (int k = threadIdx.x; k < n; k += kThreads) {
             const uint64_t code = s.list[k];
-            const double w = weight_of(q.r.level(logit_of(code)));
+            const double w = q.r.weight(logit_of(code));
             if (code >= cut && w >= q.r.min40) add64(&s.range[index_of(code) / part], units(w));
         }
         __syncthreads();
     }
-    Drawn out;
     const uint64_t mine = (int)threadIdx.x < ranges ? s.range[threadIdx.x] : 0, before = scan(mine, s, out.total);
     const uint64_t place = place_of(q.u, out.total);
     if (before <= place && place < before + mine) {
@@ -689,9 +800,9 @@ __device__ __forceinline__ Drawn draw(const T *row, uint32_t v, const Request &q
     const uint32_t a = (uint32_t)s.found[0] * part;
     const uint64_t left = s.found[1];
     __syncthreads();
-    // (an entry below the cut's step, which the ranges do not count, is below the cut)
-    out.code = draw_from_range(row, a, min(a + part, v), q.r, cut, left, s);
-    return out;
+    // (an entry behind the window is below the cut, or below min_p)
+    out.code = draw_from_range(row, a, min(a + part, v), q.r, cut, left, s, [](float x) { return x; });
+    return true;
 }
 
 __device__ __forceinline__ void answer(const SampleArgs &p, int64_t i, int64_t token, double logprob) {
@@ -717,26 +828,40 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs p) {
     const int64_t i = blockIdx.x;
     const T *row = (const T *)p.logits + i * p.ld;
     const uint32_t v = (uint32_t)p.v;
-    const Request q = request_of(p, i, top_of(row, 0, v, s));
+    const Settings settings = settings_of(p, i);
+    const Request q = request_of(p, settings, top_of(row, 0, v, s));
     if (answered(p, i, q)) return;
+    if (q.infinite) return answer(p, i, kLeft, 0.0);
     if (q.filters()) {
-        clear_histogram(s);
+        for (int k = threadIdx.x; k < kBins; k += kThreads) s.count[k] = 0;
+        __syncthreads();
         count_steps(row, 0, v, q, s);
     }
     const Border d = border_of(q, s);
     if (d.left) return answer(p, i, kLeft, 0.0);
-    if (threadIdx.x == 0) s.n = 0;
+    if (threadIdx.x == 0) {
+        s.n = 0;
+        s.rest = 0;
+    }
     __syncthreads();
     const int wave = threadIdx.x >> 6;
     const uint32_t part = ((v + kWaves - 1) / kWaves + 511) / 512 * 512, a = min(wave * part, v);
-    const uint64_t sum = collect(row, a, min(a + part, v), q, d, [&](uint64_t code) {
+    uint64_t rest;
+    const uint64_t sum = collect(row, a, min(a + part, v), q, d, rest, [&](uint64_t code) {
         s.list[min(atomicAdd(&s.n, 1), kList - 1)] = code;
     });
-    if ((threadIdx.x & 63) == 0) s.range[wave] = sum;
+    if ((threadIdx.x & 63) == 0) {
+        s.range[wave] = sum;
+        if (rest != 0) add64(&s.rest, rest);
+    }
     __syncthreads();
-    const int n = min(s.n, kList);
+    const int n = s.n;
     __syncthreads();
-    answer(p, i, q.r, draw(row, v, q, d, n, kWaves, part, s));
+    Drawn out;
+    if (n <= kList && draw(row, v, q, d, n, kWaves, part, s, out))
+        answer(p, i, q.r, out);
+    else
+        answer(p, i, kLeft, 0.0);
 }
 
 // The rows that are left over: top_k's cut, then top_p's among what that leaves, each from a histogram and what
@@ -748,19 +873,21 @@ __global__ __launch_bounds__(kThreads) void k_sample_slow(SampleArgs p) {
     if (p.tokens[i] != kLeft) return;
     const T *row = (const T *)p.logits + i * p.ld;
     const uint32_t v = (uint32_t)p.v;
-    const Request q = request_of(p, i, top_of(row, 0, v, s));
+    const Settings settings = settings_of(p, i);
+    const Request q = request_of(p, settings, top_of(row, 0, v, s));
     const Row &r = q.r;
     uint64_t cut = 0;
-    auto each = [&](auto f) { sweep<1>(row, 0, v, threadIdx.x, kThreads, f); };
+    auto map = [&](float x) { return q.infinite ? (x == INFINITY ? 0.f : -INFINITY) : x; };
+    auto each = [&](auto f) { sweep<1>(row, 0, v, threadIdx.x, kThreads, [&](float x, uint32_t j) { f(map(x), j); }); };
     for (int filter = 0; filter < 2; ++filter) {
         const bool weights = filter == 1;
         if (weights ? q.top_p >= 1.0 : q.top_k == 0) continue;
         clear_histogram(s);
         each([&](float x, uint32_t j) {
-            const float t = r.near(x);
-            if (t >= kLowestStep && code_of(x, j) >= cut) {
-                atomicAdd(&s.count[bin_of(t)], 1u);
-                if (weights) add64(&s.weight[bin_of(t)], units(weight_of(r.level(x))));
+            const float t = r.step(x);
+            if (t < kSteps && code_of(x, j) >= cut) {
+                atomicAdd(&s.count[(int)t], 1u);
+                if (weights) add64(&s.weight[(int)t], units(weight_of(r.level(x))));
             }
         });
         __syncthreads();
@@ -773,8 +900,8 @@ __global__ __launch_bounds__(kThreads) void k_sample_slow(SampleArgs p) {
         const uint64_t members = s.count[x.bin];
         __syncthreads();
         cut = refine(each, [&](float y) {
-            const float t = r.near(y);
-            return t >= kLowestStep && bin_of(t) == x.bin;
+            const float t = r.step(y);
+            return t < kSteps && (int)t == x.bin;
         }, weights, cut, x.count_before, x.weight_before, members, r, s, [&](uint64_t c, uint64_t w) {
             return weights ? (double)w >= share : c >= (uint64_t)q.top_k;
         });
@@ -782,11 +909,11 @@ __global__ __launch_bounds__(kThreads) void k_sample_slow(SampleArgs p) {
     uint64_t sum = 0;
     Drawn d;
     each([&](float x, uint32_t j) {
-        const double w = weight_of(r.level(x));
+        const double w = r.weight(x);
         if (w >= r.min40 && code_of(x, j) >= cut) sum += units(w);
     });
     scan(sum, s, d.total);
-    d.code = draw_from_range(row, 0, v, r, cut, place_of(q.u, d.total), s);
+    d.code = draw_from_range(row, 0, v, r, cut, place_of(q.u, d.total), s, map);
     answer(p, i, r, d);
 }
 
@@ -794,17 +921,18 @@ __global__ __launch_bounds__(kThreads) void k_sample_slow(SampleArgs p) {
 // A row's part of the workspace. A range is a sixteenth of a chunk.
 constexpr int kMostChunks = kRanges / kWaves;
 struct RowState {
-    uint64_t weight[kBins];
     uint32_t count[kBins];
     uint64_t list[kList];
     uint64_t range[kRanges];
     uint64_t top[kMostChunks];
+    uint64_t rest;
     int n;
 };
 __device__ __forceinline__ Request request_of(const SampleArgs &p, int64_t i, const RowState &state) {
+    const Settings settings = settings_of(p, i);
     uint64_t code = 0;
     for (int c = 0; c < p.chunks; ++c) code = max(code, state.top[c]);
-    return request_of(p, i, code);
+    return request_of(p, settings, code);
 }
 
 template <class T>
@@ -816,11 +944,11 @@ __global__ __launch_bounds__(kThreads) void k_sample_top(SampleArgs p, RowState 
     const uint64_t code = top_of((const T *)p.logits + i * p.ld, a, min(a + p.chunk, (uint32_t)p.v), s);
     if (threadIdx.x == 0) state.top[blockIdx.x] = code;
     // what the next launches add to
-    for (int k = (int)blockIdx.x * kThreads + threadIdx.x; k < kBins; k += p.chunks * kThreads) {
-        state.weight[k] = 0;
-        state.count[k] = 0;
+    for (int k = (int)blockIdx.x * kThreads + threadIdx.x; k < kBins; k += p.chunks * kThreads) state.count[k] = 0;
+    if (blockIdx.x == 0 && threadIdx.x == 0) {
+        state.rest = 0;
+        state.n = 0;
     }
-    if (blockIdx.x == 0 && threadIdx.x == 0) state.n = 0;
 }
 
 template <class T>
@@ -829,23 +957,18 @@ __global__ __launch_bounds__(kThreads) void k_sample_count(SampleArgs p, RowStat
     const int64_t i = blockIdx.y;
     RowState &state = states[i];
     const Request q = request_of(p, i, state);
-    if (q.answer != Answer::draw || !q.filters()) return;
-    clear_histogram(s);
+    if (q.answer != Answer::draw || q.infinite || !q.filters()) return;
+    for (int k = threadIdx.x; k < kBins; k += kThreads) s.count[k] = 0;
+    __syncthreads();
     const uint32_t a = blockIdx.x * p.chunk;
     count_steps((const T *)p.logits + i * p.ld, a, min(a + p.chunk, (uint32_t)p.v), q, s);
     for (int k = threadIdx.x; k < kBins; k += kThreads)
-        if (s.count[k] != 0) {
-            atomicAdd(&state.count[k], s.count[k]);
-            if (q.top_k == 0) add64(&state.weight[k], s.weight[k]);
-        }
+        if (s.count[k] != 0) atomicAdd(&state.count[k], s.count[k]);
 }
 
 __device__ __forceinline__ Border border_of(const Request &q, const RowState &state, Shared &s) {
     if (q.filters()) {
-        for (int k = threadIdx.x; k < kBins; k += kThreads) {
-            s.count[k] = state.count[k];
-            s.weight[k] = state.weight[k];
-        }
+        for (int k = threadIdx.x; k < kBins; k += kThreads) s.count[k] = state.count[k];
         __syncthreads();
     }
     return border_of(q, s);
@@ -857,15 +980,19 @@ __global__ __launch_bounds__(kThreads) void k_sample_collect(SampleArgs p, RowSt
     const int64_t i = blockIdx.y;
     RowState &state = states[i];
     const Request q = request_of(p, i, state);
-    if (q.answer != Answer::draw) return;
+    if (q.answer != Answer::draw || q.infinite) return;
     const Border d = border_of(q, state, s);
     if (d.left) return;
     const int wave = threadIdx.x >> 6;
     const uint32_t v = (uint32_t)p.v, part = p.chunk / kWaves, a = min(blockIdx.x * p.chunk + wave * part, v);
-    const uint64_t sum = collect((const T *)p.logits + i * p.ld, a, min(a + part, v), q, d, [&](uint64_t code) {
+    uint64_t rest;
+    const uint64_t sum = collect((const T *)p.logits + i * p.ld, a, min(a + part, v), q, d, rest, [&](uint64_t code) {
         state.list[min(atomicAdd(&state.n, 1), kList - 1)] = code;
     });
-    if ((threadIdx.x & 63) == 0) state.range[(int)blockIdx.x * kWaves + wave] = sum;
+    if ((threadIdx.x & 63) == 0) {
+        state.range[(int)blockIdx.x * kWaves + wave] = sum;
+        if (rest != 0) add64(&state.rest, rest);
+    }
 }
 
 template <class T>
@@ -875,18 +1002,26 @@ __global__ __launch_bounds__(kThreads) void k_sample_draw(SampleArgs p, RowState
     RowState &state = states[i];
     const Request q = request_of(p, i, state);
     if (answered(p, i, q)) return;
+    if (q.infinite) return answer(p, i, kLeft, 0.0);
     const Border d = border_of(q, state, s);
-    if (d.left) return answer(p, i, kLeft, 0.0);
-    const int n = min(state.n, kList), ranges = p.chunks * kWaves;
+    const int n = state.n, ranges = p.chunks * kWaves;
+    if (d.left || n > kList) return answer(p, i, kLeft, 0.0);
     for (int k = threadIdx.x; k < n; k += kThreads) s.list[k] = state.list[k];
     for (int k = threadIdx.x; k < ranges; k += kThreads) s.range[k] = state.range[k];
+    if (threadIdx.x == 0) s.rest = state.rest;
     __syncthreads();
-    answer(p, i, q.r, draw((const T *)p.logits + i * p.ld, (uint32_t)p.v, q, d, n, ranges, p.chunk / kWaves, s));
+    Drawn out;
+    if (draw((const T *)p.logits + i * p.ld, (uint32_t)p.v, q, d, n, ranges, p.chunk / kWaves, s, out))
+        answer(p, i, q.r, out);
+    else
+        answer(p, i, kLeft, 0.0);
 }
 
 // ---- launches ------------------------------------------------------------------------------
-// Whether a row is spread over blocks.
-bool spreads(int64_t t, int64_t v) { return t < 96 && v > 65536; }
+// Whether a row is spread over blocks: where one compute unit would take longer for it than the launches that this needs
+// (bf16, one launch against five, us: 1 x 128000: 51 against 22 without filters, 81 against 57 with top_p; 128 x 128000: 56 against
+// 42, 85 against 81, but with top_k 35 against 40; 37 x 32000: 21 against 21, 40 against 48, 18 against 28).
+bool spreads(int64_t t, int64_t v) { return t <= 96 && v > 65536; }
 int chunks_of(int64_t t, int64_t v) {
     int64_t c = (kPlanUnits + t - 1) / t;
     const int64_t most = (v + 8191) / 8192;
@@ -928,10 +1063,8 @@ int sample(SampleArgs p, RowState *states, hipStream_t s) {
             hipLaunchKernelGGL((k_sample<T>), dim3((unsigned)q.t), block, 0, s, q);
             HIP_TRY(hipGetLastError());
         }
-        if (q.v > kList) {  // (shorter rows fit the list whatever they hold)
-            hipLaunchKernelGGL((k_sample_slow<T>), dim3((unsigned)q.t), block, 0, s, q);
-            HIP_TRY(hipGetLastError());
-        }
+        hipLaunchKernelGGL((k_sample_slow<T>), dim3((unsigned)q.t), block, 0, s, q);
+        HIP_TRY(hipGetLastError());
     }
     return OZAKI2_SUCCESS;
 }

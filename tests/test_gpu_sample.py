@@ -1,7 +1,7 @@
 """The sampler (ozaki2_sample) against its definition in 64 bits.
 
-A weight is off by at most 2^-41 from its rounding and 2^-45 from the exponential, relative to the largest weight, which the sum is
-no smaller than: a running sum of v of them by at most v 2^-40.9 of the whole. Where u, or a filter's bound, is further than
+A weight is off by at most 2^-41 from its rounding and 2^-44.6 from the exponential, relative to the largest weight, which the sum is
+no smaller than: a running sum of v of them by at most v 2^-40.8 of the whole. Where u, or a filter's bound, is further than
 that from the sums next to it, the token has to be the definition's; rows where it is not are counted, and they
 are few. The logarithm of the probability is a binary64 value rounded to binary32, with a sum off by as much."""
 import math
@@ -32,7 +32,7 @@ def check(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, most_unsure
     settings = [per_row(x, t) for x in (temperature, top_k, top_p, min_p)]
     rows, us = logits.double().cpu().numpy(), u.tolist()
     unsure = 0
-    slack = v * 2.0 ** -40.9
+    slack = v * 2.0 ** -40.8
     for i in range(t):
         ref = reference(rows[i], us[i], *(s[i] for s in settings))
         if ref is None:

@@ -15,12 +15,14 @@ def test_refusals():
                    (10, -0.1), (10, float("nan")), (12, 1.1), (12, -0.1), (12, float("nan")), (14, 0)]:
         assert oz.ozaki2_sample(*good[:i], bad, *good[i + 1:]) == -(i + 1), (i, bad)
         assert oz.ozaki2_sample_ws(*good[:i], bad, *good[i + 1:], P, 1 << 30) == -(i + 1), (i, bad)
-    need = oz.ozaki2_sample_workspace_size(3, 9)
-    assert oz.ozaki2_sample_ws(*good, 0, need) == -17
-    assert oz.ozaki2_sample_ws(*good, P + 8, need) == -17
-    assert oz.ozaki2_sample_ws(*good, P, need - 1) == 2
+    v = 100000  # a few long rows need a workspace
+    long = (3, v, P, v, *good[4:])
+    need = oz.ozaki2_sample_workspace_size(3, v)
+    assert oz.ozaki2_sample_ws(*long, 0, need) == -17
+    assert oz.ozaki2_sample_ws(*long, P + 8, need) == -17
+    assert oz.ozaki2_sample_ws(*long, P, need - 1) == 2
     # a vector's value is not looked at here, and the number beside it does not matter
-    vectors = (3, 9, P, 9, oz.BF16, P, -1.0, P, 5, P, 7.0, P, 7.0, P, P, 0)
+    vectors = (3, v, P, v, oz.BF16, P, -1.0, P, 5, P, 7.0, P, 7.0, P, P, 0)
     assert oz.ozaki2_sample_ws(*vectors, P, need - 1) == 2
     assert oz.ozaki2_sample(1 << 31, *good[1:]) == 3
     v = 1 << 23
@@ -30,8 +32,9 @@ def test_refusals():
 
 def test_workspace():
     one = oz.ozaki2_sample_workspace_size(1, 128000)
-    assert 0 < one < 80 << 10
-    assert oz.ozaki2_sample_workspace_size(1 << 20, 128000) <= 1024 * one  # rows go in runs
+    assert 0 < one < 48 << 10 and oz.ozaki2_sample_workspace_size(96, 128000) <= 96 * one
+    # a block per row needs none
+    assert oz.ozaki2_sample_workspace_size(1, 32000) == oz.ozaki2_sample_workspace_size(1 << 20, 128000) == 0
     for bad in ((0, 5), (-1, 5), (5, 0), (5, -1), (1 << 31, 5), (5, 1 << 23)):
         assert oz.ozaki2_sample_workspace_size(*bad) == 0
 
