@@ -18,6 +18,28 @@
 namespace oz2 {
 namespace {
 
+// Aligned copies of two matrices in one launch (see k_pack_rows): the first block numbers are the first one's.
+struct Pack {
+    const void *in;
+    int64_t ldi, rows;  // bytes between rows
+    void *out;
+};
+__global__ __launch_bounds__(256) void k_pack_two(Pack a, Pack b, int64_t kbytes, int64_t ldo, int blocks_a) {
+    const bool first = (int)blockIdx.x < blocks_a;
+    const Pack p = first ? a : b;
+    const int block = first ? blockIdx.x : blockIdx.x - blocks_a, blocks = first ? blocks_a : gridDim.x - blocks_a;
+    const int lane = threadIdx.x & 63;
+    for (int64_t r = (int64_t)block * 4 + (threadIdx.x >> 6); r < p.rows; r += (int64_t)blocks * 4)
+        for (int64_t k = 16 * lane; k < kbytes; k += 1024)
+            *(v4i *)((char *)p.out + r * ldo + k) = load_chunk((const int8_t *)p.in + r * p.ldi, k, kbytes);
+}
+hipError_t pack_two(const Pack &a, const Pack &b, int64_t kbytes, int64_t ldo, hipStream_t s) {
+    auto blocks = [](int64_t rows) { return (int)((rows + 3) / 4 < 8192 ? (rows + 3) / 4 : 8192); };
+    hipLaunchKernelGGL(k_pack_two, dim3((unsigned)(blocks(a.rows) + blocks(b.rows))), dim3(256), 0, s, a, b, kbytes, ldo,
+                       blocks(a.rows));
+    return hipGetLastError();
+}
+
 // ---- forward ----------------------------------------------------------------------
 struct LinearArgs {
     int64_t t, n, k;
@@ -92,7 +114,6 @@ int forward(const LinearArgs &p, char *ws, hipStream_t s) {
     if (!needs_pack(2 * p.k, p.t)) return forward_rows<M, OutT>(p, ws, s);
     const int64_t pitch = pack_pitch(2 * p.k), run = pack_rows(p.n, 2 * p.k);
     char *w = ws + up256((size_t)p.t * (size_t)pitch), *planes = w + up256((size_t)run * (size_t)pitch);
-    HIP_TRY(launch_pack_rows(p.X, 2 * p.ldx, p.t, 2 * p.k, ws, pitch, s));
     for (int64_t n0 = 0; n0 < p.n; n0 += run) {
         LinearArgs q = p;
         q.n = p.n - n0 < run ? p.n - n0 : run;
@@ -104,7 +125,11 @@ int forward(const LinearArgs &p, char *ws, hipStream_t s) {
         if (q.residual) q.residual = (const OutT *)p.residual + n0;
         q.Y = (OutT *)p.Y + n0;
         if (q.Z) q.Z = (typename M::Elem *)p.Z + n0;
-        HIP_TRY(launch_pack_rows((const char *)p.W + 2 * n0 * p.ldw, 2 * p.ldw, q.n, 2 * p.k, w, pitch, s));
+        const Pack next = {(const char *)p.W + 2 * n0 * p.ldw, 2 * p.ldw, q.n, w};
+        if (n0 == 0)
+            HIP_TRY(pack_two({p.X, 2 * p.ldx, p.t, ws}, next, 2 * p.k, pitch, s));
+        else
+            HIP_TRY(launch_pack_rows(next.in, next.ldi, next.rows, 2 * p.k, w, pitch, s));
         const int st = forward_rows<M, OutT>(q, planes, s);
         if (st) return st;
     }
@@ -207,18 +232,77 @@ __global__ __launch_bounds__(256) void k_act_grad(GradArgs<T> p) {
                 p.sums[blockIdx.y * p.ldsum + c + i] =
                     (sum[i] + part[0][8 * lane + i]) + (part[1][8 * lane + i] + part[2][8 * lane + i]);
 }
-// The slabs' sums, joined in a fixed order: a block takes 64 columns, each wavefront every fourth slab.
-__global__ __launch_bounds__(256) void k_join_columns(const float *__restrict__ sums, int slabs, int64_t ld, int64_t n,
-                                                      float *__restrict__ out) {
+// The slabs' sums, joined in a fixed order: a block takes 64 columns, each wavefront every fourth slab. The blocks after those
+// join the planes of dX's slices, if there are any (both are short, and a launch takes as long as they do): four values per
+// thread, slices in order.
+struct Columns {
+    const float *sums;
+    int slabs;
+    int64_t ld, n;
+    float *out;
+    int blocks;  // 0: none
+};
+template <class T>
+struct Planes {
+    const float *planes;
+    int splits;
+    int64_t plane, ldp;
+    T *out;
+    int64_t ldo, na, nb;
+    int across;  // blocks of a row
+};
+template <class T>
+__global__ __launch_bounds__(256) void k_join_both(Columns c, Planes<T> p) {
     __shared__ float part[4][64];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
-    float s = 0.f;
-    if (c < n)
-        for (int i = wave; i < slabs; i += 4) s += sums[i * ld + c];
-    part[wave][lane] = s;
-    __syncthreads();
-    if (wave == 0 && c < n) out[c] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+    if ((int)blockIdx.x < c.blocks) {
+        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+        const int64_t at = (int64_t)blockIdx.x * 64 + lane;
+        float s = 0.f;
+        if (at < c.n) {
+            int i = wave;
+            for (; i + 28 < c.slabs; i += 32) {  // eight loads on their way at a time
+                float o[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] = c.sums[(i + 4 * j) * c.ld + at];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) s += o[j];
+            }
+            for (; i < c.slabs; i += 4) s += c.sums[i * c.ld + at];
+        }
+        part[wave][lane] = s;
+        __syncthreads();
+        if (wave == 0 && at < c.n) c.out[at] = (part[0][lane] + part[1][lane]) + (part[2][lane] + part[3][lane]);
+        return;
+    }
+    const int block = (int)blockIdx.x - c.blocks, rows = ((int)gridDim.x - c.blocks) / p.across;
+    const int64_t a = 4 * ((int64_t)(block % p.across) * 256 + threadIdx.x);
+    if (a >= p.na) return;
+    for (int64_t b = block / p.across; b < p.nb; b += rows) {
+        const float *from = p.planes + b * p.ldp + a;
+        v4f s = *(const v4f *)from;
+        int i = 1;
+        for (; i + 4 <= p.splits; i += 4) {
+            v4f o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[j] = *(const v4f *)(from + (i + j) * p.plane);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s += o[j];
+        }
+        for (; i < p.splits; ++i) s += *(const v4f *)(from + i * p.plane);
+#pragma unroll
+        for (int v = 0; v < 4; ++v)
+            if (a + v < p.na) p.out[b * p.ldo + a + v] = rounded<T>(s[v]);
+    }
+}
+template <class T>
+hipError_t join_both(const Columns &c, Planes<T> p, hipStream_t s) {
+    p.across = (int)((p.na + 1023) / 1024);
+    const int64_t most = (65536 + p.across - 1) / (p.across > 0 ? p.across : 1), rows = p.nb < most ? p.nb : most;
+    const int64_t blocks = c.blocks + (p.splits > 0 ? rows * p.across : 0);
+    if (blocks == 0) return hipSuccess;
+    if (p.across == 0) p.across = 1;
+    hipLaunchKernelGGL((k_join_both<T>), dim3((unsigned)blocks), dim3(256), 0, s, c, p);
+    return hipGetLastError();
 }
 
 __global__ __launch_bounds__(256) void k_zero_matrix16(uint16_t *out, int64_t ldo, int64_t rows, int64_t cols) {
@@ -247,8 +331,8 @@ struct GradPlan {
 };
 GradPlan plan_grad(int64_t t, int64_t n, int64_t k, bool dx, bool dw, bool db) {
     GradPlan p{};
-    // about eight blocks per compute unit, of 16 rows or more
-    const int64_t cols = (n + kGradCols - 1) / kGradCols, most = (t + 15) / 16;
+    // about eight blocks per compute unit, of 4 rows or more
+    const int64_t cols = (n + kGradCols - 1) / kGradCols, most = (t + 3) / 4;
     int64_t slabs = 8 * kPlanUnits / cols;
     slabs = slabs < 1 ? 1 : slabs > most ? most : slabs;
     if (slabs < 1) slabs = 1;
@@ -300,20 +384,20 @@ bool kmajor_ready(const void *p, int64_t ld, int64_t cols) {
     return (((uintptr_t)p | (uintptr_t)(2 * ld) | (uintptr_t)(2 * cols)) & 15) == 0 && 2 * ld < (1 << 24);
 }
 
-// R[b][a] over krows rows of k, rounded to T.
+// R[b][a] over krows rows of k, rounded to T, or its planes, which `planes` then describes for join_both.
 template <class M, bool KB>
-int kmajor_product(TileArgs ta, int64_t krows, int splits, void *out, int64_t ldo, char *planes, hipStream_t s) {
+int kmajor_product(TileArgs ta, int64_t krows, int splits, void *out, int64_t ldo, char *ws, Planes<typename M::Elem> &planes,
+                   hipStream_t s) {
     typedef typename M::Elem T;
     ta.krows = (int)krows;
+    planes = {};
     if (splits == 1) {
         HIP_TRY((launch_kmajor<M, EpiRound<T>, true, KB>(ta, {(T *)out, ldo, ta.na, ta.nb}, 1, s)));
         return OZAKI2_SUCCESS;
     }
     const int64_t ldp = plane_pitch(ta.na), plane = ta.nb * ldp;
-    HIP_TRY((launch_kmajor<M, EpiRaw, true, KB>(ta, {(uint32_t *)planes, ldp, plane, ta.na, ta.nb}, splits, s)));
-    HIP_TRY((launch_join_act<T, void, false>(planes, splits, plane, ldp,
-                                             {(T *)out, ldo, nullptr, nullptr,
-                                              {nullptr, OZAKI2_ACT_NONE, nullptr, 0, nullptr, 0}, ta.na, ta.nb}, s)));
+    HIP_TRY((launch_kmajor<M, EpiRaw, true, KB>(ta, {(uint32_t *)ws, ldp, plane, ta.na, ta.nb}, splits, s)));
+    planes = {(const float *)ws, splits, plane, ldp, (T *)out, ldo, ta.na, ta.nb, 0};
     return OZAKI2_SUCCESS;
 }
 
@@ -342,36 +426,39 @@ int backward(const GradCallArgs &c, char *ws, hipStream_t s) {
                                        db ? (float *)(ws + p.sums) : nullptr, c.n, c.t, c.n, p.slab});
         HIP_TRY(hipGetLastError());
     }
-    if (db) {
-        hipLaunchKernelGGL(k_join_columns, dim3((unsigned)((c.n + 63) / 64)), dim3(256), 0, s, (const float *)(ws + p.sums),
-                           p.slabs, c.n, c.n, c.dbias);
-        HIP_TRY(hipGetLastError());
+    Columns columns = {};
+    if (db) columns = {(const float *)(ws + p.sums), p.slabs, c.n, c.n, c.dbias, (int)((c.n + 63) / 64)};
+    const void *w = c.W, *x = c.X;
+    int64_t ldw = c.ldw, ldx = c.ldx;
+    const bool copy_w = dx && !kmajor_ready(w, ldw, c.k), copy_x = dw && !kmajor_ready(x, ldx, c.k);
+    if (copy_w) {
+        w = ws + p.w;
+        ldw = pitch16(c.k);
     }
+    if (copy_x) {
+        x = ws + p.x;
+        ldx = pitch16(c.k);
+    }
+    if (copy_w && copy_x)
+        HIP_TRY(pack_two({c.W, 2 * c.ldw, c.n, ws + p.w}, {c.X, 2 * c.ldx, c.t, ws + p.x}, 2 * c.k, 2 * pitch16(c.k), s));
+    else if (copy_w)
+        HIP_TRY(launch_pack_rows(c.W, 2 * c.ldw, c.n, 2 * c.k, ws + p.w, 2 * ldw, s));
+    else if (copy_x)
+        HIP_TRY(launch_pack_rows(c.X, 2 * c.ldx, c.t, 2 * c.k, ws + p.x, 2 * ldx, s));
+    Planes<T> planes = {};
     if (dx) {
         // rows of W as the rows of k; G's columns past n are zeros
-        const void *w = c.W;
-        int64_t ldw = c.ldw;
-        if (!kmajor_ready(w, ldw, c.k)) {
-            HIP_TRY(launch_pack_rows(w, 2 * ldw, c.n, 2 * c.k, ws + p.w, 2 * pitch16(c.k), s));
-            w = ws + p.w;
-            ldw = pitch16(c.k);
-        }
         const int st = kmajor_product<M, false>(rows_of(c.t, c.k, (c.n + 7) / 8 * 8, g, ldg, w, ldw), c.n, p.dx_splits, c.dX,
-                                                c.lddx, ws + p.planes, s);
+                                                c.lddx, ws + p.planes, planes, s);
         if (st) return st;
     }
+    HIP_TRY(join_both(columns, planes, s));
     if (dw) {
         // rows of X and of G as the rows of k
-        const void *x = c.X;
-        int64_t ldx = c.ldx;
-        if (!kmajor_ready(x, ldx, c.k)) {
-            HIP_TRY(launch_pack_rows(x, 2 * ldx, c.t, 2 * c.k, ws + p.x, 2 * pitch16(c.k), s));
-            x = ws + p.x;
-            ldx = pitch16(c.k);
-        }
         const int st = kmajor_product<M, true>(rows_of(c.n, c.k, c.t, g, ldg, x, ldx), c.t, p.dw_splits, c.dW, c.lddw,
-                                               ws + p.planes, s);
+                                               ws + p.planes, planes, s);
         if (st) return st;
+        HIP_TRY(join_both(Columns{}, planes, s));
     }
     return OZAKI2_SUCCESS;
 }

@@ -12,6 +12,7 @@
 #include <math.h>
 
 #include "common.h"
+#include "lanes.h"
 #include "ozaki2.h"
 #include "tile.h"
 
@@ -102,8 +103,7 @@ __global__ __launch_bounds__(THREADS) void k_rmsnorm_quantize(NormArgs<T> p) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) sq = fma((double)e[j], (double)e[j], sq);
         }
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) sq += __shfl_xor(sq, o, 64);
+        sq = wave_sum(sq);
         if constexpr (W > 1) {
             // (the sums of the row before were read before its second barrier)
             if ((t & 63) == 0) squares[t >> 6] = sq;
@@ -143,8 +143,7 @@ __global__ __launch_bounds__(THREADS) void k_rmsnorm_quantize(NormArgs<T> p) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) m = max(m, abs_bits(e[j]));
         }
-#pragma unroll
-        for (int o = 32; o >= 1; o >>= 1) m = max(m, (uint32_t)__shfl_xor((int)m, o, 64));
+        m = wave_max(m);
         if constexpr (W > 1) {
             if ((t & 63) == 0) tops[t >> 6] = m;
             __syncthreads();
@@ -175,22 +174,26 @@ __global__ __launch_bounds__(THREADS) void k_rmsnorm_quantize(NormArgs<T> p) {
     }
 }
 
-// The fewest threads whose registers hold a row, with two vectors each for many rows
-// (fewer wavefronts to join) and one for few.
+// The fewest threads whose registers hold a row, with one vector each for few rows (latency: 1 x 4096, bf16: 3.9 us with 512
+// threads, 4.2 with 256 of two vectors) and two for many (fewer wavefronts to join: 4096 x 4096, bf16: 25.1 us or
+// 4.7 TB/s with 256 threads, 28.4 with 512; 1024 threads of one vector 47; fp32 35.1 or 6.2 TB/s). As many blocks as run
+// at once, which go on to further rows.
 template <class T>
 hipError_t launch_rmsnorm(const NormArgs<T> &p, hipStream_t s) {
-    const int64_t most = 2048;
-    const dim3 grid((unsigned)(p.rows < most ? p.rows : most));
-    auto go = [&](auto kern, int threads) { hipLaunchKernelGGL(kern, grid, dim3(threads), 0, s, p); };
-    const bool few = p.rows <= kPlanUnits;
+    auto go = [&](auto kern, int threads) {
+        const int64_t most = threads > 256 ? 1024 : 2048;
+        hipLaunchKernelGGL(kern, dim3((unsigned)(p.rows < most ? p.rows : most)), dim3(threads), 0, s, p);
+    };
     if (p.k <= 512)
         go(k_rmsnorm_quantize<T, 64, 1>, 64);
     else if (p.k <= 2048)
         go(k_rmsnorm_quantize<T, 256, 1>, 256);
-    else if (p.k <= 4096 && !few)
+    else if (p.k <= 4096 && p.rows > 1024)
         go(k_rmsnorm_quantize<T, 256, 2>, 256);
+    else if (p.k <= 4096)
+        go(k_rmsnorm_quantize<T, 512, 1>, 512);
     else if (p.k <= 8192)
-        go(k_rmsnorm_quantize<T, 1024, 1>, 1024);
+        go(k_rmsnorm_quantize<T, 512, 2>, 512);
     else
         go(k_rmsnorm_quantize<T, 1024, 2>, 1024);
     return hipGetLastError();

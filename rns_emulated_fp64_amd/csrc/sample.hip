@@ -27,6 +27,7 @@
 #include <math.h>
 
 #include "common.h"
+#include "lanes.h"
 #include "ozaki2.h"
 #include "tile.h"
 
@@ -112,36 +113,6 @@ struct Shared {
 
 __device__ __forceinline__ uint64_t shfl_xor64(uint64_t x, int o) { return (uint64_t)__shfl_xor((unsigned long long)x, o, 64); }
 __device__ __forceinline__ void add64(uint64_t *to, uint64_t x) { atomicAdd((unsigned long long *)to, (unsigned long long)x); }
-
-// x of the lane that a DPP control names, `none` where there is none. 0x110 + i: i lanes down in a row of 16;
-// 0x142, 0x143: the last lane of the row before, of the half before.
-template <int CTRL, int ROWS>
-__device__ __forceinline__ uint64_t from_lane(uint64_t x, uint64_t none) {
-    const int lo = __builtin_amdgcn_update_dpp((int)(uint32_t)none, (int)(uint32_t)x, CTRL, ROWS, 0xf, false);
-    const int hi = __builtin_amdgcn_update_dpp((int)(uint32_t)(none >> 32), (int)(uint32_t)(x >> 32), CTRL, ROWS, 0xf, false);
-    return (uint64_t)(uint32_t)hi << 32 | (uint32_t)lo;
-}
-__device__ __forceinline__ uint64_t read_lane(uint64_t x, int lane) {
-    return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(x >> 32), lane) << 32 |
-           (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, lane);
-}
-// of(x) over the lanes up to and with this one: of its row of 16, then of the wavefront. `none` changes nothing.
-template <class Of>
-__device__ __forceinline__ uint64_t scan_row(uint64_t x, uint64_t none, Of of) {
-    x = of(x, from_lane<0x111, 0xf>(x, none));
-    x = of(x, from_lane<0x112, 0xf>(x, none));
-    x = of(x, from_lane<0x114, 0xf>(x, none));
-    return of(x, from_lane<0x118, 0xf>(x, none));
-}
-template <class Of>
-__device__ __forceinline__ uint64_t scan_wave(uint64_t x, uint64_t none, Of of) {
-    x = scan_row(x, none, of);
-    x = of(x, from_lane<0x142, 0xa>(x, none));
-    return of(x, from_lane<0x143, 0xc>(x, none));
-}
-__device__ __forceinline__ uint64_t plus(uint64_t a, uint64_t b) { return a + b; }
-// The sum over a wavefront.
-__device__ __forceinline__ uint64_t wave_sum(uint64_t x) { return read_lane(scan_wave(x, 0, plus), 63); }
 
 // The sum of x over the threads before this one; total: over all. Ends behind a barrier, so s.part is free again.
 __device__ __forceinline__ uint64_t scan(uint64_t x, Shared &s, uint64_t &total) {
