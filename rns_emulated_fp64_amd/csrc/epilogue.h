@@ -84,6 +84,22 @@ __device__ __forceinline__ void with_activation(int act, Body body) {
     }
 }
 
+// act of each x; ACT: which, or kAnyActivation: `act` says.
+constexpr int kAnyActivation = -1;
+template <int ACT, int N>
+__device__ __forceinline__ void activate(int act, float (&x)[N][4]) {
+    auto all = [&](auto a) {
+#pragma unroll
+        for (int h = 0; h < N; ++h)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) x[h][v] = activated<decltype(a)::value>(x[h][v]);
+    };
+    if constexpr (ACT == kAnyActivation)
+        with_activation(act, all);
+    else
+        all(std::integral_constant<int, ACT>{});
+}
+
 // 16 bytes of a row, of which `left` elements are the row's own; zeros beyond.
 template <class T>
 __device__ __forceinline__ U16 load_some(const T *src, int64_t left) {
@@ -128,7 +144,11 @@ struct EpiAct {
 
     template <class M, int RT, int CT, bool EDGE, bool AGPR = false>
     static __device__ __forceinline__ void run(v4i (&acc)[RT][CT], const TileWhere &w, const Args &e) {
-        with_activation(e.f.act, [&](auto act) { body<decltype(act)::value, M, RT, CT, EDGE, AGPR>(acc, w, e); });
+        // the large tiles have a body per activation, the others a choice for every eight results (half the code)
+        if constexpr (RT == 8)
+            with_activation(e.f.act, [&](auto act) { body<decltype(act)::value, M, RT, CT, EDGE, AGPR>(acc, w, e); });
+        else
+            body<kAnyActivation, M, RT, CT, EDGE, AGPR>(acc, w, e);
     }
 
     template <int ACT, class M, int RT, int CT, bool EDGE, bool AGPR>
@@ -169,13 +189,12 @@ struct EpiAct {
             for (int j = 0; j < CT; ++j) {
                 const int64_t b = b0 + 16 * j;
                 if (b >= e.nb) continue;
-                float x[4];
+                float y[1][4], (&x)[4] = y[0];
 #pragma unroll
                 for (int v = 0; v < 4; ++v) x[v] = before(acc[0][j][v], j, sa[v], bi[v]);
                 if constexpr (!std::is_void_v<PreT>)
                     if (e.f.pre) store_four(e.f.pre + b * e.f.ldpre + a0, x, left);
-#pragma unroll
-                for (int v = 0; v < 4; ++v) x[v] = activated<ACT>(x[v]);
+                activate<ACT>(e.f.act, y);
                 if (e.f.residual) {
                     const OutT *r = e.f.residual + b * e.f.ldr + a0;
 #pragma unroll
@@ -187,6 +206,21 @@ struct EpiAct {
         } else {
             constexpr int RW = sizeof(OutT) == 2 ? 1 : 2;  // 16-byte loads of the residual per pair of tiles
             const int64_t st0 = w.a0 + pair_start<OutT>(lane);
+            // the residual in the layout of the stores: that of two rows of tiles on its way at once, and with 16 bits, for
+            // which there are registers, the next ones' while these are finished (4096 x 14336 x 4096, bf16: 393 us against 407)
+            constexpr bool AHEAD = RW == 1;
+            U16 r[AHEAD ? 2 : 1][CT][RW];
+            auto load_residual = [&](int i) {
+#pragma unroll
+                for (int j = 0; j < CT; ++j)
+#pragma unroll
+                    for (int h = 0; h < RW; ++h) {
+                        const int64_t b = b0 + 16 * j, a = st0 + 16 * (i + h);
+                        const OutT *from = e.f.residual + b * e.f.ldr + a;
+                        r[AHEAD ? i >> 1 & 1 : 0][j][h] = EDGE ? load_some(from, b < e.nb ? e.na - a : 0) : *(const U16 *)from;
+                    }
+            };
+            if (AHEAD && e.f.residual) load_residual(0);
 #pragma unroll
             for (int i = 0; i < RT; i += 2) {
                 float sa[2][4], bi[2][4];
@@ -197,18 +231,7 @@ struct EpiAct {
                     for (int v = 0; v < 4; ++v) bi[h][v] = 0.f;
                     if (e.f.bias) four(e.f.bias, a0 + 16 * (i + h), bi[h]);
                 }
-                // the residual in the layout of the stores, all of it on its way at once
-                U16 r[CT][RW];
-                if (e.f.residual) {
-#pragma unroll
-                    for (int j = 0; j < CT; ++j)
-#pragma unroll
-                        for (int h = 0; h < RW; ++h) {
-                            const int64_t b = b0 + 16 * j, a = st0 + 16 * (i + h);
-                            const OutT *from = e.f.residual + b * e.f.ldr + a;
-                            r[j][h] = EDGE ? load_some(from, b < e.nb ? e.na - a : 0) : *(const U16 *)from;
-                        }
-                }
+                if (e.f.residual && (!AHEAD || i + 2 < RT)) load_residual(AHEAD ? i + 2 : i);
 #pragma unroll
                 for (int j = 0; j < CT; ++j) {
                     float x[2][4];
@@ -223,15 +246,12 @@ struct EpiAct {
                         if (e.f.pre)
                             store_pair<PreT, EDGE>(x, e.f.pre + b * e.f.ldpre, w.a0 + pair_start<PreT>(lane) + 16 * i, e.na,
                                                    b < e.nb);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int v = 0; v < 4; ++v) x[h][v] = activated<ACT>(x[h][v]);
+                    activate<ACT>(e.f.act, x);
                     if (e.f.residual) {
                         if constexpr (RW == 1) {
                             // trade_pair's exchange is its own inverse
-                            const auto p = __builtin_amdgcn_permlane16_swap(r[j][0].w[0], r[j][0].w[2], false, false);
-                            const auto q = __builtin_amdgcn_permlane16_swap(r[j][0].w[1], r[j][0].w[3], false, false);
+                            const auto p = __builtin_amdgcn_permlane16_swap(r[AHEAD ? i >> 1 & 1 : 0][j][0].w[0], r[AHEAD ? i >> 1 & 1 : 0][j][0].w[2], false, false);
+                            const auto q = __builtin_amdgcn_permlane16_swap(r[AHEAD ? i >> 1 & 1 : 0][j][0].w[1], r[AHEAD ? i >> 1 & 1 : 0][j][0].w[3], false, false);
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 float o[4];
@@ -244,7 +264,7 @@ struct EpiAct {
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                                for (int v = 0; v < 4; ++v) x[h][v] += __uint_as_float(r[j][RW - 1 < h ? 0 : h].w[v]);
+                                for (int v = 0; v < 4; ++v) x[h][v] += __uint_as_float(r[AHEAD ? i >> 1 & 1 : 0][j][RW - 1 < h ? 0 : h].w[v]);
                         }
                     }
                     store_pair<OutT, EDGE>(x, e.out + b * e.ldo, st0 + 16 * i, e.na, b < e.nb);
@@ -315,6 +335,40 @@ hipError_t launch_join_act(const void *planes, int splits, int64_t plane, int64_
     const dim3 grid((unsigned)((e.na + 1023) / 1024), (unsigned)(e.nb < 65535 ? e.nb : 65535));
     hipLaunchKernelGGL((k_join_act<OutT, PreT, SCALED>), grid, dim3(256), 0, s, (const uint32_t *)planes, splits, plane, ldp, e);
     return hipGetLastError();
+}
+
+// The tile of a layer's product, which may be cut into slices of k: choose_tile's, or a larger one in slices where that is
+// expected to take a tenth less (a few rows and a long k: bf16, 37 x 4096 x 11008: 22.3 us with 4 slices of 64 x 64 tiles against
+// 28.4 with 32 x 32 ones), or 64 x 64 ones that are a few more than compute units (fp16, 509 x 2051 x 768: 264 of them 9.4 us, 136
+// of 128 x 64 11.2).
+inline double product_us(Tile tile, int64_t na, int64_t nb, int64_t kbytes) {
+    const int s = tile_splits(tile, na, nb, kbytes);
+    const int64_t rounds = (kbytes + 127) / 128;
+    return (double)((rounds + s - 1) / s) * round_us(tile, tiles_of(tile, na, nb) * s) +
+           (s > 1 ? 4.0 + (double)s * (double)na * (double)nb * 8.0 / 4e6 : 0.0);
+}
+inline Tile choose_layer_tile(const TileArgs &t) {
+    Tile best = choose_tile(t, false);
+    if (!aligned16(t) || best == Tile::skinny || best == Tile::any || best == Tile::p8 || getenv("OZ2_LINEAR_TILE")) return best;
+    double us = product_us(best, t.na, t.nb, t.kbytes);
+    const int64_t most = ((t.lda | t.ldb) & 127) == 0 ? kPlanUnits * 11 / 10 : kPlanUnits;
+    for (Tile tile : {Tile::s22, Tile::s42, Tile::p4}) {
+        if (tile != Tile::p4 && tiles_of(tile, t.na, t.nb) > most) continue;
+        const double u = product_us(tile, t.na, t.nb, t.kbytes);
+        if (u < 0.9 * us) {
+            best = tile;
+            us = u;
+        }
+    }
+    return best;
+}
+// Its slices, from the sizes alone: operands that are not aligned take as many.
+inline int layer_splits(int64_t t, int64_t n, int64_t kbytes) {
+    TileArgs ta{};
+    ta.na = n;
+    ta.nb = t;
+    ta.kbytes = kbytes >= 256 ? (kbytes + 15) / 16 * 16 : kbytes;
+    return tile_splits(choose_layer_tile(ta), n, t, ta.kbytes);
 }
 
 // Whether two row-major matrices of t x n elements of `size` bytes share memory, from

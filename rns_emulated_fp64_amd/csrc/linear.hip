@@ -68,14 +68,7 @@ TileArgs rows_of(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, co
     ta.kbytes = 2 * k;
     return ta;
 }
-// Slices of k, from the sizes alone: operands that are not aligned take as many.
-int splits_of(int64_t t, int64_t n, int64_t k) {
-    TileArgs ta{};
-    ta.na = n;
-    ta.nb = t;
-    ta.kbytes = (2 * k + 15) / 16 * 16;
-    return tile_splits(choose_tile(ta, false), n, t, ta.kbytes);
-}
+int splits_of(int64_t t, int64_t n, int64_t k) { return layer_splits(t, n, 2 * k); }
 int64_t plane_pitch(int64_t n) { return (n + 7) / 8 * 8; }
 size_t plane_bytes(int64_t t, int64_t n, int splits) {
     return splits > 1 ? up256((size_t)splits * (size_t)t * (size_t)plane_pitch(n) * 4) : 0;
@@ -97,8 +90,8 @@ int forward_rows(const LinearArgs &p, char *ws, hipStream_t s) {
     const TileArgs ta = rows_of(p.t, p.n, p.k, p.X, p.ldx, p.W, p.ldw);
     const typename Epi::Args e = {(OutT *)p.Y, p.ldy, nullptr, nullptr,
                                   {p.bias, p.act, (const OutT *)p.residual, p.ldr, (T *)p.Z, p.ldz}, p.n, p.t};
-    const Tile tile = choose_tile(ta, false);
-    const int splits = tile == Tile::skinny ? 1 : splits_of(p.t, p.n, p.k);
+    const Tile tile = choose_layer_tile(ta);
+    const int splits = tile == Tile::skinny || tile == Tile::p8 ? 1 : splits_of(p.t, p.n, p.k);
     if (splits == 1) {
         HIP_TRY((launch_tile<M, Epi, false>(ta, e, tile, 1, s)));
         return OZAKI2_SUCCESS;
@@ -191,7 +184,7 @@ constexpr int kGradCols = 512;
 template <class T>
 __global__ __launch_bounds__(256) void k_act_grad(GradArgs<T> p) {
     __shared__ float part[3][kGradCols];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int64_t c = (int64_t)blockIdx.x * kGradCols + 8 * lane;
     const int64_t r0 = (int64_t)blockIdx.y * p.slab, r1 = min(r0 + p.slab, p.t);
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
@@ -207,12 +200,13 @@ __global__ __launch_bounds__(256) void k_act_grad(GradArgs<T> p) {
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
+                if (r + 4 * u >= r1) break;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     if constexpr (decltype(act)::value != OZAKI2_ACT_NONE) g[u][i] *= slope_of<decltype(act)::value>(z[u][i]);
                     sum[i] += g[u][i];
                 }
-                if (p.G && r + 4 * u < r1 && c < p.n) {
+                if (p.G && c < p.n) {
                     const U16 o = {{pack2<T>(g[u][0], g[u][1]), pack2<T>(g[u][2], g[u][3]), pack2<T>(g[u][4], g[u][5]),
                                     pack2<T>(g[u][6], g[u][7])}};
                     *(U16 *)(p.G + (r + 4 * u) * p.ldg + c) = o;

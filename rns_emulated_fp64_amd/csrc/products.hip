@@ -141,7 +141,8 @@ int splits_of(int64_t t, int64_t n, int64_t k) {
 }
 int64_t plane_pitch(int64_t n) { return (n + 3) / 4 * 4; }
 size_t plane_bytes(int64_t t, int64_t n, int64_t k) {
-    const int s = splits_of(t, n, k);
+    // (with an activation or a residual as many as layer_splits says)
+    const int a = splits_of(t, n, k), b = layer_splits(t, n, k), s = a > b ? a : b;
     return s > 1 ? up256((size_t)s * (size_t)t * (size_t)plane_pitch(n) * 4) : 0;
 }
 // Workspace of a product: packed rows of A (unless they are the library's own)
@@ -192,8 +193,10 @@ int product_rows(const Product &p, char *ws, hipStream_t s) {
     typedef EpiAct<OutT, void, true> Act;
     const typename Act::Args f = {(OutT *)p.C, p.ldc, p.b_scale, p.a_scale,
                                   {p.bias, p.act, (const OutT *)p.residual, p.ldr, nullptr, 0}, p.n, p.t};
-    const Tile tile = choose_tile(ta, false);
-    const int splits = tile == Tile::skinny ? 1 : splits_of(p.t, p.n, p.k);
+    const Tile tile = p.finishes() ? choose_layer_tile(ta) : choose_tile(ta, false);
+    const int splits = tile == Tile::skinny || tile == Tile::p8 ? 1
+                       : p.finishes()                           ? layer_splits(p.t, p.n, p.k)
+                                                                : splits_of(p.t, p.n, p.k);
     if (splits == 1) {
         if (p.finishes())
             HIP_TRY((launch_tile<MmaI8, Act, false>(ta, f, tile, 1, s)));
