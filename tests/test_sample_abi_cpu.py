@@ -1,9 +1,18 @@
 """The sampler without a GPU: argument checks, which come before any HIP call, its workspace, and the definition that the GPU tests
 compare with on rows that can be worked out by hand."""
+import os
+import re
+import shutil
+import subprocess
+
 import numpy as np
+import pytest
 
 import rns_emulated_fp64_amd as oz
 from sample_util import reference
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
 
 P = 1 << 20  # a pointer that is never followed
 
@@ -58,3 +67,24 @@ def test_the_definition_by_hand():
     assert reference([np.nan, 1.0], 0.5, 1.0, 0, 1.0, 0.0) is None
     assert reference([-np.inf, -np.inf], 0.5, 1.0, 0, 1.0, 0.0) is None
     assert reference([np.inf, 1.0, np.inf], 0.6, 1.0, 0, 1.0, 0.0)[2] == 2
+
+
+@pytest.mark.parametrize("source", ["sample.hip", "norm.hip"])
+def test_kernels_keep_their_state_in_registers(source):
+    """No spills, no packed FP32, and LDS for two of the sampler's blocks on a compute unit."""
+    if not os.path.exists(HIPCC):
+        pytest.skip("hipcc not available")
+    src = os.path.join(ROOT, "rns_emulated_fp64_amd", "csrc", source)
+    cmd = [HIPCC, "--offload-arch=gfx950", "-O3", "-std=c++17", "-ffp-contract=off", "-Xclang", "-target-feature",
+           "-Xclang", "-packed-fp32-ops", "-I" + os.path.join(ROOT, "include"), "--cuda-device-only", "-S", "-o", "-",
+           "-Rpass-analysis=kernel-resource-usage", src]
+    out = subprocess.run(cmd, capture_output=True, text=True, timeout=600)
+    assert out.returncode == 0, out.stderr[-2000:]
+    seen = 0
+    for line in out.stderr.splitlines():
+        m = re.search(r"remark:\s+(VGPRs Spill|ScratchSize|LDS Size)(?: \[[^\]]+\])?: (\d+)", line)
+        if m:
+            seen += 1
+            assert int(m.group(2)) <= (80 << 10 if m.group(1) == "LDS Size" else 0), line
+    assert seen > 20
+    assert not re.search(r"\n\s+v_pk_(add|mul|fma)_f32", out.stdout)
