@@ -195,7 +195,7 @@ hipError_t launch_rmsnorm(const NormArgs<T> &p, hipStream_t s) {
     else if (p.k <= 8192)
         go(k_rmsnorm_quantize<T, 512, 2>, 512);
     else
-        go(k_rmsnorm_quantize<T, 1024, 2>, 1024);
+        go(k_rmsnorm_quantize<T, 512, 4>, 512);
     return hipGetLastError();
 }
 

@@ -32,6 +32,12 @@
 #include "tile.h"
 
 namespace oz2 {
+
+// The coefficients of 2^f - 1 (see weight_of). In constant memory under an outside name, so that they come to lie in scalar registers,
+// from which a multiply-add takes them as they are (as known constants they are kept in vector registers and copied before each).
+__constant__ double kExp2[9] = {0.6931471805599453,    0.240226506958126,      0.05550410866476018,
+                                0.009618129159558177,  0.0013333558179141132,  0.00015403455703126052,
+                                1.5252686752210201e-05, 1.3255264681015647e-06, 1.0203146133663105e-07};
 namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
@@ -70,23 +76,13 @@ struct Row {
     // The weight of an entry, 0 if it is not counted.
     __device__ __forceinline__ double weight(float x) const;
 };
-// A constant in a scalar register, from which a multiply-add takes it as it is (in vector registers each would be copied first).
-__device__ __forceinline__ double scalar(double x) {
-    asm("" : "+s"(x));
-    return x;
-}
 // 2^40 2^t for t in [-100, 0]: 2^f for |f| <= 1/2 by the polynomial of degree 9 that is 1 at 0 and goes through it at nine
 // Chebyshev nodes (off by 2^-44.6), the rest in the exponent.
 __device__ __forceinline__ double weight_of(double t) {
-    const double magic = scalar(0x1.8p52), shifted = t + magic, f = t - (shifted - magic);
-    double p = fma(scalar(1.0203146133663105e-07), f, scalar(1.3255264681015647e-06));
-    p = fma(p, f, scalar(1.5252686752210201e-05));
-    p = fma(p, f, scalar(0.00015403455703126052));
-    p = fma(p, f, scalar(0.0013333558179141132));
-    p = fma(p, f, scalar(0.009618129159558177));
-    p = fma(p, f, scalar(0.05550410866476018));
-    p = fma(p, f, scalar(0.240226506958126));
-    p = fma(p, f, scalar(0.6931471805599453));
+    const double magic = 0x1.8p52, shifted = t + magic, f = t - (shifted - magic);
+    double p = kExp2[8];
+#pragma unroll
+    for (int i = 7; i >= 0; --i) p = fma(p, f, kExp2[i]);
     p = fma(p, f, 1.0);
     // (the integer is in the low bits of the shifted value)
     return __hiloint2double(__double2hiint(p) + ((__double2loint(shifted) + 40) << 20), __double2loint(p));
@@ -620,19 +616,24 @@ __device__ __forceinline__ void window_of(const Request &q, Border &d, Shared &s
         s.found[2 * threadIdx.x + 1] = ~(uint64_t)0;
     }
     uint64_t cb = scan(cs, s, entries), wb = scan(ws, s, whole);
+    // where the first and the last step of the widest window are, of the next one, of the narrowest
+    uint64_t at[6];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
+    for (int k = 0; k < 6; ++k)
+        at[k] = (uint64_t)(q.top_p * (double)whole * (1.0 + (k & 1 ? 1.0 : -1.0) * (k < 2 ? 0.0075 : k < 4 ? 0.0015 : 0.0003))) + 1;
+    // (one of them at least is among this thread's steps; a wavefront without any goes on)
+    if (wb < at[1] && wb + ws >= at[0]) {
 #pragma unroll
-        for (int k = 0; k < 6; ++k) {
-            // first and last step of the widest window, of the next one, of the narrowest
-            const double at = q.top_p * (double)whole * (1.0 + (k & 1 ? 1.0 : -1.0) * (k < 2 ? 0.0075 : k < 4 ? 0.0015 : 0.0003));
-            if ((double)wb < at && (double)(wb + w[i]) >= at) {
-                s.found[2 * k] = (uint64_t)(b0 + i);
-                s.found[2 * k + 1] = k & 1 ? cb + c[i] : cb;
-            }
+        for (int i = 0; i < PER; ++i) {
+#pragma unroll
+            for (int k = 0; k < 6; ++k)
+                if (wb < at[k] && wb + w[i] >= at[k]) {
+                    s.found[2 * k] = (uint64_t)(b0 + i);
+                    s.found[2 * k + 1] = k & 1 ? cb + c[i] : cb;
+                }
+            cb += c[i];
+            wb += w[i];
         }
-        cb += c[i];
-        wb += w[i];
     }
     __syncthreads();
     d.left = true;
