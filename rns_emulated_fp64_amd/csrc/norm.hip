@@ -35,6 +35,32 @@ struct NormArgs {
     int64_t lds;
 };
 
+// Eight elements of a row as they are in memory, zeros past its end.
+template <class T>
+struct Eight {
+    U16 u[sizeof(T) / 2];
+};
+template <class T>
+__device__ __forceinline__ Eight<T> load_eight(const T *row, int64_t at, int64_t k) {
+    Eight<T> r;
+    if (at + 8 <= k) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = *(const U16 *)((const char *)(row + at) + 16 * i);
+    } else {
+        T e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = at + i < k ? row[at + i] : (T)0.f;
+        r = __builtin_bit_cast(Eight<T>, e);
+    }
+    return r;
+}
+template <class T>
+__device__ __forceinline__ void unpack(const Eight<T> &v, float (&x)[8]) {
+    struct { T e[8]; } e = __builtin_bit_cast(decltype(e), v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = (float)e.e[i];
+}
+
 template <class T>
 __device__ __forceinline__ void store8(T *row, int64_t at, int64_t k, const float (&x)[8]) {
     T e[8];
@@ -69,6 +95,18 @@ __global__ __launch_bounds__(THREADS) void k_rmsnorm_quantize(NormArgs<T> p) {
         else
 #pragma unroll
             for (int j = 0; j < 8; ++j) w[i][j] = 1.f;
+    // the next row is on its way while this one is worked on, as far as there are registers (16384 x 4096, bf16, from memory: 94
+    // us or 5.0 TB/s, 118 without)
+    constexpr bool AHEAD = NV <= 2;
+    Eight<T> next[AHEAD ? NV : 1], next_res[AHEAD ? NV : 1];
+    auto fetch = [&](int64_t r) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) next[i] = load_eight(p.X + r * p.ldx, 8 * t + i * STEP, p.k);
+        if (p.residual)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) next_res[i] = load_eight(p.residual + r * p.ldr, 8 * t + i * STEP, p.k);
+    };
+    if constexpr (AHEAD) fetch(blockIdx.x);
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
         const T *x = p.X + r * p.ldx, *res = p.residual ? p.residual + r * p.ldr : nullptr;
         auto load_h = [&](int64_t at, float(&h)[8]) {
@@ -81,16 +119,21 @@ __global__ __launch_bounds__(THREADS) void k_rmsnorm_quantize(NormArgs<T> p) {
             }
         };
         float h[NV][8];
+        if constexpr (AHEAD) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i) load8(x, 8 * t + i * STEP, p.k, h[i]);
-        if (res) {
-            float e[NV][8];
+            for (int i = 0; i < NV; ++i) unpack(next[i], h[i]);
+            if (res)
 #pragma unroll
-            for (int i = 0; i < NV; ++i) load8(res, 8 * t + i * STEP, p.k, e[i]);
+                for (int i = 0; i < NV; ++i) {
+                    float e[8];
+                    unpack(next_res[i], e);
 #pragma unroll
-            for (int i = 0; i < NV; ++i)
+                    for (int j = 0; j < 8; ++j) h[i][j] += e[j];
+                }
+            if (r + gridDim.x < p.rows) fetch(r + gridDim.x);
+        } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) h[i][j] += e[i][j];
+            for (int i = 0; i < NV; ++i) load_h(8 * t + i * STEP, h[i]);
         }
         double sq = 0.0;
 #pragma unroll
@@ -175,9 +218,9 @@ __global__ __launch_bounds__(THREADS) void k_rmsnorm_quantize(NormArgs<T> p) {
 }
 
 // The fewest threads whose registers hold a row, with one vector each for few rows (latency: 1 x 4096, bf16: 3.9 us with 512
-// threads, 4.2 with 256 of two vectors) and two for many (fewer wavefronts to join: 4096 x 4096, bf16: 25.1 us or
-// 4.7 TB/s with 256 threads, 28.4 with 512; 1024 threads of one vector 47; fp32 35.1 or 6.2 TB/s). As many blocks as run
-// at once, which go on to further rows.
+// threads, 4.2 with 256 of two vectors) and two for many (fewer wavefronts to join: 4096 x 4096, bf16: 25.1 us with 256
+// threads, 28.4 with 512, 1024 threads of one vector 47, operands in the caches; from memory 27.5 or 4.3 TB/s). As many blocks as
+// run at once, which go on to further rows.
 template <class T>
 hipError_t launch_rmsnorm(const NormArgs<T> &p, hipStream_t s) {
     auto go = [&](auto kern, int threads) {
