@@ -13,10 +13,10 @@
 //
 // Nothing is sorted but what a filter leaves undecided. A row goes through four phases:
 //   top      its largest logit
-//   count    a histogram of the logits over 4096 steps below it, in entries or in weights; the step in which
-//            the filter cuts follows from it
-//   collect  the undecided entries, a few hundred at most as a rule, into a list: those of that step, or all down to it
-//            where they are few; and the sums of the weights of what lies above it, by ranges of indexes
+//   count    a histogram of the logits over 4081 steps below it; the step in which top_k cuts follows from it, or a few steps
+//            among which top_p does
+//   collect  the undecided entries, a few hundred as a rule, into a list: those of these steps, or all down to top_k's
+//            where they are few; and the sums of the weights of what lies above, by ranges of indexes
 //   draw     which of the list are kept; then the token among them, or the range that u falls in and the
 //            token in it
 // One block does all four where there are many rows or they are short (k_sample); few long rows are spread over
