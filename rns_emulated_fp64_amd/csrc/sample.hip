@@ -21,8 +21,8 @@
 //            token in it
 // One block does all four where there are many rows or they are short (k_sample); few long rows are spread over
 // blocks, with a launch per phase (k_sample_top, ...). Rows whose list would be too long (thousands of equal
-// logits in a step, a top_k of thousands beside a top_p) are left to k_sample_slow, which finds the cut by
-// histograms over ever smaller ranges. The row is read from memory once, and twice more mostly from caches.
+// logits in a step, a top_k of thousands beside a top_p) are answered by answer_slowly, which finds the cut by
+// histograms over ever smaller ranges of the row. The row is read from memory once, and twice more mostly from caches.
 #include <hip/hip_runtime.h>
 #include <math.h>
 
@@ -370,7 +370,7 @@ struct Request {
     Row r;
     uint64_t code;   // of the largest entry
     Answer answer;
-    bool infinite;   // the largest is +inf: entries that are have weight 1, others 0 (k_sample_slow sees to it)
+    bool infinite;   // the largest is +inf: entries that are have weight 1, others 0 (answer_slowly sees to it)
     __device__ __forceinline__ bool filters() const { return top_k > 0 || top_p < 1.0; }
     __device__ __forceinline__ double share(uint64_t whole) const { return fmax(top_p * (double)whole, 0.5); }
 };
@@ -523,7 +523,6 @@ struct SampleArgs {
     uint32_t chunk;
     int chunks;
 };
-constexpr int64_t kLeft = -2;  // in `tokens` meanwhile: the row is left to k_sample_slow
 
 template <class T>
 __device__ __forceinline__ uint64_t top_of(const T *row, uint32_t a, uint32_t b, Shared &s) {
@@ -599,7 +598,7 @@ struct Border {
 // by a step's width at most, 0.7%, since every weight is; and where there are many entries by far less. So the steps are
 // collected over which this estimate goes from top_p less 0.75% of it to as much above, or, if these hold too many
 // entries, a fifth of that, or a 25th; the exact sums that follow show whether the cut is among them (where it is not,
-// k_sample_slow has the row). That takes one exponential per entry, in `collect`, and none here.
+// answer_slowly has the row). That takes one exponential per entry, in `collect`, and none here.
 __device__ __forceinline__ void window_of(const Request &q, Border &d, Shared &s) {
     constexpr int PER = kBins / kThreads;
     const int b0 = PER * (int)threadIdx.x;
@@ -794,59 +793,12 @@ __device__ __forceinline__ bool answered(const SampleArgs &p, int64_t i, const R
 }
 
 // ---- a block per row ---------------------------------------------------------------------
+// The rows that fit no list: top_k's cut, then top_p's among what that leaves, each from a histogram and what
+// refine finds inside its step, then the sums of ranges.
 template <class T>
-__global__ __launch_bounds__(kThreads) void k_sample(SampleArgs p) {
-    __shared__ Shared s;
-    const int64_t i = blockIdx.x;
+__device__ __forceinline__ void answer_slowly(const SampleArgs &p, int64_t i, const Request &q, Shared &s) {
     const T *row = (const T *)p.logits + i * p.ld;
     const uint32_t v = (uint32_t)p.v;
-    const Settings settings = settings_of(p, i);
-    const Request q = request_of(p, settings, top_of(row, 0, v, s));
-    if (answered(p, i, q)) return;
-    if (q.infinite) return answer(p, i, kLeft, 0.0);
-    if (q.filters()) {
-        for (int k = threadIdx.x; k < kBins; k += kThreads) s.count[k] = 0;
-        __syncthreads();
-        count_steps(row, 0, v, q, s);
-    }
-    const Border d = border_of(q, s);
-    if (d.left) return answer(p, i, kLeft, 0.0);
-    if (threadIdx.x == 0) {
-        s.n = 0;
-        s.rest = 0;
-    }
-    __syncthreads();
-    const int wave = threadIdx.x >> 6;
-    const uint32_t part = ((v + kWaves - 1) / kWaves + 511) / 512 * 512, a = min(wave * part, v);
-    uint64_t rest;
-    const uint64_t sum = collect(row, a, min(a + part, v), q, d, rest, [&](uint64_t code) {
-        s.list[min(atomicAdd(&s.n, 1), kList - 1)] = code;
-    });
-    if ((threadIdx.x & 63) == 0) {
-        s.range[wave] = sum;
-        if (rest != 0) add64(&s.rest, rest);
-    }
-    __syncthreads();
-    const int n = s.n;
-    __syncthreads();
-    Drawn out;
-    if (n <= kList && draw(row, v, q, d, n, kWaves, part, s, out))
-        answer(p, i, q.r, out);
-    else
-        answer(p, i, kLeft, 0.0);
-}
-
-// The rows that are left over: top_k's cut, then top_p's among what that leaves, each from a histogram and what
-// refine finds inside its step, then the sums of ranges. (A kernel of its own, whose registers are not the others'.)
-template <class T>
-__global__ __launch_bounds__(kThreads) void k_sample_slow(SampleArgs p) {
-    __shared__ Shared s;
-    const int64_t i = blockIdx.x;
-    if (p.tokens[i] != kLeft) return;
-    const T *row = (const T *)p.logits + i * p.ld;
-    const uint32_t v = (uint32_t)p.v;
-    const Settings settings = settings_of(p, i);
-    const Request q = request_of(p, settings, top_of(row, 0, v, s));
     const Row &r = q.r;
     uint64_t cut = 0;
     auto map = [&](float x) { return q.infinite ? (x == INFINITY ? 0.f : -INFINITY) : x; };
@@ -887,6 +839,54 @@ __global__ __launch_bounds__(kThreads) void k_sample_slow(SampleArgs p) {
     scan(sum, s, d.total);
     d.code = draw_from_range(row, 0, v, r, cut, place_of(q.u, d.total), s, map);
     answer(p, i, r, d);
+}
+
+// Counts, collects and draws; false if the row has to be answered slowly.
+template <class T>
+__device__ __forceinline__ bool draw_in_block(const T *row, uint32_t v, const Request &q, Shared &s, Drawn &out) {
+    if (q.infinite) return false;
+    if (q.filters()) {
+        for (int k = threadIdx.x; k < kBins; k += kThreads) s.count[k] = 0;
+        __syncthreads();
+        count_steps(row, 0, v, q, s);
+    }
+    const Border d = border_of(q, s);
+    if (d.left) return false;
+    if (threadIdx.x == 0) {
+        s.n = 0;
+        s.rest = 0;
+    }
+    __syncthreads();
+    const int wave = threadIdx.x >> 6;
+    const uint32_t part = ((v + kWaves - 1) / kWaves + 511) / 512 * 512, a = min(wave * part, v);
+    uint64_t rest;
+    const uint64_t sum = collect(row, a, min(a + part, v), q, d, rest, [&](uint64_t code) {
+        s.list[min(atomicAdd(&s.n, 1), kList - 1)] = code;
+    });
+    if ((threadIdx.x & 63) == 0) {
+        s.range[wave] = sum;
+        if (rest != 0) add64(&s.rest, rest);
+    }
+    __syncthreads();
+    const int n = s.n;
+    __syncthreads();
+    return n <= kList && draw(row, v, q, d, n, kWaves, part, s, out);
+}
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void k_sample(SampleArgs p) {
+    __shared__ Shared s;
+    const int64_t i = blockIdx.x;
+    const T *row = (const T *)p.logits + i * p.ld;
+    const uint32_t v = (uint32_t)p.v;
+    const Settings settings = settings_of(p, i);
+    const Request q = request_of(p, settings, top_of(row, 0, v, s));
+    if (answered(p, i, q)) return;
+    Drawn out;
+    if (draw_in_block(row, v, q, s, out))
+        answer(p, i, q.r, out);
+    else
+        answer_slowly<T>(p, i, q, s);
 }
 
 // ---- a row spread over blocks -------------------------------------------------------------
@@ -967,31 +967,37 @@ __global__ __launch_bounds__(kThreads) void k_sample_collect(SampleArgs p, RowSt
     }
 }
 
+// As draw_in_block, from what the launches before have left.
 template <class T>
-__global__ __launch_bounds__(kThreads) void k_sample_draw(SampleArgs p, RowState *states) {
-    __shared__ Shared s;
-    const int64_t i = blockIdx.x;
-    RowState &state = states[i];
-    const Request q = request_of(p, i, state);
-    if (answered(p, i, q)) return;
-    if (q.infinite) return answer(p, i, kLeft, 0.0);
+__device__ __forceinline__ bool draw_from_state(const SampleArgs &p, int64_t i, const Request &q, const RowState &state,
+                                                Shared &s, Drawn &out) {
+    if (q.infinite) return false;
     const Border d = border_of(q, state, s);
     const int n = state.n, ranges = p.chunks * kWaves;
-    if (d.left || n > kList) return answer(p, i, kLeft, 0.0);
+    if (d.left || n > kList) return false;
     for (int k = threadIdx.x; k < n; k += kThreads) s.list[k] = state.list[k];
     for (int k = threadIdx.x; k < ranges; k += kThreads) s.range[k] = state.range[k];
     if (threadIdx.x == 0) s.rest = state.rest;
     __syncthreads();
+    return draw((const T *)p.logits + i * p.ld, (uint32_t)p.v, q, d, n, ranges, p.chunk / kWaves, s, out);
+}
+
+template <class T>
+__global__ __launch_bounds__(kThreads) void k_sample_draw(SampleArgs p, RowState *states) {
+    __shared__ Shared s;
+    const int64_t i = blockIdx.x;
+    const Request q = request_of(p, i, states[i]);
+    if (answered(p, i, q)) return;
     Drawn out;
-    if (draw((const T *)p.logits + i * p.ld, (uint32_t)p.v, q, d, n, ranges, p.chunk / kWaves, s, out))
+    if (draw_from_state<T>(p, i, q, states[i], s, out))
         answer(p, i, q.r, out);
     else
-        answer(p, i, kLeft, 0.0);
+        answer_slowly<T>(p, i, q, s);
 }
 
 // ---- launches ------------------------------------------------------------------------------
 // Whether a row is spread over blocks: where one compute unit would take longer for it than the launches that this needs
-// (bf16, one launch against five, us: 1 x 128000: 51 against 22 without filters, 81 against 57 with top_p; 128 x 128000: 56 against
+// (bf16, one launch against four, us: 1 x 128000: 51 against 22 without filters, 81 against 57 with top_p; 128 x 128000: 56 against
 // 42, 85 against 81, but with top_k 35 against 40; 37 x 32000: 21 against 21, 40 against 48, 18 against 28).
 bool spreads(int64_t t, int64_t v) { return t <= 96 && v > 65536; }
 int chunks_of(int64_t t, int64_t v) {
@@ -1035,8 +1041,6 @@ int sample(SampleArgs p, RowState *states, hipStream_t s) {
             hipLaunchKernelGGL((k_sample<T>), dim3((unsigned)q.t), block, 0, s, q);
             HIP_TRY(hipGetLastError());
         }
-        hipLaunchKernelGGL((k_sample_slow<T>), dim3((unsigned)q.t), block, 0, s, q);
-        HIP_TRY(hipGetLastError());
     }
     return OZAKI2_SUCCESS;
 }
