@@ -305,16 +305,19 @@ __device__ __forceinline__ Place place_in(const uint64_t *list, int n, const Row
 template <class Each, class In, class Reaches>
 __device__ __forceinline__ uint64_t refine(Each each, In in, bool weights, uint64_t cut, uint64_t count, uint64_t weight,
                                            uint64_t members, const Row &r, Shared &s, Reaches reaches) {
-    uint64_t lo = ~(uint64_t)0, hi = 0;
-    each([&](float x, uint32_t j) {
-        const uint64_t code = code_of(x, j);
-        if (code >= cut && in(x)) {
-            lo = code < lo ? code : lo;
-            hi = code > hi ? code : hi;
-        }
-    });
-    lo = extreme<false>(lo, s);
-    hi = extreme<true>(hi, s);
+    uint64_t lo = cut, hi = ~(uint64_t)0;
+    if (members > kPairs) {
+        uint64_t least = ~(uint64_t)0, most = 0;
+        each([&](float x, uint32_t j) {
+            const uint64_t code = code_of(x, j);
+            if (code >= cut && in(x)) {
+                least = code < least ? code : least;
+                most = code > most ? code : most;
+            }
+        });
+        lo = extreme<false>(least, s);
+        hi = extreme<true>(most, s);
+    }
     while (members > kPairs) {
         // (here lo < hi, since codes differ)
         const int shift = max(0, 64 - __clzll((long long)(hi - lo)) - 12);
@@ -487,23 +490,35 @@ __device__ __forceinline__ uint64_t draw_from_range(const T *row, uint32_t a, ui
         b = min(a + part, b);
         __syncthreads();
     }
-    uint64_t k[8], sum = 0, total;
-    float x[8];
-    const uint32_t j0 = a + 8 * threadIdx.x;
-    struct { T e[8]; } e = __builtin_bit_cast(decltype(e), load_eight(row, j0, b));
+    auto last = [&](auto per) {  // so many consecutive entries per thread
+        constexpr int PER = decltype(per)::value;
+        uint64_t k[PER], sum = 0, total;
+        float x[PER];
+        const uint32_t j0 = a + PER * threadIdx.x;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        x[i] = map((float)e.e[i]);
-        k[i] = kept(x[i], j0 + i);
-        sum += k[i];
-        __builtin_amdgcn_sched_barrier(0);
-    }
-    uint64_t before = scan(sum, s, total);
+        for (int i = 0; i < PER; ++i) x[i] = j0 + i < b ? map((float)row[j0 + i]) : -INFINITY;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (before <= place && place < before + k[i]) s.found[0] = code_of(x[i], j0 + i);
-        before += k[i];
-    }
+        for (int i = 0; i < PER; ++i) {
+            k[i] = kept(x[i], j0 + i);
+            sum += k[i];
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        uint64_t before = scan(sum, s, total);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if (before <= place && place < before + k[i]) s.found[0] = code_of(x[i], j0 + i);
+            before += k[i];
+        }
+    };
+    const uint32_t left = b - a;
+    if (left <= kThreads)
+        last(std::integral_constant<int, 1>{});
+    else if (left <= 2 * kThreads)
+        last(std::integral_constant<int, 2>{});
+    else if (left <= 4 * kThreads)
+        last(std::integral_constant<int, 4>{});
+    else
+        last(std::integral_constant<int, 8>{});
     __syncthreads();
     return s.found[0];
 }
@@ -740,7 +755,10 @@ __device__ __forceinline__ bool draw(const T *row, uint32_t v, const Request &q,
     if (d.cuts || n > 0) {
         uint64_t in_list = 0, decided;
         for (int k = threadIdx.x; k < n; k += kThreads) in_list += units(q.r.weight(logit_of(s.list[k])));
-        scan((int)threadIdx.x < ranges ? s.range[threadIdx.x] : 0, s, decided);
+        if (ranges <= 16)  // (every row of lanes sums them all)
+            decided = read_lane(scan_row((int)(threadIdx.x & 15) < ranges ? s.range[threadIdx.x & 15] : 0, 0, plus), 15);
+        else
+            scan((int)threadIdx.x < ranges ? s.range[threadIdx.x] : 0, s, decided);
         scan(in_list, s, in_list);
         const double share = q.share(decided + s.rest);
         auto reaches = [&](uint64_t count, uint64_t w) {
@@ -841,22 +859,13 @@ __device__ __forceinline__ void answer_slowly(const SampleArgs &p, int64_t i, co
     answer(p, i, r, d);
 }
 
-// Counts, collects and draws; false if the row has to be answered slowly.
+// Counts, collects and draws, from a clear histogram and an empty list; false if the row has to be answered slowly.
 template <class T>
 __device__ __forceinline__ bool draw_in_block(const T *row, uint32_t v, const Request &q, Shared &s, Drawn &out) {
     if (q.infinite) return false;
-    if (q.filters()) {
-        for (int k = threadIdx.x; k < kBins; k += kThreads) s.count[k] = 0;
-        __syncthreads();
-        count_steps(row, 0, v, q, s);
-    }
+    if (q.filters()) count_steps(row, 0, v, q, s);
     const Border d = border_of(q, s);
     if (d.left) return false;
-    if (threadIdx.x == 0) {
-        s.n = 0;
-        s.rest = 0;
-    }
-    __syncthreads();
     const int wave = threadIdx.x >> 6;
     const uint32_t part = ((v + kWaves - 1) / kWaves + 511) / 512 * 512, a = min(wave * part, v);
     uint64_t rest;
@@ -880,6 +889,12 @@ __global__ __launch_bounds__(kThreads) void k_sample(SampleArgs p) {
     const T *row = (const T *)p.logits + i * p.ld;
     const uint32_t v = (uint32_t)p.v;
     const Settings settings = settings_of(p, i);
+    for (int k = threadIdx.x; k < kBins; k += kThreads) s.count[k] = 0;
+    if (threadIdx.x == 0) {
+        s.n = 0;
+        s.rest = 0;
+    }
+    // (top_of's barriers are behind these)
     const Request q = request_of(p, settings, top_of(row, 0, v, s));
     if (answered(p, i, q)) return;
     Drawn out;
