@@ -165,8 +165,9 @@ struct EpiRound {
 
 // G = dY act'(Z) in 16 bits, rounded once, half a step relative (dY's own precision),
 // and the sums of its columns in binary32 over a slab of rows, before that
-// rounding. A block takes 512 columns, a wavefront every fourth row of the slab, a
-// lane 8 columns. Columns of G up to the next multiple of 8 are zeros. Memory bound.
+// rounding. A block takes 512 columns, a lane 8 of them, a wavefront every fourth row of the slab; where there are fewer
+// columns a wavefront takes several rows at once, `across` lanes each (a power of two). Columns of G up to the
+// next multiple of 8 are zeros. Memory bound (8192 x 14336, bf16: 142 us or 5.0 TB/s).
 template <class T>
 struct GradArgs {
     const T *dY;
@@ -179,47 +180,54 @@ struct GradArgs {
     float *sums;  // or null; a row per slab, ldsum apart
     int64_t ldsum;
     int64_t t, n, slab;  // rows of a slab
+    int across;
 };
 constexpr int kGradCols = 512;
 template <class T>
 __global__ __launch_bounds__(256) void k_act_grad(GradArgs<T> p) {
     __shared__ float part[3][kGradCols];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int64_t c = (int64_t)blockIdx.x * kGradCols + 8 * lane;
+    const int64_t c = (int64_t)blockIdx.x * kGradCols + 8 * (lane & (p.across - 1));
+    const int rows = 64 / p.across;  // of a wavefront at once; this lane's is `row`
+    const int64_t row = lane / p.across;
     const int64_t r0 = (int64_t)blockIdx.y * p.slab, r1 = min(r0 + p.slab, p.t);
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     with_activation(p.act, [&](auto act) {
-        constexpr int U = 4;  // rows on their way at a time
-        for (int64_t r = r0 + wave; r < r1; r += 4 * U) {
+        constexpr int U = 4;  // of a lane's rows on their way at a time
+        for (int64_t r = r0 + wave * rows; r < r1; r += 4 * U * rows) {
             float g[U][8], z[U][8];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t at = r + 4 * u < r1 ? c : p.n;  // past the end: zeros
-                load8(p.dY + (r + 4 * u) * p.lddy, at, p.n, g[u]);
-                if constexpr (decltype(act)::value != OZAKI2_ACT_NONE) load8(p.Z + (r + 4 * u) * p.ldz, at, p.n, z[u]);
+                const int64_t at = r + 4 * u * rows + row, from = at < r1 ? c : p.n;  // past the end: zeros
+                load8(p.dY + at * p.lddy, from, p.n, g[u]);
+                if constexpr (decltype(act)::value != OZAKI2_ACT_NONE) load8(p.Z + at * p.ldz, from, p.n, z[u]);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (r + 4 * u >= r1) break;
+                if (r + 4 * u * rows >= r1) break;
+                const int64_t at = r + 4 * u * rows + row;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     if constexpr (decltype(act)::value != OZAKI2_ACT_NONE) g[u][i] *= slope_of<decltype(act)::value>(z[u][i]);
                     sum[i] += g[u][i];
                 }
-                if (p.G && c < p.n) {
+                if (p.G && at < r1 && c < p.n) {
                     const U16 o = {{pack2<T>(g[u][0], g[u][1]), pack2<T>(g[u][2], g[u][3]), pack2<T>(g[u][4], g[u][5]),
                                     pack2<T>(g[u][6], g[u][7])}};
-                    *(U16 *)(p.G + (r + 4 * u) * p.ldg + c) = o;
+                    *(U16 *)(p.G + at * p.ldg + c) = o;
                 }
             }
         }
     });
     if (p.sums == nullptr) return;
+    for (int o = p.across; o < 64; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] += __shfl_xor(sum[i], o, 64);
     if (wave > 0)
 #pragma unroll
         for (int i = 0; i < 8; ++i) part[wave - 1][8 * lane + i] = sum[i];
     __syncthreads();
-    if (wave == 0)
+    if (wave == 0 && lane < p.across)
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (c + i < p.n)
@@ -318,6 +326,7 @@ int kmajor_splits(int64_t t, int64_t n, int64_t k) {
 }
 
 struct GradPlan {
+    int across;  // lanes of a row of G
     int slabs;
     int64_t slab;
     int dx_splits, dw_splits;
@@ -325,13 +334,17 @@ struct GradPlan {
 };
 GradPlan plan_grad(int64_t t, int64_t n, int64_t k, bool dx, bool dw, bool db) {
     GradPlan p{};
-    // about eight blocks per compute unit, of 4 rows or more
-    const int64_t cols = (n + kGradCols - 1) / kGradCols, most = (t + 3) / 4;
-    int64_t slabs = 8 * kPlanUnits / cols;
-    slabs = slabs < 1 ? 1 : slabs > most ? most : slabs;
+    // about eight blocks per compute unit, of a row for every lane or more, and no more slabs than are soon joined (7457 x 28:
+    // 1865 slabs took 30 us)
+    const int64_t cols = (n + kGradCols - 1) / kGradCols;
+    p.across = 1;
+    while (8 * p.across < n && p.across < 64) p.across *= 2;
+    const int64_t least = 4 * (64 / p.across), most = (t + least - 1) / least;
+    int64_t slabs = cols > 0 ? 8 * kPlanUnits / cols : 1;
+    if (slabs > 256) slabs = 256;
+    if (slabs > most) slabs = most;
     if (slabs < 1) slabs = 1;
     if (t / slabs > ((int64_t)1 << 20)) slabs = (t >> 20) + 1;
-    if (slabs > 65535) slabs = 65535;
     p.slab = (t + slabs - 1) / slabs;
     if (p.slab < 1) p.slab = 1;
     p.slabs = (int)((t + p.slab - 1) / p.slab);
@@ -417,7 +430,7 @@ int backward(const GradCallArgs &c, char *ws, hipStream_t s) {
         const dim3 grid((unsigned)((c.n + kGradCols - 1) / kGradCols), (unsigned)p.slabs);
         hipLaunchKernelGGL((k_act_grad<T>), grid, dim3(256), 0, s,
                            GradArgs<T>{(const T *)c.dY, c.lddy, (const T *)c.Z, c.ldz, c.act, makes_g ? (T *)g : nullptr, ldg,
-                                       db ? (float *)(ws + p.sums) : nullptr, c.n, c.t, c.n, p.slab});
+                                       db ? (float *)(ws + p.sums) : nullptr, c.n, c.t, c.n, p.slab, p.across});
         HIP_TRY(hipGetLastError());
     }
     Columns columns = {};

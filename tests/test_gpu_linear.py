@@ -238,7 +238,8 @@ def grad_operands(t, n, k, dtype, seed, pad=0):
 
 
 GRADS = [(1, 1, 1), (1, 300, 512), (3, 17, 15), (16, 100, 304), (33, 129, 1000), (65, 66, 65), (128, 256, 256), (129, 264, 136),
-         (200, 1030, 77), (257, 300, 400), (300, 511, 1023), (520, 520, 520), (1500, 64, 72), (2000, 130, 264)]
+         (200, 1030, 77), (257, 300, 400), (300, 511, 1023), (520, 520, 520), (1500, 64, 72), (2000, 130, 264), (7457, 28, 64),
+         (5000, 8, 40), (4099, 1, 16), (3001, 513, 24)]
 
 
 @pytest.mark.parametrize("t,n,k", GRADS)
