@@ -608,12 +608,14 @@ struct Border {
     bool cuts;              // top_k or top_p cuts among them
     bool open;              // ... or keeps them all
     uint64_t count_before;  // entries before `first`
+    int sure;               // the filters' cut is in this step or a later one
 };
 // For top_p alone: the histogram's counts, each times its step's middle weight, give a share of the whole up to a step that is off
 // by a step's width at most, 0.7%, since every weight is; and where there are many entries by far less. So the steps are
 // collected over which this estimate goes from top_p less 0.75% of it to as much above, or, if these hold too many
 // entries, a fifth of that, or a 25th; the exact sums that follow show whether the cut is among them (where it is not,
-// answer_slowly has the row). That takes one exponential per entry, in `collect`, and none here.
+// answer_slowly has the row). Without these sums only the widest window's first step is a bound of the cut. That takes one exponential
+// per entry, in `collect`, and none here.
 __device__ __forceinline__ void window_of(const Request &q, Border &d, Shared &s) {
     constexpr int PER = kBins / kThreads;
     const int b0 = PER * (int)threadIdx.x;
@@ -664,10 +666,11 @@ __device__ __forceinline__ void window_of(const Request &q, Border &d, Shared &s
         }
     }
     d.cuts = true;
+    d.sure = (int)s.found[0];
     __syncthreads();
 }
 __device__ __forceinline__ Border border_of(const Request &q, Shared &s) {
-    Border d = {kBins, kBins - 1, false, false, false, false, 0};
+    Border d = {kBins, kBins - 1, false, false, false, false, 0, kBins};
     if (q.top_k > 0) {
         const Crossing x = crossing<false>(s, false, [&](uint64_t count, uint64_t, const Crossing &) {
             return count >= (uint64_t)q.top_k;
@@ -680,7 +683,7 @@ __device__ __forceinline__ Border border_of(const Request &q, Shared &s) {
         } else if (q.top_p < 1.0) {
             d.left = true;
         } else if (x.bin >= 0) {  // (else top_k is more than there are entries of any weight)
-            d.first = d.last = x.bin;
+            d.first = d.last = d.sure = x.bin;
             d.count_before = x.count_before;
             d.cuts = true;
         }
@@ -691,11 +694,11 @@ __device__ __forceinline__ Border border_of(const Request &q, Shared &s) {
         // min_p's own step, and one on either side for binary32's roundings
         const float t = fminf(__builtin_amdgcn_logf((float)(q.r.min40 / kUnit)) * -kStepsPerOctave, kSteps);
         const int lower = max((int)t - 1, 0), upper = min((int)t + 1, kBins - 1);
-        if (upper < d.first) {  // above the other filters' cut
+        if (upper < d.sure) {  // above the other filters' cut
             d.first = lower;
             d.last = upper;
             d.cuts = false;
-        } else {
+        } else {  // (between `sure` and `first` the exact sums show which of the two comes first)
             if (lower < d.first) {
                 for (int b = lower; b < d.first; ++b) d.count_before -= d.cuts && q.top_k > 0 ? s.count[b] : 0;
                 d.first = lower;
