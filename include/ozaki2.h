@@ -477,7 +477,8 @@ int ozaki2_i8linear_ws(int64_t t, int64_t n, int64_t k, const void *X, int64_t l
  *   activation   an ozaki2_activation.
  *   residual, ldr   DEVICE of type ctype, element (i, j) at residual[i*ldr + j], ldr >= max(1, n), or NULL for none (ldr is
  *             then not looked at). It must not share memory with C (refused, from the first byte of each to its last).
- * Workspaces: those of ozaki2_i8gemm_workspace_size and ozaki2_i8linear_workspace_size.
+ * Workspaces: the _ws forms take what the plain ones do (ozaki2_i8gemm_workspace_size, ozaki2_i8linear_workspace_size); given
+ * the bytes of the size calls below, as many or more, they may cut a long k into more slices where there are few rows, which is faster.
  * Returns as ozaki2_i8gemm and ozaki2_i8linear with three more arguments: -1..-16 (the bias is never
  * invalid; -12 for a residual that shares memory with C), -17 for the workspace.
  */
@@ -491,12 +492,14 @@ enum ozaki2_activation {
 int ozaki2_i8gemm_act(int64_t t, int64_t n, int64_t k, const int8_t *A, int64_t lda, const float *a_scale, const int8_t *B,
                       int64_t ldb, const float *b_scale, const float *bias, int activation, const void *residual, int64_t ldr,
                       void *C, int64_t ldc, int ctype, void *stream);
+size_t ozaki2_i8gemm_act_workspace_size(int64_t t, int64_t n, int64_t k);
 int ozaki2_i8gemm_act_ws(int64_t t, int64_t n, int64_t k, const int8_t *A, int64_t lda, const float *a_scale, const int8_t *B,
                          int64_t ldb, const float *b_scale, const float *bias, int activation, const void *residual,
                          int64_t ldr, void *C, int64_t ldc, int ctype, void *workspace, size_t workspace_bytes, void *stream);
 int ozaki2_i8linear_act(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, int xtype, const int8_t *B, int64_t ldb,
                         const float *b_scale, const float *bias, int activation, const void *residual, int64_t ldr, void *C,
                         int64_t ldc, int ctype, void *stream);
+size_t ozaki2_i8linear_act_workspace_size(int64_t t, int64_t n, int64_t k);
 int ozaki2_i8linear_act_ws(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, int xtype, const int8_t *B, int64_t ldb,
                            const float *b_scale, const float *bias, int activation, const void *residual, int64_t ldr, void *C,
                            int64_t ldc, int ctype, void *workspace, size_t workspace_bytes, void *stream);

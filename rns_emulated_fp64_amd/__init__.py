@@ -43,6 +43,7 @@ EXPORTS = (
     "ozaki2_rmsnorm_quantize", "ozaki2_i8gemm_act", "ozaki2_i8gemm_act_ws", "ozaki2_i8linear_act", "ozaki2_i8linear_act_ws",
     "ozaki2_linear", "ozaki2_linear_ws", "ozaki2_linear_workspace_size", "ozaki2_linear_grad", "ozaki2_linear_grad_ws",
     "ozaki2_linear_grad_workspace_size", "ozaki2_sample", "ozaki2_sample_ws", "ozaki2_sample_workspace_size",
+    "ozaki2_i8gemm_act_workspace_size", "ozaki2_i8linear_act_workspace_size",
 )
 
 _lib = None
@@ -125,6 +126,8 @@ def lib() -> ctypes.CDLL:
     for name in ("ozaki2_i8gemm_act", "ozaki2_i8linear_act"):
         getattr(L, name).restype = i32
         getattr(L, name + "_ws").restype = i32
+        getattr(L, name + "_workspace_size").argtypes = [i64, i64, i64]
+        getattr(L, name + "_workspace_size").restype = sz
     for name in ("ozaki2_i8gemm", "ozaki2_i8linear"):
         getattr(L, name).restype = i32
         getattr(L, name + "_ws").restype = i32
@@ -367,6 +370,14 @@ def ozaki2_i8linear_act_ws(t, n, k, X, ldx, xtype, B, ldb, b_scale, bias, activa
                            workspace_bytes, stream=0) -> int:
     return lib().ozaki2_i8linear_act_ws(t, n, k, X, ldx, xtype, B, ldb, b_scale, bias, activation, residual, ldr, C, ldc, ctype,
                                         workspace, workspace_bytes, stream)
+
+
+def ozaki2_i8gemm_act_workspace_size(t, n, k) -> int:
+    return lib().ozaki2_i8gemm_act_workspace_size(t, n, k)
+
+
+def ozaki2_i8linear_act_workspace_size(t, n, k) -> int:
+    return lib().ozaki2_i8linear_act_workspace_size(t, n, k)
 
 
 def ozaki2_linear(t, n, k, X, ldx, W, ldw, type, bias, activation, residual, ldr, Y, ldy, ytype, Z, ldz, stream=0) -> int:
@@ -700,7 +711,8 @@ def i8gemm(A, B, a_scale, b_scale, bias=None, out_dtype=None, out=None, workspac
     B (n, k), the layout of a linear layer (ozaki2_i8gemm_ws; with an activation, a name from ACTIVATIONS, or a residual
     ozaki2_i8gemm_act_ws). The scales and the bias are float32; ``out_dtype`` is bfloat16 (default), float16 or
     float32; the residual has that dtype and shares no memory with ``out``; ``workspace`` (optional) a tensor of
-    ``ozaki2_i8gemm_workspace_size`` bytes."""
+    ``ozaki2_i8gemm_workspace_size`` bytes (with an activation or a residual ``ozaki2_i8gemm_act_workspace_size`` bytes are faster
+    for a few rows and a long k)."""
     torch = _torch or _load_torch()
     dt = out_dtype if out_dtype is not None else out.dtype if out is not None else torch.bfloat16
     ctype = _type_of(dt, "out_dtype")
@@ -720,13 +732,14 @@ def i8gemm(A, B, a_scale, b_scale, bias=None, out_dtype=None, out=None, workspac
         bias = _vector(bias, n, torch.float32, device, "bias")
     C, ldc = _product_out(t, n, dt, out, device, A)
     L = lib()
-    ws, wp, wb = _workspace(L.ozaki2_i8gemm_workspace_size(t, n, k), workspace, device)
     if act or residual is not None:
+        ws, wp, wb = _workspace(L.ozaki2_i8gemm_act_workspace_size(t, n, k), workspace, device)
         residual, rp, ldr = _residual(residual, t, n, dt, device)
         _call(L.ozaki2_i8gemm_act_ws, "ozaki2_i8gemm_act_ws", device, t, n, k, A.data_ptr(), lda, a_scale.data_ptr(),
               B.data_ptr(), ldb, b_scale.data_ptr(), None if bias is None else bias.data_ptr(), act, rp, ldr, C.data_ptr(), ldc,
               ctype, wp, wb)
         return C
+    ws, wp, wb = _workspace(L.ozaki2_i8gemm_workspace_size(t, n, k), workspace, device)
     _call(L.ozaki2_i8gemm_ws, "ozaki2_i8gemm_ws", device, t, n, k, A.data_ptr(), lda, a_scale.data_ptr(), B.data_ptr(),
           ldb, b_scale.data_ptr(), None if bias is None else bias.data_ptr(), C.data_ptr(), ldc, ctype, wp, wb)
     return C
@@ -756,12 +769,13 @@ def i8linear(X, B, b_scale, bias=None, out_dtype=None, out=None, workspace=None,
         bias = _vector(bias, n, torch.float32, device, "bias")
     C, ldc = _product_out(t, n, dt, out, device, X)
     L = lib()
-    ws, wp, wb = _workspace(L.ozaki2_i8linear_workspace_size(t, n, k), workspace, device)
     if act or residual is not None:
+        ws, wp, wb = _workspace(L.ozaki2_i8linear_act_workspace_size(t, n, k), workspace, device)
         residual, rp, ldr = _residual(residual, t, n, dt, device)
         _call(L.ozaki2_i8linear_act_ws, "ozaki2_i8linear_act_ws", device, t, n, k, X.data_ptr(), ldx, xtype, B.data_ptr(), ldb,
               b_scale.data_ptr(), None if bias is None else bias.data_ptr(), act, rp, ldr, C.data_ptr(), ldc, ctype, wp, wb)
         return C
+    ws, wp, wb = _workspace(L.ozaki2_i8linear_workspace_size(t, n, k), workspace, device)
     _call(L.ozaki2_i8linear_ws, "ozaki2_i8linear_ws", device, t, n, k, X.data_ptr(), ldx, xtype, B.data_ptr(), ldb,
           b_scale.data_ptr(), None if bias is None else bias.data_ptr(), C.data_ptr(), ldc, ctype, wp, wb)
     return C

@@ -140,19 +140,19 @@ int splits_of(int64_t t, int64_t n, int64_t k) {
     return tile_splits(choose_tile(ta, false), n, t, ta.kbytes);
 }
 int64_t plane_pitch(int64_t n) { return (n + 3) / 4 * 4; }
-size_t plane_bytes(int64_t t, int64_t n, int64_t k) {
-    // (with an activation or a residual as many as layer_splits says)
-    const int a = splits_of(t, n, k), b = layer_splits(t, n, k), s = a > b ? a : b;
+// layer: room for as many slices as layer_splits says too, which a product with an activation or a residual takes where it can.
+size_t plane_bytes(int64_t t, int64_t n, int64_t k, bool layer) {
+    const int a = splits_of(t, n, k), b = layer ? layer_splits(t, n, k) : 1, s = a > b ? a : b;
     return s > 1 ? up256((size_t)s * (size_t)t * (size_t)plane_pitch(n) * 4) : 0;
 }
 // Workspace of a product: packed rows of A (unless they are the library's own)
 // and of a run of B, and the planes. The last run has fewer channels than the
 // others, and with them more slices, whose planes can be the larger ones (256 x
 // 12100 x 8193: 1 slice of 12032 channels, 8 slices of 68).
-size_t product_bytes(int64_t t, int64_t n, int64_t k, bool own_a) {
-    if (!needs_pack(k, t)) return plane_bytes(t, n, k);
+size_t product_bytes(int64_t t, int64_t n, int64_t k, bool own_a, bool layer) {
+    if (!needs_pack(k, t)) return plane_bytes(t, n, k, layer);
     const int64_t run = pack_rows(n, k), rest = n % run;
-    const size_t full = plane_bytes(t, run, k), last = rest ? plane_bytes(t, rest, k) : 0;
+    const size_t full = plane_bytes(t, run, k, layer), last = rest ? plane_bytes(t, rest, k, layer) : 0;
     return (own_a ? 0 : up256((size_t)t * (size_t)pack_pitch(k))) + up256((size_t)run * (size_t)pack_pitch(k)) +
            (full > last ? full : last);
 }
@@ -176,6 +176,7 @@ struct Product {
     int act;
     const void *residual;  // of C's type, or null
     int64_t ldr;
+    bool layer;  // the workspace has room for layer_splits' slices
     bool finishes() const { return act != OZAKI2_ACT_NONE || residual != nullptr; }
 };
 
@@ -193,9 +194,11 @@ int product_rows(const Product &p, char *ws, hipStream_t s) {
     typedef EpiAct<OutT, void, true> Act;
     const typename Act::Args f = {(OutT *)p.C, p.ldc, p.b_scale, p.a_scale,
                                   {p.bias, p.act, (const OutT *)p.residual, p.ldr, nullptr, 0}, p.n, p.t};
-    const Tile tile = p.finishes() ? choose_layer_tile(ta) : choose_tile(ta, false);
+    // (random int8, residual: 37 x 4096 x 11008 15.9 us with layer_splits' tile and slices, 19.2 without; 48 x 8192 x 28672 49.2, 59.1;
+    // 64 x 5120 x 13824 24.3, 27.9; 24 x 4096 x 14336 17.7, 18.0; the same bits either way)
+    const Tile tile = p.layer ? choose_layer_tile(ta) : choose_tile(ta, false);
     const int splits = tile == Tile::skinny || tile == Tile::p8 ? 1
-                       : p.finishes()                           ? layer_splits(p.t, p.n, p.k)
+                       : p.layer                                ? layer_splits(p.t, p.n, p.k)
                                                                 : splits_of(p.t, p.n, p.k);
     if (splits == 1) {
         if (p.finishes())
@@ -315,6 +318,17 @@ int check_finish(int64_t t, int64_t n, int act, const void *residual, int64_t ld
 }
 int type_size(int type) { return type == OZAKI2_FP32 ? 4 : 2; }
 
+// Of a call's workspace: the bytes that it takes, of `least` without layer_splits' slices and `most` with them. The
+// cached workspace has as many as are wanted, a caller's as many as it has.
+struct Room {
+    size_t need;
+    bool layer;
+};
+Room room_of(bool finishes, size_t least, size_t most, bool cached, size_t bytes) {
+    const bool layer = finishes && (cached || bytes >= most);
+    return {layer ? most : least, layer};
+}
+
 struct GemmCall {
     int64_t t, n, k, lda, ldb, ldc;
     const int8_t *A, *B;
@@ -327,6 +341,8 @@ struct GemmCall {
     int act = OZAKI2_ACT_NONE;
     const void *residual = nullptr;
     int64_t ldr = 0;
+    bool layer = false;  // see Product
+    bool finishes() const { return act != OZAKI2_ACT_NONE || residual != nullptr; }
 };
 // The status of a call's arguments, from that of those that its plain form has too.
 template <class Call>
@@ -342,7 +358,8 @@ int checked(const Call &c, int st) {
 }
 int run_i8gemm(void *ctx, char *ws) {
     const GemmCall &c = *(const GemmCall *)ctx;
-    return product({c.t, c.n, c.k, c.A, c.lda, c.a_scale, c.B, c.ldb, c.b_scale, c.bias, c.C, c.ldc, c.act, c.residual, c.ldr},
+    return product({c.t, c.n, c.k, c.A, c.lda, c.a_scale, c.B, c.ldb, c.b_scale, c.bias, c.C, c.ldc, c.act, c.residual, c.ldr,
+                    c.layer},
                    false, c.ctype, ws, c.s);
 }
 int front_i8gemm(GemmCall c, bool cached, void *workspace, size_t bytes) {
@@ -350,11 +367,14 @@ int front_i8gemm(GemmCall c, bool cached, void *workspace, size_t bytes) {
     if (st) return st;
     if (!fits(c.t, c.n, c.k)) return OZAKI2_ERR_UNSUPPORTED;
     if (c.t == 0 || c.n == 0) return OZAKI2_SUCCESS;
-    const size_t need = product_bytes(c.t, c.n, c.k, false);
-    if (need == 0) return run_i8gemm(&c, nullptr);
-    if (cached) return with_workspace(need, c.s, run_i8gemm, &c);
+    const Room r = room_of(c.finishes(), product_bytes(c.t, c.n, c.k, false, false),
+                           c.finishes() ? product_bytes(c.t, c.n, c.k, false, true) : 0, cached,
+                           workspace != nullptr ? bytes : 0);
+    c.layer = r.layer;
+    if (r.need == 0) return run_i8gemm(&c, nullptr);
+    if (cached) return with_workspace(r.need, c.s, run_i8gemm, &c);
     if (workspace == nullptr || ((uintptr_t)workspace & (kWsAlign - 1)) != 0) return c.acts ? -17 : -14;
-    if (bytes < need) return OZAKI2_ERR_WORKSPACE;
+    if (bytes < r.need) return OZAKI2_ERR_WORKSPACE;
     return run_i8gemm(&c, (char *)workspace);
 }
 
@@ -389,17 +409,19 @@ struct LinearCall {
     int act = OZAKI2_ACT_NONE;
     const void *residual = nullptr;
     int64_t ldr = 0;
+    bool layer = false;  // see Product
+    bool finishes() const { return act != OZAKI2_ACT_NONE || residual != nullptr; }
 };
 // Workspace of ozaki2_i8linear: the quantised rows, their scales, the product's own.
 int64_t q_pitch(int64_t k) { return pack_pitch(k); }
 size_t q_bytes(int64_t t, int64_t k) { return up256((size_t)t * (size_t)q_pitch(k)); }
-size_t i8linear_bytes(int64_t t, int64_t n, int64_t k) {
+size_t i8linear_bytes(int64_t t, int64_t n, int64_t k, bool layer) {
     if (quantises_in_product(t, k)) return 0;
-    return q_bytes(t, k) + up256(4 * (size_t)t) + product_bytes(t, n, k, true);
+    return q_bytes(t, k) + up256(4 * (size_t)t) + product_bytes(t, n, k, true, layer);
 }
 int run_i8linear(void *ctx, char *ws) {
     const LinearCall &c = *(const LinearCall *)ctx;
-    Product p = {c.t, c.n, c.k, nullptr, 0, nullptr, c.B, c.ldb, c.b_scale, c.bias, c.C, c.ldc, c.act, c.residual, c.ldr};
+    Product p = {c.t, c.n, c.k, nullptr, 0, nullptr, c.B, c.ldb, c.b_scale, c.bias, c.C, c.ldc, c.act, c.residual, c.ldr, c.layer};
     if (quantises_in_product(c.t, c.k)) {
         HIP_TRY(few_rows(p, c.X, c.ldx, c.xtype, c.ctype, c.s));
         return OZAKI2_SUCCESS;
@@ -418,11 +440,14 @@ int front_i8linear(LinearCall c, bool cached, void *workspace, size_t bytes) {
     if (st) return st;
     if (!fits(c.t, c.n, c.k)) return OZAKI2_ERR_UNSUPPORTED;
     if (c.t == 0 || c.n == 0) return OZAKI2_SUCCESS;
-    const size_t need = i8linear_bytes(c.t, c.n, c.k);
-    if (need == 0) return run_i8linear(&c, nullptr);
-    if (cached) return with_workspace(need, c.s, run_i8linear, &c);
+    const Room r = room_of(c.finishes(), i8linear_bytes(c.t, c.n, c.k, false),
+                           c.finishes() ? i8linear_bytes(c.t, c.n, c.k, true) : 0, cached,
+                           workspace != nullptr ? bytes : 0);
+    c.layer = r.layer;
+    if (r.need == 0) return run_i8linear(&c, nullptr);
+    if (cached) return with_workspace(r.need, c.s, run_i8linear, &c);
     if (workspace == nullptr || ((uintptr_t)workspace & (kWsAlign - 1)) != 0) return c.acts ? -17 : -14;
-    if (bytes < need) return OZAKI2_ERR_WORKSPACE;
+    if (bytes < r.need) return OZAKI2_ERR_WORKSPACE;
     return run_i8linear(&c, (char *)workspace);
 }
 
@@ -457,7 +482,12 @@ int ozaki2_i8gemm(int64_t t, int64_t n, int64_t k, const int8_t *A, int64_t lda,
 
 size_t ozaki2_i8gemm_workspace_size(int64_t t, int64_t n, int64_t k) {
     if (t <= 0 || n <= 0 || k < 0 || !fits(t, n, k)) return 0;
-    return product_bytes(t, n, k, false);
+    return product_bytes(t, n, k, false, false);
+}
+
+size_t ozaki2_i8gemm_act_workspace_size(int64_t t, int64_t n, int64_t k) {
+    if (t <= 0 || n <= 0 || k < 0 || !fits(t, n, k)) return 0;
+    return product_bytes(t, n, k, false, true);
 }
 
 int ozaki2_i8gemm_ws(int64_t t, int64_t n, int64_t k, const int8_t *A, int64_t lda, const float *a_scale,
@@ -475,7 +505,12 @@ int ozaki2_i8linear(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx,
 
 size_t ozaki2_i8linear_workspace_size(int64_t t, int64_t n, int64_t k) {
     if (t <= 0 || n <= 0 || k < 0 || !fits(t, n, k)) return 0;
-    return i8linear_bytes(t, n, k);
+    return i8linear_bytes(t, n, k, false);
+}
+
+size_t ozaki2_i8linear_act_workspace_size(int64_t t, int64_t n, int64_t k) {
+    if (t <= 0 || n <= 0 || k < 0 || !fits(t, n, k)) return 0;
+    return i8linear_bytes(t, n, k, true);
 }
 
 int ozaki2_i8linear_ws(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx, int xtype, const int8_t *B,
