@@ -485,7 +485,8 @@ int ozaki2_i8linear_ws(int64_t t, int64_t n, int64_t k, const void *X, int64_t l
 enum ozaki2_activation {
     OZAKI2_ACT_NONE = 0,
     OZAKI2_ACT_RELU = 1,      /* max(z, 0) */
-    OZAKI2_ACT_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2, the factor of z off by 4e-7 at most */
+    OZAKI2_ACT_GELU = 2,      /* z (1 + erf(z / sqrt 2)) / 2, the factor of z off by 4e-7 at most, and for z above -13 by
+                                 1e-6 of itself (in 16-bit outputs 5e-5, a tenth of fp16's half step) */
     OZAKI2_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
     OZAKI2_ACT_SILU = 4       /* z / (1 + exp(-z)) */
 };                            /* (the last three give NaN for -inf) */

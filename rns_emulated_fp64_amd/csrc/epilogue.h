@@ -18,30 +18,55 @@ constexpr bool is_activation(int act) { return act >= OZAKI2_ACT_NONE && act <= 
 __device__ __forceinline__ float sigmoid(float x) {
     return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-kLog2e * x));
 }
-// The two parts of the normal distribution's function at z: below min(z, -z), and exp(-z^2 / 2).
-// erfc(x) = t (a1 + .. + a5 t^4) exp(-x^2), t = 1 / (1 + p x), by Abramowitz and
-// Stegun, Handbook of Mathematical Functions, 7.1.26: off by 1.5e-7 at most, and less
-// where the exponential is small.
+// Phi(-|z|), Phi the normal distribution's function, and exp(-z^2 / 2), with errors relative to themselves, since gelu's own values in the tail
+// are as small: Phi(-|z|) = erfc(x) / 2 = t P(t) exp(-x^2), x = |z| / sqrt 2, t = 1 / (1 + p x), P a polynomial whose largest weighted error for
+// x up to 9.7, where the exponential leaves binary32, is least (least squares, reweighted by the errors: Lawson's method).
+//   FINE, for 32-bit results: degree 7, off by 9e-8 of itself, and the roundings of the exponential's argument put back (7e-6
+//     of it at z = -12): 1e-6 of itself at most.
+//   Otherwise, for 16-bit results and slopes: degree 5, off by 1.5e-7 and by 3e-5 of itself, a sixteenth of fp16's half step (8192 x
+//     14336 x 4096, bf16: 711 us, with FINE 752; its gradients' G: 125 us against 140).
+template <bool FINE>
 __device__ __forceinline__ float normal_tail(float z, float &bell) {
-    const float x = fabsf(z);
-    const float t = __builtin_amdgcn_rcpf(fmaf(0.3275911f * 0.70710678f, x, 1.f));
-    float p = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
-    p = fmaf(t, p, 0.5f * 1.421413741f);
-    p = fmaf(t, p, 0.5f * -0.284496736f);
-    p = fmaf(t, p, 0.5f * 0.254829592f);
-    bell = __builtin_amdgcn_exp2f(z * z * (-0.5f * kLog2e));
+    constexpr float kP = (FINE ? 0.43f : 0.42f) * 0.70710678f;
+    constexpr float kArg = -0.5f * kLog2e, kArgRest = -9.62981494545945e-09f;  // -log2(e) / 2 in two parts
+    const float t = __builtin_amdgcn_rcpf(fmaf(kP, fabsf(z), 1.f));
+    float p;
+    if constexpr (FINE) {
+        p = fmaf(t, 0.0367676876f, -0.154837146f);
+        p = fmaf(t, p, 0.19126673f);
+        p = fmaf(t, p, -0.0423372537f);
+        p = fmaf(t, p, 0.123150863f);
+        p = fmaf(t, p, 0.102555946f);
+        p = fmaf(t, p, 0.122175097f);
+        p = fmaf(t, p, 0.12125811f);
+    } else {
+        p = fmaf(t, -0.0818484873f, 0.238672853f);
+        p = fmaf(t, p, -0.040130157f);
+        p = fmaf(t, p, 0.153957814f);
+        p = fmaf(t, p, 0.110308036f);
+        p = fmaf(t, p, 0.119039789f);
+    }
+    const float square = z * z, arg = square * kArg;
+    bell = __builtin_amdgcn_exp2f(arg);
+    if constexpr (FINE) {
+        // (past where the exponential is 0 there is nothing to put back, and infinities are no numbers there)
+        float rest = fmaf(square, kArg, -arg);
+        rest = fmaf(fmaf(z, z, -square), kArg, rest);
+        rest = fmaf(square, kArgRest, rest);
+        bell = bell > 0.f ? fmaf(bell, kLn2 * rest, bell) : bell;
+    }
     return t * p * bell;
 }
 constexpr float kTanhScale = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kTanhCubic = 0.044715f;
 
-// act(z). -inf gives NaN for the last three, as z times 0 does.
-template <int ACT>
+// act(z). -inf gives NaN for the last three, as z times 0 does. FINE: see normal_tail.
+template <int ACT, bool FINE>
 __device__ __forceinline__ float activated(float z) {
     if constexpr (ACT == OZAKI2_ACT_RELU) return z < 0.f ? 0.f : z;
     if constexpr (ACT == OZAKI2_ACT_GELU) {
         float bell;
-        const float tail = normal_tail(z, bell);
+        const float tail = normal_tail<FINE>(z, bell);
         return z * (z > 0.f ? 1.f - tail : tail);
     }
     // (1 + tanh u) / 2 = sigmoid(2 u)
@@ -57,7 +82,7 @@ __device__ __forceinline__ float slope_of(float z) {
     if constexpr (ACT == OZAKI2_ACT_RELU) return z > 0.f ? 1.f : z <= 0.f ? 0.f : z;
     if constexpr (ACT == OZAKI2_ACT_GELU) {
         float bell;
-        const float tail = normal_tail(z, bell);
+        const float tail = normal_tail<false>(z, bell);
         return fmaf(near, 0.3989422804f * bell, z > 0.f ? 1.f - tail : tail);
     }
     if constexpr (ACT == OZAKI2_ACT_GELU_TANH || ACT == OZAKI2_ACT_SILU) {
@@ -86,13 +111,13 @@ __device__ __forceinline__ void with_activation(int act, Body body) {
 
 // act of each x; ACT: which, or kAnyActivation: `act` says.
 constexpr int kAnyActivation = -1;
-template <int ACT, int N>
+template <int ACT, bool FINE, int N>
 __device__ __forceinline__ void activate(int act, float (&x)[N][4]) {
     auto all = [&](auto a) {
 #pragma unroll
         for (int h = 0; h < N; ++h)
 #pragma unroll
-            for (int v = 0; v < 4; ++v) x[h][v] = activated<decltype(a)::value>(x[h][v]);
+            for (int v = 0; v < 4; ++v) x[h][v] = activated<decltype(a)::value, FINE>(x[h][v]);
     };
     if constexpr (ACT == kAnyActivation)
         with_activation(act, all);
@@ -194,7 +219,7 @@ struct EpiAct {
                 for (int v = 0; v < 4; ++v) x[v] = before(acc[0][j][v], j, sa[v], bi[v]);
                 if constexpr (!std::is_void_v<PreT>)
                     if (e.f.pre) store_four(e.f.pre + b * e.f.ldpre + a0, x, left);
-                activate<ACT>(e.f.act, y);
+                activate<ACT, sizeof(OutT) == 4>(e.f.act, y);
                 if (e.f.residual) {
                     const OutT *r = e.f.residual + b * e.f.ldr + a0;
 #pragma unroll
@@ -246,7 +271,7 @@ struct EpiAct {
                         if (e.f.pre)
                             store_pair<PreT, EDGE>(x, e.f.pre + b * e.f.ldpre, w.a0 + pair_start<PreT>(lane) + 16 * i, e.na,
                                                    b < e.nb);
-                    activate<ACT>(e.f.act, x);
+                    activate<ACT, sizeof(OutT) == 4>(e.f.act, x);
                     if (e.f.residual) {
                         if constexpr (RW == 1) {
                             // trade_pair's exchange is its own inverse
@@ -322,7 +347,7 @@ __global__ __launch_bounds__(256) void k_join_act(const uint32_t *__restrict__ p
                     x = s[v] + bias;
                 if constexpr (!std::is_void_v<PreT>)
                     if (e.f.pre) e.f.pre[b * e.f.ldpre + a + v] = rounded<PreT>(x);
-                x = activated<decltype(act)::value>(x);
+                x = activated<decltype(act)::value, sizeof(OutT) == 4>(x);
                 if (e.f.residual) x += (float)e.f.residual[b * e.f.ldr + a + v];
                 e.out[b * e.ldo + a + v] = rounded<OutT>(x);
             }
