@@ -13,6 +13,7 @@
 
 #include "common.h"
 #include "epilogue.h"
+#include "lanes.h"
 #include "ozaki2.h"
 
 namespace oz2 {
@@ -130,12 +131,13 @@ int forward(const LinearArgs &p, char *ws, hipStream_t s) {
 }
 
 // ---- backward ---------------------------------------------------------------------
-// out[b][a] = round(R).
+// out[b][a] = round(R * *unit).
 template <class OutT>
 struct EpiRound {
     struct Args {
         OutT *out;
         int64_t ldo;
+        const float *unit;  // of G (see k_act_grad), or null: 1
         int64_t na, nb;
     };
     static constexpr int STORES = 1;
@@ -145,6 +147,7 @@ struct EpiRound {
     static __device__ __forceinline__ void run(v4i (&acc)[RT][CT], const TileWhere &w, const Args &e) {
         const int lane = fresh_lane();
         const int64_t st0 = w.a0 + pair_start<OutT>(lane), b0 = w.b0 + (lane & 15);
+        const float unit = M::HALF && e.unit != nullptr ? *e.unit : 1.f;
 #pragma unroll
         for (int i = 0; i < RT; i += 2)
 #pragma unroll
@@ -155,7 +158,8 @@ struct EpiRound {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) x[h][v] = M::value(acc[i + h][j][v]);
+                    for (int v = 0; v < 4; ++v)
+                        x[h][v] = M::HALF ? M::value(acc[i + h][j][v]) * unit : M::value(acc[i + h][j][v]);
                 const int64_t b = b0 + 16 * j;
                 store_pair<OutT, EDGE>(x, e.out + b * e.ldo, st0 + 16 * i, e.na, b < e.nb);
                 __builtin_amdgcn_sched_barrier(0);
@@ -165,7 +169,10 @@ struct EpiRound {
 
 // G = dY act'(Z) in 16 bits, rounded once, half a step relative (dY's own precision),
 // and the sums of its columns in binary32 over a slab of rows, before that
-// rounding. A block takes 512 columns, a lane 8 of them, a wavefront every fourth row of the slab; where there are fewer
+// rounding. In fp16, whose range is small, G is in units of a power of two in which the largest finite |dY| is 2^14 to 2^15 (slopes
+// reach 1.13): small gradients keep their bits (of a dY of 1e-5 times a slope of 1e-2 one is left without), and none overflows where dX
+// does not. The products' sums are multiplied by the unit before they are rounded. That takes a pass over dY first, k_grad_top (509 x 2051 x 768: 36.6
+// us with it, 31.5 without; 8192 x 14336 x 4096: 1685 and 1637). A block takes 512 columns, a lane 8 of them, a wavefront every fourth row of the slab; where there are fewer
 // columns a wavefront takes several rows at once, `across` lanes each (a power of two). Columns of G up to the
 // next multiple of 8 are zeros. Memory bound (8192 x 14336, bf16: 142 us or 5.0 TB/s).
 template <class T>
@@ -181,8 +188,47 @@ struct GradArgs {
     int64_t ldsum;
     int64_t t, n, slab;  // rows of a slab
     int across;
+    const uint32_t *tops;  // k_grad_top's results, or null: the unit is 1
+    int ntops;
+    float *unit;
 };
 constexpr int kGradCols = 512;
+// The largest x of a block of 256 threads. Ends behind a barrier.
+__device__ __forceinline__ uint32_t block_max(uint32_t x) {
+    __shared__ uint32_t top[4];
+    x = wave_max(x);
+    if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = x;
+    __syncthreads();
+    return max(max(top[0], top[1]), max(top[2], top[3]));
+}
+// The largest finite |dY| of a block's slab and columns, as bits of a binary32; a grid as k_act_grad's. (An infinite or NaN entry, whose
+// results are so too, does not set the unit of the others.)
+template <class T>
+__global__ __launch_bounds__(256) void k_grad_top(GradArgs<T> p, uint32_t *tops) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int64_t c = (int64_t)blockIdx.x * kGradCols + 8 * (lane & (p.across - 1));
+    const int rows = 64 / p.across;
+    const int64_t r0 = (int64_t)blockIdx.y * p.slab, r1 = min(r0 + p.slab, p.t);
+    uint32_t m = 0;
+    constexpr int U = 4;
+    for (int64_t r = r0 + wave * rows + lane / p.across; r < r1; r += 4 * U * rows) {
+        float g[U][8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t at = r + 4 * u * rows;
+            load8(p.dY + at * p.lddy, at < r1 ? c : p.n, p.n, g[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t b = abs_bits(g[u][i]);
+                m = max(m, b < 0x7f800000u ? b : 0);
+            }
+    }
+    m = block_max(m);
+    if (threadIdx.x == 0) tops[(int64_t)blockIdx.y * gridDim.x + blockIdx.x] = m;
+}
 template <class T>
 __global__ __launch_bounds__(256) void k_act_grad(GradArgs<T> p) {
     __shared__ float part[3][kGradCols];
@@ -191,6 +237,15 @@ __global__ __launch_bounds__(256) void k_act_grad(GradArgs<T> p) {
     const int rows = 64 / p.across;  // of a wavefront at once; this lane's is `row`
     const int64_t row = lane / p.across;
     const int64_t r0 = (int64_t)blockIdx.y * p.slab, r1 = min(r0 + p.slab, p.t);
+    float up = 1.f;
+    if (p.tops != nullptr) {
+        uint32_t m = 0;
+        for (int i = threadIdx.x; i < p.ntops; i += 256) m = max(m, p.tops[i]);
+        m = block_max(m);
+        const float unit = m != 0 ? __uint_as_float((m & 0x7f800000u) - (14u << 23)) : 1.f;
+        up = 1.f / unit;  // exact
+        if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.unit = unit;
+    }
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     with_activation(p.act, [&](auto act) {
         constexpr int U = 4;  // of a lane's rows on their way at a time
@@ -210,6 +265,7 @@ __global__ __launch_bounds__(256) void k_act_grad(GradArgs<T> p) {
                 for (int i = 0; i < 8; ++i) {
                     if constexpr (decltype(act)::value != OZAKI2_ACT_NONE) g[u][i] *= slope_of<decltype(act)::value>(z[u][i]);
                     sum[i] += g[u][i];
+                    if constexpr (std::is_same_v<T, _Float16>) g[u][i] *= up;
                 }
                 if (p.G && at < r1 && c < p.n) {
                     const U16 o = {{pack2<T>(g[u][0], g[u][1]), pack2<T>(g[u][2], g[u][3]), pack2<T>(g[u][4], g[u][5]),
@@ -251,6 +307,7 @@ struct Planes {
     int64_t plane, ldp;
     T *out;
     int64_t ldo, na, nb;
+    const float *unit;  // of G, or null: 1
     int across;  // blocks of a row
 };
 template <class T>
@@ -279,6 +336,7 @@ __global__ __launch_bounds__(256) void k_join_both(Columns c, Planes<T> p) {
     const int block = (int)blockIdx.x - c.blocks, rows = ((int)gridDim.x - c.blocks) / p.across;
     const int64_t a = 4 * ((int64_t)(block % p.across) * 256 + threadIdx.x);
     if (a >= p.na) return;
+    const float unit = p.unit != nullptr ? *p.unit : 1.f;
     for (int64_t b = block / p.across; b < p.nb; b += rows) {
         const float *from = p.planes + b * p.ldp + a;
         v4f s = *(const v4f *)from;
@@ -293,7 +351,7 @@ __global__ __launch_bounds__(256) void k_join_both(Columns c, Planes<T> p) {
         for (; i < p.splits; ++i) s += *(const v4f *)(from + i * p.plane);
 #pragma unroll
         for (int v = 0; v < 4; ++v)
-            if (a + v < p.na) p.out[b * p.ldo + a + v] = rounded<T>(s[v]);
+            if (a + v < p.na) p.out[b * p.ldo + a + v] = rounded<T>(s[v] * unit);
     }
 }
 template <class T>
@@ -330,7 +388,7 @@ struct GradPlan {
     int slabs;
     int64_t slab;
     int dx_splits, dw_splits;
-    size_t sums, g, x, w, planes, total;
+    size_t sums, tops, unit, g, x, w, planes, total;
 };
 GradPlan plan_grad(int64_t t, int64_t n, int64_t k, bool dx, bool dw, bool db) {
     GradPlan p{};
@@ -358,7 +416,9 @@ GradPlan plan_grad(int64_t t, int64_t n, int64_t k, bool dx, bool dw, bool db) {
         return at;
     };
     p.sums = take(db ? 4 * (size_t)p.slabs * (size_t)n : 0);
-    // (sizes alone do not say what is aligned)
+    // (sizes alone do not say what is aligned, nor that the type is fp16)
+    p.tops = take(dx || dw ? 4 * (size_t)p.slabs * (size_t)cols : 0);
+    p.unit = take(dx || dw ? 4 : 0);
     p.g = take(dx || dw ? 2 * (size_t)t * (size_t)pitch16(n) : 0);
     p.x = take(dw ? 2 * (size_t)t * (size_t)pitch16(k) : 0);
     p.w = take(dx ? 2 * (size_t)n * (size_t)pitch16(k) : 0);
@@ -391,20 +451,20 @@ bool kmajor_ready(const void *p, int64_t ld, int64_t cols) {
     return (((uintptr_t)p | (uintptr_t)(2 * ld) | (uintptr_t)(2 * cols)) & 15) == 0 && 2 * ld < (1 << 24);
 }
 
-// R[b][a] over krows rows of k, rounded to T, or its planes, which `planes` then describes for join_both.
+// R[b][a] *unit over krows rows of k, rounded to T, or its planes, which `planes` then describes for join_both.
 template <class M, bool KB>
-int kmajor_product(TileArgs ta, int64_t krows, int splits, void *out, int64_t ldo, char *ws, Planes<typename M::Elem> &planes,
-                   hipStream_t s) {
+int kmajor_product(TileArgs ta, int64_t krows, int splits, void *out, int64_t ldo, const float *unit, char *ws,
+                   Planes<typename M::Elem> &planes, hipStream_t s) {
     typedef typename M::Elem T;
     ta.krows = (int)krows;
     planes = {};
     if (splits == 1) {
-        HIP_TRY((launch_kmajor<M, EpiRound<T>, true, KB>(ta, {(T *)out, ldo, ta.na, ta.nb}, 1, s)));
+        HIP_TRY((launch_kmajor<M, EpiRound<T>, true, KB>(ta, {(T *)out, ldo, unit, ta.na, ta.nb}, 1, s)));
         return OZAKI2_SUCCESS;
     }
     const int64_t ldp = plane_pitch(ta.na), plane = ta.nb * ldp;
     HIP_TRY((launch_kmajor<M, EpiRaw, true, KB>(ta, {(uint32_t *)ws, ldp, plane, ta.na, ta.nb}, splits, s)));
-    planes = {(const float *)ws, splits, plane, ldp, (T *)out, ldo, ta.na, ta.nb, 0};
+    planes = {(const float *)ws, splits, plane, ldp, (T *)out, ldo, ta.na, ta.nb, unit, 0};
     return OZAKI2_SUCCESS;
 }
 
@@ -421,6 +481,7 @@ int backward(const GradCallArgs &c, char *ws, hipStream_t s) {
     const GradPlan p = plan_grad(c.t, c.n, c.k, dx, dw, db);
     const void *g = c.dY;
     int64_t ldg = c.lddy;
+    const float *unit = nullptr;  // of G
     const bool makes_g = (dx || dw) && (c.act != OZAKI2_ACT_NONE || !kmajor_ready(c.dY, c.lddy, c.n));
     if (makes_g) {
         g = ws + p.g;
@@ -428,9 +489,18 @@ int backward(const GradCallArgs &c, char *ws, hipStream_t s) {
     }
     if (makes_g || db) {
         const dim3 grid((unsigned)((c.n + kGradCols - 1) / kGradCols), (unsigned)p.slabs);
-        hipLaunchKernelGGL((k_act_grad<T>), grid, dim3(256), 0, s,
-                           GradArgs<T>{(const T *)c.dY, c.lddy, (const T *)c.Z, c.ldz, c.act, makes_g ? (T *)g : nullptr, ldg,
-                                       db ? (float *)(ws + p.sums) : nullptr, c.n, c.t, c.n, p.slab, p.across});
+        GradArgs<T> a = {(const T *)c.dY, c.lddy, (const T *)c.Z, c.ldz, c.act, makes_g ? (T *)g : nullptr, ldg,
+                         db ? (float *)(ws + p.sums) : nullptr, c.n, c.t, c.n, p.slab, p.across, nullptr, 0, nullptr};
+        // (relu's slopes, and none, leave dY's own values)
+        if constexpr (M::HALF)
+            if (makes_g && c.act != OZAKI2_ACT_NONE && c.act != OZAKI2_ACT_RELU) {
+                a.tops = (const uint32_t *)(ws + p.tops);
+                a.ntops = (int)(grid.x * grid.y);
+                unit = a.unit = (float *)(ws + p.unit);
+                hipLaunchKernelGGL((k_grad_top<T>), grid, dim3(256), 0, s, a, (uint32_t *)(ws + p.tops));
+                HIP_TRY(hipGetLastError());
+            }
+        hipLaunchKernelGGL((k_act_grad<T>), grid, dim3(256), 0, s, a);
         HIP_TRY(hipGetLastError());
     }
     Columns columns = {};
@@ -456,14 +526,14 @@ int backward(const GradCallArgs &c, char *ws, hipStream_t s) {
     if (dx) {
         // rows of W as the rows of k; G's columns past n are zeros
         const int st = kmajor_product<M, false>(rows_of(c.t, c.k, (c.n + 7) / 8 * 8, g, ldg, w, ldw), c.n, p.dx_splits, c.dX,
-                                                c.lddx, ws + p.planes, planes, s);
+                                                c.lddx, unit, ws + p.planes, planes, s);
         if (st) return st;
     }
     HIP_TRY(join_both(columns, planes, s));
     if (dw) {
         // rows of X and of G as the rows of k
         const int st = kmajor_product<M, true>(rows_of(c.n, c.k, c.t, g, ldg, x, ldx), c.t, p.dw_splits, c.dW, c.lddw,
-                                               ws + p.planes, planes, s);
+                                               unit, ws + p.planes, planes, s);
         if (st) return st;
         HIP_TRY(join_both(Columns{}, planes, s));
     }
