@@ -1235,7 +1235,7 @@ hipError_t launch_skinny(const TileArgs &t, const typename Epi::Args &e, const t
     } else {
         if (bt <= 1) {
             if (few)
-                go(k_skinny<M, Epi, 1, 1, 16, 4 * M::BYTES, Src>, 1, 1, 16, 0);
+                go(k_skinny<M, Epi, 1, 1, 16, 4, Src>, 1, 1, 16, 0);
             else
                 go(k_skinny<M, Epi, 1, 1, 4, 4, Src>, 1, 1, 4, 0);
         } else if (bt == 2) {
