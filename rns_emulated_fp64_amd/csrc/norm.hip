@@ -219,12 +219,13 @@ __global__ __launch_bounds__(THREADS) void k_rmsnorm_quantize(NormArgs<T> p) {
 
 // The fewest threads whose registers hold a row, with one vector each for few rows (latency: 1 x 4096, bf16: 3.9 us with 512
 // threads, 4.2 with 256 of two vectors) and two for many (fewer wavefronts to join: 4096 x 4096, bf16: 25.1 us with 256
-// threads, 28.4 with 512, 1024 threads of one vector 47, operands in the caches; from memory 27.5 or 4.3 TB/s). As many blocks as
-// run at once, which go on to further rows.
+// threads, 28.4 with 512, 1024 threads of one vector 47, operands in the caches; from memory 27.5 or 4.3 TB/s). As many wavefronts as
+// fit on a whole MI355X at most, in blocks that go on to further rows (65536 x 128, bf16: 41 us with 8192 blocks of one wavefront, 59 with
+// 2048; 65536 x 512 45 and 59).
 template <class T>
 hipError_t launch_rmsnorm(const NormArgs<T> &p, hipStream_t s) {
     auto go = [&](auto kern, int threads) {
-        const int64_t most = threads > 256 ? 1024 : 2048;
+        const int64_t most = (1 << 19) / threads;
         hipLaunchKernelGGL(kern, dim3((unsigned)(p.rows < most ? p.rows : most)), dim3(threads), 0, s, p);
     };
     if (p.k <= 512)
