@@ -1014,12 +1014,19 @@ __global__ __launch_bounds__(kThreads) void k_sample_draw(SampleArgs p, RowState
 }
 
 // ---- launches ------------------------------------------------------------------------------
-// Whether a row is spread over blocks: where one compute unit would take longer for it than the launches that this needs
-// (bf16, one launch against four, us: 1 x 128000: 51 against 22 without filters, 81 against 57 with top_p; 128 x 128000: 56 against
-// 42, 85 against 81, but with top_k 35 against 40; 37 x 32000: 21 against 21, 40 against 48, 18 against 28).
-bool spreads(int64_t t, int64_t v) { return t <= 96 && v > 65536; }
+// Whether a row is spread over blocks: where one compute unit would take longer for it than the launches that this needs. One launch
+// against four, us, without filters, with top_k and top_p, with top_p alone, bf16 (fp32 much the same to 64 rows, at 96 four
+// launches take 2 to 13 more):
+//    3 x  70000: 32 : 18, 23 : 27, 57 : 52      3 x 128000: 50 : 20, 32 : 28, 78 : 52
+//   48 x  70000: 32 : 21, 23 : 28, 58 : 56     60 x  70000: 32 : 23, 23 : 31, 59 : 59     96 x 70000: 33 : 29, 23 : 33, 58 : 68
+//   64 x 100000: 43 : 26, 28 : 32, 67 : 57     96 x 100000: 43 : 34, 28 : 36, 67 : 69    128 x 100000: 45 : 36, 30 : 38, 70 : 71
+//   96 x 128000: 51 : 38, 33 : 38, 80 : 75     96 x 200000: 77 : 53, 47 : 47, 116 : 102
+//    8 x  65536: 28 : 18, 22 : 27, 53 : 51      8 x  32000: 18 : 17, 17 : 27, 35 : 43
+bool spreads(int64_t t, int64_t v) { return t <= 96 && v > (t <= 48 ? 65536 : 98304); }
+// Blocks of a row: all rows' together no more than compute units (48 x 128000, top_p: 58 us with 5 each, 65 with 6), so that none waits for
+// another.
 int chunks_of(int64_t t, int64_t v) {
-    int64_t c = (kPlanUnits + t - 1) / t;
+    int64_t c = kPlanUnits / t;
     const int64_t most = (v + 8191) / 8192;
     if (c > most) c = most;
     return (int)(c < 1 ? 1 : c > kMostChunks ? kMostChunks : c);
