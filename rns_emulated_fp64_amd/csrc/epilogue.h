@@ -364,8 +364,9 @@ hipError_t launch_join_act(const void *planes, int splits, int64_t plane, int64_
 
 // The tile of a layer's product, which may be cut into slices of k: choose_tile's, or a larger one in slices where that is
 // expected to take a tenth less (a few rows and a long k: bf16, 37 x 4096 x 11008: 22.3 us with 4 slices of 64 x 64 tiles against
-// 28.4 with 32 x 32 ones), or 64 x 64 ones that are a few more than compute units (fp16, 509 x 2051 x 768: 264 of them 9.4 us, 136
-// of 128 x 64 11.2).
+// 28.4 with 32 x 32 ones), or 64 x 64 ones that are up to a tenth more than compute units (fp16, against as many 128 x 64 ones as there
+// are then, us: 264 tiles, 509 x 2051 x 768 8.0 : 9.1, x 2048 13.4 : 15.7, 384 x 2816 x 4096 23.0 : 25.5; 272, 1024 x 1080 x 768 7.2 : 8.2;
+// 280, 512 x 2240 x 768 7.1 : 8.2, 512 x 2200 x 1024 8.2 : 9.7; at 297, 520 x 2112 x 768, 8.2 and 8.3).
 inline double product_us(Tile tile, int64_t na, int64_t nb, int64_t kbytes) {
     const int s = tile_splits(tile, na, nb, kbytes);
     const int64_t rounds = (kbytes + 127) / 128;

@@ -7,7 +7,7 @@ U32 = 2.0 ** -24  # half a step of binary32, relative
 HALF = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}  # half a step relative to the value
 TINY = {torch.bfloat16: 2.0 ** -134, torch.float16: 2.0 ** -25, torch.float32: 2.0 ** -150}  # half the subnormal step
 NAMES = ["none", "relu", "gelu", "gelu_tanh", "silu"]
-#: The factor of z in gelu and its slope: 1.5e-7 of the published formula, halved, and about a dozen roundings of values
+#: The factor of z in gelu and its slope: 1.5e-7 of its polynomial, and about a dozen roundings of values
 #: below 1 in its series, reciprocal and exponential.
 GELU = 4e-7
 

@@ -49,7 +49,7 @@ def check(got, want, has_sum=True):
         assert got[2] is None
 
 
-# every kernel: 64, 256 (one and two vectors) and 1024 threads, rows longer than the registers, more rows than blocks
+# kernels of 64, 256 and 512 threads, rows longer than the registers
 SIZES = [(1, 1), (3, 7), (2, 64), (5, 511), (4, 513), (1, 2048), (300, 2049), (257, 4096), (7, 4096), (2, 8191), (3, 8193),
          (2, 16384), (3, 16391), (2, 50000), (2300, 130), (4100, 33)]
 

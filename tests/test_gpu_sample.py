@@ -57,7 +57,7 @@ def inputs(t, v, dtype, seed, spread=2.0):
     return z.to(dtype), torch.rand(t, generator=g, device="cuda", dtype=torch.float64)
 
 
-# one block per row and several, ragged ends, rows that fit the list and rows that do not, more rows than one run
+# one block per row and several, ragged ends, rows that fit the list and rows that do not
 SIZES = [(1, 1), (3, 2), (7, 100), (5, 4096), (4, 4097), (1, 8192), (2, 8193), (1, 50001), (3, 32000), (40, 9001), (600, 500),
          (1500, 70), (2, 300001)]
 SETTINGS = [dict(), dict(temperature=0.7), dict(temperature=0.0), dict(top_k=1), dict(top_k=50), dict(top_k=50, top_p=0.9),
@@ -237,7 +237,7 @@ def test_frequencies():
 
 
 def test_same_tokens_however_rows_are_spread():
-    # a row alone is spread over several blocks, among many it has one
+    # a row alone and among many
     z, u = inputs(520, 40000, torch.bfloat16, 12)
     for s in (dict(), dict(top_k=40), dict(top_p=0.95), dict(top_p=0.95, temperature=0.5)):
         tokens, logs = oz.sample(z, u, **s)
