@@ -710,7 +710,7 @@ def i8gemm(A, B, a_scale, b_scale, bias=None, out_dtype=None, out=None, workspac
     """C[t, n] = act((sum_k A[t, k] B[n, k]) * a_scale[t] * b_scale[n] + bias[n]) + residual[t, n] for int8 A (t, k) and
     B (n, k), the layout of a linear layer (ozaki2_i8gemm_ws; with an activation, a name from ACTIVATIONS, or a residual
     ozaki2_i8gemm_act_ws). The scales and the bias are float32; ``out_dtype`` is bfloat16 (default), float16 or
-    float32; the residual has that dtype and shares no memory with ``out``; ``workspace`` (optional) a tensor of
+    float32; the residual has that dtype and shares no memory with ``out``, nor do A and B; ``workspace`` (optional) a tensor of
     ``ozaki2_i8gemm_workspace_size`` bytes (with an activation or a residual ``ozaki2_i8gemm_act_workspace_size`` bytes are faster
     for a few rows and a long k)."""
     torch = _torch or _load_torch()
@@ -839,7 +839,7 @@ def linear(X, W, bias=None, activation=None, residual=None, out_dtype=None, out=
     """A linear layer with what follows it: (Y, Z) with Z = X @ W.T + bias and Y = act(Z) + residual (ozaki2_linear_ws).
     X (t, k) and W (n, k) are bfloat16 or float16, the bias float32 (n,), the activation a name from ACTIVATIONS. Y has
     X's dtype unless ``out_dtype`` or ``out`` says float32, and the residual (t, n) has Y's and shares no memory with
-    ``out``. Z, in X's dtype, is what linear_grad needs of a layer with an activation; it is None unless ``want_pre``.
+    ``out``, nor do X and W. Z, in X's dtype, is what linear_grad needs of a layer with an activation; it is None unless ``want_pre``.
     Autograd does not see the call."""
     torch = _torch or _load_torch()
     device, kind, t, n, k, X, ldx, W, ldw = _layer_operands(X, W)
