@@ -571,7 +571,8 @@ int ozaki2_linear_ws(int64_t t, int64_t n, int64_t k, const void *X, int64_t ldx
  *   dX[i][h] = sum_j G[i][j] W[j][h],  dW[j][h] = sum_i G[i][j] X[i][h],  dbias[j] = sum_i G[i][j].
  * G is rounded once to `type` for the two products (without an activation it is dY itself) and not for dbias; sums are
  * binary32, rounded once to `type`. In fp16 G is held in units of a power of two near the largest finite |dY| / 2^15, so that it neither
- * loses bits below 2^-14 (what is below 2^-40 of that |dY| does) nor overflows where dX and dW do not. act'(0) = 0 for relu; a Z that overflowed its type has the slope of its infinity.
+ * loses bits below 2^-14 (what is below 2^-40 of that |dY| does) nor overflows where dX and dW do not.
+ * act'(0) = 0 for relu; a Z that overflowed its type has the slope of its infinity.
  *   t, n, k   as for ozaki2_linear, with n, k < 2^22.
  *   dY, lddy  DEVICE, of `type`, lddy >= max(1, n).
  *   Z, ldz    DEVICE, of `type`, as ozaki2_linear wrote it; not looked at with OZAKI2_ACT_NONE.
